@@ -152,6 +152,99 @@ int mxg_router_bwd(const uint16_t* x, const uint16_t* w_router, const int32_t* i
                    size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* ----------------------------------------------------------------------------
+ * Balance loss of the router.  [Grouped] Fig. 1 (a router picks a few experts
+ * per token); the page trains no router, so this is an addition for callers
+ * that do.  With p = softmax of a token's logits over all E experts, c_e the
+ * number of times expert e is among the ids, P_e the sum of p[t][e] and n the
+ * number of tokens, all over the tokens that token_mask keeps,
+ *   loss = coef * E * sum_e (c_e / (k n)) * (P_e / n)          (0 if n = 0)
+ *   logits      fp32 [T][E]; -inf switches an expert off for the token (a row
+ *               of -inf has p = 0); NaN and +inf give NaN
+ *   ids         int32 [T][k], the route (mxg_route_topk, mxg_router_fwd)
+ *   token_mask  nullable uint8 [T]: 0 = the token (padding) does not count
+ *   loss        fp32 [1] out;  counts int32 [E] out: c_e
+ *   prob_sums   fp32 [E] out: P_e;  n_tokens int32 [1] out: n
+ *   workspace   >= mxg_balance_loss_workspace_bytes(T, E) bytes
+ * Deterministic (fixed-order sums).  Expert ids outside [0, E) are not counted
+ * and reported as MXG_ERR_EXPERT_ID through dev_status.  With tokens spread
+ * over ranks, all-reduce counts, prob_sums and n_tokens: the loss over all of
+ * them is the formula above, and its gradient mxg_balance_loss_bwd with them.
+ * Requires 1 <= k <= E <= 256, k <= 32, T k < 2^31.
+ */
+size_t mxg_balance_loss_workspace_bytes(int T, int E);
+int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, const uint8_t* token_mask, int T, int E, int k,
+                         float coef, float* loss, int32_t* counts, float* prob_sums, int32_t* n_tokens,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Gradient of the balance loss (the counts carry none), and, when ids, probs
+ * and dprobs are given, of the route as well (mxg_router_bwd's dlogit), as one
+ * dense matrix for mxg_router_linear_bwd:
+ *   dlogits[t][e] = dloss coef E / n * p[t][e] (f_e - sum_i p[t][i] f_i),  f_e = c_e / (k n)
+ *                   (0 for tokens that token_mask drops, and if n = 0)
+ *                 + sum over j with ids[t][j] = e of probs[t][j] (dprobs[t][j] - sum_i probs[t][i] dprobs[t][i])
+ *   counts, n_tokens      from mxg_balance_loss_fwd (or summed over ranks)
+ *   dloss                 nullable fp32 [1]: the loss's own gradient (1 if null)
+ *   ids, probs, dprobs    all three or none: int32, fp32, fp32 [T][k]
+ *   dlogits               fp32 [T][E] out
+ * Requirements and reporting as mxg_balance_loss_fwd. */
+int mxg_balance_loss_bwd(const float* logits, const uint8_t* token_mask, const int32_t* counts,
+                         const int32_t* n_tokens, int T, int E, int k, float coef, const float* dloss,
+                         const int32_t* ids, const float* probs, const float* dprobs, float* dlogits,
+                         int32_t* dev_status, void* stream);
+
+/* Backward of the router's linear layer for dense logit gradients (those of
+ * mxg_balance_loss_bwd; mxg_router_bwd takes the chosen experts' only):
+ *   dx        = dx_in + dlogits W_r    (bf16, rounded once)
+ *   dw_router = dlogits^T x            (fp32, overwritten; fixed-order sums)
+ *   x, w_router  bf16 as in mxg_router_fwd;  dlogits fp32 [T][E]
+ *   dx_in        nullable bf16 [T][H] (the MLP's dx; zero if null); may be dx
+ *   dx           bf16 [T][H] out;  dw_router fp32 [E][H] out
+ *   workspace    >= mxg_router_linear_bwd_workspace_bytes(T, H, E) bytes
+ * Requires H % 128 == 0, E <= 256. */
+size_t mxg_router_linear_bwd_workspace_bytes(int T, int H, int E);
+int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router, const float* dlogits, const uint16_t* dx_in,
+                          int T, int H, int E, uint16_t* dx, float* dw_router, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Orthogonalised momentum update (Muon) of a batch of matrices [batch][rows]
+ * [cols]: the experts' weights from the gradients of mxg_grouped_mlp_bwd (bf16
+ * dW or the fp32 main_grad).  An addition: the pages stop at the gradients.
+ *   mom' = mu mom + grad;  u = grad + mu mom' (nesterov) or mom'
+ *   X    = u / |u|_F (a zero matrix stays zero), then `steps` times
+ *          A = X X^T,  X <- a X + (b A + c A A) X     (X^T X for a tall matrix)
+ *   update = scale X                                  (bf16, rounded once)
+ *   w_out  = w_in (1 - lr weight_decay) - lr scale X  (bf16, rounded once)
+ * The products take fp16 operands scaled by powers of two and add up in fp32;
+ * a, b, c must keep the singular values of X within about 2 (3.4445, -4.7750,
+ * 2.0315 keep them below 1.3).  Matrices are independent: a NaN or infinity
+ * stays in its own.
+ * Pointers are 32-byte aligned; momentum_out may be momentum_in and w_out may
+ * be w_in, other buffers do not overlap.
+ * Requires batch <= 65535, rows and cols <= 2^21, batch * max(rows, cols) < 2^31 - 256. */
+typedef struct {
+  int32_t batch, rows, cols;
+  int32_t grad_f32;           /* 0: grad is bf16, 1: fp32                                */
+  const void* grad;
+  const float* momentum_in;   /* nullable: zeros (mom' = grad)                           */
+  float* momentum_out;        /* nullable if momentum_in is: no momentum, u = grad       */
+  float mu;
+  int32_t nesterov;
+  int32_t steps;              /* 1 .. 64                                                 */
+  float a, b, c;
+  float scale;
+  uint16_t* update;           /* nullable bf16 out                                       */
+  const uint16_t* w_in;       /* nullable bf16, with w_out; one of update, w_out is set  */
+  uint16_t* w_out;
+  float lr, weight_decay;
+  void* workspace;            /* >= mxg_muon_workspace_bytes(batch, rows, cols) bytes    */
+  uint64_t workspace_bytes;
+  int32_t* dev_status;
+} mxg_muon_args;
+size_t mxg_muon_workspace_bytes(int batch, int rows, int cols);
+int mxg_muon_update(const mxg_muon_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
  * Permute index: counting sort of the flat index f = t*k + j by expert id,
  * stable in f (bit-exact, deterministic).  [Grouped] "Grouping fragmented
  * expert workloads" (split_sizes: one token count per expert); [Overhead]

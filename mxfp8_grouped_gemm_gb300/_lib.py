@@ -39,6 +39,8 @@ EXPORTS = [
     "mxg_mxfp8_grouped_rows_capacity", "mxg_mxfp8_quantize_grouped", "mxg_gather_rows", "mxg_combine",
     "mxg_mlp_grouped_saved_bytes", "mxg_mlp_grouped_workspace_bytes", "mxg_grouped_mlp_fwd_grouped",
     "mxg_router_fwd_permute", "mxg_grouped_mlp_fwd_grouped_mx",
+    "mxg_balance_loss_workspace_bytes", "mxg_balance_loss_fwd", "mxg_balance_loss_bwd",
+    "mxg_router_linear_bwd_workspace_bytes", "mxg_router_linear_bwd", "mxg_muon_workspace_bytes", "mxg_muon_update",
 ]
 
 FWD_STAGES = ["permute", "quant_weights", "quant_x", "gate_up", "down", "combine"]
@@ -91,6 +93,17 @@ class MlpBwdArgs(ctypes.Structure):
                 ("main_grad_gate_up", ctypes.c_void_p), ("main_grad_down", ctypes.c_void_p)]
 
 
+class MuonArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("grad_f32", ctypes.c_int32), ("grad", ctypes.c_void_p), ("momentum_in", ctypes.c_void_p),
+                ("momentum_out", ctypes.c_void_p), ("mu", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("scale", ctypes.c_float), ("update", ctypes.c_void_p), ("w_in", ctypes.c_void_p),
+                ("w_out", ctypes.c_void_p), ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("dev_status", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -103,6 +116,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m mxfp8_grouped_gemm_gb300.build`")
     L = ctypes.CDLL(LIB_PATH)
     I32, I64, U64, SZ, P = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t, ctypes.c_void_p
+    F32 = ctypes.c_float
     sig = {
         "mxg_status_string": (ctypes.c_char_p, [I32]),
         "mxg_device_supported": (I32, []),
@@ -156,6 +170,13 @@ def lib() -> ctypes.CDLL:
         "mxg_grouped_mlp_fwd_grouped": (I32, [ctypes.POINTER(MlpGroupedFwdArgs), P]),
         "mxg_router_fwd_permute": (I32, [P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P, P]),
         "mxg_grouped_mlp_fwd_grouped_mx": (I32, [ctypes.POINTER(MlpGroupedFwdMxArgs), P]),
+        "mxg_balance_loss_workspace_bytes": (SZ, [I32, I32]),
+        "mxg_balance_loss_fwd": (I32, [P, P, P, I32, I32, I32, F32, P, P, P, P, P, SZ, P, P]),
+        "mxg_balance_loss_bwd": (I32, [P, P, P, P, I32, I32, I32, F32, P, P, P, P, P, P, P]),
+        "mxg_router_linear_bwd_workspace_bytes": (SZ, [I32, I32, I32]),
+        "mxg_router_linear_bwd": (I32, [P, P, P, P, I32, I32, I32, P, P, P, SZ, P, P]),
+        "mxg_muon_workspace_bytes": (SZ, [I32, I32, I32]),
+        "mxg_muon_update": (I32, [ctypes.POINTER(MuonArgs), P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -252,6 +273,144 @@ def mxg_router_bwd(x, w_router, ids, probs, dprobs, dx, dev_status, dw_router=No
         _ptr(dx, torch.bfloat16, "dx"), _ptr(dw_router, torch.float32, "dw_router"), _ptr(workspace), workspace.numel(),
         _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
     return dw_router
+
+
+def _shape(t: torch.Tensor | None, shape: tuple, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _mask_ptr(mask: torch.Tensor | None, T: int) -> int | None:
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"token_mask must be bool or uint8, got {mask.dtype}")
+    _shape(mask, (T,), "token_mask")
+    return _ptr(mask, None, "token_mask")
+
+
+def mxg_balance_loss_workspace_bytes(T, E) -> int:
+    return int(lib().mxg_balance_loss_workspace_bytes(T, E))
+
+
+def mxg_balance_loss_fwd(logits, ids, coef: float, dev_status, token_mask=None, loss=None, counts=None, prob_sums=None,
+                         n_tokens=None, workspace=None, stream=None):
+    """Balance loss of the router -> (loss fp32 [1], counts int32 [E], prob_sums fp32 [E], n_tokens int32 [1])."""
+    T, E = logits.shape
+    k = ids.shape[-1]
+    dev = logits.device
+    _shape(ids, (T, k), "ids")
+    loss = torch.empty(1, dtype=torch.float32, device=dev) if loss is None else loss
+    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
+    prob_sums = torch.empty(E, dtype=torch.float32, device=dev) if prob_sums is None else prob_sums
+    n_tokens = torch.empty(1, dtype=torch.int32, device=dev) if n_tokens is None else n_tokens
+    _shape(loss, (1,), "loss")
+    _shape(counts, (E,), "counts")
+    _shape(prob_sums, (E,), "prob_sums")
+    _shape(n_tokens, (1,), "n_tokens")
+    if workspace is None:
+        workspace = torch.empty(max(mxg_balance_loss_workspace_bytes(T, E), 32), dtype=torch.uint8, device=dev)
+    _check("mxg_balance_loss_fwd", lib().mxg_balance_loss_fwd(
+        _ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _mask_ptr(token_mask, T), T, E, k, coef,
+        _ptr(loss, torch.float32, "loss"), _ptr(counts, torch.int32, "counts"),
+        _ptr(prob_sums, torch.float32, "prob_sums"), _ptr(n_tokens, torch.int32, "n_tokens"), _ptr(workspace),
+        workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    return loss, counts, prob_sums, n_tokens
+
+
+def mxg_balance_loss_bwd(logits, counts, n_tokens, k: int, coef: float, dev_status, dloss=None, token_mask=None,
+                         route=None, dlogits=None, stream=None):
+    """Gradient of the balance loss on the logits, fp32 [T, E]; route = (ids, probs, dprobs) adds the route's own."""
+    T, E = logits.shape
+    dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device) if dlogits is None else dlogits
+    ids, probs, dprobs = (None, None, None) if route is None else route
+    _shape(dlogits, (T, E), "dlogits")
+    _shape(counts, (E,), "counts")
+    _shape(n_tokens, (1,), "n_tokens")
+    _shape(dloss, (1,), "dloss")
+    _shape(ids, (T, k), "ids")
+    _shape(probs, (T, k), "probs")
+    _shape(dprobs, (T, k), "dprobs")
+    _check("mxg_balance_loss_bwd", lib().mxg_balance_loss_bwd(
+        _ptr(logits, torch.float32, "logits"), _mask_ptr(token_mask, T), _ptr(counts, torch.int32, "counts"),
+        _ptr(n_tokens, torch.int32, "n_tokens"), T, E, k, coef, _ptr(dloss, torch.float32, "dloss"),
+        _ptr(ids, torch.int32, "ids"), _ptr(probs, torch.float32, "probs"), _ptr(dprobs, torch.float32, "dprobs"),
+        _ptr(dlogits, torch.float32, "dlogits"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    return dlogits
+
+
+def mxg_router_linear_bwd_workspace_bytes(T, H, E) -> int:
+    return int(lib().mxg_router_linear_bwd_workspace_bytes(T, H, E))
+
+
+def mxg_router_linear_bwd(x, w_router, dlogits, dx_in, dev_status, dx=None, dw_router=None, workspace=None,
+                          stream=None):
+    """Router linear layer's backward for dense logit gradients: (dx = dx_in + dlogits W_r, dW_r = dlogits^T x).
+    dx_in None: no other gradient; dx may be dx_in."""
+    T, H = x.shape
+    E = w_router.shape[0]
+    dev = x.device
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if dx is None else dx
+    dw_router = torch.empty((E, H), dtype=torch.float32, device=dev) if dw_router is None else dw_router
+    _shape(w_router, (E, H), "w_router")
+    _shape(dlogits, (T, E), "dlogits")
+    _shape(dx_in, (T, H), "dx_in")
+    _shape(dx, (T, H), "dx")
+    _shape(dw_router, (E, H), "dw_router")
+    if workspace is None:
+        workspace = torch.empty(max(mxg_router_linear_bwd_workspace_bytes(T, H, E), 32), dtype=torch.uint8, device=dev)
+    _check("mxg_router_linear_bwd", lib().mxg_router_linear_bwd(
+        _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.bfloat16, "w_router"),
+        _ptr(dlogits, torch.float32, "dlogits"), _ptr(dx_in, torch.bfloat16, "dx_in"), T, H, E,
+        _ptr(dx, torch.bfloat16, "dx"), _ptr(dw_router, torch.float32, "dw_router"), _ptr(workspace),
+        workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    return dx, dw_router
+
+
+def mxg_muon_workspace_bytes(batch, rows, cols) -> int:
+    return int(lib().mxg_muon_workspace_bytes(batch, rows, cols))
+
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def mxg_muon_update(grad, dev_status, momentum=None, momentum_out=None, mu: float = 0.95, nesterov: bool = True,
+                    steps: int = 5, coefficients=MUON_COEFFICIENTS, scale: float = 1.0, update=None, weights=None,
+                    weights_out=None, lr: float = 0.0, weight_decay: float = 0.0, workspace=None, stream=None):
+    """Orthogonalised momentum update of grad [batch, rows, cols] (or [rows, cols]; bf16 or fp32).
+
+    momentum (fp32) is read and momentum_out written (momentum itself if not given); with momentum_out alone the
+    momentum starts at zero, with neither there is none.  weights (bf16): the new weights go to weights_out
+    (weights itself if not given) and are returned; otherwise the bf16 update is (also where `update` is given)."""
+    shape = tuple(grad.shape)
+    if grad.dim() not in (2, 3):
+        raise ValueError(f"grad must be [rows, cols] or [batch, rows, cols], got {list(shape)}")
+    if grad.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"grad must be bfloat16 or float32, got {grad.dtype}")
+    if weights_out is not None and weights is None:
+        raise ValueError("weights_out needs weights")
+    batch, rows, cols = shape if grad.dim() == 3 else (1, *shape)
+    dev = grad.device
+    momentum_out = momentum if momentum_out is None else momentum_out
+    weights_out = weights if weights_out is None else weights_out
+    if update is None and weights is None:
+        update = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    for name, t in (("momentum", momentum), ("momentum_out", momentum_out), ("update", update), ("weights", weights),
+                    ("weights_out", weights_out)):
+        _shape(t, shape, name)
+    if workspace is None:
+        workspace = torch.empty(max(mxg_muon_workspace_bytes(batch, rows, cols), 32), dtype=torch.uint8, device=dev)
+    a, b, c = coefficients
+    args = MuonArgs(batch=batch, rows=rows, cols=cols, grad_f32=int(grad.dtype == torch.float32),
+                    grad=_ptr(grad, None, "grad"), momentum_in=_ptr(momentum, torch.float32, "momentum"),
+                    momentum_out=_ptr(momentum_out, torch.float32, "momentum_out"), mu=mu, nesterov=int(nesterov),
+                    steps=steps, a=a, b=b, c=c, scale=scale, update=_ptr(update, torch.bfloat16, "update"),
+                    w_in=_ptr(weights, torch.bfloat16, "weights"),
+                    w_out=_ptr(weights_out, torch.bfloat16, "weights_out"), lr=lr, weight_decay=weight_decay,
+                    workspace=_ptr(workspace), workspace_bytes=workspace.numel(),
+                    dev_status=_ptr(dev_status, torch.int32, "dev_status"))
+    _check("mxg_muon_update", lib().mxg_muon_update(ctypes.byref(args), _stream(stream)))
+    return update if weights is None else weights_out
 
 
 def mxg_route_permute(ids: torch.Tensor, E: int, dev_status: torch.Tensor, stream=None) -> dict:

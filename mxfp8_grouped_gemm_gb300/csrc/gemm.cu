@@ -1496,6 +1496,11 @@ bool tma_map_bf16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
   return encode_bf16(m, base, cols, rows, box_rows);
 }
 
+bool tma_map_f16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows) {
+  return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, rows, ld * 2, 64, box_rows,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 int gemm_pick_bn(int epi, int N) {
   if (epi == EPI_SWIGLU) return 256;
   return N % 256 == 0 ? 256 : 128;

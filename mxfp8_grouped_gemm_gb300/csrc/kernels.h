@@ -108,6 +108,9 @@ cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);
 // past the matrix's edges fill zeros.
 bool tma_map_bf16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t box_rows);
 
+// The same over an fp16 matrix whose rows are `ld` elements apart (a multiple of 8).
+bool tma_map_f16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows);
+
 // Router logits on the tensor cores and the top-k route (router_mma.cu):
 // logits fp32 [T][E] = x [T][H] W_r [E][H]^T, then ids / probs as the route.
 // When counts is given (zeroed by the caller), every CTA also adds its
