@@ -175,9 +175,12 @@ constexpr int kNsK = 64;                  // contraction elements per stage: one
 constexpr int kNsRows = 128;              // rows of each operand per SM and stage
 constexpr int kNsOpBytes = kNsRows * kNsK * 2;
 constexpr int kNsStageBytes = 2 * kNsOpBytes;
-constexpr int kNsStages = 6;
+constexpr int kNsStages = 5;
+constexpr int kNsBox = 2048;              // 32 x 32 fp16: one store box
+constexpr int kNsWarpOut = 4 * kNsBox;    // per epilogue warp: two boxes of D and two of D^T
 constexpr int kNsCtrl = 1024;
-constexpr int kNsSmem = 1024 + kNsStages * kNsStageBytes + kNsCtrl;
+constexpr int kNsSmem = 1024 + kNsStages * kNsStageBytes + 8 * kNsWarpOut + kNsCtrl;
+static_assert(32 * 33 * 4 <= kNsWarpOut, "the last product stages 32 x 32 fp32 values");
 static_assert(kNsSmem <= 232448, "shared memory budget");
 
 struct NsArgs {
@@ -188,12 +191,8 @@ struct NsArgs {
   int64_t total;                          // tiles of all matrices
   int p_rows, q_rows;                     // operand rows per matrix
   float alpha, beta;                      // D = alpha P Q^T + beta C
-  const __half* c;                        // [batch][m][ldc], nullable
+  const __half* c;                        // [batch][m][ldc], nullable; ldc a multiple of 16
   int64_t ldc, sc;
-  __half* o;                              // D in fp16, nullable
-  int64_t ldo, so;
-  __half* ot;                             // D^T in fp16, nullable
-  int64_t ldt, st;
   // the last product: bf16 update, or new weights, in the caller's layout
   uint16_t* update;                       // nullable
   const uint16_t* w_in;
@@ -227,16 +226,103 @@ __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   return r;
 }
 
-template <bool PAIR>
+// 32 columns of C for this thread's row, zero past the matrix.
+__device__ __forceinline__ void ns_load_c(const NsArgs& P, int b, int row, int col, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (row < P.m && col + 16 * h < P.n) {          // whole 32-byte pieces: ldc is a multiple of 16
+      ld_global_nc_v8(P.c + b * P.sc + row * P.ldc + col + 16 * h, w + 8 * h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[8 * h + i] = 0u;
+    }
+  }
+}
+
+// One 32 x 32 block of D = alpha acc + beta C as fp16, to D and (mirror) D^T:
+// staged in two 2 KB boxes (64-byte rows, 16-byte chunk j of row r at
+// j ^ ((r / 2) % 4): the tensor maps' 64-byte swizzle) and stored by TMA, which
+// also cuts the block at the matrix's edges.  A lane writes its row of D in
+// four 16-byte pieces and its column of D^T in 2-byte pieces, 32 lanes side by
+// side: both free of bank conflicts.
+__device__ __forceinline__ void ns_store_block(const NsArgs& P, const uint32_t (&r)[32], const uint32_t (&c)[16],
+                                               uint8_t* box, const CUtensorMap* tmO, const CUtensorMap* tmT, int row0,
+                                               int col0, int b, bool mirror, int lane) {
+  uint32_t h[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
+    const __half2 v = __floats2half2_rn(fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r[2 * i])),
+                                        fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r[2 * i + 1])));
+    h[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  // the boxes written two blocks ago have left shared memory
+  if (lane == 0) bulk_wait_group_read<1>();
+  __syncwarp();
+  const int sw = (lane >> 1) & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ sw) << 4)) =
+        make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+  if (mirror) {
+    uint8_t* tb = box + kNsBox;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {                   // row i of the transposed box, column `lane`
+      const uint16_t v = static_cast<uint16_t>(i & 1 ? h[i / 2] >> 16 : h[i / 2]);
+      *reinterpret_cast<uint16_t*>(tb + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2) = v;
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(tmO, box, col0, row0, b);
+    if (mirror) tma_store_3d(tmT, box + kNsBox, row0, col0, b);
+    bulk_commit_group();
+  }
+}
+
+// One 32 x 32 block of the last product to the caller's bf16 matrix, whose
+// rows may start at any even address: staged in fp32 (rows of 33 words) and
+// written row by row of the caller's matrix, 32 lanes side by side.
+__device__ __forceinline__ void ns_store_last(const NsArgs& P, const uint32_t (&r)[32], const uint32_t (&c)[16],
+                                              float* buf, int row0, int col0, int b, int lane) {
+  __syncwarp();                                      // the previous block has been read
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
+    buf[lane * 33 + 2 * i] = fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r[2 * i]));
+    buf[lane * 33 + 2 * i + 1] = fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r[2 * i + 1]));
+  }
+  __syncwarp();
+  const int y0 = P.flip ? col0 : row0, x0 = P.flip ? row0 : col0;      // of the caller's matrix
+  const int ny = min(32, (P.flip ? P.n : P.m) - y0);
+  const bool in = x0 + lane < (P.flip ? P.m : P.n);
+  const int64_t base = b * P.su + static_cast<int64_t>(y0) * P.ldu + x0 + lane;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    if (i < ny && in) {
+      const float v = P.flip ? buf[lane * 33 + i] : buf[i * 33 + lane];
+      const int64_t u = base + i * P.ldu;
+      if (P.update != nullptr) P.update[u] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+      if (P.w_out != nullptr)
+        P.w_out[u] =
+            static_cast<uint16_t>(pack_bf16x2(fmaf(-P.lr, v, bf16_bits_to_float(P.w_in[u]) * P.w_keep), 0.f));
+    }
+  }
+}
+
+template <bool PAIR, bool LAST>
 __global__ void __launch_bounds__(kNsThreads, 1)
     ns_product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmT,
                       const __grid_constant__ NsArgs P) {
   constexpr int CG = PAIR ? 2 : 1;
   constexpr int BN = PAIR ? 256 : 128;    // columns of a tile (and accumulator columns)
   constexpr int TM = PAIR ? 256 : 128;    // rows of a tile, both CTAs
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kNsStages * kNsStageBytes);
+  uint8_t* boxes = sm + kNsStages * kNsStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 8 * kNsWarpOut);
   uint64_t* empty = full + kNsStages;
   uint64_t* tfull = empty + kNsStages;
   uint64_t* tempty = tfull + 2;
@@ -378,9 +464,24 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     constexpr int COLS = BN / 2;
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
-    uint32_t acc = 0, acc_phase = 0;
+    uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
+    uint32_t acc = 0, acc_phase = 0, flip = 0;
     for (int64_t t = tile0; t < P.total; t += tstep) {
       const NsTile tc = ns_tile(P, t);
+      const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
+      const int col0 = tc.tj * BN + hf * COLS;
+      const bool mirror = P.sym == 0 || tc.ti != tc.tj;
+      // the addend is on its way while the tile's MMAs run
+      uint32_t cv[COLS / 32][16];
+#pragma unroll
+      for (int c = 0; c < COLS / 32; ++c) {
+        if (P.c != nullptr) {
+          ns_load_c(P, tc.b, row0 + lane, col0 + 32 * c, cv[c]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) cv[c][i] = 0u;
+        }
+      }
       bool got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs);
       got = __all_sync(0xffffffffu, got);
       if (!got) {
@@ -389,45 +490,37 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       }
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
-      const int row = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32 + lane;
-      const int col0 = tc.tj * BN + hf * COLS;
-      const bool mirror = P.sym ? tc.ti != tc.tj : true;
-#pragma unroll 1
-      for (int c = 0; c < COLS; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tb + c, r);
-        tmem_ld_wait();
-        if (row < P.m) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int col = col0 + c + i;
-            if (col < P.n) {
-              float v = P.alpha * __uint_as_float(r[i]);
-              if (P.c != nullptr) v = fmaf(P.beta, __half2float(P.c[tc.b * P.sc + row * P.ldc + col]), v);
-              const __half h = __float2half_rn(v);
-              if (P.o != nullptr) P.o[tc.b * P.so + row * P.ldo + col] = h;
-              if (P.ot != nullptr && mirror) P.ot[tc.b * P.st + col * P.ldt + row] = h;
-              const int64_t u = tc.b * P.su + (P.flip ? col * P.ldu + row : row * P.ldu + col);
-              if (P.update != nullptr) P.update[u] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-              if (P.w_out != nullptr)
-                P.w_out[u] = static_cast<uint16_t>(
-                    pack_bf16x2(fmaf(-P.lr, v, bf16_bits_to_float(P.w_in[u]) * P.w_keep), 0.f));
-            }
+      for (int c = 0; c < COLS / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tb + 32 * c, r);
+        tmem_ld_wait();
+        if (c == COLS / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR && rank == 1)
+              st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
+                                   map_to_rank(smem_u32(&tempty[acc]), 0));
+            else
+              mbar_arrive(&tempty[acc]);
           }
         }
-        __syncwarp();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR && rank == 1)
-          st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
-                               map_to_rank(smem_u32(&tempty[acc]), 0));
-        else
-          mbar_arrive(&tempty[acc]);
+        if (row0 < P.m && col0 + 32 * c < P.n) {
+          if constexpr (LAST) {
+            ns_store_last(P, r, cv[c], reinterpret_cast<float*>(box), row0, col0 + 32 * c, tc.b, lane);
+          } else {
+            ns_store_block(P, r, cv[c], box + flip * 2 * kNsBox, &tmO, &tmT, row0, col0 + 32 * c, tc.b, mirror, lane);
+            flip ^= 1;
+          }
+        }
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
+    }
+    if (!LAST) {
+      if (lane == 0) bulk_wait_group<0>();           // the stores have completed before the CTA exits
+      __syncwarp();
     }
   }
 
@@ -446,9 +539,10 @@ int sm_count() {
   return n > 0 ? n : 1;
 }
 
-template <bool PAIR>
-cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const NsArgs& a, cudaStream_t s) {
-  auto kern = ns_product_kernel<PAIR>;
+template <bool PAIR, bool LAST>
+cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, const CUtensorMap& mt,
+                      const NsArgs& a, cudaStream_t s) {
+  auto kern = ns_product_kernel<PAIR, LAST>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
   if (err != cudaSuccess) return err;
   const int64_t units = PAIR ? sm_count() / 2 : sm_count();
@@ -467,28 +561,45 @@ cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const NsArgs
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  err = cudaLaunchKernelEx(&cfg, kern, mp, mq, a);
+  err = cudaLaunchKernelEx(&cfg, kern, mp, mq, mo, mt, a);
   count_launch();
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// D of one product over the batch.  p, q: fp16 operands [batch][rows][ld].
-cudaError_t ns_product(NsArgs a, const __half* p, int64_t ldp, const __half* q, int64_t ldq, cudaStream_t s) {
-  CUtensorMap mp, mq;
-  if (!tma_map_f16(&mp, p, a.k, static_cast<int64_t>(a.batch) * a.p_rows, ldp, kNsRows) ||
-      !tma_map_f16(&mq, q, a.k, static_cast<int64_t>(a.batch) * a.q_rows, ldq, kNsRows))
+struct NsMat {                            // fp16 [batch][rows][cols], rows ld apart
+  __half* p;
+  int rows, cols;
+  int64_t ld;
+};
+
+// D of one product over the batch: operands p and q, D and D^T to o and t
+// (none for the last product, whose outputs are in a).
+cudaError_t ns_product(NsArgs a, const NsMat& p, const NsMat& q, const NsMat* o, const NsMat* t, cudaStream_t s) {
+  CUtensorMap mp, mq, mo, mt;
+  a.p_rows = p.rows;
+  a.q_rows = q.rows;
+  a.m = p.rows;
+  a.n = q.rows;
+  a.k = p.cols;
+  if (!tma_map_f16(&mp, p.p, p.cols, static_cast<int64_t>(a.batch) * p.rows, p.ld, kNsRows) ||
+      !tma_map_f16(&mq, q.p, q.cols, static_cast<int64_t>(a.batch) * q.rows, q.ld, kNsRows))
     return cudaErrorInvalidValue;
-  auto tiles = [&](int t) {
-    a.tiles_m = (a.m + t - 1) / t;
-    a.tiles_n = (a.n + t - 1) / t;
+  mo = mt = mp;
+  if (o != nullptr && (!tma_map_f16_boxes(&mo, o->p, o->cols, o->rows, a.batch, o->ld) ||
+                       !tma_map_f16_boxes(&mt, t->p, t->cols, t->rows, a.batch, t->ld)))
+    return cudaErrorInvalidValue;
+  auto tiles = [&](int w) {
+    a.tiles_m = (a.m + w - 1) / w;
+    a.tiles_n = (a.n + w - 1) / w;
     const int64_t per = a.sym ? static_cast<int64_t>(a.tiles_m) * (a.tiles_m + 1) / 2
                               : static_cast<int64_t>(a.tiles_m) * a.tiles_n;
     a.total = per * a.batch;
     return a.total;
   };
-  if (tiles(256) >= sm_count() / 2) return launch_ns<true>(mp, mq, a, s);
+  if (tiles(256) >= sm_count() / 2)
+    return o != nullptr ? launch_ns<true, false>(mp, mq, mo, mt, a, s) : launch_ns<true, true>(mp, mq, mo, mt, a, s);
   tiles(128);
-  return launch_ns<false>(mp, mq, a, s);
+  return o != nullptr ? launch_ns<false, false>(mp, mq, mo, mt, a, s) : launch_ns<false, true>(mp, mq, mo, mt, a, s);
 }
 
 struct NsPlan {
@@ -556,11 +667,12 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   api::NvtxRange nvtx("mxg.muon_update");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* part = api::at<double>(a->workspace, p.part);
-  __half* x[2] = {api::at<__half>(a->workspace, p.x0), api::at<__half>(a->workspace, p.x1)};
-  __half* xt[2] = {api::at<__half>(a->workspace, p.t0), api::at<__half>(a->workspace, p.t1)};
-  __half* am = api::at<__half>(a->workspace, p.a);
-  __half* bm = api::at<__half>(a->workspace, p.b);
-  const int64_t sx = p.m * p.ldx, st = p.n * p.ldt, sa = p.m * p.ldt;
+  const NsMat x[2] = {{api::at<__half>(a->workspace, p.x0), p.m, p.n, p.ldx},
+                      {api::at<__half>(a->workspace, p.x1), p.m, p.n, p.ldx}};
+  const NsMat xt[2] = {{api::at<__half>(a->workspace, p.t0), p.n, p.m, p.ldt},
+                       {api::at<__half>(a->workspace, p.t1), p.n, p.m, p.ldt}};
+  const NsMat am{api::at<__half>(a->workspace, p.a), p.m, p.m, p.ldt};
+  const NsMat bm{api::at<__half>(a->workspace, p.b), p.m, p.m, p.ldt};
   int ex = 0;                             // 2^ex ~ sqrt(n)
   while ((1ll << (2 * ex)) < p.n) ++ex;
 
@@ -571,64 +683,52 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   count_launch();
   const dim3 cgrid(static_cast<unsigned>((a->cols + kMoTile - 1) / kMoTile),
                    static_cast<unsigned>((a->rows + kMoTile - 1) / kMoTile), static_cast<unsigned>(a->batch));
-  cast_kernel<<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, p.tall ? xt[0] : x[0], p.tall ? p.ldt : p.ldx,
-                                           p.tall ? st : sx, p.tall ? x[0] : xt[0], p.tall ? p.ldx : p.ldt,
-                                           p.tall ? sx : st);
+  const NsMat& u = p.tall ? xt[0] : x[0];
+  const NsMat& ut = p.tall ? x[0] : xt[0];
+  cast_kernel<<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, u.p, u.ld, u.rows * u.ld, ut.p, ut.ld,
+                                           ut.rows * ut.ld);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
 
   for (int i = 0; i < a->steps; ++i) {
     const int cur = i & 1, nxt = cur ^ 1;
-    NsArgs g{};
-    g.batch = a->batch;
-    g.status = a->dev_status;
-    // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex)
-    g.sym = 1;
-    g.m = g.n = p.m;
-    g.k = p.n;
-    g.p_rows = g.q_rows = p.m;
-    g.alpha = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
-    g.o = g.ot = am;
-    g.ldo = g.ldt = p.ldt;
-    g.so = g.st = sa;
-    MXG_TRY(ns_product(g, x[cur], p.ldx, x[cur], p.ldx, s));
-    // B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
-    g.k = p.m;
-    g.alpha = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
-    g.beta = a->b;
-    g.c = am;
-    g.ldc = p.ldt;
-    g.sc = sa;
-    g.o = g.ot = bm;
-    MXG_TRY(ns_product(g, am, p.ldt, am, p.ldt, s));
-    // X' 2^ex = a (X 2^ex) + 2^-12 (B 2^12)(X 2^ex); the last one leaves as scale X'
     const bool last = i + 1 == a->steps;
+    // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex)
+    NsArgs ga{};
+    ga.batch = a->batch;
+    ga.status = a->dev_status;
+    ga.sym = 1;
+    ga.alpha = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
+    MXG_TRY(ns_product(ga, x[cur], x[cur], &am, &am, s));
+    // B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
+    NsArgs gb = ga;
+    gb.alpha = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
+    gb.beta = a->b;
+    gb.c = am.p;
+    gb.ldc = am.ld;
+    gb.sc = am.rows * am.ld;
+    MXG_TRY(ns_product(gb, am, am, &bm, &bm, s));
+    // X' 2^ex = a (X 2^ex) + 2^-12 (B 2^12)(X 2^ex); the last one leaves as scale X'
     const double f = last ? a->scale * std::ldexp(1.0, -ex) : 1.0;
-    g.sym = 0;
-    g.n = p.n;
-    g.q_rows = p.n;
-    g.alpha = static_cast<float>(f * std::ldexp(1.0, -kExpA));
-    g.beta = static_cast<float>(f * a->a);
-    g.c = x[cur];
-    g.ldc = p.ldx;
-    g.sc = sx;
-    g.o = last ? nullptr : x[nxt];
-    g.ldo = p.ldx;
-    g.so = sx;
-    g.ot = last ? nullptr : xt[nxt];
-    g.ldt = p.ldt;
-    g.st = st;
+    NsArgs gx{};
+    gx.batch = a->batch;
+    gx.status = a->dev_status;
+    gx.alpha = static_cast<float>(f * std::ldexp(1.0, -kExpA));
+    gx.beta = static_cast<float>(f * a->a);
+    gx.c = x[cur].p;
+    gx.ldc = x[cur].ld;
+    gx.sc = x[cur].rows * x[cur].ld;
     if (last) {
-      g.update = a->update;
-      g.w_in = a->w_in;
-      g.w_out = a->w_out;
-      g.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
-      g.lr = a->lr;
-      g.flip = p.tall;
-      g.ldu = a->cols;
-      g.su = mo.per;
+      gx.update = a->update;
+      gx.w_in = a->w_in;
+      gx.w_out = a->w_out;
+      gx.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
+      gx.lr = a->lr;
+      gx.flip = p.tall;
+      gx.ldu = a->cols;
+      gx.su = mo.per;
     }
-    MXG_TRY(ns_product(g, bm, p.ldt, xt[cur], p.ldt, s));
+    MXG_TRY(ns_product(gx, bm, xt[cur], last ? nullptr : &x[nxt], last ? nullptr : &xt[nxt], s));
   }
   return MXG_OK;
 }
