@@ -1496,21 +1496,17 @@ bool tma_map_bf16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
   return encode_bf16(m, base, cols, rows, box_rows);
 }
 
-bool tma_map_f16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows) {
-  return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, rows, ld * 2, 64, box_rows,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-}
-
-bool tma_map_f16_boxes(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld) {
+bool tma_map_b16_3d(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
+                    uint32_t box_rows) {
   EncodeTiledFn enc = get_encode();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(batch)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld * rows) * 2};
-  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t box[3] = {64, box_rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

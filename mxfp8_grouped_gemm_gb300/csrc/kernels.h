@@ -108,13 +108,12 @@ cudaError_t launch_permute(const PermuteParams& p, cudaStream_t s);
 // past the matrix's edges fill zeros.
 bool tma_map_bf16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t box_rows);
 
-// The same over an fp16 matrix whose rows are `ld` elements apart (a multiple of 8).
-bool tma_map_f16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows);
-
-// 32 x 32 boxes (64-byte swizzle) of fp16 matrices [batch][rows][cols], rows
-// `ld` elements apart (a multiple of 8) and matrices rows * ld: store boxes
-// are cut at each matrix's own edges.
-bool tma_map_f16_boxes(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld);
+// Boxes of 64 columns (one 128-byte swizzled row) x box_rows rows of 16-bit
+// matrices [batch][rows][cols], rows `ld` elements apart (a multiple of 8) and
+// matrices rows * ld: loads read zeros past each matrix's own edges, stores
+// write nothing there.
+bool tma_map_b16_3d(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
+                    uint32_t box_rows);
 
 // Router logits on the tensor cores and the top-k route (router_mma.cu):
 // logits fp32 [T][E] = x [T][H] W_r [E][H]^T, then ids / probs as the route.

@@ -9,14 +9,16 @@
 // The odd quintic drives every singular value of X towards one, so X becomes
 // the orthogonal factor of u.
 //
-// The matrix is taken with its short side first (X [M][N], M <= N; a tall one
-// transposed), since A is then the smaller product.  Every product is one of
-// tcgen05 kind::f16 on operands stored with the contraction contiguous:
-//   A  = X X^T        rows of X with rows of X
-//   B  = b A + c A A  rows of A with rows of A   (A is symmetric)
-//   X' = a X + B X    rows of B with rows of X^T
-// so X is kept together with its transpose.  A and B are symmetric: only the
-// tiles on and above the diagonal are computed, each stored twice.
+// Every matrix is stored once, in the caller's orientation.  With M the short
+// side and N the long one, the three products of a step contract over
+//   A  = X X^T           N   (a tall X [N][M]: A = X^T X)
+//   B  = b A + c A A     M
+//   X' = a X + B X       M   (tall: X' = a X + X B)
+// on tcgen05 kind::f16, whose operands may be read with the contraction
+// contiguous (K-major) or across it (MN-major), so no transposed copy is kept.
+// A and B are symmetric: only their tiles on and above the diagonal are
+// computed and stored, and a block below it is read as the transpose of the
+// one above (see ns_transposed).
 //
 // Number format.  Operands are fp16: X, A and B are bounded (|X|_F = 1 at the
 // start, singular values at most ~1.2 afterwards), so the eleven-bit
@@ -65,7 +67,7 @@ struct SumSq {
 };
 
 constexpr int kMoThreads = 256;
-constexpr int kMoTile = 64;               // the cast works on 64 x 64 tiles
+constexpr int kMoVec = 8;                 // elements a thread takes at once
 
 struct MomentumArgs {
   const void* grad;                       // bf16 or fp32 [batch][rows][cols]
@@ -74,36 +76,77 @@ struct MomentumArgs {
   float* mom_out;                         // nullable
   float mu;
   int nesterov;
-  int rows, cols;                         // as the caller has them
-  int64_t per;                            // rows * cols
+  int64_t per;                            // elements of a matrix
 };
 
-__device__ __forceinline__ float load_grad(const MomentumArgs& P, int64_t i) {
-  return P.grad_f32 ? static_cast<const float*>(P.grad)[i]
-                    : bf16_bits_to_float(static_cast<const uint16_t*>(P.grad)[i]);
-}
-
-// Momentum of element i (new, written when asked) -> u.
-template <bool WRITE>
-__device__ __forceinline__ float momentum_u(const MomentumArgs& P, int64_t i) {
-  const float g = load_grad(P, i);
-  float m;
-  if (WRITE || P.mom_out == nullptr) {
-    m = P.mom_in != nullptr ? fmaf(P.mu, P.mom_in[i], g) : g;
-    if (WRITE && P.mom_out != nullptr) P.mom_out[i] = m;
+template <bool VEC>
+__device__ __forceinline__ void load_f32(const float* p, int64_t i, int n, float (&v)[kMoVec]) {
+  if constexpr (VEC) {
+    uint32_t w[8];
+    ld_global_v8(p + i, w);
+#pragma unroll
+    for (int j = 0; j < kMoVec; ++j) v[j] = __uint_as_float(w[j]);
   } else {
-    m = P.mom_out[i];
+#pragma unroll
+    for (int j = 0; j < kMoVec; ++j) v[j] = j < n ? p[i + j] : 0.f;
   }
-  return P.mom_out != nullptr ? (P.nesterov ? fmaf(P.mu, m, g) : m) : g;
 }
 
-// New momentum and the sum of squares of u: one partial per block.
+template <bool VEC>
+__device__ __forceinline__ void load_grad(const MomentumArgs& P, int64_t i, int n, float (&v)[kMoVec]) {
+  if (P.grad_f32) {
+    load_f32<VEC>(static_cast<const float*>(P.grad), i, n, v);
+  } else {
+    const uint16_t* g = static_cast<const uint16_t*>(P.grad) + i;
+    if constexpr (VEC) {
+      const uint4 q = *reinterpret_cast<const uint4*>(g);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) v[j] = j < n ? bf16_bits_to_float(g[j]) : 0.f;
+    }
+  }
+}
+
+// New momentum and the sum of squares of u: one partial per block.  VEC: every
+// matrix starts on a 32-byte boundary of each buffer.
+template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part) {
   const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
   SumSq s{0.f, 0.f, 0.f};
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x; i < P.per;
-       i += static_cast<int64_t>(chunks) * kMoThreads)
-    s.add(momentum_u<true>(P, base + i));
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
+       i += static_cast<int64_t>(chunks) * kMoThreads * kMoVec) {
+    const int n = static_cast<int>(P.per - i < kMoVec ? P.per - i : kMoVec);
+    float g[kMoVec], m[kMoVec];
+    load_grad<VEC>(P, base + i, n, g);
+    if (P.mom_in != nullptr) {
+      load_f32<VEC>(P.mom_in, base + i, n, m);
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) m[j] = fmaf(P.mu, m[j], g[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) m[j] = g[j];
+    }
+    if (P.mom_out != nullptr) {
+      if constexpr (VEC) {
+        st_global_v8(P.mom_out + base + i, reinterpret_cast<const uint32_t*>(m));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kMoVec; ++j)
+          if (j < n) P.mom_out[base + i + j] = m[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) s.add(P.nesterov ? fmaf(P.mu, m[j], g[j]) : m[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) s.add(g[j]);
+    }
+  }
   double t = s.total();
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
@@ -117,17 +160,25 @@ __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, in
   }
 }
 
-// X0 and its transpose in fp16: u / |u|_F 2^ex.  One 64 x 64 tile per block.
-// x: the matrix in the caller's orientation, xt: its transpose.
+// X0 = u / |u|_F 2^ex in fp16, rows ld apart.  A block takes whole rows; its
+// first act is the matrix's norm from the partials (the same sum, in the same
+// order, in every block).
+template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int chunks, const double* __restrict__ part,
-                                                         int ex, __half* __restrict__ x, int64_t ldx, int64_t sx,
-                                                         __half* __restrict__ xt, int64_t ldt, int64_t st) {
-  __shared__ __half tile[kMoTile][kMoTile + 2];
+                                                         int ex, int rows, int cols, __half* __restrict__ x,
+                                                         int64_t ld) {
+  __shared__ double s_w[kMoThreads / 32];
   __shared__ float s_f[3];
-  const int b = blockIdx.z;
+  const int b = blockIdx.y;
+  double n2 = 0.0;
+  for (int i = threadIdx.x; i < chunks; i += kMoThreads) n2 += part[static_cast<int64_t>(b) * chunks + i];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, off);
+  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = n2;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    double n2 = 0.0;
-    for (int i = 0; i < chunks; ++i) n2 += part[static_cast<int64_t>(b) * chunks + i];
+    n2 = 0.0;
+    for (int i = 0; i < kMoThreads / 32; ++i) n2 += s_w[i];
     // u / |u| 2^ex as three factors, so no intermediate leaves fp32's range
     const double norm = sqrt(n2);
     if (norm == 0.0) {
@@ -145,61 +196,88 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
   }
   __syncthreads();
   const float f0 = s_f[0], f1 = s_f[1], f2 = s_f[2];
-  const int r0 = blockIdx.y * kMoTile, c0 = blockIdx.x * kMoTile;
-  for (int i = threadIdx.x; i < kMoTile * kMoTile; i += kMoThreads) {
-    const int r = i / kMoTile, c = i % kMoTile;
-    if (r0 + r < P.rows && c0 + c < P.cols) {
-      const float u = momentum_u<false>(P, b * P.per + static_cast<int64_t>(r0 + r) * P.cols + c0 + c);
-      const __half h = __float2half_rn(u * f0 * f1 * f2);
-      tile[r][c] = h;
-      x[b * sx + static_cast<int64_t>(r0 + r) * ldx + c0 + c] = h;
+  const int groups = (cols + kMoVec - 1) / kMoVec;          // of a row
+  const int64_t total = static_cast<int64_t>(rows) * groups;
+  for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x; gi < total;
+       gi += static_cast<int64_t>(gridDim.x) * kMoThreads) {
+    const int64_t r = gi / groups;
+    const int c = static_cast<int>(gi - r * groups) * kMoVec;
+    const int n = min(kMoVec, cols - c);
+    const int64_t i = b * P.per + r * cols + c;
+    float u[kMoVec];
+    if (P.mom_out == nullptr || P.nesterov) load_grad<VEC>(P, i, n, u);
+    if (P.mom_out != nullptr) {
+      float m[kMoVec];
+      load_f32<VEC>(P.mom_out, i, n, m);
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) u[j] = P.nesterov ? fmaf(P.mu, m[j], u[j]) : m[j];
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kMoTile * kMoTile; i += kMoThreads) {
-    const int c = i / kMoTile, r = i % kMoTile;
-    if (r0 + r < P.rows && c0 + c < P.cols) xt[b * st + static_cast<int64_t>(c0 + c) * ldt + r0 + r] = tile[r][c];
+    uint32_t h[kMoVec / 2];
+#pragma unroll
+    for (int j = 0; j < kMoVec / 2; ++j) {
+      const __half2 v = __floats2half2_rn(u[2 * j] * f0 * f1 * f2, u[2 * j + 1] * f0 * f1 * f2);
+      h[j] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    // ld is a multiple of 16, so a group of eight starts on 16 bytes and fits the row's padding
+    *reinterpret_cast<uint4*>(x + (static_cast<int64_t>(b) * rows + r) * ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
 // ------------------------------------------------------------------ products
-// D = P Q^T over fp16 operands [batch][rows][K], tiles of 128 x 128 on one SM
-// or 256 x 256 on a CTA pair (cta_group::2, each SM holding its 128 rows of
-// both operands).  Warp 0 issues TMA, warp 1 owns TMEM and issues the MMAs,
-// warps 4-11 run the epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and
-// half of the tile's columns.  Persistent over the tiles of all matrices, the
-// accumulator double-buffered in TMEM.  Every wait is bounded; one that gives
-// up records MXG_ERR_TIMEOUT and stops the CTA's pipeline.
+// D = P Q^T over fp16 operands, tiles of 128 x 128 on one SM or 256 x 256 on a
+// CTA pair (cta_group::2, each SM holding its 128 rows of both operands).
+// Warp 0 issues TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run the
+// epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
+// columns.  Persistent over the tiles of all matrices, the accumulator
+// double-buffered in TMEM.  Every wait is bounded; one that gives up records
+// MXG_ERR_TIMEOUT and stops the CTA's pipeline.
+//
+// An operand's 128 rows x 64 contraction elements come as two 64 x 64 boxes of
+// 128-byte swizzled rows, 8 KB each.  K-major: box h holds rows 64 h ..; the
+// two follow one another as 128 rows of 128 bytes (8-row groups 1024 bytes
+// apart; a K = 16 step is 32 bytes).  MN-major: box h holds the 64 contraction
+// rows of operand rows 64 h .. (leading offset 8192 between them, 8-row groups
+// 1024 bytes apart; a K = 16 step is 16 rows, 2048 bytes).
 constexpr int kNsThreads = 384;
-constexpr int kNsK = 64;                  // contraction elements per stage: one 128-byte swizzled row
+constexpr int kNsK = 64;                  // contraction elements per stage
 constexpr int kNsRows = 128;              // rows of each operand per SM and stage
-constexpr int kNsOpBytes = kNsRows * kNsK * 2;
+constexpr int kNsBoxBytes = 64 * 64 * 2;
+constexpr int kNsOpBytes = 2 * kNsBoxBytes;
 constexpr int kNsStageBytes = 2 * kNsOpBytes;
 constexpr int kNsStages = 5;
-constexpr int kNsBox = 2048;              // 32 x 32 fp16: one store box
-constexpr int kNsWarpOut = 4 * kNsBox;    // per epilogue warp: two boxes of D and two of D^T
+constexpr int kNsOut = 32 * 64 * 2;       // 32 rows x 64 columns of D: one store box
+constexpr int kNsWarpOut = 2 * kNsOut;    // two per epilogue warp
 constexpr int kNsCtrl = 1024;
 constexpr int kNsSmem = 1024 + kNsStages * kNsStageBytes + 8 * kNsWarpOut + kNsCtrl;
-static_assert(32 * 33 * 4 <= kNsWarpOut, "the last product stages 32 x 32 fp32 values");
+constexpr int kNsSym = 256;               // a symmetric matrix is stored in full within diagonal blocks of this size
 static_assert(kNsSmem <= 232448, "shared memory budget");
+static_assert(32 * 33 * 4 <= kNsWarpOut, "unaligned outputs stage 32 x 32 fp32 values");
+
+// How an operand lies in memory.
+enum NsForm { NS_K = 0,                   // [rows][k]
+              NS_MN = 1,                  // [k][rows]
+              NS_SYM = 2 };               // symmetric [rows][rows], blocks on and above the diagonal
+
+enum NsOut { NS_F16 = 0,                  // D to fp16 boxes
+             NS_LAST = 1,                 // D, or weights, to the caller's bf16 matrix by TMA
+             NS_ROWS = 2 };               // the same by plain stores (rows that TMA cannot address, or both outputs)
 
 struct NsArgs {
-  int sym;                                // only tiles on and above the diagonal; stored twice
+  int sym;                                // only tiles on and above the diagonal
   int m, n, k;                            // D [m][n], contraction k
   int batch;
   int tiles_m, tiles_n;                   // per matrix
+  int n_fast;                             // column tiles vary fastest
   int64_t total;                          // tiles of all matrices
-  int p_rows, q_rows;                     // operand rows per matrix
+  int p_form, q_form;
   float alpha, beta;                      // D = alpha P Q^T + beta C
   const __half* c;                        // [batch][m][ldc], nullable; ldc a multiple of 16
-  int64_t ldc, sc;
-  // the last product: bf16 update, or new weights, in the caller's layout
+  int64_t ldc;
+  // the last product: bf16 [batch][m][n]
   uint16_t* update;                       // nullable
   const uint16_t* w_in;
   uint16_t* w_out;                        // nullable: w_in * w_keep - D * lr
   float w_keep, lr;
-  int flip;                               // the caller's matrix is D^T
-  int64_t ldu, su;
   int32_t* status;
 };
 
@@ -207,6 +285,14 @@ struct NsTile {
   int b, ti, tj;
 };
 
+// First column tile of row tile ti of a symmetric matrix: tiles of 128 fill
+// the diagonal blocks of kNsSym as well.
+template <bool PAIR>
+__host__ __device__ __forceinline__ int ns_first(int ti) {
+  return PAIR ? ti : ti & ~1;
+}
+
+template <bool PAIR>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   NsTile r;
   const int per = static_cast<int>(P.total / P.batch);
@@ -214,24 +300,54 @@ __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   int l = static_cast<int>(t - static_cast<int64_t>(r.b) * per);
   if (P.sym) {
     r.ti = 0;
-    while (l >= P.tiles_m - r.ti) {
-      l -= P.tiles_m - r.ti;
+    while (l >= P.tiles_m - ns_first<PAIR>(r.ti)) {
+      l -= P.tiles_m - ns_first<PAIR>(r.ti);
       ++r.ti;
     }
-    r.tj = r.ti + l;
+    r.tj = ns_first<PAIR>(r.ti) + l;
+  } else if (P.n_fast) {
+    r.ti = l / P.tiles_n;
+    r.tj = l - r.ti * P.tiles_n;
   } else {
-    r.tj = l / P.tiles_m;                 // the short side fastest: B stays in L2
+    r.tj = l / P.tiles_m;
     r.ti = l - r.tj * P.tiles_m;
   }
   return r;
 }
 
-// 32 columns of C for this thread's row, zero past the matrix.
-__device__ __forceinline__ void ns_load_c(const NsArgs& P, int b, int row, int col, uint32_t (&w)[16]) {
+// Whether the 64 contraction elements from k0 of operand rows row0 .. are read
+// MN-major: below the diagonal a symmetric matrix holds nothing, and the block
+// (rows, k) is the transpose of (k, rows).
+__device__ __forceinline__ bool ns_transposed(int form, int row0, int k0) {
+  return form == NS_MN || (form == NS_SYM && k0 / kNsSym < row0 / kNsSym);
+}
+
+template <bool PEER>
+__device__ __forceinline__ void ns_load(uint8_t* dst, const CUtensorMap* map, bool mn, int row0, int k0, int b,
+                                        uint64_t* bar, uint32_t peer_bar) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (row < P.m && col + 16 * h < P.n) {          // whole 32-byte pieces: ldc is a multiple of 16
-      ld_global_nc_v8(P.c + b * P.sc + row * P.ldc + col + 16 * h, w + 8 * h);
+    const int x = mn ? row0 + 64 * h : k0, y = mn ? k0 : row0 + 64 * h;
+    if (PEER) tma_load_3d_pair(dst + h * kNsBoxBytes, map, x, y, b, peer_bar);
+    else tma_load_3d(dst + h * kNsBoxBytes, map, x, y, b, bar);
+  }
+}
+
+__device__ __forceinline__ uint64_t ns_desc(const uint8_t* op, bool mn) {
+  return smem_desc(smem_u32(op), mn ? kNsBoxBytes : 0, 1024, kLayoutSwizzle128B);
+}
+
+// 64 columns of a row of C, zero past the matrix's edge (whole 32-byte pieces:
+// rows are padded to 16).  NC: nothing writes the matrix during the kernel.
+template <bool NC>
+__device__ __forceinline__ void ns_load_row(const void* base, int64_t off, bool in, int col, int n,
+                                            uint32_t (&w)[32]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if (in && col + 16 * h < n) {
+      const uint16_t* src = static_cast<const uint16_t*>(base) + off + 16 * h;
+      if (NC) ld_global_nc_v8(src, w + 8 * h);
+      else ld_global_v8(src, w + 8 * h);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[8 * h + i] = 0u;
@@ -239,83 +355,61 @@ __device__ __forceinline__ void ns_load_c(const NsArgs& P, int b, int row, int c
   }
 }
 
-// One 32 x 32 block of D = alpha acc + beta C as fp16, to D and (mirror) D^T:
-// staged in two 2 KB boxes (64-byte rows, 16-byte chunk j of row r at
-// j ^ ((r / 2) % 4): the tensor maps' 64-byte swizzle) and stored by TMA, which
-// also cuts the block at the matrix's edges.  A lane writes its row of D in
-// four 16-byte pieces and its column of D^T in 2-byte pieces, 32 lanes side by
-// side: both free of bank conflicts.
-__device__ __forceinline__ void ns_store_block(const NsArgs& P, const uint32_t (&r)[32], const uint32_t (&c)[16],
-                                               uint8_t* box, const CUtensorMap* tmO, const CUtensorMap* tmT, int row0,
-                                               int col0, int b, bool mirror, int lane) {
-  uint32_t h[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
-    const __half2 v = __floats2half2_rn(fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r[2 * i])),
-                                        fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r[2 * i + 1])));
-    h[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  // the boxes written two blocks ago have left shared memory
-  if (lane == 0) bulk_wait_group_read<1>();
+__device__ __forceinline__ float2 ns_value(const NsArgs& P, uint32_t r0, uint32_t r1, uint32_t c) {
+  const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c));
+  return make_float2(fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r0)),
+                     fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r1)));
+}
+
+// 32 rows x 64 columns of packed 16-bit results (this lane's row in h) to
+// global memory: staged as 128-byte rows (16-byte piece j of row r at
+// j ^ (r % 8): the tensor map's 128-byte swizzle, free of bank conflicts) and
+// stored by one TMA box, which is cut at the matrix's edges.
+__device__ __forceinline__ void ns_store_box(const uint32_t (&h)[32], uint8_t* box, const CUtensorMap* tm, int row0,
+                                             int col0, int b, int lane) {
+  if (lane == 0) bulk_wait_group_read<1>();          // the box written two boxes ago has left shared memory
   __syncwarp();
-  const int sw = (lane >> 1) & 3;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ sw) << 4)) =
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
         make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-  if (mirror) {
-    uint8_t* tb = box + kNsBox;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {                   // row i of the transposed box, column `lane`
-      const uint16_t v = static_cast<uint16_t>(i & 1 ? h[i / 2] >> 16 : h[i / 2]);
-      *reinterpret_cast<uint16_t*>(tb + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2) = v;
-    }
-  }
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    tma_store_3d(tmO, box, col0, row0, b);
-    if (mirror) tma_store_3d(tmT, box + kNsBox, row0, col0, b);
+    tma_store_3d(tm, box, col0, row0, b);
     bulk_commit_group();
   }
 }
 
-// One 32 x 32 block of the last product to the caller's bf16 matrix, whose
-// rows may start at any even address: staged in fp32 (rows of 33 words) and
-// written row by row of the caller's matrix, 32 lanes side by side.
-__device__ __forceinline__ void ns_store_last(const NsArgs& P, const uint32_t (&r)[32], const uint32_t (&c)[16],
-                                              float* buf, int row0, int col0, int b, int lane) {
+// One 32 x 32 block of the last product to a bf16 matrix whose rows may start
+// at any even address: staged in fp32 (rows of 33 words) and written row by
+// row, 32 lanes side by side.
+__device__ __forceinline__ void ns_store_rows(const NsArgs& P, const float (&v)[32], float* buf, int row0, int col0,
+                                              int b, int lane) {
   __syncwarp();                                      // the previous block has been read
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
-    buf[lane * 33 + 2 * i] = fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r[2 * i]));
-    buf[lane * 33 + 2 * i + 1] = fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r[2 * i + 1]));
-  }
+  for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = v[i];
   __syncwarp();
-  const int y0 = P.flip ? col0 : row0, x0 = P.flip ? row0 : col0;      // of the caller's matrix
-  const int ny = min(32, (P.flip ? P.n : P.m) - y0);
-  const bool in = x0 + lane < (P.flip ? P.m : P.n);
-  const int64_t base = b * P.su + static_cast<int64_t>(y0) * P.ldu + x0 + lane;
+  const int ny = min(32, P.m - row0);
+  const bool in = col0 + lane < P.n;
+  const int64_t base = (static_cast<int64_t>(b) * P.m + row0) * P.n + col0 + lane;
 #pragma unroll 8
   for (int i = 0; i < 32; ++i) {
     if (i < ny && in) {
-      const float v = P.flip ? buf[lane * 33 + i] : buf[i * 33 + lane];
-      const int64_t u = base + i * P.ldu;
-      if (P.update != nullptr) P.update[u] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+      const float x = buf[i * 33 + lane];
+      const int64_t u = base + static_cast<int64_t>(i) * P.n;
+      if (P.update != nullptr) P.update[u] = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
       if (P.w_out != nullptr)
         P.w_out[u] =
-            static_cast<uint16_t>(pack_bf16x2(fmaf(-P.lr, v, bf16_bits_to_float(P.w_in[u]) * P.w_keep), 0.f));
+            static_cast<uint16_t>(pack_bf16x2(fmaf(-P.lr, x, bf16_bits_to_float(P.w_in[u]) * P.w_keep), 0.f));
     }
   }
 }
 
-template <bool PAIR, bool LAST>
+template <bool PAIR, int OUT>
 __global__ void __launch_bounds__(kNsThreads, 1)
     ns_product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmT,
-                      const __grid_constant__ NsArgs P) {
+                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ NsArgs P) {
   constexpr int CG = PAIR ? 2 : 1;
   constexpr int BN = PAIR ? 256 : 128;    // columns of a tile (and accumulator columns)
   constexpr int TM = PAIR ? 256 : 128;    // rows of a tile, both CTAs
@@ -353,6 +447,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
+    if (OUT != NS_ROWS) tma_prefetch_desc(&tmO);
   }
   __syncthreads();
   if (warp == 1) {
@@ -378,9 +473,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       bool aborted = false;
       const uint32_t full0 = PAIR ? map_to_rank(smem_u32(full), 0) : 0u;
       for (int64_t t = tile0; t < P.total && !aborted; t += tstep) {
-        const NsTile tc = ns_tile(P, t);
-        const int prow = tc.b * P.p_rows + tc.ti * TM + static_cast<int>(rank) * kNsRows;
-        const int qrow = tc.b * P.q_rows + tc.tj * BN + static_cast<int>(rank) * kNsRows;
+        const NsTile tc = ns_tile<PAIR>(P, t);
+        const int prow = tc.ti * TM + static_cast<int>(rank) * kNsRows;
+        const int qrow = tc.tj * BN + static_cast<int>(rank) * kNsRows;
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
@@ -389,13 +484,15 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           }
           uint8_t* sP = sm + stage * kNsStageBytes;
           uint8_t* sQ = sP + kNsOpBytes;
+          const int k0 = kb * kNsK;
+          const bool pmn = ns_transposed(P.p_form, prow, k0), qmn = ns_transposed(P.q_form, qrow, k0);
           if (!PAIR || rank == 0) {
             mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);     // both CTAs' bytes
-            tma_load_2d(sP, &tmP, kb * kNsK, prow, &full[stage]);
-            tma_load_2d(sQ, &tmQ, kb * kNsK, qrow, &full[stage]);
+            ns_load<false>(sP, &tmP, pmn, prow, k0, tc.b, &full[stage], 0u);
+            ns_load<false>(sQ, &tmQ, qmn, qrow, k0, tc.b, &full[stage], 0u);
           } else {
-            tma_load_2d_pair(sP, &tmP, kb * kNsK, prow, full0 + stage * 8);
-            tma_load_2d_pair(sQ, &tmQ, kb * kNsK, qrow, full0 + stage * 8);
+            ns_load<true>(sP, &tmP, pmn, prow, k0, tc.b, nullptr, full0 + stage * 8);
+            ns_load<true>(sQ, &tmQ, qmn, qrow, k0, tc.b, nullptr, full0 + stage * 8);
           }
           if (++stage == kNsStages) {
             stage = 0;
@@ -414,6 +511,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       bool aborted = false;
       int64_t done = 0;
       for (int64_t t = tile0; t < P.total && !aborted; t += tstep) {
+        const NsTile tc = ns_tile<PAIR>(P, t);
         const bool got = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)
                               : mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs);
         if (!got) {
@@ -431,12 +529,16 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             break;
           }
           tc_fence_after();
-          uint8_t* sP = sm + stage * kNsStageBytes;
-          const uint64_t pd = smem_desc(smem_u32(sP), 0, 1024, kLayoutSwizzle128B);
-          const uint64_t qd = smem_desc(smem_u32(sP + kNsOpBytes), 0, 1024, kLayoutSwizzle128B);
+          // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
+          const bool pmn = ns_transposed(P.p_form, tc.ti * TM, kb * kNsK);
+          const bool qmn = ns_transposed(P.q_form, tc.tj * BN, kb * kNsK);
+          const uint8_t* sP = sm + stage * kNsStageBytes;
+          const uint64_t pd = ns_desc(sP, pmn), qd = ns_desc(sP + kNsOpBytes, qmn);
+          const uint32_t pstep = pmn ? 2048 >> 4 : 32 >> 4, qstep = qmn ? 2048 >> 4 : 32 >> 4;
+          const uint32_t id = idesc_f16(TM, BN) | (pmn ? kIdescAMn : 0u) | (qmn ? kIdescBMn : 0u);
 #pragma unroll
-          for (int k = 0; k < kNsK / 16; ++k)
-            mma_bf16<CG>(d_t, pd + 2 * k, qd + 2 * k, idesc_f16(TM, BN), (kb | k) != 0 ? 1u : 0u);
+          for (uint32_t k = 0; k < kNsK / 16; ++k)
+            mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kb | k) != 0 ? 1u : 0u);
           mma_commit<CG>(&empty[stage]);
           if (++stage == kNsStages) {
             stage = 0;
@@ -462,24 +564,26 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     }
   } else if (warp >= 4) {
     constexpr int COLS = BN / 2;
+    constexpr int BOXES = COLS / 64;
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
     uint32_t acc = 0, acc_phase = 0, flip = 0;
     for (int64_t t = tile0; t < P.total; t += tstep) {
-      const NsTile tc = ns_tile(P, t);
+      const NsTile tc = ns_tile<PAIR>(P, t);
       const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
       const int col0 = tc.tj * BN + hf * COLS;
-      const bool mirror = P.sym == 0 || tc.ti != tc.tj;
+      const bool in = row0 + lane < P.m;
       // the addend is on its way while the tile's MMAs run
-      uint32_t cv[COLS / 32][16];
+      uint32_t cv[BOXES][32];
 #pragma unroll
-      for (int c = 0; c < COLS / 32; ++c) {
+      for (int c = 0; c < BOXES; ++c) {
         if (P.c != nullptr) {
-          ns_load_c(P, tc.b, row0 + lane, col0 + 32 * c, cv[c]);
+          ns_load_row<true>(P.c, (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.ldc + col0 + 64 * c, in,
+                      col0 + 64 * c, P.n, cv[c]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) cv[c][i] = 0u;
+          for (int i = 0; i < 32; ++i) cv[c][i] = 0u;
         }
       }
       bool got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs);
@@ -491,34 +595,65 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
 #pragma unroll
-      for (int c = 0; c < COLS / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tb + 32 * c, r);
-        tmem_ld_wait();
-        if (c == COLS / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR && rank == 1)
-              st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
-                                   map_to_rank(smem_u32(&tempty[acc]), 0));
-            else
-              mbar_arrive(&tempty[acc]);
+      for (int c = 0; c < BOXES; ++c) {
+        const int col = col0 + 64 * c;
+        const bool any = row0 < P.m && col < P.n;
+        uint32_t h[32], w[32];
+        if (OUT == NS_LAST && P.w_out != nullptr)
+          ns_load_row<false>(P.w_in, (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.n + col, in, col, P.n, w);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tb + 64 * c + 32 * half, r);
+          tmem_ld_wait();
+          if (c == BOXES - 1 && half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (PAIR && rank == 1)
+                st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
+                                     map_to_rank(smem_u32(&tempty[acc]), 0));
+              else
+                mbar_arrive(&tempty[acc]);
+            }
+          }
+          if constexpr (OUT == NS_ROWS) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = ns_value(P, r[2 * i], r[2 * i + 1], cv[c][16 * half + i]);
+              v[2 * i] = x.x;
+              v[2 * i + 1] = x.y;
+            }
+            if (any && col + 32 * half < P.n)
+              ns_store_rows(P, v, reinterpret_cast<float*>(box), row0, col + 32 * half, tc.b, lane);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 x = ns_value(P, r[2 * i], r[2 * i + 1], cv[c][16 * half + i]);
+              if constexpr (OUT == NS_F16) {
+                const __half2 v = __floats2half2_rn(x.x, x.y);
+                h[16 * half + i] = *reinterpret_cast<const uint32_t*>(&v);
+              } else {
+                if (P.w_out != nullptr) {
+                  const uint32_t wv = w[16 * half + i];
+                  x.x = fmaf(-P.lr, x.x, __uint_as_float(wv << 16) * P.w_keep);
+                  x.y = fmaf(-P.lr, x.y, __uint_as_float(wv & 0xffff0000u) * P.w_keep);
+                }
+                h[16 * half + i] = pack_bf16x2(x.x, x.y);
+              }
+            }
           }
         }
-        if (row0 < P.m && col0 + 32 * c < P.n) {
-          if constexpr (LAST) {
-            ns_store_last(P, r, cv[c], reinterpret_cast<float*>(box), row0, col0 + 32 * c, tc.b, lane);
-          } else {
-            ns_store_block(P, r, cv[c], box + flip * 2 * kNsBox, &tmO, &tmT, row0, col0 + 32 * c, tc.b, mirror, lane);
-            flip ^= 1;
-          }
+        if (OUT != NS_ROWS && any) {
+          ns_store_box(h, box + flip * kNsOut, &tmO, row0, col, tc.b, lane);
+          flip ^= 1;
         }
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-    if (!LAST) {
+    if (OUT != NS_ROWS) {
       if (lane == 0) bulk_wait_group<0>();           // the stores have completed before the CTA exits
       __syncwarp();
     }
@@ -539,10 +674,18 @@ int sm_count() {
   return n > 0 ? n : 1;
 }
 
-template <bool PAIR, bool LAST>
-cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, const CUtensorMap& mt,
-                      const NsArgs& a, cudaStream_t s) {
-  auto kern = ns_product_kernel<PAIR, LAST>;
+template <bool PAIR, int OUT>
+cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, NsArgs a, cudaStream_t s) {
+  constexpr int W = PAIR ? 256 : 128;
+  a.tiles_m = (a.m + W - 1) / W;
+  a.tiles_n = (a.n + W - 1) / W;
+  int64_t per = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+  if (a.sym) {
+    per = 0;
+    for (int i = 0; i < a.tiles_m; ++i) per += a.tiles_m - ns_first<PAIR>(i);
+  }
+  a.total = per * a.batch;
+  auto kern = ns_product_kernel<PAIR, OUT>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
   if (err != cudaSuccess) return err;
   const int64_t units = PAIR ? sm_count() / 2 : sm_count();
@@ -561,52 +704,42 @@ cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const CUtens
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  err = cudaLaunchKernelEx(&cfg, kern, mp, mq, mo, mt, a);
+  err = cudaLaunchKernelEx(&cfg, kern, mp, mq, mo, a);
   count_launch();
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-struct NsMat {                            // fp16 [batch][rows][cols], rows ld apart
-  __half* p;
+struct NsMat {                            // 16-bit [batch][rows][cols], rows ld apart
+  void* p;
   int rows, cols;
   int64_t ld;
 };
 
-// D of one product over the batch: operands p and q, D and D^T to o and t
-// (none for the last product, whose outputs are in a).
-cudaError_t ns_product(NsArgs a, const NsMat& p, const NsMat& q, const NsMat* o, const NsMat* t, cudaStream_t s) {
-  CUtensorMap mp, mq, mo, mt;
-  a.p_rows = p.rows;
-  a.q_rows = q.rows;
-  a.m = p.rows;
-  a.n = q.rows;
-  a.k = p.cols;
-  if (!tma_map_f16(&mp, p.p, p.cols, static_cast<int64_t>(a.batch) * p.rows, p.ld, kNsRows) ||
-      !tma_map_f16(&mq, q.p, q.cols, static_cast<int64_t>(a.batch) * q.rows, q.ld, kNsRows))
+// D of one product over the batch: operands p and q in their forms, D to o
+// (fp16, or the caller's bf16 matrix as a says).
+cudaError_t ns_product(NsArgs a, const NsMat& p, const NsMat& q, const NsMat& o, int out, cudaStream_t s) {
+  CUtensorMap mp, mq, mo;
+  a.m = o.rows;
+  a.n = o.cols;
+  a.k = a.p_form == NS_K ? p.cols : p.rows;
+  if (!tma_map_b16_3d(&mp, p.p, p.cols, p.rows, a.batch, p.ld, 64) ||
+      !tma_map_b16_3d(&mq, q.p, q.cols, q.rows, a.batch, q.ld, 64))
     return cudaErrorInvalidValue;
-  mo = mt = mp;
-  if (o != nullptr && (!tma_map_f16_boxes(&mo, o->p, o->cols, o->rows, a.batch, o->ld) ||
-                       !tma_map_f16_boxes(&mt, t->p, t->cols, t->rows, a.batch, t->ld)))
-    return cudaErrorInvalidValue;
-  auto tiles = [&](int w) {
-    a.tiles_m = (a.m + w - 1) / w;
-    a.tiles_n = (a.n + w - 1) / w;
-    const int64_t per = a.sym ? static_cast<int64_t>(a.tiles_m) * (a.tiles_m + 1) / 2
-                              : static_cast<int64_t>(a.tiles_m) * a.tiles_n;
-    a.total = per * a.batch;
-    return a.total;
-  };
-  if (tiles(256) >= sm_count() / 2)
-    return o != nullptr ? launch_ns<true, false>(mp, mq, mo, mt, a, s) : launch_ns<true, true>(mp, mq, mo, mt, a, s);
-  tiles(128);
-  return o != nullptr ? launch_ns<false, false>(mp, mq, mo, mt, a, s) : launch_ns<false, true>(mp, mq, mo, mt, a, s);
+  mo = mp;
+  if (out != NS_ROWS && !tma_map_b16_3d(&mo, o.p, o.cols, o.rows, a.batch, o.ld, 32)) return cudaErrorInvalidValue;
+  const int64_t tm = (a.m + 255) / 256, tn = (a.n + 255) / 256;
+  const bool pair = (a.sym ? tm * (tm + 1) / 2 : tm * tn) * a.batch >= sm_count() / 2;
+  if (out == NS_F16) return pair ? launch_ns<true, NS_F16>(mp, mq, mo, a, s) : launch_ns<false, NS_F16>(mp, mq, mo, a, s);
+  if (out == NS_LAST)
+    return pair ? launch_ns<true, NS_LAST>(mp, mq, mo, a, s) : launch_ns<false, NS_LAST>(mp, mq, mo, a, s);
+  return pair ? launch_ns<true, NS_ROWS>(mp, mq, mo, a, s) : launch_ns<false, NS_ROWS>(mp, mq, mo, a, s);
 }
 
 struct NsPlan {
-  int m, n, tall;                         // X is [m][n], m <= n; tall: the caller's matrix is X^T
-  int64_t ldx, ldt;                       // row lengths of X [m][ldx] and X^T [n][ldt] (also of A and B)
+  int m, n, tall;                         // short and long side; tall: the matrix is [n][m]
+  int64_t ldx, lda;                       // row lengths of X and of A and B, padded to 16
   int chunks;                             // partial sums of squares per matrix
-  int64_t part, x0, x1, t0, t1, a, b, bytes;
+  int64_t part, x0, x1, a, b, bytes;
 };
 
 NsPlan ns_plan(int batch, int rows, int cols) {
@@ -614,19 +747,17 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   p.tall = rows > cols;
   p.m = p.tall ? cols : rows;
   p.n = p.tall ? rows : cols;
-  p.ldx = api::align_up(p.n, 16);
-  p.ldt = api::align_up(p.m, 16);
+  p.ldx = api::align_up(cols, 16);
+  p.lda = api::align_up(p.m, 16);
   const int64_t per = static_cast<int64_t>(rows) * cols;
-  int64_t c = (per + kMoThreads * 16 - 1) / (kMoThreads * 16);
+  const int64_t c = (per + kMoThreads * kMoVec - 1) / (kMoThreads * kMoVec);
   const int64_t most = (152 * 8 + batch - 1) / batch;
   p.chunks = static_cast<int>(c < most ? c : most);
   api::Carver w;
   p.part = w.take(8ll * batch * p.chunks);
-  const int64_t xb = 2ll * batch * p.m * p.ldx, tb = 2ll * batch * p.n * p.ldt, ab = 2ll * batch * p.m * p.ldt;
+  const int64_t xb = 2ll * batch * rows * p.ldx, ab = 2ll * batch * p.m * p.lda;
   p.x0 = w.take(xb);
   p.x1 = w.take(xb);
-  p.t0 = w.take(tb);
-  p.t1 = w.take(tb);
   p.a = w.take(ab);
   p.b = w.take(ab);
   p.bytes = w.off;
@@ -667,26 +798,24 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   api::NvtxRange nvtx("mxg.muon_update");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* part = api::at<double>(a->workspace, p.part);
-  const NsMat x[2] = {{api::at<__half>(a->workspace, p.x0), p.m, p.n, p.ldx},
-                      {api::at<__half>(a->workspace, p.x1), p.m, p.n, p.ldx}};
-  const NsMat xt[2] = {{api::at<__half>(a->workspace, p.t0), p.n, p.m, p.ldt},
-                       {api::at<__half>(a->workspace, p.t1), p.n, p.m, p.ldt}};
-  const NsMat am{api::at<__half>(a->workspace, p.a), p.m, p.m, p.ldt};
-  const NsMat bm{api::at<__half>(a->workspace, p.b), p.m, p.m, p.ldt};
+  const NsMat x[2] = {{api::at<void>(a->workspace, p.x0), a->rows, a->cols, p.ldx},
+                      {api::at<void>(a->workspace, p.x1), a->rows, a->cols, p.ldx}};
+  const NsMat am{api::at<void>(a->workspace, p.a), p.m, p.m, p.lda};
+  const NsMat bm{api::at<void>(a->workspace, p.b), p.m, p.m, p.lda};
   int ex = 0;                             // 2^ex ~ sqrt(n)
   while ((1ll << (2 * ex)) < p.n) ++ex;
 
-  MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, a->rows, a->cols,
-                  static_cast<int64_t>(a->rows) * a->cols};
-  momentum_kernel<<<dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(a->batch)), kMoThreads, 0, s>>>(
-      mo, p.chunks, part);
+  const int64_t per = static_cast<int64_t>(a->rows) * a->cols;
+  const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
+  const unsigned nb = static_cast<unsigned>(a->batch);
+  // 32-byte loads where every matrix (and, for the cast, every row) starts on 32 bytes of each buffer
+  if (per % 16 == 0) momentum_kernel<true><<<dim3(static_cast<unsigned>(p.chunks), nb), kMoThreads, 0, s>>>(mo, p.chunks, part);
+  else momentum_kernel<false><<<dim3(static_cast<unsigned>(p.chunks), nb), kMoThreads, 0, s>>>(mo, p.chunks, part);
   count_launch();
-  const dim3 cgrid(static_cast<unsigned>((a->cols + kMoTile - 1) / kMoTile),
-                   static_cast<unsigned>((a->rows + kMoTile - 1) / kMoTile), static_cast<unsigned>(a->batch));
-  const NsMat& u = p.tall ? xt[0] : x[0];
-  const NsMat& ut = p.tall ? x[0] : xt[0];
-  cast_kernel<<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, u.p, u.ld, u.rows * u.ld, ut.p, ut.ld,
-                                           ut.rows * ut.ld);
+  const dim3 cgrid(static_cast<unsigned>(p.chunks), nb);
+  __half* x0 = static_cast<__half*>(x[0].p);
+  if (a->cols % 16 == 0) cast_kernel<true><<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x0, p.ldx);
+  else cast_kernel<false><<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x0, p.ldx);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
 
@@ -698,37 +827,43 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
     ga.batch = a->batch;
     ga.status = a->dev_status;
     ga.sym = 1;
+    ga.p_form = ga.q_form = p.tall ? NS_MN : NS_K;
     ga.alpha = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
-    MXG_TRY(ns_product(ga, x[cur], x[cur], &am, &am, s));
+    MXG_TRY(ns_product(ga, x[cur], x[cur], am, NS_F16, s));
     // B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
     NsArgs gb = ga;
+    gb.p_form = gb.q_form = NS_SYM;
     gb.alpha = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
     gb.beta = a->b;
-    gb.c = am.p;
+    gb.c = static_cast<const __half*>(am.p);
     gb.ldc = am.ld;
-    gb.sc = am.rows * am.ld;
-    MXG_TRY(ns_product(gb, am, am, &bm, &bm, s));
-    // X' 2^ex = a (X 2^ex) + 2^-12 (B 2^12)(X 2^ex); the last one leaves as scale X'
+    MXG_TRY(ns_product(gb, am, am, bm, NS_F16, s));
+    // X' 2^ex = a (X 2^ex) + 2^-12 (B 2^12)(X 2^ex), X B when tall; the last one leaves as scale X'.
+    // The short side's tiles vary fastest, so B stays in L2 and X streams.
     const double f = last ? a->scale * std::ldexp(1.0, -ex) : 1.0;
     NsArgs gx{};
     gx.batch = a->batch;
     gx.status = a->dev_status;
+    gx.n_fast = p.tall;
+    gx.p_form = p.tall ? NS_K : NS_SYM;
+    gx.q_form = p.tall ? NS_SYM : NS_MN;
     gx.alpha = static_cast<float>(f * std::ldexp(1.0, -kExpA));
     gx.beta = static_cast<float>(f * a->a);
-    gx.c = x[cur].p;
+    gx.c = static_cast<const __half*>(x[cur].p);
     gx.ldc = x[cur].ld;
-    gx.sc = x[cur].rows * x[cur].ld;
+    NsMat o = x[nxt];
+    int out = NS_F16;
     if (last) {
       gx.update = a->update;
       gx.w_in = a->w_in;
       gx.w_out = a->w_out;
       gx.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
       gx.lr = a->lr;
-      gx.flip = p.tall;
-      gx.ldu = a->cols;
-      gx.su = mo.per;
+      o = NsMat{a->w_out ? a->w_out : a->update, a->rows, a->cols, a->cols};
+      // whole 32-byte pieces of the caller's rows, one output
+      out = a->cols % 16 == 0 && !(a->w_out && a->update) ? NS_LAST : NS_ROWS;
     }
-    MXG_TRY(ns_product(gx, bm, xt[cur], last ? nullptr : &x[nxt], last ? nullptr : &xt[nxt], s));
+    MXG_TRY(ns_product(gx, p.tall ? x[cur] : bm, p.tall ? bm : x[cur], o, out, s));
   }
   return MXG_OK;
 }
