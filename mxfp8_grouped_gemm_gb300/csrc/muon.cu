@@ -11,9 +11,9 @@
 //
 // Every matrix is stored once, in the caller's orientation.  With M the short
 // side and N the long one, the three products of a step contract over
-//   A  = X X^T           N   (a tall X [N][M]: A = X^T X)
-//   B  = b A + c A A     M
-//   X' = a X + B X       M   (tall: X' = a X + X B)
+//   A  = X X^T                 N   (a tall X [N][M]: A = X^T X)
+//   B  = a I + b A + c A A     M
+//   X' = B X                   M   (tall: X' = X B)
 // on tcgen05 kind::f16, whose operands may be read with the contraction
 // contiguous (K-major) or across it (MN-major), so no transposed copy is kept.
 // A and B are symmetric: only their tiles on and above the diagonal are
@@ -25,7 +25,9 @@
 // significand is worth more than bf16's range, and each is stored times a
 // power of two that puts its entries well inside fp16's normal range:
 //   X 2^ex, 2^ex ~ sqrt(N)  (an orthogonal X has entries of size 1 / sqrt(N)),
-//   A 2^12, B 2^12          (entries at most ~1.5 and ~3).
+//   A 2^12, B 2^12          (entries at most ~1.5 and ~5).
+// Folding a I into B rounds a + B_ii to eleven bits, an error of the size of
+// X's own rounding, and spares the last product a second read of X.
 // Sums are fp32 (tensor-core accumulators); momentum and norms are fp32/fp64.
 #include <cuda_fp16.h>
 
@@ -259,6 +261,7 @@ enum NsForm { NS_K = 0,                   // [rows][k]
               NS_SYM = 2 };               // symmetric [rows][rows], blocks on and above the diagonal
 
 enum NsOut { NS_F16 = 0,                  // D to fp16 boxes
+             NS_POLY = 3,                 // the same with beta C + diag I added
              NS_LAST = 1,                 // D, or weights, to the caller's bf16 matrix by TMA
              NS_ROWS = 2 };               // the same by plain stores (rows that TMA cannot address, or both outputs)
 
@@ -270,7 +273,7 @@ struct NsArgs {
   int n_fast;                             // column tiles vary fastest
   int64_t total;                          // tiles of all matrices
   int p_form, q_form;
-  float alpha, beta;                      // D = alpha P Q^T + beta C
+  float alpha, beta, diag;                // D = alpha P Q^T + beta C + diag I
   const __half* c;                        // [batch][m][ldc], nullable; ldc a multiple of 16
   int64_t ldc;
   // the last product: bf16 [batch][m][n]
@@ -355,10 +358,16 @@ __device__ __forceinline__ void ns_load_row(const void* base, int64_t off, bool 
   }
 }
 
-__device__ __forceinline__ float2 ns_value(const NsArgs& P, uint32_t r0, uint32_t r1, uint32_t c) {
-  const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c));
-  return make_float2(fmaf(P.beta, cf.x, P.alpha * __uint_as_float(r0)),
-                     fmaf(P.beta, cf.y, P.alpha * __uint_as_float(r1)));
+// alpha acc, and for a polynomial in A (ADD) + beta C + diag where row == col.
+template <bool ADD>
+__device__ __forceinline__ float2 ns_value(const NsArgs& P, uint32_t r0, uint32_t r1, uint32_t c, int row, int col) {
+  float2 v = make_float2(P.alpha * __uint_as_float(r0), P.alpha * __uint_as_float(r1));
+  if constexpr (ADD) {
+    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c));
+    v.x = fmaf(P.beta, cf.x, v.x) + (row == col ? P.diag : 0.f);
+    v.y = fmaf(P.beta, cf.y, v.y) + (row == col + 1 ? P.diag : 0.f);
+  }
+  return v;
 }
 
 // 32 rows x 64 columns of packed 16-bit results (this lane's row in h) to
@@ -565,6 +574,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   } else if (warp >= 4) {
     constexpr int COLS = BN / 2;
     constexpr int BOXES = COLS / 64;
+    constexpr bool ADD = OUT == NS_POLY;
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
@@ -575,16 +585,12 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       const int col0 = tc.tj * BN + hf * COLS;
       const bool in = row0 + lane < P.m;
       // the addend is on its way while the tile's MMAs run
-      uint32_t cv[BOXES][32];
+      uint32_t cv[ADD ? BOXES : 1][32];
+      if constexpr (ADD) {
 #pragma unroll
-      for (int c = 0; c < BOXES; ++c) {
-        if (P.c != nullptr) {
+        for (int c = 0; c < BOXES; ++c)
           ns_load_row<true>(P.c, (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.ldc + col0 + 64 * c, in,
-                      col0 + 64 * c, P.n, cv[c]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) cv[c][i] = 0u;
-        }
+                            col0 + 64 * c, P.n, cv[c]);
       }
       bool got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs);
       got = __all_sync(0xffffffffu, got);
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             float v[32];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 x = ns_value(P, r[2 * i], r[2 * i + 1], cv[c][16 * half + i]);
+              const float2 x = ns_value<false>(P, r[2 * i], r[2 * i + 1], 0u, 0, 0);
               v[2 * i] = x.x;
               v[2 * i + 1] = x.y;
             }
@@ -630,8 +636,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float2 x = ns_value(P, r[2 * i], r[2 * i + 1], cv[c][16 * half + i]);
-              if constexpr (OUT == NS_F16) {
+              float2 x = ns_value<ADD>(P, r[2 * i], r[2 * i + 1], cv[ADD ? c : 0][16 * half + i], row0 + lane,
+                                       col + 32 * half + 2 * i);
+              if constexpr (OUT == NS_F16 || ADD) {
                 const __half2 v = __floats2half2_rn(x.x, x.y);
                 h[16 * half + i] = *reinterpret_cast<const uint32_t*>(&v);
               } else {
@@ -729,6 +736,8 @@ cudaError_t ns_product(NsArgs a, const NsMat& p, const NsMat& q, const NsMat& o,
   if (out != NS_ROWS && !tma_map_b16_3d(&mo, o.p, o.cols, o.rows, a.batch, o.ld, 32)) return cudaErrorInvalidValue;
   const int64_t tm = (a.m + 255) / 256, tn = (a.n + 255) / 256;
   const bool pair = (a.sym ? tm * (tm + 1) / 2 : tm * tn) * a.batch >= sm_count() / 2;
+  if (out == NS_POLY)
+    return pair ? launch_ns<true, NS_POLY>(mp, mq, mo, a, s) : launch_ns<false, NS_POLY>(mp, mq, mo, a, s);
   if (out == NS_F16) return pair ? launch_ns<true, NS_F16>(mp, mq, mo, a, s) : launch_ns<false, NS_F16>(mp, mq, mo, a, s);
   if (out == NS_LAST)
     return pair ? launch_ns<true, NS_LAST>(mp, mq, mo, a, s) : launch_ns<false, NS_LAST>(mp, mq, mo, a, s);
@@ -830,27 +839,24 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
     ga.p_form = ga.q_form = p.tall ? NS_MN : NS_K;
     ga.alpha = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
     MXG_TRY(ns_product(ga, x[cur], x[cur], am, NS_F16, s));
-    // B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
+    // B 2^12 = a 2^12 I + b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
     NsArgs gb = ga;
     gb.p_form = gb.q_form = NS_SYM;
     gb.alpha = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
     gb.beta = a->b;
+    gb.diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
     gb.c = static_cast<const __half*>(am.p);
     gb.ldc = am.ld;
-    MXG_TRY(ns_product(gb, am, am, bm, NS_F16, s));
-    // X' 2^ex = a (X 2^ex) + 2^-12 (B 2^12)(X 2^ex), X B when tall; the last one leaves as scale X'.
+    MXG_TRY(ns_product(gb, am, am, bm, NS_POLY, s));
+    // X' 2^ex = 2^-12 (B 2^12)(X 2^ex), X B when tall; the last one leaves as scale X'.
     // The short side's tiles vary fastest, so B stays in L2 and X streams.
-    const double f = last ? a->scale * std::ldexp(1.0, -ex) : 1.0;
     NsArgs gx{};
     gx.batch = a->batch;
     gx.status = a->dev_status;
     gx.n_fast = p.tall;
     gx.p_form = p.tall ? NS_K : NS_SYM;
     gx.q_form = p.tall ? NS_SYM : NS_MN;
-    gx.alpha = static_cast<float>(f * std::ldexp(1.0, -kExpA));
-    gx.beta = static_cast<float>(f * a->a);
-    gx.c = static_cast<const __half*>(x[cur].p);
-    gx.ldc = x[cur].ld;
+    gx.alpha = static_cast<float>(last ? a->scale * std::ldexp(1.0, -kExpA - ex) : std::ldexp(1.0, -kExpA));
     NsMat o = x[nxt];
     int out = NS_F16;
     if (last) {
