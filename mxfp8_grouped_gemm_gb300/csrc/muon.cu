@@ -31,6 +31,7 @@
 // Sums are fp32 (tensor-core accumulators); momentum and norms are fp32/fp64.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -115,10 +116,22 @@ __device__ __forceinline__ void load_grad(const MomentumArgs& P, int64_t i, int 
   }
 }
 
-// New momentum and the sum of squares of u: one partial per block.  VEC: every
-// matrix starts on a 32-byte boundary of each buffer.
+// Two values as fp16 (returned) and what the rounding left, as fp16 too.
+__device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// New momentum and the sum of squares of u: one partial per block; the
+// products' counters are cleared.  VEC: every matrix starts on a 32-byte
+// boundary of each buffer.
 template <bool VEC>
-__global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part) {
+__global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
+                                                             int32_t* __restrict__ done) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) done[blockIdx.y] = 0;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
   SumSq s{0.f, 0.f, 0.f};
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
@@ -168,7 +181,7 @@ __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, in
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int chunks, const double* __restrict__ part,
                                                          int ex, int rows, int cols, __half* __restrict__ x,
-                                                         int64_t ld) {
+                                                         int64_t ld, int64_t lo_off) {
   __shared__ double s_w[kMoThreads / 32];
   __shared__ float s_f[3];
   const int b = blockIdx.y;
@@ -214,14 +227,13 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 #pragma unroll
       for (int j = 0; j < kMoVec; ++j) u[j] = P.nesterov ? fmaf(P.mu, m[j], u[j]) : m[j];
     }
-    uint32_t h[kMoVec / 2];
+    uint32_t h[kMoVec / 2], l[kMoVec / 2];
 #pragma unroll
-    for (int j = 0; j < kMoVec / 2; ++j) {
-      const __half2 v = __floats2half2_rn(u[2 * j] * f0 * f1 * f2, u[2 * j + 1] * f0 * f1 * f2);
-      h[j] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    for (int j = 0; j < kMoVec / 2; ++j) h[j] = split_half2(u[2 * j] * f0 * f1 * f2, u[2 * j + 1] * f0 * f1 * f2, l[j]);
     // ld is a multiple of 16, so a group of eight starts on 16 bytes and fits the row's padding
-    *reinterpret_cast<uint4*>(x + (static_cast<int64_t>(b) * rows + r) * ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
+    __half* dst = x + (static_cast<int64_t>(b) * rows + r) * ld + c;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (lo_off != 0) *reinterpret_cast<uint4*>(dst + lo_off) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -230,9 +242,17 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // CTA pair (cta_group::2, each SM holding its 128 rows of both operands).
 // Warp 0 issues TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run the
 // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
-// columns.  Persistent over the tiles of all matrices, the accumulator
-// double-buffered in TMEM.  Every wait is bounded; one that gives up records
-// MXG_ERR_TIMEOUT and stops the CTA's pipeline.
+// columns.  The accumulator is double-buffered in TMEM.
+//
+// One launch runs all products of all steps: the tiles of the whole run form
+// one list that the CTAs (or pairs) deal out in turn, so a product's last
+// tiles overlap the next one's first, and a small matrix pays no launch per
+// product.  A tile needs the earlier products of its own matrix: every epilogue
+// warp adds one to the matrix's counter once its part is in memory, and the
+// loads wait for the count of the products before.  What a tile waits for is
+// earlier in the list and the launch is cooperative (all CTAs resident), so
+// the waits end.  Every wait is bounded all the same; one that gives up
+// records MXG_ERR_TIMEOUT and stops the CTA's pipeline.
 //
 // An operand's 128 rows x 64 contraction elements come as two 64 x 64 boxes of
 // 128-byte swizzled rows, 8 KB each.  K-major: box h holds rows 64 h ..; the
@@ -260,32 +280,32 @@ enum NsForm { NS_K = 0,                   // [rows][k]
               NS_MN = 1,                  // [k][rows]
               NS_SYM = 2 };               // symmetric [rows][rows], blocks on and above the diagonal
 
-enum NsOut { NS_F16 = 0,                  // D to fp16 boxes
-             NS_POLY = 3,                 // the same with beta C + diag I added
-             NS_LAST = 1,                 // D, or weights, to the caller's bf16 matrix by TMA
-             NS_ROWS = 2 };               // the same by plain stores (rows that TMA cannot address, or both outputs)
+// The three products of a step, in order.
+enum NsOp { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };
 
 struct NsArgs {
-  int sym;                                // only tiles on and above the diagonal
-  int m, n, k;                            // D [m][n], contraction k
-  int batch;
-  int tiles_m, tiles_n;                   // per matrix
-  int n_fast;                             // column tiles vary fastest
-  int64_t total;                          // tiles of all matrices
-  int p_form, q_form;
-  float alpha, beta, diag;                // D = alpha P Q^T + beta C + diag I
-  const __half* c;                        // [batch][m][ldc], nullable; ldc a multiple of 16
-  int64_t ldc;
-  // the last product: bf16 [batch][m][n]
-  uint16_t* update;                       // nullable
+  CUtensorMap x[2], a, b;                 // loads: 64 x 64 boxes
+  CUtensorMap xs[2], as, bs, out;         // stores: 64 columns x 32 rows
+  int rows, cols, m;                      // X [rows][cols], m the short side
+  int tall;                               // rows > cols
+  int batch, steps;
+  int sym_tiles;                          // tiles of A (and of B) of one matrix
+  int app_m, app_n;                       // row and column tiles of X
+  float alpha[3], alpha_last;             // each product's factor on the accumulators
+  float beta, diag;                       // POLY: + beta A + diag I
+  const __half* ap;                       // A, [batch (x 2)][m][lda], lda a multiple of 16
+  int64_t lda;
+  uint16_t* update;                       // bf16 [batch][rows][cols], nullable
   const uint16_t* w_in;
-  uint16_t* w_out;                        // nullable: w_in * w_keep - D * lr
+  uint16_t* w_out;                        // nullable: w_in * w_keep - lr * value
   float w_keep, lr;
+  int32_t* done;                          // [batch]: epilogue warps that have stored their part of a tile
   int32_t* status;
 };
 
 struct NsTile {
-  int b, ti, tj;
+  int step, op, b, ti, tj;
+  int need;                               // done[b] once every earlier product of the matrix is stored
 };
 
 // First column tile of row tile ti of a symmetric matrix: tiles of 128 fill
@@ -295,27 +315,68 @@ __host__ __device__ __forceinline__ int ns_first(int ti) {
   return PAIR ? ti : ti & ~1;
 }
 
+// Tile t of the whole run: step by step, product by product, matrix by matrix.
 template <bool PAIR>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
+  constexpr int kArrive = PAIR ? 16 : 8;  // epilogue warps of a tile
   NsTile r;
-  const int per = static_cast<int>(P.total / P.batch);
-  r.b = static_cast<int>(t / per);
-  int l = static_cast<int>(t - static_cast<int64_t>(r.b) * per);
-  if (P.sym) {
+  const int app = P.app_m * P.app_n;
+  const int64_t sym_all = static_cast<int64_t>(P.sym_tiles) * P.batch;
+  const int64_t per_step = 2 * sym_all + static_cast<int64_t>(app) * P.batch;
+  r.step = static_cast<int>(t / per_step);
+  int64_t l = t - r.step * per_step;
+  r.op = l < sym_all ? NS_GRAM : l < 2 * sym_all ? NS_POLY : NS_APPLY;
+  l -= r.op * sym_all;
+  r.need = kArrive * (r.step * (2 * P.sym_tiles + app) + r.op * P.sym_tiles);
+  if (r.op != NS_APPLY) {
+    r.b = static_cast<int>(l / P.sym_tiles);
+    int i = static_cast<int>(l - static_cast<int64_t>(r.b) * P.sym_tiles);
+    const int tiles = P.tall ? P.app_n : P.app_m;      // of the short side
     r.ti = 0;
-    while (l >= P.tiles_m - ns_first<PAIR>(r.ti)) {
-      l -= P.tiles_m - ns_first<PAIR>(r.ti);
+    while (i >= tiles - ns_first<PAIR>(r.ti)) {
+      i -= tiles - ns_first<PAIR>(r.ti);
       ++r.ti;
     }
-    r.tj = ns_first<PAIR>(r.ti) + l;
-  } else if (P.n_fast) {
-    r.ti = l / P.tiles_n;
-    r.tj = l - r.ti * P.tiles_n;
+    r.tj = ns_first<PAIR>(r.ti) + i;
   } else {
-    r.tj = l / P.tiles_m;
-    r.ti = l - r.tj * P.tiles_m;
+    // the short side's tiles vary fastest: B stays in L2, X streams
+    r.b = static_cast<int>(l / app);
+    const int i = static_cast<int>(l - static_cast<int64_t>(r.b) * app);
+    const int f = P.tall ? P.app_n : P.app_m;
+    r.ti = P.tall ? i / f : i % f;
+    r.tj = P.tall ? i % f : i / f;
   }
   return r;
+}
+
+struct NsOperands {
+  const CUtensorMap *p, *q;
+  int p_form, q_form;
+  int nk;                                 // stages of the contraction, of one pair of parts
+};
+
+__device__ __forceinline__ NsOperands ns_operands(const NsArgs& P, const NsTile& tc) {
+  const CUtensorMap* x = &P.x[tc.step & 1];
+  const int short_k = (P.m + kNsK - 1) / kNsK;
+  if (tc.op == NS_GRAM) {
+    const int f = P.tall ? NS_MN : NS_K;
+    return {x, x, f, f, ((P.tall ? P.rows : P.cols) + kNsK - 1) / kNsK};
+  }
+  if (tc.op == NS_POLY) return {&P.a, &P.a, NS_SYM, NS_SYM, short_k};
+  if (P.tall) return {x, &P.b, NS_K, NS_SYM, short_k};
+  return {&P.b, x, NS_SYM, NS_MN, short_k};
+}
+
+// Waits until the products before tile tc of its matrix are in memory.
+__device__ __forceinline__ bool ns_wait_done(const NsArgs& P, const NsTile& tc, volatile int* abort) {
+  const int32_t* c = P.done + tc.b;
+  if (ld_acquire_gpu(c) >= tc.need) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 32; ++i)          // the clock is read now and then: it takes longer than the count
+      if (ld_acquire_gpu(c) >= tc.need) return true;
+    if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
 }
 
 // Whether the 64 contraction elements from k0 of operand rows row0 .. are read
@@ -340,34 +401,19 @@ __device__ __forceinline__ uint64_t ns_desc(const uint8_t* op, bool mn) {
   return smem_desc(smem_u32(op), mn ? kNsBoxBytes : 0, 1024, kLayoutSwizzle128B);
 }
 
-// 64 columns of a row of C, zero past the matrix's edge (whole 32-byte pieces:
-// rows are padded to 16).  NC: nothing writes the matrix during the kernel.
-template <bool NC>
+// 64 columns of a row, zero past the matrix's edge (whole 32-byte pieces: rows
+// are padded to 16), through L2: other SMs wrote A during this kernel.
 __device__ __forceinline__ void ns_load_row(const void* base, int64_t off, bool in, int col, int n,
                                             uint32_t (&w)[32]) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     if (in && col + 16 * h < n) {
-      const uint16_t* src = static_cast<const uint16_t*>(base) + off + 16 * h;
-      if (NC) ld_global_nc_v8(src, w + 8 * h);
-      else ld_global_v8(src, w + 8 * h);
+      ld_global_cg_v8(static_cast<const uint16_t*>(base) + off + 16 * h, w + 8 * h);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[8 * h + i] = 0u;
     }
   }
-}
-
-// alpha acc, and for a polynomial in A (ADD) + beta C + diag where row == col.
-template <bool ADD>
-__device__ __forceinline__ float2 ns_value(const NsArgs& P, uint32_t r0, uint32_t r1, uint32_t c, int row, int col) {
-  float2 v = make_float2(P.alpha * __uint_as_float(r0), P.alpha * __uint_as_float(r1));
-  if constexpr (ADD) {
-    const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&c));
-    v.x = fmaf(P.beta, cf.x, v.x) + (row == col ? P.diag : 0.f);
-    v.y = fmaf(P.beta, cf.y, v.y) + (row == col + 1 ? P.diag : 0.f);
-  }
-  return v;
 }
 
 // 32 rows x 64 columns of packed 16-bit results (this lane's row in h) to
@@ -399,14 +445,14 @@ __device__ __forceinline__ void ns_store_rows(const NsArgs& P, const float (&v)[
 #pragma unroll
   for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = v[i];
   __syncwarp();
-  const int ny = min(32, P.m - row0);
-  const bool in = col0 + lane < P.n;
-  const int64_t base = (static_cast<int64_t>(b) * P.m + row0) * P.n + col0 + lane;
+  const int ny = min(32, P.rows - row0);
+  const bool in = col0 + lane < P.cols;
+  const int64_t base = (static_cast<int64_t>(b) * P.rows + row0) * P.cols + col0 + lane;
 #pragma unroll 8
   for (int i = 0; i < 32; ++i) {
     if (i < ny && in) {
       const float x = buf[i * 33 + lane];
-      const int64_t u = base + static_cast<int64_t>(i) * P.n;
+      const int64_t u = base + static_cast<int64_t>(i) * P.cols;
       if (P.update != nullptr) P.update[u] = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
       if (P.w_out != nullptr)
         P.w_out[u] =
@@ -415,10 +461,91 @@ __device__ __forceinline__ void ns_store_rows(const NsArgs& P, const float (&v)[
   }
 }
 
-template <bool PAIR, int OUT>
-__global__ void __launch_bounds__(kNsThreads, 1)
-    ns_product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ NsArgs P) {
+// What an epilogue warp does with its 32 rows x 64 columns of a tile.
+enum NsKind { NS_STORE,                   // alpha acc to fp16
+              NS_POLYNOMIAL,              // alpha acc + beta A + diag I to fp16
+              NS_UPDATE,                  // alpha acc to bf16
+              NS_WEIGHTS,                 // w_in * w_keep - lr alpha acc to bf16
+              NS_BY_ROWS };               // update and / or weights by plain stores
+
+// Reads the 64 columns from TMEM at taddr, lets release() run once they are in
+// registers, and stores them (row0, col: of D; any: the block is not wholly
+// outside it).
+template <int KIND, bool SPLIT, typename F>
+__device__ __forceinline__ void ns_epilogue(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* boxes,
+                                            uint32_t& flip, const CUtensorMap* dst, int row0, int col, int b, bool any,
+                                            int lane, F release) {
+  constexpr int ADD = KIND == NS_POLYNOMIAL || KIND == NS_WEIGHTS ? 32 : 1;
+  uint32_t w[ADD], wl[SPLIT && KIND == NS_POLYNOMIAL ? 32 : 1];
+  if constexpr (KIND == NS_POLYNOMIAL) {
+    const bool in = row0 + lane < P.m;
+    const int64_t off = (static_cast<int64_t>(b) * P.m + row0 + lane) * P.lda + col;
+    ns_load_row(P.ap, off, in, col, P.m, w);
+    if constexpr (SPLIT) ns_load_row(P.ap + static_cast<int64_t>(P.batch) * P.m * P.lda, off, in, col, P.m, wl);
+  }
+  if constexpr (KIND == NS_WEIGHTS)
+    ns_load_row(P.w_in, (static_cast<int64_t>(b) * P.rows + row0 + lane) * P.cols + col, row0 + lane < P.rows, col,
+                P.cols, w);
+  uint32_t h[32], l[SPLIT ? 32 : 1];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + 32 * half, r);
+    tmem_ld_wait();
+    if (half == 1) release();
+    if constexpr (KIND == NS_BY_ROWS) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = alpha * __uint_as_float(r[i]);
+      if (any && col + 32 * half < P.cols)
+        ns_store_rows(P, v, reinterpret_cast<float*>(boxes), row0, col + 32 * half, b, lane);
+    } else {
+      const int d = row0 + lane - col - 32 * half;             // row - column of the first value
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = 16 * half + i;
+        float x = alpha * __uint_as_float(r[2 * i]), y = alpha * __uint_as_float(r[2 * i + 1]);
+        if constexpr (KIND == NS_POLYNOMIAL) {
+          float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          if constexpr (SPLIT) {
+            const float2 al = __half22float2(*reinterpret_cast<const __half2*>(&wl[j]));
+            a.x += al.x;
+            a.y += al.y;
+          }
+          x = fmaf(P.beta, a.x, x) + (d == 2 * i ? P.diag : 0.f);
+          y = fmaf(P.beta, a.y, y) + (d == 2 * i + 1 ? P.diag : 0.f);
+        }
+        if constexpr (KIND == NS_WEIGHTS) {
+          x = fmaf(-P.lr, x, __uint_as_float(w[j] << 16) * P.w_keep);
+          y = fmaf(-P.lr, y, __uint_as_float(w[j] & 0xffff0000u) * P.w_keep);
+        }
+        if constexpr (KIND == NS_UPDATE || KIND == NS_WEIGHTS) {
+          h[j] = pack_bf16x2(x, y);
+        } else if constexpr (SPLIT) {
+          h[j] = split_half2(x, y, l[j]);
+        } else {
+          const __half2 v = __floats2half2_rn(x, y);
+          h[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+    }
+  }
+  if constexpr (KIND != NS_BY_ROWS) {
+    if (any) {
+      ns_store_box(h, boxes + flip * kNsOut, dst, row0, col, b, lane);
+      flip ^= 1;
+      if constexpr (SPLIT && (KIND == NS_STORE || KIND == NS_POLYNOMIAL)) {
+        ns_store_box(l, boxes + flip * kNsOut, dst, row0, col, b + P.batch, lane);
+        flip ^= 1;
+      }
+    }
+  }
+}
+
+// ROWS: the last product leaves by plain stores (rows that TMA cannot address,
+// or both outputs at once).  SPLIT: operands in two fp16 parts.
+template <bool PAIR, bool ROWS, bool SPLIT>
+__global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsArgs P) {
   constexpr int CG = PAIR ? 2 : 1;
   constexpr int BN = PAIR ? 256 : 128;    // columns of a tile (and accumulator columns)
   constexpr int TM = PAIR ? 256 : 128;    // rows of a tile, both CTAs
@@ -454,9 +581,12 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmP);
-    tma_prefetch_desc(&tmQ);
-    if (OUT != NS_ROWS) tma_prefetch_desc(&tmO);
+    tma_prefetch_desc(&P.x[0]);
+    tma_prefetch_desc(&P.a);
+    tma_prefetch_desc(&P.b);
+    tma_prefetch_desc(&P.as);
+    tma_prefetch_desc(&P.bs);
+    tma_prefetch_desc(&P.xs[1]);
   }
   __syncthreads();
   if (warp == 1) {
@@ -470,7 +600,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
   const int64_t tstep = PAIR ? gridDim.x / 2 : gridDim.x;
-  const int nk = (P.k + kNsK - 1) / kNsK;
+  const int64_t total = static_cast<int64_t>(P.steps) * P.batch * (2 * P.sym_tiles + P.app_m * P.app_n);
+  // in parts: first (high, low), (low, high), then (high, high)
+  constexpr int parts = SPLIT ? 3 : 1;
   auto fail = [&]() {
     report(P.status, MXG_ERR_TIMEOUT);
     *abort_flag = 1;
@@ -481,11 +613,19 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       uint32_t stage = 0, phase = 0;
       bool aborted = false;
       const uint32_t full0 = PAIR ? map_to_rank(smem_u32(full), 0) : 0u;
-      for (int64_t t = tile0; t < P.total && !aborted; t += tstep) {
+      for (int64_t t = tile0; t < total && !aborted; t += tstep) {
         const NsTile tc = ns_tile<PAIR>(P, t);
         const int prow = tc.ti * TM + static_cast<int>(rank) * kNsRows;
         const int qrow = tc.tj * BN + static_cast<int>(rank) * kNsRows;
-        for (int kb = 0; kb < nk; ++kb) {
+        const NsOperands o = ns_operands(P, tc);
+        if (!ns_wait_done(P, tc, abort_flag)) {
+          fail();
+          aborted = true;
+          break;
+        }
+        fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
+        for (int kp = 0, kb = 0, part = 0; kp < parts * o.nk; ++kp) {
+          const int pz = tc.b + (SPLIT && part == 1 ? P.batch : 0), qz = tc.b + (SPLIT && part == 0 ? P.batch : 0);
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
@@ -494,18 +634,22 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           uint8_t* sP = sm + stage * kNsStageBytes;
           uint8_t* sQ = sP + kNsOpBytes;
           const int k0 = kb * kNsK;
-          const bool pmn = ns_transposed(P.p_form, prow, k0), qmn = ns_transposed(P.q_form, qrow, k0);
+          const bool pmn = ns_transposed(o.p_form, prow, k0), qmn = ns_transposed(o.q_form, qrow, k0);
           if (!PAIR || rank == 0) {
             mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);     // both CTAs' bytes
-            ns_load<false>(sP, &tmP, pmn, prow, k0, tc.b, &full[stage], 0u);
-            ns_load<false>(sQ, &tmQ, qmn, qrow, k0, tc.b, &full[stage], 0u);
+            ns_load<false>(sP, o.p, pmn, prow, k0, pz, &full[stage], 0u);
+            ns_load<false>(sQ, o.q, qmn, qrow, k0, qz, &full[stage], 0u);
           } else {
-            ns_load<true>(sP, &tmP, pmn, prow, k0, tc.b, nullptr, full0 + stage * 8);
-            ns_load<true>(sQ, &tmQ, qmn, qrow, k0, tc.b, nullptr, full0 + stage * 8);
+            ns_load<true>(sP, o.p, pmn, prow, k0, pz, nullptr, full0 + stage * 8);
+            ns_load<true>(sQ, o.q, qmn, qrow, k0, qz, nullptr, full0 + stage * 8);
           }
           if (++stage == kNsStages) {
             stage = 0;
             phase ^= 1;
+          }
+          if (++kb == o.nk) {
+            kb = 0;
+            ++part;
           }
         }
       }
@@ -519,7 +663,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool aborted = false;
       int64_t done = 0;
-      for (int64_t t = tile0; t < P.total && !aborted; t += tstep) {
+      for (int64_t t = tile0; t < total && !aborted; t += tstep) {
         const NsTile tc = ns_tile<PAIR>(P, t);
         const bool got = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)
                               : mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs);
@@ -529,7 +673,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         tc_fence_after();
         const uint32_t d_t = tmem + acc * BN;
-        for (int kb = 0; kb < nk; ++kb) {
+        const NsOperands o = ns_operands(P, tc);
+        for (int kp = 0, kb = 0; kp < parts * o.nk; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
           if (!in) {
@@ -539,16 +684,17 @@ __global__ void __launch_bounds__(kNsThreads, 1)
           }
           tc_fence_after();
           // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
-          const bool pmn = ns_transposed(P.p_form, tc.ti * TM, kb * kNsK);
-          const bool qmn = ns_transposed(P.q_form, tc.tj * BN, kb * kNsK);
+          const bool pmn = ns_transposed(o.p_form, tc.ti * TM, kb * kNsK);
+          const bool qmn = ns_transposed(o.q_form, tc.tj * BN, kb * kNsK);
           const uint8_t* sP = sm + stage * kNsStageBytes;
           const uint64_t pd = ns_desc(sP, pmn), qd = ns_desc(sP + kNsOpBytes, qmn);
           const uint32_t pstep = pmn ? 2048 >> 4 : 32 >> 4, qstep = qmn ? 2048 >> 4 : 32 >> 4;
           const uint32_t id = idesc_f16(TM, BN) | (pmn ? kIdescAMn : 0u) | (qmn ? kIdescBMn : 0u);
 #pragma unroll
           for (uint32_t k = 0; k < kNsK / 16; ++k)
-            mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kb | k) != 0 ? 1u : 0u);
+            mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kp | k) != 0 ? 1u : 0u);
           mma_commit<CG>(&empty[stage]);
+          if (++kb == o.nk) kb = 0;
           if (++stage == kNsStages) {
             stage = 0;
             phase ^= 1;
@@ -574,25 +720,23 @@ __global__ void __launch_bounds__(kNsThreads, 1)
   } else if (warp >= 4) {
     constexpr int COLS = BN / 2;
     constexpr int BOXES = COLS / 64;
-    constexpr bool ADD = OUT == NS_POLY;
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
     uint32_t acc = 0, acc_phase = 0, flip = 0;
-    for (int64_t t = tile0; t < P.total; t += tstep) {
+    for (int64_t t = tile0; t < total; t += tstep) {
       const NsTile tc = ns_tile<PAIR>(P, t);
+      const bool last = tc.op == NS_APPLY && tc.step + 1 == P.steps;
       const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
       const int col0 = tc.tj * BN + hf * COLS;
-      const bool in = row0 + lane < P.m;
-      // the addend is on its way while the tile's MMAs run
-      uint32_t cv[ADD ? BOXES : 1][32];
-      if constexpr (ADD) {
-#pragma unroll
-        for (int c = 0; c < BOXES; ++c)
-          ns_load_row<true>(P.c, (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.ldc + col0 + 64 * c, in,
-                            col0 + 64 * c, P.n, cv[c]);
+      const int dm = tc.op == NS_APPLY ? P.rows : P.m, dn = tc.op == NS_APPLY ? P.cols : P.m;   // of D
+      // A is read by plain loads here, so this warp, too, waits for it
+      bool got = true;
+      if (tc.op == NS_POLY) {
+        if (lane == 0) got = ns_wait_done(P, tc, abort_flag);
+        __syncwarp();
       }
-      bool got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs);
+      got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs) && got;
       got = __all_sync(0xffffffffu, got);
       if (!got) {
         if (lane == 0) fail();
@@ -600,70 +744,48 @@ __global__ void __launch_bounds__(kNsThreads, 1)
       }
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < BOXES; ++c) {
         const int col = col0 + 64 * c;
-        const bool any = row0 < P.m && col < P.n;
-        uint32_t h[32], w[32];
-        if (OUT == NS_LAST && P.w_out != nullptr)
-          ns_load_row<false>(P.w_in, (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.n + col, in, col, P.n, w);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tb + 64 * c + 32 * half, r);
-          tmem_ld_wait();
-          if (c == BOXES - 1 && half == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (PAIR && rank == 1)
-                st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
-                                     map_to_rank(smem_u32(&tempty[acc]), 0));
-              else
-                mbar_arrive(&tempty[acc]);
-            }
+        const bool any = row0 < dm && col < dn;
+        auto release = [&]() {            // after the last columns: the accumulator may be overwritten
+          if (c != BOXES - 1) return;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR && rank == 1)
+              st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
+                                   map_to_rank(smem_u32(&tempty[acc]), 0));
+            else
+              mbar_arrive(&tempty[acc]);
           }
-          if constexpr (OUT == NS_ROWS) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = ns_value<false>(P, r[2 * i], r[2 * i + 1], 0u, 0, 0);
-              v[2 * i] = x.x;
-              v[2 * i + 1] = x.y;
-            }
-            if (any && col + 32 * half < P.n)
-              ns_store_rows(P, v, reinterpret_cast<float*>(box), row0, col + 32 * half, tc.b, lane);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 x = ns_value<ADD>(P, r[2 * i], r[2 * i + 1], cv[ADD ? c : 0][16 * half + i], row0 + lane,
-                                       col + 32 * half + 2 * i);
-              if constexpr (OUT == NS_F16 || ADD) {
-                const __half2 v = __floats2half2_rn(x.x, x.y);
-                h[16 * half + i] = *reinterpret_cast<const uint32_t*>(&v);
-              } else {
-                if (P.w_out != nullptr) {
-                  const uint32_t wv = w[16 * half + i];
-                  x.x = fmaf(-P.lr, x.x, __uint_as_float(wv << 16) * P.w_keep);
-                  x.y = fmaf(-P.lr, x.y, __uint_as_float(wv & 0xffff0000u) * P.w_keep);
-                }
-                h[16 * half + i] = pack_bf16x2(x.x, x.y);
-              }
-            }
-          }
-        }
-        if (OUT != NS_ROWS && any) {
-          ns_store_box(h, box + flip * kNsOut, &tmO, row0, col, tc.b, lane);
-          flip ^= 1;
-        }
+        };
+        const uint32_t ta = tb + 64 * c;
+        if (tc.op == NS_GRAM)
+          ns_epilogue<NS_STORE, SPLIT>(P, P.alpha[NS_GRAM], ta, box, flip, &P.as, row0, col, tc.b, any, lane, release);
+        else if (tc.op == NS_POLY)
+          ns_epilogue<NS_POLYNOMIAL, SPLIT>(P, P.alpha[NS_POLY], ta, box, flip, &P.bs, row0, col, tc.b, any, lane,
+                                            release);
+        else if (!last)
+          ns_epilogue<NS_STORE, SPLIT>(P, P.alpha[NS_APPLY], ta, box, flip, &P.xs[(tc.step & 1) ^ 1], row0, col, tc.b,
+                                       any, lane, release);
+        else if (ROWS)
+          ns_epilogue<NS_BY_ROWS, SPLIT>(P, P.alpha_last, ta, box, flip, nullptr, row0, col, tc.b, any, lane, release);
+        else if (P.w_out != nullptr)
+          ns_epilogue<NS_WEIGHTS, SPLIT>(P, P.alpha_last, ta, box, flip, &P.out, row0, col, tc.b, any, lane, release);
+        else
+          ns_epilogue<NS_UPDATE, SPLIT>(P, P.alpha_last, ta, box, flip, &P.out, row0, col, tc.b, any, lane, release);
+      }
+      if (!last && lane == 0) {
+        bulk_wait_group<0>();             // the stores are in memory,
+        fence_proxy_async_global();
+        red_release_gpu_add(P.done + tc.b, 1);
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-    if (OUT != NS_ROWS) {
-      if (lane == 0) bulk_wait_group<0>();           // the stores have completed before the CTA exits
-      __syncwarp();
-    }
+    if (lane == 0) bulk_wait_group<0>();  // the stores have completed before the CTA exits
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -681,75 +803,82 @@ int sm_count() {
   return n > 0 ? n : 1;
 }
 
-template <bool PAIR, int OUT>
-cudaError_t launch_ns(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, NsArgs a, cudaStream_t s) {
-  constexpr int W = PAIR ? 256 : 128;
-  a.tiles_m = (a.m + W - 1) / W;
-  a.tiles_n = (a.n + W - 1) / W;
-  int64_t per = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
-  if (a.sym) {
-    per = 0;
-    for (int i = 0; i < a.tiles_m; ++i) per += a.tiles_m - ns_first<PAIR>(i);
-  }
-  a.total = per * a.batch;
-  auto kern = ns_product_kernel<PAIR, OUT>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
-  if (err != cudaSuccess) return err;
-  const int64_t units = PAIR ? sm_count() / 2 : sm_count();
-  const int64_t n = a.total < units ? a.total : units;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * n : n));
-  cfg.blockDim = dim3(kNsThreads);
-  cfg.dynamicSmemBytes = kNsSmem;
-  cfg.stream = s;
+// CTAs (or pairs) of a kernel that the device holds at once.
+template <bool PAIR, bool ROWS, bool SPLIT>
+int ns_resident() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && known[dev].load() > 0) return known[dev].load();
+  auto kern = ns_kernel<PAIR, ROWS, SPLIT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess) return 0;
+  int n = 0;
   if (PAIR) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kNsThreads);
+    cfg.dynamicSmemBytes = kNsSmem;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  } else {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kNsThreads, kNsSmem) != cudaSuccess) return 0;
+    n *= sm_count();
   }
-  err = cudaLaunchKernelEx(&cfg, kern, mp, mq, mo, a);
+  if (dev < 64) known[dev].store(n);
+  return n;
+}
+
+template <bool PAIR, bool ROWS, bool SPLIT>
+cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
+  constexpr int W = PAIR ? 256 : 128;
+  a.app_m = (a.rows + W - 1) / W;
+  a.app_n = (a.cols + W - 1) / W;
+  const int t = a.tall ? a.app_n : a.app_m;
+  a.sym_tiles = 0;
+  for (int i = 0; i < t; ++i) a.sym_tiles += t - ns_first<PAIR>(i);
+  const int64_t most = static_cast<int64_t>(a.app_m) * a.app_n * a.batch;     // of any product
+  const int64_t units = ns_resident<PAIR, ROWS, SPLIT>();
+  if (units <= 0) return cudaErrorCooperativeLaunchTooLarge;
+  const int64_t n = most < units ? most : units;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * n : n));
+  cfg.blockDim = dim3(kNsThreads);
+  cfg.dynamicSmemBytes = kNsSmem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ns_kernel<PAIR, ROWS, SPLIT>, a);
   count_launch();
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-struct NsMat {                            // 16-bit [batch][rows][cols], rows ld apart
-  void* p;
-  int rows, cols;
-  int64_t ld;
-};
-
-// D of one product over the batch: operands p and q in their forms, D to o
-// (fp16, or the caller's bf16 matrix as a says).
-cudaError_t ns_product(NsArgs a, const NsMat& p, const NsMat& q, const NsMat& o, int out, cudaStream_t s) {
-  CUtensorMap mp, mq, mo;
-  a.m = o.rows;
-  a.n = o.cols;
-  a.k = a.p_form == NS_K ? p.cols : p.rows;
-  if (!tma_map_b16_3d(&mp, p.p, p.cols, p.rows, a.batch, p.ld, 64) ||
-      !tma_map_b16_3d(&mq, q.p, q.cols, q.rows, a.batch, q.ld, 64))
-    return cudaErrorInvalidValue;
-  mo = mp;
-  if (out != NS_ROWS && !tma_map_b16_3d(&mo, o.p, o.cols, o.rows, a.batch, o.ld, 32)) return cudaErrorInvalidValue;
-  const int64_t tm = (a.m + 255) / 256, tn = (a.n + 255) / 256;
-  const bool pair = (a.sym ? tm * (tm + 1) / 2 : tm * tn) * a.batch >= sm_count() / 2;
-  if (out == NS_POLY)
-    return pair ? launch_ns<true, NS_POLY>(mp, mq, mo, a, s) : launch_ns<false, NS_POLY>(mp, mq, mo, a, s);
-  if (out == NS_F16) return pair ? launch_ns<true, NS_F16>(mp, mq, mo, a, s) : launch_ns<false, NS_F16>(mp, mq, mo, a, s);
-  if (out == NS_LAST)
-    return pair ? launch_ns<true, NS_LAST>(mp, mq, mo, a, s) : launch_ns<false, NS_LAST>(mp, mq, mo, a, s);
-  return pair ? launch_ns<true, NS_ROWS>(mp, mq, mo, a, s) : launch_ns<false, NS_ROWS>(mp, mq, mo, a, s);
-}
-
 struct NsPlan {
   int m, n, tall;                         // short and long side; tall: the matrix is [n][m]
+  int split;
   int64_t ldx, lda;                       // row lengths of X and of A and B, padded to 16
   int chunks;                             // partial sums of squares per matrix
-  int64_t part, x0, x1, a, b, bytes;
+  int64_t part, done, x0, x1, a, b, bytes;
 };
+
+// A short side up to this is computed in two fp16 parts (high and low, three
+// products instead of one).  Simulated in 64 bits, gradients of a few strong
+// directions over noise, the error of the bf16 update against an exact run
+// (its own rounding alone is 1.66e-3): one part 3.1e-3 at 8 x 8, 2.4e-3 at
+// 16 x 2000, 2.2e-3 from 64 x 64 to 256 x 256; two parts 1.67e-3.
+constexpr int kNsSplitMost = 64;          // not above 128: pairs do not split
 
 NsPlan ns_plan(int batch, int rows, int cols) {
   NsPlan p{};
@@ -763,8 +892,11 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   const int64_t most = (152 * 8 + batch - 1) / batch;
   p.chunks = static_cast<int>(c < most ? c : most);
   api::Carver w;
+  p.split = p.m <= kNsSplitMost;
   p.part = w.take(8ll * batch * p.chunks);
-  const int64_t xb = 2ll * batch * rows * p.ldx, ab = 2ll * batch * p.m * p.lda;
+  p.done = w.take(4ll * batch);
+  const int64_t one = p.split ? 4 : 2;    // bytes of an element
+  const int64_t xb = one * batch * rows * p.ldx, ab = one * batch * p.m * p.lda;
   p.x0 = w.take(xb);
   p.x1 = w.take(xb);
   p.a = w.take(ab);
@@ -776,8 +908,11 @@ NsPlan ns_plan(int batch, int rows, int cols) {
 int muon_shape(int batch, int rows, int cols) {
   if (batch <= 0 || rows <= 0 || cols <= 0) return MXG_ERR_ARG;
   const int64_t longest = rows > cols ? rows : cols;
-  // grid and tensor-map coordinates are 32-bit
-  if (batch > 65535 || longest > (1 << 21) || batch * longest > INT32_MAX - 256) return MXG_ERR_SHAPE;
+  // grid and tensor-map coordinates are 32-bit, and so are the counts of finished parts of a matrix (sixteen
+  // warps on each of at most three tiles per 128 x 128 elements, 64 steps)
+  const int64_t tiles = static_cast<int64_t>((rows + 127) / 128) * ((cols + 127) / 128);
+  if (batch > 65535 || longest > (1 << 21) || batch * longest > INT32_MAX - 256 || tiles > INT32_MAX / (16 * 3 * 64))
+    return MXG_ERR_SHAPE;
   return MXG_OK;
 }
 
@@ -807,10 +942,10 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   api::NvtxRange nvtx("mxg.muon_update");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* part = api::at<double>(a->workspace, p.part);
-  const NsMat x[2] = {{api::at<void>(a->workspace, p.x0), a->rows, a->cols, p.ldx},
-                      {api::at<void>(a->workspace, p.x1), a->rows, a->cols, p.ldx}};
-  const NsMat am{api::at<void>(a->workspace, p.a), p.m, p.m, p.lda};
-  const NsMat bm{api::at<void>(a->workspace, p.b), p.m, p.m, p.lda};
+  int32_t* done = api::at<int32_t>(a->workspace, p.done);
+  __half* x[2] = {api::at<__half>(a->workspace, p.x0), api::at<__half>(a->workspace, p.x1)};
+  __half* am = api::at<__half>(a->workspace, p.a);
+  __half* bm = api::at<__half>(a->workspace, p.b);
   int ex = 0;                             // 2^ex ~ sqrt(n)
   while ((1ll << (2 * ex)) < p.n) ++ex;
 
@@ -818,58 +953,60 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
   const unsigned nb = static_cast<unsigned>(a->batch);
   // 32-byte loads where every matrix (and, for the cast, every row) starts on 32 bytes of each buffer
-  if (per % 16 == 0) momentum_kernel<true><<<dim3(static_cast<unsigned>(p.chunks), nb), kMoThreads, 0, s>>>(mo, p.chunks, part);
-  else momentum_kernel<false><<<dim3(static_cast<unsigned>(p.chunks), nb), kMoThreads, 0, s>>>(mo, p.chunks, part);
+  const dim3 mgrid(static_cast<unsigned>(p.chunks), nb);
+  if (per % 16 == 0) momentum_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done);
+  else momentum_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done);
   count_launch();
-  const dim3 cgrid(static_cast<unsigned>(p.chunks), nb);
-  __half* x0 = static_cast<__half*>(x[0].p);
-  if (a->cols % 16 == 0) cast_kernel<true><<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x0, p.ldx);
-  else cast_kernel<false><<<cgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x0, p.ldx);
+  const int64_t lo_off = p.split ? static_cast<int64_t>(a->batch) * a->rows * p.ldx : 0;
+  if (a->cols % 16 == 0)
+    cast_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x[0], p.ldx, lo_off);
+  else cast_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x[0], p.ldx, lo_off);
   count_launch();
   if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
 
-  for (int i = 0; i < a->steps; ++i) {
-    const int cur = i & 1, nxt = cur ^ 1;
-    const bool last = i + 1 == a->steps;
-    // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex)
-    NsArgs ga{};
-    ga.batch = a->batch;
-    ga.status = a->dev_status;
-    ga.sym = 1;
-    ga.p_form = ga.q_form = p.tall ? NS_MN : NS_K;
-    ga.alpha = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
-    MXG_TRY(ns_product(ga, x[cur], x[cur], am, NS_F16, s));
-    // B 2^12 = a 2^12 I + b (A 2^12) + c 2^-12 (A 2^12)(A 2^12)
-    NsArgs gb = ga;
-    gb.p_form = gb.q_form = NS_SYM;
-    gb.alpha = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
-    gb.beta = a->b;
-    gb.diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
-    gb.c = static_cast<const __half*>(am.p);
-    gb.ldc = am.ld;
-    MXG_TRY(ns_product(gb, am, am, bm, NS_POLY, s));
-    // X' 2^ex = 2^-12 (B 2^12)(X 2^ex), X B when tall; the last one leaves as scale X'.
-    // The short side's tiles vary fastest, so B stays in L2 and X streams.
-    NsArgs gx{};
-    gx.batch = a->batch;
-    gx.status = a->dev_status;
-    gx.n_fast = p.tall;
-    gx.p_form = p.tall ? NS_K : NS_SYM;
-    gx.q_form = p.tall ? NS_SYM : NS_MN;
-    gx.alpha = static_cast<float>(last ? a->scale * std::ldexp(1.0, -kExpA - ex) : std::ldexp(1.0, -kExpA));
-    NsMat o = x[nxt];
-    int out = NS_F16;
-    if (last) {
-      gx.update = a->update;
-      gx.w_in = a->w_in;
-      gx.w_out = a->w_out;
-      gx.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
-      gx.lr = a->lr;
-      o = NsMat{a->w_out ? a->w_out : a->update, a->rows, a->cols, a->cols};
-      // whole 32-byte pieces of the caller's rows, one output
-      out = a->cols % 16 == 0 && !(a->w_out && a->update) ? NS_LAST : NS_ROWS;
-    }
-    MXG_TRY(ns_product(gx, p.tall ? x[cur] : bm, p.tall ? bm : x[cur], o, out, s));
+  NsArgs n{};
+  n.rows = a->rows;
+  n.cols = a->cols;
+  n.m = p.m;
+  n.tall = p.tall;
+  n.batch = a->batch;
+  n.steps = a->steps;
+  // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex);  B 2^12 = a 2^12 I + b (A 2^12) + c 2^-12 (A 2^12)(A 2^12);
+  // X' 2^ex = 2^-12 (B 2^12)(X 2^ex), the last one scale X'
+  n.alpha[NS_GRAM] = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
+  n.alpha[NS_POLY] = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
+  n.alpha[NS_APPLY] = static_cast<float>(std::ldexp(1.0, -kExpA));
+  n.alpha_last = static_cast<float>(std::ldexp(static_cast<double>(a->scale), -kExpA - ex));
+  n.beta = a->b;
+  n.diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
+  n.ap = am;
+  n.lda = p.lda;
+  n.update = a->update;
+  n.w_in = a->w_in;
+  n.w_out = a->w_out;
+  n.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
+  n.lr = a->lr;
+  n.done = done;
+  n.status = a->dev_status;
+  const int64_t mats = static_cast<int64_t>(a->batch) * (p.split ? 2 : 1);
+  bool ok = true;
+  for (int i = 0; i < 2; ++i) {
+    ok = ok && tma_map_b16_3d(&n.x[i], x[i], a->cols, a->rows, mats, p.ldx, 64);
+    ok = ok && tma_map_b16_3d(&n.xs[i], x[i], a->cols, a->rows, mats, p.ldx, 32);
   }
-  return MXG_OK;
+  ok = ok && tma_map_b16_3d(&n.a, am, p.m, p.m, mats, p.lda, 64) && tma_map_b16_3d(&n.as, am, p.m, p.m, mats, p.lda, 32);
+  ok = ok && tma_map_b16_3d(&n.b, bm, p.m, p.m, mats, p.lda, 64) && tma_map_b16_3d(&n.bs, bm, p.m, p.m, mats, p.lda, 32);
+  // whole 32-byte pieces of the caller's rows, one output
+  const bool by_rows = a->cols % 16 != 0 || (a->w_out && a->update);
+  if (!by_rows)
+    ok = ok && tma_map_b16_3d(&n.out, a->w_out ? a->w_out : a->update, a->cols, a->rows, a->batch, a->cols, 32);
+  if (!ok) return MXG_ERR_CUDA;
+  // a pair's 256 x 256 tiles read half as much per product; with fewer of them than pairs, or a short side that
+  // fills only one of the two SMs, the smaller tiles keep more SMs busy
+  const int64_t t256 = static_cast<int64_t>((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
+  cudaError_t err;
+  if (t256 >= sm_count() / 2 && p.m > 128) err = by_rows ? launch_ns<true, true, false>(n, s) : launch_ns<true, false, false>(n, s);
+  else if (p.split) err = by_rows ? launch_ns<false, true, true>(n, s) : launch_ns<false, false, true>(n, s);
+  else err = by_rows ? launch_ns<false, true, false>(n, s) : launch_ns<false, false, false>(n, s);
+  return api::cuda_status(err);
 }

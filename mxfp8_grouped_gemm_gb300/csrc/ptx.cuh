@@ -245,6 +245,16 @@ __device__ __forceinline__ void ld_global_cg_v8(const void* src, uint32_t* w) {
                : "l"(src)
                : "memory");
 }
+// Counter in global memory shared by CTAs: a load that acquires what a
+// releasing add of another CTA published (gpu scope).
+__device__ __forceinline__ int32_t ld_acquire_gpu(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release_gpu_add(int32_t* p, int32_t v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 // Plain arrive on this CTA's mbarrier, given as a shared-window address.
 __device__ __forceinline__ void mbar_arrive_u32(uint32_t saddr) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr) : "memory");
