@@ -4,88 +4,506 @@
 // on the whole softmax (the balance loss) gives every logit one.  With
 // G = dlogits [T][E]:
 //   dx        = dx_in + G W_r      (bf16, rounded once)
-//   dw_router = G^T x              (fp32, fixed-order sums over token chunks)
+//   dw_router = G^T x              (fp32, fixed-order sums)
+// At most 256 experts make both products thin: reading x and dx_in and writing
+// dx (6 bytes an element) bounds them, so they run on the tensor cores beside
+// the stream of tiles.
+//
+// Precision.  x and W_r are bf16 already; an fp32 gradient is cut into three
+// bf16 parts of eight significant bits each (g = high + mid + low exactly).
+// dx takes high and mid (2^-16 of g, far below its own rounding); dW takes all
+// three, each into columns of its own.  The tensor cores cut their running sums
+// instead of rounding them (measured: 2e-7 of the result after 16 MMAs, 9e-7
+// after 64, 4e-6 after 256), so an accumulator is read out every 256 tokens
+// and added up in fp32 registers.
+//
+// One launch: some CTAs compute dW, the others dx, shared out by bytes moved.
+//  dW: a unit is 128 hidden columns x up to 64 experts.  D[h][part, e] =
+//      x[t][h]^T G[t][part, e], both operands read across the contraction
+//      (MN-major), 128 tokens a stage.  The line of all (unit, token block)
+//      is cut into equal pieces, one per CTA; a CTA leaves one partial per unit
+//      it touches, numbered unit + CTA (unique: along the line one of the two
+//      grows at every seam), and a last kernel adds a unit's partials in order.
+//  dx: 128 tokens x 128 hidden columns a tile, K = 64 experts x 2 parts a
+//      stage (W_r read across); dx_in comes by TMA into the buffer that the
+//      result leaves from.
 #include <climits>
 
 #include "api_common.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace mxg {
 namespace {
 
-constexpr int kRlCols = 512;                  // hidden columns per CTA, two per thread
-constexpr int kRlThreads = kRlCols / 2;
-constexpr int kRlChunk = 256;                 // tokens per partial sum
-constexpr int kRlGroup = 16;                  // experts per CTA of the dW pass
+constexpr int kRlTok = 128;                       // tokens of a block
+constexpr int kRlCols = 128;                      // hidden columns of a unit or tile
+constexpr int kRlGroup = 64;                      // most experts of a group
+constexpr int kRlThreads = 384;
+constexpr int kRlBox = kRlTok * 128;              // 128 rows of 128 bytes
+constexpr int kRlFlush = 2;                       // token blocks per accumulator (256 tokens)
+constexpr int kRlRing = 196608;                   // bytes of all rings
+constexpr int kRlOpStage = 3 * kRlBox;            // dx: two boxes of G, 64 experts x 128 columns of W_r
+constexpr int kRlOpStages = 2;
+constexpr int kRlIo = 2 * kRlBox;                 // dx: one tile of dx_in / dx
+constexpr int kRlIos = 3;
+constexpr int kRlMaxStages = 4;
+constexpr int kRlSmem = 1024 + kRlRing + 1024;
+static_assert(kRlOpStages * kRlOpStage + kRlIos * kRlIo <= kRlRing, "dx rings");
+static_assert(kRlSmem <= 232448, "shared memory budget");
 
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+struct RlArgs {
+  int T, H, E;
+  int eg;                                         // experts of a group, padded to 16
+  int groups;
+  int tb;                                         // token blocks
+  int units;                                      // dW: (H / 128) x groups
+  int n_dw, n_dx;                                 // CTAs of each kind
+  int stages, stage_bytes, g_boxes;               // dW ring
+  int has_in;
+  float* part;                                    // [units + n_dw][eg][128]
+  int32_t* status;
+};
 
-__global__ void __launch_bounds__(kRlThreads) router_linear_dx_kernel(const uint32_t* __restrict__ w,
-                                                                     const float* __restrict__ g,
-                                                                     const uint32_t* dx_in, int T, int H, int E,
-                                                                     uint32_t* dx) {
-  const int hp = blockIdx.x * kRlThreads + threadIdx.x;
-  if (hp >= H / 2) return;
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
-    float lo = 0.f, hi = 0.f;
-    for (int e = 0; e < E; ++e) {
-      const float d = g[t * E + e];
-      const uint32_t wv = w[static_cast<int64_t>(e) * (H / 2) + hp];
-      lo = fmaf(d, lo16(wv), lo);
-      hi = fmaf(d, hi16(wv), hi);
+__device__ __forceinline__ int64_t rl_cut(int64_t n, int i, int parts) { return n * i / parts; }
+
+struct RlBars {
+  uint64_t *full, *empty, *tfull, *tempty, *io_full, *io_empty, *drained;
+  volatile int* abort_flag;
+  volatile int* never_set;
+};
+
+// dW CTA c of n_dw.
+__device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap* tmG, uint8_t* sm, const RlBars& B,
+                      uint32_t tmem, int warp, int lane, int c) {
+  const int64_t all = static_cast<int64_t>(P.units) * P.tb;
+  const int64_t lo = rl_cut(all, c, P.n_dw), hi = rl_cut(all, c + 1, P.n_dw);
+  const int N = 3 * P.eg;
+  auto fail = [&]() {
+    report(P.status, MXG_ERR_TIMEOUT);
+    *B.abort_flag = 1;
+  };
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool aborted = false;
+      for (int64_t i = lo; i < hi; ++i) {
+        const int u = static_cast<int>(i / P.tb), t0 = static_cast<int>(i - static_cast<int64_t>(u) * P.tb) * kRlTok;
+        const int ht = u / P.groups, g = u - ht * P.groups;
+        if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+          fail();
+          aborted = true;
+          break;
+        }
+        uint8_t* s = sm + stage * P.stage_bytes;
+        mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(P.stage_bytes));
+        for (int h = 0; h < 2; ++h) tma_load_2d(s + h * kRlBox, tmX, ht * kRlCols + 64 * h, t0, &B.full[stage]);
+        for (int h = 0; h < P.g_boxes; ++h)
+          tma_load_2d(s + (2 + h) * kRlBox, tmG, g * N + 64 * h, t0, &B.full[stage]);
+        if (++stage == static_cast<uint32_t>(P.stages)) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (aborted) {                              // let copies already in flight land before the CTA exits
+        const uint64_t w0 = globaltimer_ns();
+        while (globaltimer_ns() - w0 < 1000000ull) __nanosleep(1000);
+      }
     }
-    if (dx_in != nullptr) {
-      const uint32_t v = dx_in[t * (H / 2) + hp];
-      lo += lo16(v);
-      hi += hi16(v);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      const uint32_t id = idesc_bf16(kRlCols, N) | kIdescAMn | kIdescBMn;
+      int64_t i = lo;
+      bool aborted = false;
+      while (i < hi && !aborted) {
+        // a run of blocks of one unit that shares an accumulator
+        int64_t end = (i / P.tb + 1) * P.tb;
+        end = end < hi ? end : hi;
+        end = end < i + kRlFlush ? end : i + kRlFlush;
+        if (!mbar_wait_bounded(&B.tempty[acc], acc_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        bool first = true;
+        for (; i < end; ++i) {
+          if (!mbar_wait_bounded(&B.full[stage], phase, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t s = smem_u32(sm + stage * P.stage_bytes);
+          const uint64_t xd = smem_desc(s, kRlBox, 1024, kLayoutSwizzle128B);
+          const uint64_t gd = smem_desc(s + 2 * kRlBox, kRlBox, 1024, kLayoutSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < kRlTok / 16; ++k)   // 16 tokens: 16 rows of 128 bytes
+            mma_bf16<1>(tmem + acc * 256, xd + k * (2048 >> 4), gd + k * (2048 >> 4), id, first && k == 0 ? 0u : 1u);
+          first = false;
+          mma_commit<1>(&B.empty[stage]);
+          if (++stage == static_cast<uint32_t>(P.stages)) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (aborted) break;
+        mma_commit<1>(&B.tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      mma_commit<1>(B.drained);
+      mbar_wait_bounded(B.drained, 0, B.never_set, kWaitLimitNs);
     }
-    dx[t * (H / 2) + hp] = pack_bf16x2(lo, hi);
+  } else if (warp >= 4) {
+    // lane = hidden column; warps 4-7 the first half of the group's experts, warps 8-11 the second
+    const int q = warp & 3, hf = (warp - 4) >> 2;
+    const int half = P.eg / 2;                    // 8, 16, 24 or 32
+    const int row = q * 32 + lane;
+    float sum[kRlGroup / 2];
+#pragma unroll
+    for (int e = 0; e < kRlGroup / 2; ++e) sum[e] = 0.f;
+    uint32_t acc = 0, acc_phase = 0;
+    int64_t i = lo;
+    while (i < hi) {
+      const int u = static_cast<int>(i / P.tb);
+      const int64_t unit_end = static_cast<int64_t>(u + 1) * P.tb;
+      int64_t end = unit_end < hi ? unit_end : hi;
+      const int64_t stop = end;
+      end = end < i + kRlFlush ? end : i + kRlFlush;
+      bool got = mbar_wait_bounded(&B.tfull[acc], acc_phase, B.abort_flag, kWaitLimitNs);
+      got = __all_sync(0xffffffffu, got);
+      if (!got) {
+        if (lane == 0) fail();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256 + hf * half;
+#pragma unroll
+      for (int j = 0; j < kRlGroup / 16; ++j) {
+        if (8 * j < half) {
+          uint32_t a[8], b[8], d[8];
+          tmem_ld_32x32b_x8(ta + 8 * j, a);
+          tmem_ld_32x32b_x8(ta + P.eg + 8 * j, b);
+          tmem_ld_32x32b_x8(ta + 2 * P.eg + 8 * j, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sum[8 * j + e] += (__uint_as_float(d[e]) + __uint_as_float(b[e])) + __uint_as_float(a[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+      if (end == stop) {                          // the unit, or this CTA's share of it, is complete
+        float* dst = P.part + (static_cast<int64_t>(u + c) * P.eg + hf * half) * kRlCols + row;
+#pragma unroll
+        for (int e = 0; e < kRlGroup / 2; ++e) {
+          if (e < half) dst[e * kRlCols] = sum[e];
+          sum[e] = 0.f;
+        }
+      }
+      i = end;
+    }
   }
 }
 
-__global__ void __launch_bounds__(kRlThreads) router_linear_dw_kernel(const uint32_t* __restrict__ x,
-                                                                     const float* __restrict__ g, int T, int H, int E,
-                                                                     float* __restrict__ part) {
-  __shared__ float s_g[kRlChunk][kRlGroup];
-  const int hp = blockIdx.x * kRlThreads + threadIdx.x;
-  const int e0 = blockIdx.z * kRlGroup;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kRlChunk;
-  const int nt = static_cast<int>(T - t0 < kRlChunk ? T - t0 : kRlChunk);
-  for (int i = threadIdx.x; i < nt * kRlGroup; i += kRlThreads) {
-    const int e = e0 + i % kRlGroup;
-    s_g[i / kRlGroup][i % kRlGroup] = e < E ? g[(t0 + i / kRlGroup) * E + e] : 0.f;
+// dx CTA c of n_dx.
+__device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap* tmW, const CUtensorMap* tmIn,
+                      const CUtensorMap* tmOut, uint8_t* sm, const RlBars& B, uint32_t tmem, int warp, int lane,
+                      int c) {
+  const int hts = P.H / kRlCols;
+  const int64_t all = static_cast<int64_t>(P.tb) * hts;
+  const int64_t lo = rl_cut(all, c, P.n_dx), hi = rl_cut(all, c + 1, P.n_dx);
+  uint8_t* io = sm + kRlOpStages * kRlOpStage;
+  const int a_boxes = (2 * P.eg + 63) / 64;       // high and mid of the group
+  auto fail = [&]() {
+    report(P.status, MXG_ERR_TIMEOUT);
+    *B.abort_flag = 1;
+  };
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, ib = 0, ib_phase = 0;
+      bool aborted = false;
+      for (int64_t i = lo; i < hi && !aborted; ++i) {
+        const int t0 = static_cast<int>(i / hts) * kRlTok, h0 = static_cast<int>(i % hts) * kRlCols;
+        if (P.has_in) {
+          if (!mbar_wait_bounded(&B.io_empty[ib], ib_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&B.io_full[ib], kRlIo);
+          for (int h = 0; h < 2; ++h) tma_load_2d(io + ib * kRlIo + h * kRlBox, tmIn, h0 + 64 * h, t0, &B.io_full[ib]);
+          if (++ib == kRlIos) {
+            ib = 0;
+            ib_phase ^= 1;
+          }
+        }
+        for (int g = 0; g < P.groups; ++g) {
+          if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
+          uint8_t* s = sm + stage * kRlOpStage;
+          const int w_box = P.eg * 128;
+          mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(a_boxes * kRlBox + 2 * w_box));
+          for (int h = 0; h < a_boxes; ++h) tma_load_2d(s + h * kRlBox, tmG, g * 3 * P.eg + 64 * h, t0, &B.full[stage]);
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(s + 2 * kRlBox + h * w_box, tmW, h0 + 64 * h, g * P.eg, &B.full[stage]);
+          if (++stage == kRlOpStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (aborted) {
+        const uint64_t w0 = globaltimer_ns();
+        while (globaltimer_ns() - w0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      const uint32_t id = idesc_bf16(kRlTok, kRlCols) | kIdescBMn;
+      bool aborted = false;
+      for (int64_t i = lo; i < hi && !aborted; ++i) {
+        if (!mbar_wait_bounded(&B.tempty[acc], acc_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        uint32_t on = 0;
+        for (int g = 0; g < P.groups; ++g) {
+          if (!mbar_wait_bounded(&B.full[stage], phase, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t s = smem_u32(sm + stage * kRlOpStage);
+          const uint64_t wd = smem_desc(s + 2 * kRlBox, P.eg * 128, 1024, kLayoutSwizzle128B);
+          for (int part = 1; part >= 0; --part)
+            for (int k = 0; k < P.eg / 16; ++k) {
+              const int col = part * P.eg + 16 * k;
+              const uint64_t ad = smem_desc(s + (col >> 6) * kRlBox, 0, 1024, kLayoutSwizzle128B) + ((col & 63) * 2 >> 4);
+              mma_bf16<1>(tmem + acc * 256, ad, wd + k * (2048 >> 4), id, on);
+              on = 1;
+            }
+          mma_commit<1>(&B.empty[stage]);
+          if (++stage == kRlOpStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (aborted) break;
+        mma_commit<1>(&B.tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      mma_commit<1>(B.drained);
+      mbar_wait_bounded(B.drained, 0, B.never_set, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {
+    // rows 32 q .., columns 64 hf ..: 32 rows of 128 bytes of an io buffer belong to this warp
+    const int q = warp & 3, hf = (warp - 4) >> 2;
+    uint32_t acc = 0, acc_phase = 0, ib = 0, ib_phase = 0;
+    for (int64_t i = lo; i < hi; ++i) {
+      const int t0 = static_cast<int>(i / hts) * kRlTok, h0 = static_cast<int>(i % hts) * kRlCols;
+      uint8_t* buf = io + ib * kRlIo + hf * kRlBox + q * 4096 + lane * 128;
+      bool got = true;
+      if (P.has_in) {
+        got = mbar_wait_bounded(&B.io_full[ib], ib_phase, B.abort_flag, kWaitLimitNs);
+      } else {
+        if (lane == 0) bulk_wait_group_read<kRlIos - 1>();    // this buffer's last store has been read out
+        __syncwarp();
+      }
+      got = mbar_wait_bounded(&B.tfull[acc], acc_phase, B.abort_flag, kWaitLimitNs) && got;
+      got = __all_sync(0xffffffffu, got);
+      if (!got) {
+        if (lane == 0) fail();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256 + hf * 64;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(ta + 32 * half, r);
+        tmem_ld_wait();
+        if (half == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.tempty[acc]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {             // 16-byte piece 4 half + j of the row, 128-byte swizzle
+          uint4* p = reinterpret_cast<uint4*>(buf + (((4 * half + j) ^ (lane & 7)) << 4));
+          uint32_t v[4] = {0u, 0u, 0u, 0u};
+          if (P.has_in) {
+            const uint4 d = *p;
+            v[0] = d.x;
+            v[1] = d.y;
+            v[2] = d.z;
+            v[3] = d.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(v[e] << 16) + __uint_as_float(r[8 * j + 2 * e]),
+                               __uint_as_float(v[e] & 0xffff0000u) + __uint_as_float(r[8 * j + 2 * e + 1]));
+          *p = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (t0 + q * 32 < P.T)
+          tma_store_2d(tmOut, io + ib * kRlIo + hf * kRlBox + q * 4096, h0 + 64 * hf, t0 + q * 32);
+        bulk_commit_group();
+        if (P.has_in) {
+          bulk_wait_group_read<0>();
+          mbar_arrive(&B.io_empty[ib]);
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+      if (++ib == kRlIos) {
+        ib = 0;
+        ib_phase ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();          // the stores have completed before the CTA exits
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(kRlThreads, 1)
+    router_linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
+                         const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmIn,
+                         const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ RlArgs P) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kRlRing);
+  RlBars B;
+  B.full = bars;
+  B.empty = B.full + kRlMaxStages;
+  B.tfull = B.empty + kRlMaxStages;
+  B.tempty = B.tfull + 2;
+  B.io_full = B.tempty + 2;
+  B.io_empty = B.io_full + kRlIos;
+  B.drained = B.io_empty + kRlIos;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(B.drained + 1);
+  B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  B.never_set = B.abort_flag + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRlMaxStages; ++s) {
+      mbar_init(&B.full[s], 1);
+      mbar_init(&B.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&B.tfull[a], 1);
+      mbar_init(&B.tempty[a], 8);
+    }
+    for (int i = 0; i < kRlIos; ++i) {
+      mbar_init(&B.io_full[i], 1);
+      mbar_init(&B.io_empty[i], 8);
+    }
+    mbar_init(B.drained, 1);
+    *B.abort_flag = 0;
+    *B.never_set = 0;
+    fence_barrier_init();
   }
   __syncthreads();
-  if (hp >= H / 2) return;
-  float2 acc[kRlGroup];
-#pragma unroll
-  for (int i = 0; i < kRlGroup; ++i) acc[i] = make_float2(0.f, 0.f);
-  for (int t = 0; t < nt; ++t) {
-    const uint32_t xv = x[(t0 + t) * (H / 2) + hp];
-#pragma unroll
-    for (int i = 0; i < kRlGroup; ++i) {
-      acc[i].x = fmaf(s_g[t][i], lo16(xv), acc[i].x);
-      acc[i].y = fmaf(s_g[t][i], hi16(xv), acc[i].y);
-    }
+  if (warp == 1) {
+    tmem_alloc<1>(tmem_slot, 512);
+    tmem_relinquish<1>();
   }
-#pragma unroll
-  for (int i = 0; i < kRlGroup; ++i)
-    if (e0 + i < E)
-      *reinterpret_cast<float2*>(part + (static_cast<int64_t>(blockIdx.y) * E + e0 + i) * H + 2 * hp) = acc[i];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int c = blockIdx.x;
+  if (c < P.n_dw) rl_dw(P, &tmX, &tmG, sm, B, tmem, warp, lane, c);
+  else rl_dx(P, &tmG, &tmW, &tmIn, &tmOut, sm, B, tmem, warp, lane, c - P.n_dw);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<1>(tmem, 512);
 }
 
-__global__ void __launch_bounds__(256) router_linear_sum_kernel(const float* __restrict__ part, int chunks,
-                                                               int64_t n, float* __restrict__ dw) {
+// G in three bf16 parts: parts[t][group][part][eg], zero past E.  Each part
+// takes the next eight significant bits (cut, so that the parts add up to g
+// exactly and none overflows); an infinity or NaN stays in the first.
+__global__ void __launch_bounds__(256) router_split_kernel(const float* __restrict__ g, int T, int E, int eg,
+                                                          int groups, uint16_t* __restrict__ parts) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n) return;
+  const int per = groups * eg;
+  if (i >= static_cast<int64_t>(T) * per) return;
+  const int64_t t = i / per;
+  const int e = static_cast<int>(i - t * per);
+  const uint32_t v = e < E ? __float_as_uint(g[t * E + e]) : 0u;
+  const uint32_t a = v & 0xffff0000u;
+  uint32_t b = 0u, d = 0u;
+  if ((v & 0x7f800000u) != 0x7f800000u) {
+    const float r = __uint_as_float(v) - __uint_as_float(a);
+    b = __float_as_uint(r) & 0xffff0000u;
+    d = __float_as_uint(r - __uint_as_float(b)) & 0xffff0000u;
+  }
+  uint16_t* p = parts + t * 3 * per + (e / eg) * 3 * eg + e % eg;
+  p[0] = static_cast<uint16_t>(a >> 16);
+  p[eg] = static_cast<uint16_t>(b >> 16);
+  p[2 * eg] = static_cast<uint16_t>(d >> 16);
+}
+
+// dw[e][h]: the partials of its unit in the order of the CTAs that left them.
+__global__ void __launch_bounds__(256) router_linear_sum_kernel(const float* __restrict__ part, int H, int E, int eg,
+                                                               int groups, int tb, int units, int n_dw,
+                                                               float* __restrict__ dw) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= static_cast<int64_t>(E) * H) return;
+  const int e = static_cast<int>(i / H), h = static_cast<int>(i - static_cast<int64_t>(e) * H);
+  const int u = (h / kRlCols) * groups + e / eg;
+  const int64_t all = static_cast<int64_t>(units) * tb, lo = static_cast<int64_t>(u) * tb, hi = lo + tb;
+  int c = static_cast<int>(lo * n_dw / all);      // the CTA whose piece holds the unit's first block, or one before
+  while (rl_cut(all, c + 1, n_dw) <= lo) ++c;
   float s = 0.f;
-  for (int c = 0; c < chunks; ++c) s += part[c * n + i];
+  for (; c < n_dw && rl_cut(all, c, n_dw) < hi; ++c)
+    s += part[(static_cast<int64_t>(u + c) * eg + e % eg) * kRlCols + h % kRlCols];
   dw[i] = s;
 }
 
-int rl_chunks(int T) { return (T + kRlChunk - 1) / kRlChunk; }
+int device_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
+constexpr int kRlMostDw = 1024;                   // partials are sized for this many dW CTAs at most
+
+struct RlPlan {
+  int eg, groups, tb, units;
+  int64_t parts, part, bytes;
+};
+
+RlPlan rl_plan(int T, int H, int E) {
+  RlPlan p{};
+  p.groups = (E + kRlGroup - 1) / kRlGroup;
+  p.eg = p.groups > 1 ? kRlGroup : (E + 15) / 16 * 16;
+  p.tb = (T + kRlTok - 1) / kRlTok;
+  p.units = H / kRlCols * p.groups;
+  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb;
+  api::Carver w;
+  p.parts = w.take(2ll * T * p.groups * p.eg * 3);
+  p.part = w.take(4ll * (p.units + (blocks < kRlMostDw ? blocks : kRlMostDw)) * p.eg * kRlCols);
+  p.bytes = w.off;
+  return p;
+}
 
 }  // namespace
 }  // namespace mxg
@@ -93,8 +511,8 @@ int rl_chunks(int T) { return (T + kRlChunk - 1) / kRlChunk; }
 using namespace mxg;
 
 extern "C" size_t mxg_router_linear_bwd_workspace_bytes(int T, int H, int E) {
-  if (T <= 0 || H <= 0 || E <= 0) return 0;
-  return static_cast<size_t>(4ll * rl_chunks(T) * E * H);
+  if (T <= 0 || H <= 0 || E <= 0 || H % kRlCols != 0 || E > 256) return 0;
+  return static_cast<size_t>(rl_plan(T, H, E).bytes);
 }
 
 extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router, const float* dlogits,
@@ -102,24 +520,54 @@ extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router
                                      void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   if (!x || !w_router || !dlogits || !dx || !dw_router || !workspace || !dev_status) return MXG_ERR_ARG;
   if (T <= 0 || H <= 0 || E <= 0) return MXG_ERR_ARG;
-  if (H % 128 != 0 || E > 256) return MXG_ERR_SHAPE;
+  if (H % kRlCols != 0 || E > 256) return MXG_ERR_SHAPE;
   if (!api::aligned32(x) || !api::aligned32(w_router) || !api::aligned32(dlogits) || !api::aligned32(dx_in) ||
       !api::aligned32(dx) || !api::aligned32(dw_router) || !api::aligned32(workspace))
     return MXG_ERR_ALIGN;
   if (workspace_bytes < mxg_router_linear_bwd_workspace_bytes(T, H, E)) return MXG_ERR_WORKSPACE;
   api::NvtxRange nvtx("mxg.router_linear_bwd");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned cols = static_cast<unsigned>((H / 2 + kRlThreads - 1) / kRlThreads);
-  router_linear_dx_kernel<<<dim3(cols, static_cast<unsigned>(T < 4096 ? T : 4096)), kRlThreads, 0, s>>>(
-      reinterpret_cast<const uint32_t*>(w_router), dlogits, reinterpret_cast<const uint32_t*>(dx_in), T, H, E,
-      reinterpret_cast<uint32_t*>(dx));
+  const RlPlan p = rl_plan(T, H, E);
+  uint16_t* parts = api::at<uint16_t>(workspace, p.parts);
+  RlArgs a{};
+  a.T = T;
+  a.H = H;
+  a.E = E;
+  a.eg = p.eg;
+  a.groups = p.groups;
+  a.tb = p.tb;
+  a.units = p.units;
+  a.g_boxes = (3 * p.eg + 63) / 64;
+  a.stage_bytes = (2 + a.g_boxes) * kRlBox;
+  a.stages = kRlRing / a.stage_bytes < kRlMaxStages ? kRlRing / a.stage_bytes : kRlMaxStages;
+  a.has_in = dx_in != nullptr;
+  a.part = api::at<float>(workspace, p.part);
+  a.status = dev_status;
+  // CTAs by the bytes each product moves: x once per expert group, dx_in and dx
+  const int sms = device_sms();
+  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tb) * (H / kRlCols);
+  int64_t n_dw = (sms * static_cast<int64_t>(p.groups) + (p.groups + (dx_in ? 2 : 1)) / 2) / (p.groups + (dx_in ? 2 : 1));
+  if (n_dw < 1) n_dw = 1;
+  if (n_dw > kRlMostDw) n_dw = kRlMostDw;
+  a.n_dw = static_cast<int>(n_dw < blocks ? n_dw : blocks);
+  const int64_t n_dx = sms > n_dw ? sms - n_dw : 1;
+  a.n_dx = static_cast<int>(n_dx < tiles ? n_dx : tiles);
+
+  const int64_t pn = static_cast<int64_t>(T) * p.groups * p.eg;
+  if ((pn + 255) / 256 > INT32_MAX) return MXG_ERR_SHAPE;
+  CUtensorMap mx, mg, mw, mi, mo;
+  if (!tma_map_bf16(&mx, x, H, T, kRlTok) || !tma_map_bf16(&mg, parts, 3ll * p.groups * p.eg, T, kRlTok) ||
+      !tma_map_bf16(&mw, w_router, H, E, static_cast<uint32_t>(p.eg)) ||
+      !tma_map_bf16(&mi, dx_in ? dx_in : dx, H, T, kRlTok) || !tma_map_bf16(&mo, dx, H, T, 32))
+    return MXG_ERR_CUDA;
+  router_split_kernel<<<static_cast<unsigned>((pn + 255) / 256), 256, 0, s>>>(dlogits, T, E, p.eg, p.groups, parts);
   count_launch();
-  float* part = static_cast<float*>(workspace);
-  router_linear_dw_kernel<<<dim3(cols, static_cast<unsigned>(rl_chunks(T)), static_cast<unsigned>((E + kRlGroup - 1) / kRlGroup)),
-                            kRlThreads, 0, s>>>(reinterpret_cast<const uint32_t*>(x), dlogits, T, H, E, part);
+  MXG_TRY(cudaFuncSetAttribute(router_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRlSmem));
+  router_linear_kernel<<<static_cast<unsigned>(a.n_dw + a.n_dx), kRlThreads, kRlSmem, s>>>(mx, mg, mw, mi, mo, a);
   count_launch();
   const int64_t n = static_cast<int64_t>(E) * H;
-  router_linear_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(part, rl_chunks(T), n, dw_router);
+  router_linear_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a.part, H, E, p.eg, p.groups, p.tb,
+                                                                                 p.units, a.n_dw, dw_router);
   count_launch();
   return api::cuda_status(cudaGetLastError());
 }
