@@ -209,7 +209,8 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor") -> int | None
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle itself: building a Stream object costs more than a kernel launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -275,8 +276,18 @@ def mxg_router_bwd(x, w_router, ids, probs, dprobs, dx, dev_status, dw_router=No
     return dw_router
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`: from that stream's own pool, so that neither what used the memory before
+    nor what uses it next overlaps the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _shape(t: torch.Tensor | None, shape: tuple, name: str):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
@@ -300,16 +311,16 @@ def mxg_balance_loss_fwd(logits, ids, coef: float, dev_status, token_mask=None, 
     k = ids.shape[-1]
     dev = logits.device
     _shape(ids, (T, k), "ids")
-    loss = torch.empty(1, dtype=torch.float32, device=dev) if loss is None else loss
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    prob_sums = torch.empty(E, dtype=torch.float32, device=dev) if prob_sums is None else prob_sums
-    n_tokens = torch.empty(1, dtype=torch.int32, device=dev) if n_tokens is None else n_tokens
+    loss = _empty(1, torch.float32, dev, stream) if loss is None else loss
+    counts = _empty(E, torch.int32, dev, stream) if counts is None else counts
+    prob_sums = _empty(E, torch.float32, dev, stream) if prob_sums is None else prob_sums
+    n_tokens = _empty(1, torch.int32, dev, stream) if n_tokens is None else n_tokens
     _shape(loss, (1,), "loss")
     _shape(counts, (E,), "counts")
     _shape(prob_sums, (E,), "prob_sums")
     _shape(n_tokens, (1,), "n_tokens")
     if workspace is None:
-        workspace = torch.empty(max(mxg_balance_loss_workspace_bytes(T, E), 32), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(mxg_balance_loss_workspace_bytes(T, E), 32), torch.uint8, dev, stream)
     _check("mxg_balance_loss_fwd", lib().mxg_balance_loss_fwd(
         _ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _mask_ptr(token_mask, T), T, E, k, coef,
         _ptr(loss, torch.float32, "loss"), _ptr(counts, torch.int32, "counts"),
@@ -322,7 +333,7 @@ def mxg_balance_loss_bwd(logits, counts, n_tokens, k: int, coef: float, dev_stat
                          route=None, dlogits=None, stream=None):
     """Gradient of the balance loss on the logits, fp32 [T, E]; route = (ids, probs, dprobs) adds the route's own."""
     T, E = logits.shape
-    dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device) if dlogits is None else dlogits
+    dlogits = _empty((T, E), torch.float32, logits.device, stream) if dlogits is None else dlogits
     ids, probs, dprobs = (None, None, None) if route is None else route
     _shape(dlogits, (T, E), "dlogits")
     _shape(counts, (E,), "counts")
@@ -350,15 +361,15 @@ def mxg_router_linear_bwd(x, w_router, dlogits, dx_in, dev_status, dx=None, dw_r
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
-    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if dx is None else dx
-    dw_router = torch.empty((E, H), dtype=torch.float32, device=dev) if dw_router is None else dw_router
+    dx = _empty((T, H), torch.bfloat16, dev, stream) if dx is None else dx
+    dw_router = _empty((E, H), torch.float32, dev, stream) if dw_router is None else dw_router
     _shape(w_router, (E, H), "w_router")
     _shape(dlogits, (T, E), "dlogits")
     _shape(dx_in, (T, H), "dx_in")
     _shape(dx, (T, H), "dx")
     _shape(dw_router, (E, H), "dw_router")
     if workspace is None:
-        workspace = torch.empty(max(mxg_router_linear_bwd_workspace_bytes(T, H, E), 32), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(mxg_router_linear_bwd_workspace_bytes(T, H, E), 32), torch.uint8, dev, stream)
     _check("mxg_router_linear_bwd", lib().mxg_router_linear_bwd(
         _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.bfloat16, "w_router"),
         _ptr(dlogits, torch.float32, "dlogits"), _ptr(dx_in, torch.bfloat16, "dx_in"), T, H, E,
@@ -394,12 +405,12 @@ def mxg_muon_update(grad, dev_status, momentum=None, momentum_out=None, mu: floa
     momentum_out = momentum if momentum_out is None else momentum_out
     weights_out = weights if weights_out is None else weights_out
     if update is None and weights is None:
-        update = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        update = _empty(shape, torch.bfloat16, dev, stream)
     for name, t in (("momentum", momentum), ("momentum_out", momentum_out), ("update", update), ("weights", weights),
                     ("weights_out", weights_out)):
         _shape(t, shape, name)
     if workspace is None:
-        workspace = torch.empty(max(mxg_muon_workspace_bytes(batch, rows, cols), 32), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(mxg_muon_workspace_bytes(batch, rows, cols), 32), torch.uint8, dev, stream)
     a, b, c = coefficients
     args = MuonArgs(batch=batch, rows=rows, cols=cols, grad_f32=int(grad.dtype == torch.float32),
                     grad=_ptr(grad, None, "grad"), momentum_in=_ptr(momentum, torch.float32, "momentum"),

@@ -14,21 +14,41 @@
 //
 // A token's logits are read by a group of LPT lanes, eight experts per lane
 // (LPT = the power of two that covers E), so one warp handles 32 / LPT tokens
-// at a time and every lane keeps its experts' sums in registers.
+// at a time and every lane keeps its experts' sums in registers.  Where E is a
+// multiple of four (VEC) a lane's experts are two 16-byte pieces of the row.
+// Both passes are bound by the logits stream, and below a megabyte or so by
+// the latency of the launch and of one trip to memory.
 #include <climits>
 #include <cmath>
 
 #include "api_common.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace mxg {
 namespace {
 
-constexpr int kBlThreads = 256;
-constexpr int kBlWarps = kBlThreads / 32;
 constexpr int kBlVals = 8;               // experts per lane
+constexpr int kBlFwdThreads = 1024;
+constexpr int kBlFwdWarps = kBlFwdThreads / 32;
 constexpr int kBlMaxBlocks = 152;        // partial sums of the forward: one block per SM
+constexpr int kBlBwdThreads = 256;
+constexpr int kBlBwdWarps = kBlBwdThreads / 32;
+
+// Expert of value i of lane gl of a group, and the inverse.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int expert_of(int gl, int i) {
+  return VEC ? 4 * (gl + LPT * (i >> 2)) + (i & 3) : gl + LPT * i;
+}
+template <int LPT, bool VEC>
+__device__ __forceinline__ int lane_of(int e) {
+  return (VEC ? e >> 2 : e) % LPT;
+}
+template <int LPT, bool VEC>
+__device__ __forceinline__ int value_of(int e) {
+  return VEC ? ((e >> 2) / LPT) * 4 + (e & 3) : e / LPT;
+}
 
 // The group's softmax of one token: z[i] = logit of expert lane_in_group + LPT i
 // (-inf past E) becomes the probability.  A row without a finite logit gives
@@ -54,112 +74,184 @@ __device__ __forceinline__ void group_softmax(float (&z)[kBlVals]) {
   for (int i = 0; i < kBlVals; ++i) z[i] *= inv;
 }
 
-template <int LPT>
+template <int LPT, bool VEC>
 __device__ __forceinline__ void load_logits(const float* __restrict__ row, int E, int gl, bool live,
                                             float (&z)[kBlVals]) {
+  if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < kBlVals; ++i) {
-    const int e = gl + LPT * i;
-    z[i] = live && e < E ? row[e] : -INFINITY;
+    for (int i = 0; i < kBlVals; i += 4) {
+      const int e = expert_of<LPT, VEC>(gl, i);
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (live && e < E) v = *reinterpret_cast<const float4*>(row + e);
+      z[i] = v.x;
+      z[i + 1] = v.y;
+      z[i + 2] = v.z;
+      z[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBlVals; ++i) {
+      const int e = expert_of<LPT, VEC>(gl, i);
+      z[i] = live && e < E ? row[e] : -INFINITY;
+    }
+  }
+}
+
+// The counts and the loss from s_sum / s_cnt / n (whole block, at least 256
+// threads; the sums and counts of all experts are in shared memory).
+__device__ __forceinline__ void balance_finish(const float* s_sum, const int* s_cnt, int n, float* s_term, int E,
+                                               int k, float coef, float* loss, int32_t* counts, float* prob_sums,
+                                               int32_t* n_tokens) {
+  const int e = threadIdx.x;
+  if (e < 256) {
+    const float nf = static_cast<float>(n);
+    float term = 0.f;
+    if (e < E) {
+      prob_sums[e] = s_sum[e];
+      counts[e] = s_cnt[e];
+      if (n > 0) term = (static_cast<float>(s_cnt[e]) / (static_cast<float>(k) * nf)) * (s_sum[e] / nf);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+    if ((e & 31) == 0) s_term[e >> 5] = term;
+  }
+  __syncthreads();
+  if (e == 0) {
+    float t = 0.f;
+    for (int i = 0; i < 8; ++i) t += s_term[i];
+    *loss = coef * static_cast<float>(E) * t;
+    *n_tokens = n;
   }
 }
 
 // Sums of the probabilities and counts of the chosen ids over the block's
-// tokens, one partial per block and expert.
-template <int LPT>
-__global__ void __launch_bounds__(kBlThreads) balance_partial_kernel(
+// tokens: one partial per block and expert, or, when one block covers all
+// tokens, the results.
+template <int LPT, bool VEC>
+__global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
-    int k, float* __restrict__ part, int32_t* __restrict__ part_counts, int32_t* __restrict__ part_tokens,
-    int32_t* status) {
-  __shared__ float s_sum[kBlWarps][256];
+    int k, float coef, float* __restrict__ part, int32_t* __restrict__ part_counts, int32_t* __restrict__ part_tokens,
+    float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob_sums,
+    int32_t* __restrict__ n_tokens, int32_t* status) {
+  __shared__ float s_sum[kBlFwdWarps][256];
+  __shared__ float s_term[8];
   __shared__ int s_cnt[256];
   __shared__ int s_tok;
   constexpr int TPW = 32 / LPT;          // tokens a warp takes at once
+  launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
-  for (int e = threadIdx.x; e < E; e += kBlThreads) s_cnt[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kBlFwdThreads) s_cnt[e] = 0;
   if (threadIdx.x == 0) s_tok = 0;
   __syncthreads();
   float acc[kBlVals];
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) acc[i] = 0.f;
   int tokens = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlWarps * TPW;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlWarps + warp) * TPW; t0 < T; t0 += step) {
-    const int64_t t = t0 + grp;
-    const bool live = t < T && (mask == nullptr || mask[t] != 0);
-    float z[kBlVals];
-    load_logits<LPT>(logits + t * E, E, gl, live, z);
-    group_softmax<LPT>(z);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlFwdWarps * TPW;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlFwdWarps + warp) * TPW; t0 < T; t0 += 2 * step) {
+    // two tokens per group in flight
+    float z[2][kBlVals];
+    bool live[2];
 #pragma unroll
-    for (int i = 0; i < kBlVals; ++i) acc[i] += z[i];
-    if (live) {
-      tokens += gl == 0;
-      for (int j = gl; j < k; j += LPT) {
-        const int e = ids[t * k + j];
-        if (e < 0 || e >= E) report(status, MXG_ERR_EXPERT_ID);
-        else atomicAdd(&s_cnt[e], 1);
+    for (int u = 0; u < 2; ++u) {
+      const int64_t t = t0 + u * step + grp;
+      live[u] = t < T && (mask == nullptr || mask[t] != 0);
+      load_logits<LPT, VEC>(logits + t * E, E, gl, live[u], z[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t t = t0 + u * step + grp;
+      if (live[u]) {
+        tokens += gl == 0;
+        for (int j = gl; j < k; j += LPT) {
+          const int e = ids[t * k + j];
+          if (e < 0 || e >= E) report(status, MXG_ERR_EXPERT_ID);
+          else atomicAdd(&s_cnt[e], 1);
+        }
       }
+      __syncwarp();
+      group_softmax<LPT>(z[u]);
+#pragma unroll
+      for (int i = 0; i < kBlVals; ++i) acc[i] += z[u][i];
     }
   }
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) {
 #pragma unroll
     for (int off = 16; off >= LPT; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-    if (grp == 0 && gl + LPT * i < E) s_sum[warp][gl + LPT * i] = acc[i];
+    const int e = expert_of<LPT, VEC>(gl, i);
+    if (grp == 0 && e < E) s_sum[warp][e] = acc[i];
   }
   if (tokens != 0) atomicAdd(&s_tok, tokens);
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kBlThreads) {
+  if (threadIdx.x < E) {
+    const int e = threadIdx.x;
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kBlWarps; ++w) s += s_sum[w][e];
-    part[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-    part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+    for (int w = 0; w < kBlFwdWarps; ++w) s += s_sum[w][e];
+    if (gridDim.x > 1) {
+      part[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+      part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+    } else {
+      s_sum[0][e] = s;                   // read and written by this thread only
+    }
   }
-  if (threadIdx.x == 0) part_tokens[blockIdx.x] = s_tok;
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) part_tokens[blockIdx.x] = s_tok;
+    return;
+  }
+  __syncthreads();
+  balance_finish(s_sum[0], s_cnt, s_tok, s_term, E, k, coef, loss, counts, prob_sums, n_tokens);
 }
 
-// The partials in block order, the counts and the loss.
-__global__ void __launch_bounds__(256) balance_finish_kernel(const float* __restrict__ part,
-                                                            const int32_t* __restrict__ part_counts,
-                                                            const int32_t* __restrict__ part_tokens, int nblk, int E,
-                                                            int k, float coef, float* __restrict__ loss,
-                                                            int32_t* __restrict__ counts,
-                                                            float* __restrict__ prob_sums,
-                                                            int32_t* __restrict__ n_tokens) {
-  __shared__ float s_term[256];
+// The partials: 1024 / W threads share an expert (W: E rounded up to a power of
+// two, at least 32), each adding every (1024 / W)-th block in order, then their
+// sums in order.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const float* __restrict__ part,
+                                                             const int32_t* __restrict__ part_counts,
+                                                             const int32_t* __restrict__ part_tokens, int nblk, int E,
+                                                             int W, int k, float coef, float* __restrict__ loss,
+                                                             int32_t* __restrict__ counts,
+                                                             float* __restrict__ prob_sums,
+                                                             int32_t* __restrict__ n_tokens) {
+  __shared__ float s_sum[1024];
+  __shared__ int s_cnt[1024];
+  __shared__ float s_term[8];
   __shared__ int s_n;
-  const int e = threadIdx.x;
-  if (e == 0) {
-    int n = 0;
-    for (int b = 0; b < nblk; ++b) n += part_tokens[b];
-    s_n = n;
-    *n_tokens = n;
-  }
-  float sum = 0.f;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  dependency_wait();
+  const int e = threadIdx.x % W, r = threadIdx.x / W, R = 1024 / W;
+  float s = 0.f;
   int c = 0;
   if (e < E) {
-    for (int b = 0; b < nblk; ++b) {
-      sum += part[static_cast<int64_t>(b) * E + e];
+#pragma unroll 8
+    for (int b = r; b < nblk; b += R) {
+      s += part[static_cast<int64_t>(b) * E + e];
       c += part_counts[static_cast<int64_t>(b) * E + e];
     }
-    prob_sums[e] = sum;
-    counts[e] = c;
+  }
+  s_sum[threadIdx.x] = s;
+  s_cnt[threadIdx.x] = c;
+  int n = threadIdx.x < nblk ? part_tokens[threadIdx.x] : 0;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((threadIdx.x & 31) == 0 && n != 0) atomicAdd(&s_n, n);
+  __syncthreads();
+  if (r == 0) {
+    for (int i = 1; i < R; ++i) {
+      s += s_sum[i * W + e];
+      c += s_cnt[i * W + e];
+    }
+    s_sum[e] = s;                        // this thread's own slots
+    s_cnt[e] = c;
   }
   __syncthreads();
-  const float n = static_cast<float>(s_n);
-  s_term[e] = e < E && s_n > 0 ? (static_cast<float>(c) / (static_cast<float>(k) * n)) * (sum / n) : 0.f;
-  __syncthreads();
-  for (int off = 128; off > 0; off >>= 1) {
-    if (e < off) s_term[e] += s_term[e + off];
-    __syncthreads();
-  }
-  if (e == 0) *loss = coef * static_cast<float>(E) * s_term[0];
+  balance_finish(s_sum, s_cnt, s_n, s_term, E, k, coef, loss, counts, prob_sums, n_tokens);
 }
 
-template <int LPT>
-__global__ void __launch_bounds__(kBlThreads) balance_bwd_kernel(
+template <int LPT, bool VEC>
+__global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
     const float* __restrict__ logits, const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
     const int32_t* __restrict__ n_tokens, int T, int E, int k, float coef, const float* __restrict__ dloss,
     const int32_t* __restrict__ ids, const float* __restrict__ probs, const float* __restrict__ dprobs,
@@ -167,58 +259,81 @@ __global__ void __launch_bounds__(kBlThreads) balance_bwd_kernel(
   constexpr int TPW = 32 / LPT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlBwdWarps * TPW;
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlBwdWarps + warp) * TPW;
+  // the first logits are on their way while the counts arrive
+  bool in = t0 + grp < T, live = in && (mask == nullptr || mask[t0 + grp] != 0);
+  float z[kBlVals];
+  load_logits<LPT, VEC>(logits + (t0 + grp) * E, E, gl, live, z);
+  int cnt[kBlVals];
+#pragma unroll
+  for (int i = 0; i < kBlVals; ++i) {
+    const int e = expert_of<LPT, VEC>(gl, i);
+    cnt[i] = e < E ? counts[e] : 0;
+  }
   const int n = *n_tokens;
   const float up = n > 0 ? (dloss != nullptr ? *dloss : 1.f) * coef / static_cast<float>(n) : 0.f;
   // deviations of the lane's experts: (E c - k n) / (k n), the numerator exact
+  const int64_t kn = static_cast<int64_t>(k) * n;
+  const float inv = n > 0 ? 1.f / static_cast<float>(kn) : 0.f;
   float dev[kBlVals];
 #pragma unroll
-  for (int i = 0; i < kBlVals; ++i) {
-    const int e = gl + LPT * i;
-    const int64_t kn = static_cast<int64_t>(k) * n;
-    dev[i] = e < E && n > 0 ? static_cast<float>(static_cast<int64_t>(E) * counts[e] - kn) / static_cast<float>(kn)
-                            : 0.f;
-  }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlWarps * TPW;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlWarps + warp) * TPW; t0 < T; t0 += step) {
+  for (int i = 0; i < kBlVals; ++i) dev[i] = static_cast<float>(static_cast<int64_t>(E) * cnt[i] - kn) * inv;
+  while (t0 < T) {
     const int64_t t = t0 + grp;
-    const bool in = t < T;
-    const bool live = in && (mask == nullptr || mask[t] != 0);
-    float z[kBlVals];
-    load_logits<LPT>(logits + t * E, E, gl, live, z);
     group_softmax<LPT>(z);
     float mean = 0.f;
 #pragma unroll
     for (int i = 0; i < kBlVals; ++i) mean = fmaf(z[i], dev[i], mean);
 #pragma unroll
     for (int off = LPT / 2; off > 0; off >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, off);
+    float d[kBlVals];
 #pragma unroll
-    for (int i = 0; i < kBlVals; ++i) z[i] = live ? up * z[i] * (dev[i] - mean) : 0.f;
+    for (int i = 0; i < kBlVals; ++i) d[i] = live ? up * z[i] * (dev[i] - mean) : 0.f;
+    const bool here = in;
+    t0 += step;
+    in = t0 + grp < T;
+    live = in && (mask == nullptr || mask[t0 + grp] != 0);
+    if (t0 < T) load_logits<LPT, VEC>(logits + (t0 + grp) * E, E, gl, live, z);
     if (probs != nullptr) {
       // the route's gradient at the chosen experts: q_j (dq_j - sum_i q_i dq_i)
       float inner = 0.f;
       for (int j = gl; j < k; j += LPT)
-        if (in) inner = fmaf(probs[t * k + j], dprobs[t * k + j], inner);
+        if (here) inner = fmaf(probs[t * k + j], dprobs[t * k + j], inner);
 #pragma unroll
       for (int off = LPT / 2; off > 0; off >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, off);
-      if (in) {
+      if (here) {
         for (int j = 0; j < k; ++j) {
           const int e = ids[t * k + j];
           if (e < 0 || e >= E) {
             if (gl == 0) report(status, MXG_ERR_EXPERT_ID);
-          } else if (e % LPT == gl) {
+          } else if (lane_of<LPT, VEC>(e) == gl) {
             const float q = probs[t * k + j];
-            const float d = q * (dprobs[t * k + j] - inner);
+            const float g = q * (dprobs[t * k + j] - inner);
+            const int v = value_of<LPT, VEC>(e);
 #pragma unroll
             for (int i = 0; i < kBlVals; ++i)
-              if (e / LPT == i) z[i] += d;
+              if (v == i) d[i] += g;
           }
         }
       }
+      __syncwarp();
     }
-    if (in) {
+    if (here) {
+      float* row = dlogits + t * E;
+      if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < kBlVals; ++i)
-        if (gl + LPT * i < E) dlogits[t * E + gl + LPT * i] = z[i];
+        for (int i = 0; i < kBlVals; i += 4) {
+          const int e = expert_of<LPT, VEC>(gl, i);
+          if (e < E) *reinterpret_cast<float4*>(row + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBlVals; ++i) {
+          const int e = expert_of<LPT, VEC>(gl, i);
+          if (e < E) row[e] = d[i];
+        }
+      }
     }
   }
 }
@@ -229,26 +344,33 @@ int lanes_per_token(int E) {
   return l;
 }
 
-// Blocks of a pass over T tokens: enough for one trip each, at most `most`.
-int balance_blocks(int T, int E, int most) {
-  const int64_t per = static_cast<int64_t>(kBlWarps) * (32 / lanes_per_token(E));
+// Blocks of `warps` warps for a pass over T tokens: enough for one trip each, at most `most`.
+int balance_blocks(int T, int E, int warps, int most) {
+  const int64_t per = static_cast<int64_t>(warps) * (32 / lanes_per_token(E));
   const int64_t n = (T + per - 1) / per;
   return static_cast<int>(n < most ? n : most);
 }
 
-template <typename F>
-void with_lanes(int E, F f) {
-  switch (lanes_per_token(E)) {
-    case 1: f(std::integral_constant<int, 1>{}); break;
-    case 2: f(std::integral_constant<int, 2>{}); break;
-    case 4: f(std::integral_constant<int, 4>{}); break;
-    case 8: f(std::integral_constant<int, 8>{}); break;
-    case 16: f(std::integral_constant<int, 16>{}); break;
-    default: f(std::integral_constant<int, 32>{}); break;
+template <bool VEC, typename F>
+void with_lanes(int lanes, F f) {
+  using V = std::integral_constant<bool, VEC>;
+  switch (lanes) {
+    case 1: f(std::integral_constant<int, 1>{}, V{}); break;
+    case 2: f(std::integral_constant<int, 2>{}, V{}); break;
+    case 4: f(std::integral_constant<int, 4>{}, V{}); break;
+    case 8: f(std::integral_constant<int, 8>{}, V{}); break;
+    case 16: f(std::integral_constant<int, 16>{}, V{}); break;
+    default: f(std::integral_constant<int, 32>{}, V{}); break;
   }
 }
+template <typename F>
+void with_layout(int E, F f) {
+  if (E % 4 == 0) with_lanes<true>(lanes_per_token(E), f);
+  else with_lanes<false>(lanes_per_token(E), f);
+}
 
-int64_t part_floats(int T, int E) { return api::align_up(4ll * balance_blocks(T, E, kBlMaxBlocks) * E, api::kAlign); }
+int fwd_blocks(int T, int E) { return balance_blocks(T, E, kBlFwdWarps, kBlMaxBlocks); }
+int64_t part_floats(int T, int E) { return api::align_up(4ll * fwd_blocks(T, E) * E, api::kAlign); }
 
 int balance_shape(int T, int E, int k) {
   if (T <= 0 || E <= 0 || k <= 0) return MXG_ERR_ARG;
@@ -278,19 +400,23 @@ extern "C" int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, con
   if (workspace_bytes < mxg_balance_loss_workspace_bytes(T, E)) return MXG_ERR_WORKSPACE;
   api::NvtxRange nvtx("mxg.balance_loss_fwd");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int nblk = balance_blocks(T, E, kBlMaxBlocks);
+  const int nblk = fwd_blocks(T, E);
   float* part = api::at<float>(workspace, 0);
   int32_t* part_counts = api::at<int32_t>(workspace, part_floats(T, E));
   int32_t* part_tokens = api::at<int32_t>(workspace, 2 * part_floats(T, E));
-  with_lanes(E, [&](auto l) {
-    balance_partial_kernel<l.value><<<nblk, kBlThreads, 0, s>>>(logits, ids, token_mask, T, E, k, part, part_counts,
-                                                                part_tokens, dev_status);
+  with_layout(E, [&](auto l, auto v) {
+    balance_partial_kernel<l.value, v.value><<<nblk, kBlFwdThreads, 0, s>>>(
+        logits, ids, token_mask, T, E, k, coef, part, part_counts, part_tokens, loss, counts, prob_sums, n_tokens,
+        dev_status);
   });
   count_launch();
-  balance_finish_kernel<<<1, 256, 0, s>>>(part, part_counts, part_tokens, nblk, E, k, coef, loss, counts, prob_sums,
-                                          n_tokens);
-  count_launch();
-  return api::cuda_status(cudaGetLastError());
+  MXG_TRY(cudaGetLastError());
+  if (nblk == 1) return MXG_OK;
+  int W = 32;
+  while (W < E) W *= 2;
+  MXG_TRY(launch_after(balance_finish_kernel, dim3(1), dim3(1024), 0, s, part, part_counts, part_tokens, nblk, E, W, k,
+                       coef, loss, counts, prob_sums, n_tokens));
+  return MXG_OK;
 }
 
 extern "C" int mxg_balance_loss_bwd(const float* logits, const uint8_t* token_mask, const int32_t* counts,
@@ -306,8 +432,8 @@ extern "C" int mxg_balance_loss_bwd(const float* logits, const uint8_t* token_ma
     return MXG_ERR_ALIGN;
   api::NvtxRange nvtx("mxg.balance_loss_bwd");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  with_lanes(E, [&](auto l) {
-    balance_bwd_kernel<l.value><<<balance_blocks(T, E, 152 * 8), kBlThreads, 0, s>>>(
+  with_layout(E, [&](auto l, auto v) {
+    balance_bwd_kernel<l.value, v.value><<<balance_blocks(T, E, kBlBwdWarps, 152 * 8), kBlBwdThreads, 0, s>>>(
         logits, token_mask, counts, n_tokens, T, E, k, coef, dloss, ids, probs, dprobs, dlogits, dev_status);
   });
   count_launch();

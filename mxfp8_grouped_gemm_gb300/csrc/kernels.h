@@ -10,6 +10,26 @@ namespace mxg {
 
 void count_launch();
 
+// Launches a kernel whose preamble may overlap the end of the kernel before it
+// in the stream; it calls dependency_wait() before it touches that kernel's
+// outputs (or anything that kernel still reads).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+  count_launch();
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 // ---------------------------------------------------------------- quantiser
 struct QuantParams {
   const uint16_t* x;          // bf16 source
