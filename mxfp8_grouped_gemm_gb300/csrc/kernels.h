@@ -3,12 +3,39 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
 namespace mxg {
 
 void count_launch();
+
+// SMs of the current device (looked up once per device).
+inline int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < 64 && (n = known[dev].load()) > 0) return n;
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (n <= 0) return 1;
+  if (dev < 64) known[dev].store(n);
+  return n;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory (once per kernel and device).
+template <typename K>
+cudaError_t allow_smem(K* kern, int bytes) {
+  static std::atomic<const void*> done[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const void* id = reinterpret_cast<const void*>(kern);
+  if (dev < 64 && done[dev].load() == id) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && dev < 64) done[dev].store(id);
+  return err;
+}
 
 // Launches a kernel whose preamble may overlap the end of the kernel before it
 // in the stream; it calls dependency_wait() before it touches that kernel's

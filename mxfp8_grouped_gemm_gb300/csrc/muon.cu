@@ -796,13 +796,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
 }
 
 // --------------------------------------------------------------------- host
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 // CTAs (or pairs) of a kernel that the device holds at once.
 template <bool PAIR, bool ROWS, bool SPLIT>
 int ns_resident() {
@@ -828,7 +821,7 @@ int ns_resident() {
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
   } else {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kNsThreads, kNsSmem) != cudaSuccess) return 0;
-    n *= sm_count();
+    n *= device_sms();
   }
   if (dev < 64) known[dev].store(n);
   return n;
@@ -1005,7 +998,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   // fills only one of the two SMs, the smaller tiles keep more SMs busy
   const int64_t t256 = static_cast<int64_t>((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
   cudaError_t err;
-  if (t256 >= sm_count() / 2 && p.m > 128) err = by_rows ? launch_ns<true, true, false>(n, s) : launch_ns<true, false, false>(n, s);
+  if (t256 >= device_sms() / 2 && p.m > 128) err = by_rows ? launch_ns<true, true, false>(n, s) : launch_ns<true, false, false>(n, s);
   else if (p.split) err = by_rows ? launch_ns<false, true, true>(n, s) : launch_ns<false, false, true>(n, s);
   else err = by_rows ? launch_ns<false, true, false>(n, s) : launch_ns<false, false, false>(n, s);
   return api::cuda_status(err);

@@ -23,10 +23,12 @@
 //      (MN-major), 128 tokens a stage.  The line of all (unit, token block)
 //      is cut into equal pieces, one per CTA; a CTA leaves one partial per unit
 //      it touches, numbered unit + CTA (unique: along the line one of the two
-//      grows at every seam), and a last kernel adds a unit's partials in order.
-//  dx: 128 tokens x 128 hidden columns a tile, K = 64 experts x 2 parts a
-//      stage (W_r read across); dx_in comes by TMA into the buffer that the
-//      result leaves from.
+//      grows at every seam), and the CTA that brings a unit's count of partials
+//      to its end adds them up in order.  No CTA waits for another.
+//  dx: 128 tokens x 128 hidden columns a tile, K = 64 experts x 2 parts a step
+//      (W_r read across).  Up to 64 experts, G stays while the CTA goes along
+//      the tokens' columns.  dx_in comes by TMA into the buffer that the result
+//      leaves from.
 #include <climits>
 
 #include "api_common.h"
@@ -44,13 +46,14 @@ constexpr int kRlThreads = 384;
 constexpr int kRlBox = kRlTok * 128;              // 128 rows of 128 bytes
 constexpr int kRlFlush = 2;                       // token blocks per accumulator (256 tokens)
 constexpr int kRlRing = 196608;                   // bytes of all rings
-constexpr int kRlOpStage = 3 * kRlBox;            // dx: two boxes of G, 64 experts x 128 columns of W_r
-constexpr int kRlOpStages = 2;
+constexpr int kRlG = 2 * kRlBox;                  // dx: high and mid of a group for 128 tokens
+constexpr int kRlW = kRlGroup * 256;              // dx: 64 experts x 128 columns of W_r
+constexpr int kRlOps = 2;                         // of each
 constexpr int kRlIo = 2 * kRlBox;                 // dx: one tile of dx_in / dx
 constexpr int kRlIos = 3;
 constexpr int kRlMaxStages = 4;
 constexpr int kRlSmem = 1024 + kRlRing + 1024;
-static_assert(kRlOpStages * kRlOpStage + kRlIos * kRlIo <= kRlRing, "dx rings");
+static_assert(kRlOps * (kRlG + kRlW) + kRlIos * kRlIo <= kRlRing, "dx rings");
 static_assert(kRlSmem <= 232448, "shared memory budget");
 
 struct RlArgs {
@@ -63,16 +66,35 @@ struct RlArgs {
   int stages, stage_bytes, g_boxes;               // dW ring
   int has_in;
   float* part;                                    // [units + n_dw][eg][128]
+  int32_t* count;                                 // [units], zero: partials left so far
+  float* dw;                                      // [E][H]
   int32_t* status;
 };
 
 __device__ __forceinline__ int64_t rl_cut(int64_t n, int i, int parts) { return n * i / parts; }
 
+// The CTA of n whose piece of a line of `all` blocks holds block i.
+__device__ __forceinline__ int rl_owner(int64_t all, int64_t i, int n) {
+  int c = static_cast<int>(i * n / all);          // its piece starts at or before i
+  while (rl_cut(all, c + 1, n) <= i) ++c;
+  return c;
+}
+
 struct RlBars {
-  uint64_t *full, *empty, *tfull, *tempty, *io_full, *io_empty, *drained;
+  uint64_t *full, *empty, *tfull, *tempty, *io_full, *io_empty, *g_full, *g_empty, *drained, *join;
   volatile int* abort_flag;
   volatile int* never_set;
+  volatile int* last;                             // this CTA left a unit's last partial
 };
+
+// Joins the eight epilogue warps, bounded like every wait; false: some warp gave up.
+__device__ __forceinline__ bool epilogue_sync(const RlBars& B, uint32_t& phase, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(B.join);
+  const bool ok = mbar_wait_bounded(B.join, phase, B.abort_flag, kWaitLimitNs);
+  phase ^= 1;
+  return __all_sync(0xffffffffu, ok);
+}
 
 // dW CTA c of n_dw.
 __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap* tmG, uint8_t* sm, const RlBars& B,
@@ -164,7 +186,7 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
     float sum[kRlGroup / 2];
 #pragma unroll
     for (int e = 0; e < kRlGroup / 2; ++e) sum[e] = 0.f;
-    uint32_t acc = 0, acc_phase = 0;
+    uint32_t acc = 0, acc_phase = 0, join_phase = 0;
     int64_t i = lo;
     while (i < hi) {
       const int u = static_cast<int>(i / P.tb);
@@ -199,11 +221,43 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
       if (end == stop) {                          // the unit, or this CTA's share of it, is complete
-        float* dst = P.part + (static_cast<int64_t>(u + c) * P.eg + hf * half) * kRlCols + row;
+        const int64_t u0 = unit_end - P.tb;
+        const int c0 = rl_owner(all, u0, P.n_dw), c1 = rl_owner(all, unit_end - 1, P.n_dw);
+        const int ht = u / P.groups, e0 = (u - ht * P.groups) * P.eg;
+        float* part = P.part + (static_cast<int64_t>(u + c) * P.eg + hf * half) * kRlCols + row;
+        float* out = P.dw + static_cast<int64_t>(e0 + hf * half) * P.H + ht * kRlCols + row;
 #pragma unroll
         for (int e = 0; e < kRlGroup / 2; ++e) {
-          if (e < half) dst[e * kRlCols] = sum[e];
+          if (e < half) {
+            if (c0 != c1) part[e * kRlCols] = sum[e];
+            else if (e0 + hf * half + e < P.E) out[static_cast<int64_t>(e) * P.H] = sum[e];
+          }
           sum[e] = 0.f;
+        }
+        if (c0 != c1) {
+          __threadfence();
+          bool ok = epilogue_sync(B, join_phase, lane);
+          if (ok && warp == 4 && lane == 0) *B.last = atomicAdd(P.count + u, 1) == c1 - c0;
+          ok = ok && epilogue_sync(B, join_phase, lane);
+          if (ok && *B.last) {
+            __threadfence();
+            for (int k = c0; k <= c1; ++k) {      // in order; a partial's values are requested together
+              const float* from = P.part + (static_cast<int64_t>(u + k) * P.eg + hf * half) * kRlCols + row;
+#pragma unroll
+              for (int e = 0; e < kRlGroup / 2; ++e)
+                if (e < half) sum[e] += __ldcg(from + e * kRlCols);
+            }
+#pragma unroll
+            for (int e = 0; e < kRlGroup / 2; ++e) {
+              if (e < half && e0 + hf * half + e < P.E) out[static_cast<int64_t>(e) * P.H] = sum[e];
+              sum[e] = 0.f;
+            }
+          }
+          ok = ok && epilogue_sync(B, join_phase, lane);         // the flag may be written again
+          if (!ok) {
+            if (lane == 0) fail();
+            break;
+          }
         }
       }
       i = end;
@@ -218,19 +272,46 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
   const int hts = P.H / kRlCols;
   const int64_t all = static_cast<int64_t>(P.tb) * hts;
   const int64_t lo = rl_cut(all, c, P.n_dx), hi = rl_cut(all, c + 1, P.n_dx);
-  uint8_t* io = sm + kRlOpStages * kRlOpStage;
-  const int a_boxes = (2 * P.eg + 63) / 64;       // high and mid of the group
+  uint8_t* wr = sm + kRlOps * kRlG;
+  uint8_t* io = wr + kRlOps * kRlW;
+  const int g_boxes = (2 * P.eg + 63) / 64;       // high and mid of the group
+  const bool keep = P.groups == 1;                // G serves all tiles of its tokens
   auto fail = [&]() {
     report(P.status, MXG_ERR_TIMEOUT);
     *B.abort_flag = 1;
   };
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, ib = 0, ib_phase = 0;
+      uint32_t stage = 0, phase = 0, gs = 0, g_phase = 0, ib = 0, ib_phase = 0;
       bool aborted = false;
       for (int64_t i = lo; i < hi && !aborted; ++i) {
-        const int t0 = static_cast<int>(i / hts) * kRlTok, h0 = static_cast<int>(i % hts) * kRlCols;
-        if (P.has_in) {
+        const int t0 = static_cast<int>(i / hts) * kRlTok, hi_t = static_cast<int>(i % hts), h0 = hi_t * kRlCols;
+        for (int g = 0; g < P.groups; ++g) {
+          if (!keep || i == lo || hi_t == 0) {
+            if (!mbar_wait_bounded(&B.g_empty[gs], g_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+              fail();
+              aborted = true;
+              break;
+            }
+            mbar_arrive_expect_tx(&B.g_full[gs], static_cast<uint32_t>(g_boxes * kRlBox));
+            for (int h = 0; h < g_boxes; ++h)
+              tma_load_2d(sm + gs * kRlG + h * kRlBox, tmG, g * 3 * P.eg + 64 * h, t0, &B.g_full[gs]);
+            gs ^= 1;
+            if (gs == 0) g_phase ^= 1;
+          }
+          if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
+          const int w_box = P.eg * 128;
+          mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(2 * w_box));
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(wr + stage * kRlW + h * w_box, tmW, h0 + 64 * h, g * P.eg, &B.full[stage]);
+          stage ^= 1;
+          if (stage == 0) phase ^= 1;
+        }
+        if (P.has_in && !aborted) {
           if (!mbar_wait_bounded(&B.io_empty[ib], ib_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
@@ -243,23 +324,6 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
             ib_phase ^= 1;
           }
         }
-        for (int g = 0; g < P.groups; ++g) {
-          if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
-            fail();
-            aborted = true;
-            break;
-          }
-          uint8_t* s = sm + stage * kRlOpStage;
-          const int w_box = P.eg * 128;
-          mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(a_boxes * kRlBox + 2 * w_box));
-          for (int h = 0; h < a_boxes; ++h) tma_load_2d(s + h * kRlBox, tmG, g * 3 * P.eg + 64 * h, t0, &B.full[stage]);
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(s + 2 * kRlBox + h * w_box, tmW, h0 + 64 * h, g * P.eg, &B.full[stage]);
-          if (++stage == kRlOpStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
       }
       if (aborted) {
         const uint64_t w0 = globaltimer_ns();
@@ -268,25 +332,31 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      uint32_t stage = 0, phase = 0, gs = 0, g_phase = 0, acc = 0, acc_phase = 0;
       const uint32_t id = idesc_bf16(kRlTok, kRlCols) | kIdescBMn;
       bool aborted = false;
       for (int64_t i = lo; i < hi && !aborted; ++i) {
+        const int hi_t = static_cast<int>(i % hts);
         if (!mbar_wait_bounded(&B.tempty[acc], acc_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
           fail();
           break;
         }
-        tc_fence_after();
         uint32_t on = 0;
         for (int g = 0; g < P.groups; ++g) {
+          if ((!keep || i == lo || hi_t == 0) &&
+              !mbar_wait_bounded(&B.g_full[gs], g_phase, B.abort_flag, kWaitLimitNs)) {
+            fail();
+            aborted = true;
+            break;
+          }
           if (!mbar_wait_bounded(&B.full[stage], phase, B.abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t s = smem_u32(sm + stage * kRlOpStage);
-          const uint64_t wd = smem_desc(s + 2 * kRlBox, P.eg * 128, 1024, kLayoutSwizzle128B);
+          const uint32_t s = smem_u32(sm + gs * kRlG);
+          const uint64_t wd = smem_desc(smem_u32(wr + stage * kRlW), P.eg * 128, 1024, kLayoutSwizzle128B);
           for (int part = 1; part >= 0; --part)
             for (int k = 0; k < P.eg / 16; ++k) {
               const int col = part * P.eg + 16 * k;
@@ -295,9 +365,12 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
               on = 1;
             }
           mma_commit<1>(&B.empty[stage]);
-          if (++stage == kRlOpStages) {
-            stage = 0;
-            phase ^= 1;
+          stage ^= 1;
+          if (stage == 0) phase ^= 1;
+          if (!keep || hi_t == hts - 1) {         // the last use of this G
+            mma_commit<1>(&B.g_empty[gs]);
+            gs ^= 1;
+            if (gs == 0) g_phase ^= 1;
           }
         }
         if (aborted) break;
@@ -395,10 +468,14 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   B.tempty = B.tfull + 2;
   B.io_full = B.tempty + 2;
   B.io_empty = B.io_full + kRlIos;
-  B.drained = B.io_empty + kRlIos;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(B.drained + 1);
+  B.g_full = B.io_empty + kRlIos;
+  B.g_empty = B.g_full + kRlOps;
+  B.drained = B.g_empty + kRlOps;
+  B.join = B.drained + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(B.join + 1);
   B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   B.never_set = B.abort_flag + 1;
+  B.last = B.abort_flag + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRlMaxStages; ++s) {
@@ -413,7 +490,12 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       mbar_init(&B.io_full[i], 1);
       mbar_init(&B.io_empty[i], 8);
     }
+    for (int i = 0; i < kRlOps; ++i) {
+      mbar_init(&B.g_full[i], 1);
+      mbar_init(&B.g_empty[i], 1);
+    }
     mbar_init(B.drained, 1);
+    mbar_init(B.join, 8);
     *B.abort_flag = 0;
     *B.never_set = 0;
     fence_barrier_init();
@@ -427,6 +509,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dependency_wait();                              // the parts of G; whatever else the stream did before
   const int c = blockIdx.x;
   if (c < P.n_dw) rl_dw(P, &tmX, &tmG, sm, B, tmem, warp, lane, c);
   else rl_dx(P, &tmG, &tmW, &tmIn, &tmOut, sm, B, tmem, warp, lane, c - P.n_dw);
@@ -440,55 +523,55 @@ __global__ void __launch_bounds__(kRlThreads, 1)
 // takes the next eight significant bits (cut, so that the parts add up to g
 // exactly and none overflows); an infinity or NaN stays in the first.
 __global__ void __launch_bounds__(256) router_split_kernel(const float* __restrict__ g, int T, int E, int eg,
-                                                          int groups, uint16_t* __restrict__ parts) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int per = groups * eg;
-  if (i >= static_cast<int64_t>(T) * per) return;
-  const int64_t t = i / per;
-  const int e = static_cast<int>(i - t * per);
-  const uint32_t v = e < E ? __float_as_uint(g[t * E + e]) : 0u;
-  const uint32_t a = v & 0xffff0000u;
-  uint32_t b = 0u, d = 0u;
-  if ((v & 0x7f800000u) != 0x7f800000u) {
-    const float r = __uint_as_float(v) - __uint_as_float(a);
-    b = __float_as_uint(r) & 0xffff0000u;
-    d = __float_as_uint(r - __uint_as_float(b)) & 0xffff0000u;
+                                                          int groups, uint16_t* __restrict__ parts, int units,
+                                                          int32_t* __restrict__ count) {
+  launch_dependents();
+  const int quads = groups * eg / 4;              // four experts per thread
+  const int tpb = 256 / quads;                    // tokens per block (quads <= 64)
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < units; i += gridDim.x * 256) count[i] = 0;
+  if (threadIdx.x >= tpb * quads) return;
+  const int tl = threadIdx.x / quads, e = 4 * (threadIdx.x - tl * quads);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * tpb + tl;
+  if (t >= T) return;
+  const float* src = g + t * E + e;
+  uint32_t v[4] = {0u, 0u, 0u, 0u};
+  if (E % 4 == 0) {
+    if (e < E) {
+      const float4 f = *reinterpret_cast<const float4*>(src);
+      v[0] = __float_as_uint(f.x);
+      v[1] = __float_as_uint(f.y);
+      v[2] = __float_as_uint(f.z);
+      v[3] = __float_as_uint(f.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i < E) v[i] = __float_as_uint(src[i]);
   }
-  uint16_t* p = parts + t * 3 * per + (e / eg) * 3 * eg + e % eg;
-  p[0] = static_cast<uint16_t>(a >> 16);
-  p[eg] = static_cast<uint16_t>(b >> 16);
-  p[2 * eg] = static_cast<uint16_t>(d >> 16);
-}
-
-// dw[e][h]: the partials of its unit in the order of the CTAs that left them.
-__global__ void __launch_bounds__(256) router_linear_sum_kernel(const float* __restrict__ part, int H, int E, int eg,
-                                                               int groups, int tb, int units, int n_dw,
-                                                               float* __restrict__ dw) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<int64_t>(E) * H) return;
-  const int e = static_cast<int>(i / H), h = static_cast<int>(i - static_cast<int64_t>(e) * H);
-  const int u = (h / kRlCols) * groups + e / eg;
-  const int64_t all = static_cast<int64_t>(units) * tb, lo = static_cast<int64_t>(u) * tb, hi = lo + tb;
-  int c = static_cast<int>(lo * n_dw / all);      // the CTA whose piece holds the unit's first block, or one before
-  while (rl_cut(all, c + 1, n_dw) <= lo) ++c;
-  float s = 0.f;
-  for (; c < n_dw && rl_cut(all, c, n_dw) < hi; ++c)
-    s += part[(static_cast<int64_t>(u + c) * eg + e % eg) * kRlCols + h % kRlCols];
-  dw[i] = s;
-}
-
-int device_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
+  uint32_t p[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[0][i] = v[i] >> 16;
+    p[1][i] = p[2][i] = 0u;
+    if ((v[i] & 0x7f800000u) != 0x7f800000u) {
+      const float r = __uint_as_float(v[i]) - __uint_as_float(v[i] & 0xffff0000u);
+      const uint32_t b = __float_as_uint(r) & 0xffff0000u;
+      p[1][i] = b >> 16;
+      p[2][i] = __float_as_uint(r - __uint_as_float(b)) >> 16;
+    }
+  }
+  const int grp = e / eg;
+  uint16_t* dst = parts + (t * groups + grp) * 3 * eg + (e - grp * eg);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<uint2*>(dst + k * eg) = make_uint2(p[k][0] | p[k][1] << 16, p[k][2] | p[k][3] << 16);
 }
 
 constexpr int kRlMostDw = 1024;                   // partials are sized for this many dW CTAs at most
 
 struct RlPlan {
   int eg, groups, tb, units;
-  int64_t parts, part, bytes;
+  int64_t parts, part, count, bytes;
 };
 
 RlPlan rl_plan(int T, int H, int E) {
@@ -501,6 +584,7 @@ RlPlan rl_plan(int T, int H, int E) {
   api::Carver w;
   p.parts = w.take(2ll * T * p.groups * p.eg * 3);
   p.part = w.take(4ll * (p.units + (blocks < kRlMostDw ? blocks : kRlMostDw)) * p.eg * kRlCols);
+  p.count = w.take(4ll * p.units);
   p.bytes = w.off;
   return p;
 }
@@ -543,31 +627,35 @@ extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router
   a.has_in = dx_in != nullptr;
   a.part = api::at<float>(workspace, p.part);
   a.status = dev_status;
-  // CTAs by the bytes each product moves: x once per expert group, dx_in and dx
+  a.count = api::at<int32_t>(workspace, p.count);
+  a.dw = dw_router;
+  // CTAs by the bytes each product moves through an SM: x and three parts of G a block; dx_in, dx, W_r and two
+  // parts of G (kept along the columns up to 64 experts) a tile
   const int sms = device_sms();
-  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tb) * (H / kRlCols);
-  int64_t n_dw = (sms * static_cast<int64_t>(p.groups) + (p.groups + (dx_in ? 2 : 1)) / 2) / (p.groups + (dx_in ? 2 : 1));
-  if (n_dw < 1) n_dw = 1;
+  const int hts = H / kRlCols;
+  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tb) * hts;
+  const int64_t g2 = static_cast<int64_t>((2 * p.eg + 63) / 64) * kRlBox;
+  const int64_t dw_cost = blocks * a.stage_bytes;
+  const int64_t dx_cost = tiles * ((dx_in ? 2 : 1) * kRlIo + p.groups * (p.eg * 256ll) + (p.groups > 1 ? p.groups * g2 : g2 / hts));
+  int64_t n_dw = (sms * dw_cost + (dw_cost + dx_cost) / 2) / (dw_cost + dx_cost);
+  if (n_dw > sms - 1) n_dw = sms - 1;
   if (n_dw > kRlMostDw) n_dw = kRlMostDw;
+  if (n_dw < 1) n_dw = 1;
   a.n_dw = static_cast<int>(n_dw < blocks ? n_dw : blocks);
-  const int64_t n_dx = sms > n_dw ? sms - n_dw : 1;
+  const int64_t n_dx = sms > a.n_dw ? sms - a.n_dw : 1;
   a.n_dx = static_cast<int>(n_dx < tiles ? n_dx : tiles);
 
-  const int64_t pn = static_cast<int64_t>(T) * p.groups * p.eg;
-  if ((pn + 255) / 256 > INT32_MAX) return MXG_ERR_SHAPE;
   CUtensorMap mx, mg, mw, mi, mo;
   if (!tma_map_bf16(&mx, x, H, T, kRlTok) || !tma_map_bf16(&mg, parts, 3ll * p.groups * p.eg, T, kRlTok) ||
       !tma_map_bf16(&mw, w_router, H, E, static_cast<uint32_t>(p.eg)) ||
       !tma_map_bf16(&mi, dx_in ? dx_in : dx, H, T, kRlTok) || !tma_map_bf16(&mo, dx, H, T, 32))
     return MXG_ERR_CUDA;
-  router_split_kernel<<<static_cast<unsigned>((pn + 255) / 256), 256, 0, s>>>(dlogits, T, E, p.eg, p.groups, parts);
+  const int tpb = 256 / (p.groups * p.eg / 4);
+  router_split_kernel<<<static_cast<unsigned>((T + static_cast<int64_t>(tpb) - 1) / tpb), 256, 0, s>>>(
+      dlogits, T, E, p.eg, p.groups, parts, p.units, a.count);
   count_launch();
-  MXG_TRY(cudaFuncSetAttribute(router_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRlSmem));
-  router_linear_kernel<<<static_cast<unsigned>(a.n_dw + a.n_dx), kRlThreads, kRlSmem, s>>>(mx, mg, mw, mi, mo, a);
-  count_launch();
-  const int64_t n = static_cast<int64_t>(E) * H;
-  router_linear_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a.part, H, E, p.eg, p.groups, p.tb,
-                                                                                 p.units, a.n_dw, dw_router);
-  count_launch();
-  return api::cuda_status(cudaGetLastError());
+  MXG_TRY(cudaGetLastError());
+  MXG_TRY(allow_smem(router_linear_kernel, kRlSmem));
+  return api::cuda_status(launch_after(router_linear_kernel, dim3(static_cast<unsigned>(a.n_dw + a.n_dx)),
+                                       dim3(kRlThreads), kRlSmem, s, mx, mg, mw, mi, mo, a));
 }
