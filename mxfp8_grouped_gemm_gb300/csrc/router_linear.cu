@@ -20,7 +20,7 @@
 // One launch: some CTAs compute dW, the others dx, shared out by bytes moved.
 //  dW: a unit is 128 hidden columns x up to 64 experts.  D[h][part, e] =
 //      x[t][h]^T G[t][part, e], both operands read across the contraction
-//      (MN-major), 128 tokens a stage.  The line of all (unit, token block)
+//      (MN-major), 64 tokens a stage.  The line of all (unit, token block)
 //      is cut into equal pieces, one per CTA; a CTA leaves one partial per unit
 //      it touches, numbered unit + CTA (unique: along the line one of the two
 //      grows at every seam), and the CTA that brings a unit's count of partials
@@ -39,28 +39,36 @@
 namespace mxg {
 namespace {
 
-constexpr int kRlTok = 128;                       // tokens of a block
+constexpr int kRlTok = 128;                       // tokens of a dx tile
+constexpr int kRlStep = 64;                       // tokens of a dW block
 constexpr int kRlCols = 128;                      // hidden columns of a unit or tile
 constexpr int kRlGroup = 64;                      // most experts of a group
-constexpr int kRlThreads = 384;
+// warp 0 TMA, warp 1 MMA, warp 2 TMA of dx_in, warps 4-19 epilogue (dW: 4-11)
+constexpr int kRlThreads = 640;
 constexpr int kRlBox = kRlTok * 128;              // 128 rows of 128 bytes
-constexpr int kRlFlush = 2;                       // token blocks per accumulator (256 tokens)
-constexpr int kRlRing = 196608;                   // bytes of all rings
+constexpr int kRlSmallBox = kRlStep * 128;        // 64 rows
+constexpr int kRlFlush = 4;                       // dW blocks per accumulator (256 tokens)
+constexpr int kRlRing = 229376;                   // bytes of all rings
 constexpr int kRlG = 2 * kRlBox;                  // dx: high and mid of a group for 128 tokens
 constexpr int kRlW = kRlGroup * 256;              // dx: 64 experts x 128 columns of W_r
 constexpr int kRlOps = 2;                         // of each
 constexpr int kRlIo = 2 * kRlBox;                 // dx: one tile of dx_in / dx
-constexpr int kRlIos = 3;
-constexpr int kRlMaxStages = 4;
+constexpr int kRlIos = 4;                         // even: a buffer always serves the same group of epilogue warps
+constexpr int kRlMaxStages = 8;
 constexpr int kRlSmem = 1024 + kRlRing + 1024;
 static_assert(kRlOps * (kRlG + kRlW) + kRlIos * kRlIo <= kRlRing, "dx rings");
 static_assert(kRlSmem <= 232448, "shared memory budget");
+// The two epilogue groups take turns at the tiles.  With an odd number of
+// buffers a group would see only every second phase of a buffer's barrier, and
+// a parity wait cannot tell the phase it waits for from the one before last.
+static_assert(kRlIos % 2 == 0, "each buffer belongs to one epilogue group");
 
 struct RlArgs {
   int T, H, E;
   int eg;                                         // experts of a group, padded to 16
   int groups;
-  int tb;                                         // token blocks
+  int tb;                                         // dW blocks of tokens
+  int tiles_t;                                    // dx tiles of tokens
   int units;                                      // dW: (H / 128) x groups
   int n_dw, n_dx;                                 // CTAs of each kind
   int stages, stage_bytes, g_boxes;               // dW ring
@@ -110,9 +118,10 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       bool aborted = false;
+      int u = static_cast<int>(lo / P.tb), tb = static_cast<int>(lo - static_cast<int64_t>(u) * P.tb);
+      int ht = u / P.groups, g = u - ht * P.groups;
       for (int64_t i = lo; i < hi; ++i) {
-        const int u = static_cast<int>(i / P.tb), t0 = static_cast<int>(i - static_cast<int64_t>(u) * P.tb) * kRlTok;
-        const int ht = u / P.groups, g = u - ht * P.groups;
+        const int t0 = tb * kRlStep;
         if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
           fail();
           aborted = true;
@@ -120,9 +129,16 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
         }
         uint8_t* s = sm + stage * P.stage_bytes;
         mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(P.stage_bytes));
-        for (int h = 0; h < 2; ++h) tma_load_2d(s + h * kRlBox, tmX, ht * kRlCols + 64 * h, t0, &B.full[stage]);
+        for (int h = 0; h < 2; ++h) tma_load_2d(s + h * kRlSmallBox, tmX, ht * kRlCols + 64 * h, t0, &B.full[stage]);
         for (int h = 0; h < P.g_boxes; ++h)
-          tma_load_2d(s + (2 + h) * kRlBox, tmG, g * N + 64 * h, t0, &B.full[stage]);
+          tma_load_2d(s + (2 + h) * kRlSmallBox, tmG, g * N + 64 * h, t0, &B.full[stage]);
+        if (++tb == P.tb) {
+          tb = 0;
+          if (++g == P.groups) {
+            g = 0;
+            ++ht;
+          }
+        }
         if (++stage == static_cast<uint32_t>(P.stages)) {
           stage = 0;
           phase ^= 1;
@@ -137,12 +153,12 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
     if (lane == 0) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       const uint32_t id = idesc_bf16(kRlCols, N) | kIdescAMn | kIdescBMn;
-      int64_t i = lo;
+      int64_t i = lo, unit_end = (lo / P.tb + 1) * P.tb;
       bool aborted = false;
       while (i < hi && !aborted) {
         // a run of blocks of one unit that shares an accumulator
-        int64_t end = (i / P.tb + 1) * P.tb;
-        end = end < hi ? end : hi;
+        if (i == unit_end) unit_end += P.tb;
+        int64_t end = unit_end < hi ? unit_end : hi;
         end = end < i + kRlFlush ? end : i + kRlFlush;
         if (!mbar_wait_bounded(&B.tempty[acc], acc_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
           fail();
@@ -158,10 +174,10 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
           }
           tc_fence_after();
           const uint32_t s = smem_u32(sm + stage * P.stage_bytes);
-          const uint64_t xd = smem_desc(s, kRlBox, 1024, kLayoutSwizzle128B);
-          const uint64_t gd = smem_desc(s + 2 * kRlBox, kRlBox, 1024, kLayoutSwizzle128B);
+          const uint64_t xd = smem_desc(s, kRlSmallBox, 1024, kLayoutSwizzle128B);
+          const uint64_t gd = smem_desc(s + 2 * kRlSmallBox, kRlSmallBox, 1024, kLayoutSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < kRlTok / 16; ++k)   // 16 tokens: 16 rows of 128 bytes
+          for (int k = 0; k < kRlStep / 16; ++k)   // 16 tokens: 16 rows of 128 bytes
             mma_bf16<1>(tmem + acc * 256, xd + k * (2048 >> 4), gd + k * (2048 >> 4), id, first && k == 0 ? 0u : 1u);
           first = false;
           mma_commit<1>(&B.empty[stage]);
@@ -178,7 +194,7 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
       mma_commit<1>(B.drained);
       mbar_wait_bounded(B.drained, 0, B.never_set, kWaitLimitNs);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // lane = hidden column; warps 4-7 the first half of the group's experts, warps 8-11 the second
     const int q = warp & 3, hf = (warp - 4) >> 2;
     const int half = P.eg / 2;                    // 8, 16, 24 or 32
@@ -187,10 +203,13 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
 #pragma unroll
     for (int e = 0; e < kRlGroup / 2; ++e) sum[e] = 0.f;
     uint32_t acc = 0, acc_phase = 0, join_phase = 0;
-    int64_t i = lo;
+    int u = static_cast<int>(lo / P.tb);
+    int64_t i = lo, unit_end = static_cast<int64_t>(u + 1) * P.tb;
     while (i < hi) {
-      const int u = static_cast<int>(i / P.tb);
-      const int64_t unit_end = static_cast<int64_t>(u + 1) * P.tb;
+      if (i == unit_end) {
+        ++u;
+        unit_end += P.tb;
+      }
       int64_t end = unit_end < hi ? unit_end : hi;
       const int64_t stop = end;
       end = end < i + kRlFlush ? end : i + kRlFlush;
@@ -241,11 +260,23 @@ __device__ void rl_dw(const RlArgs& P, const CUtensorMap* tmX, const CUtensorMap
           ok = ok && epilogue_sync(B, join_phase, lane);
           if (ok && *B.last) {
             __threadfence();
-            for (int k = c0; k <= c1; ++k) {      // in order; a partial's values are requested together
-              const float* from = P.part + (static_cast<int64_t>(u + k) * P.eg + hf * half) * kRlCols + row;
+            const float* from = P.part + (static_cast<int64_t>(u) * P.eg + hf * half) * kRlCols + row;
 #pragma unroll
-              for (int e = 0; e < kRlGroup / 2; ++e)
-                if (e < half) sum[e] += __ldcg(from + e * kRlCols);
+            for (int e1 = 0; e1 < kRlGroup / 2; e1 += 16) {
+              // two partials requested together, added in order; past the half and the last one the loads
+              // repeat a valid value, so that no branch makes them wait for one another
+              for (int k = c0; k <= c1; k += 2) {
+                float v[2][16];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    v[j][e] = __ldcg(from + (static_cast<int64_t>(min(k + j, c1)) * P.eg + (e1 + e < half ? e1 + e : 0)) * kRlCols);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) sum[e1 + e] += k + j <= c1 ? v[j][e] : 0.f;
+              }
             }
 #pragma unroll
             for (int e = 0; e < kRlGroup / 2; ++e) {
@@ -270,8 +301,9 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
                       const CUtensorMap* tmOut, uint8_t* sm, const RlBars& B, uint32_t tmem, int warp, int lane,
                       int c) {
   const int hts = P.H / kRlCols;
-  const int64_t all = static_cast<int64_t>(P.tb) * hts;
+  const int64_t all = static_cast<int64_t>(P.tiles_t) * hts;
   const int64_t lo = rl_cut(all, c, P.n_dx), hi = rl_cut(all, c + 1, P.n_dx);
+  const int t_lo = static_cast<int>(lo / hts) * kRlTok, h_lo = static_cast<int>(lo % hts);
   uint8_t* wr = sm + kRlOps * kRlG;
   uint8_t* io = wr + kRlOps * kRlW;
   const int g_boxes = (2 * P.eg + 63) / 64;       // high and mid of the group
@@ -282,10 +314,11 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
   };
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, gs = 0, g_phase = 0, ib = 0, ib_phase = 0;
+      uint32_t stage = 0, phase = 0, gs = 0, g_phase = 0;
       bool aborted = false;
+      int hi_t = h_lo, t0 = t_lo;
       for (int64_t i = lo; i < hi && !aborted; ++i) {
-        const int t0 = static_cast<int>(i / hts) * kRlTok, hi_t = static_cast<int>(i % hts), h0 = hi_t * kRlCols;
+        const int h0 = hi_t * kRlCols;
         for (int g = 0; g < P.groups; ++g) {
           if (!keep || i == lo || hi_t == 0) {
             if (!mbar_wait_bounded(&B.g_empty[gs], g_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
@@ -311,18 +344,9 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
           stage ^= 1;
           if (stage == 0) phase ^= 1;
         }
-        if (P.has_in && !aborted) {
-          if (!mbar_wait_bounded(&B.io_empty[ib], ib_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
-            fail();
-            aborted = true;
-            break;
-          }
-          mbar_arrive_expect_tx(&B.io_full[ib], kRlIo);
-          for (int h = 0; h < 2; ++h) tma_load_2d(io + ib * kRlIo + h * kRlBox, tmIn, h0 + 64 * h, t0, &B.io_full[ib]);
-          if (++ib == kRlIos) {
-            ib = 0;
-            ib_phase ^= 1;
-          }
+        if (++hi_t == hts) {
+          hi_t = 0;
+          t0 += kRlTok;
         }
       }
       if (aborted) {
@@ -335,8 +359,9 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
       uint32_t stage = 0, phase = 0, gs = 0, g_phase = 0, acc = 0, acc_phase = 0;
       const uint32_t id = idesc_bf16(kRlTok, kRlCols) | kIdescBMn;
       bool aborted = false;
+      int hi_t = h_lo - 1;
       for (int64_t i = lo; i < hi && !aborted; ++i) {
-        const int hi_t = static_cast<int>(i % hts);
+        if (++hi_t == hts) hi_t = 0;
         if (!mbar_wait_bounded(&B.tempty[acc], acc_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
           fail();
           break;
@@ -355,13 +380,12 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
             break;
           }
           tc_fence_after();
-          const uint32_t s = smem_u32(sm + gs * kRlG);
+          const uint64_t gd = smem_desc(smem_u32(sm + gs * kRlG), 0, 1024, kLayoutSwizzle128B);
           const uint64_t wd = smem_desc(smem_u32(wr + stage * kRlW), P.eg * 128, 1024, kLayoutSwizzle128B);
           for (int part = 1; part >= 0; --part)
             for (int k = 0; k < P.eg / 16; ++k) {
               const int col = part * P.eg + 16 * k;
-              const uint64_t ad = smem_desc(s + (col >> 6) * kRlBox, 0, 1024, kLayoutSwizzle128B) + ((col & 63) * 2 >> 4);
-              mma_bf16<1>(tmem + acc * 256, ad, wd + k * (2048 >> 4), id, on);
+              mma_bf16<1>(tmem + acc * 256, gd + (((col >> 6) * kRlBox + (col & 63) * 2) >> 4), wd + k * (2048 >> 4), id, on);
               on = 1;
             }
           mma_commit<1>(&B.empty[stage]);
@@ -381,20 +405,49 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
       mma_commit<1>(B.drained);
       mbar_wait_bounded(B.drained, 0, B.never_set, kWaitLimitNs);
     }
-  } else if (warp >= 4) {
-    // rows 32 q .., columns 64 hf ..: 32 rows of 128 bytes of an io buffer belong to this warp
-    const int q = warp & 3, hf = (warp - 4) >> 2;
-    uint32_t acc = 0, acc_phase = 0, ib = 0, ib_phase = 0;
-    for (int64_t i = lo; i < hi; ++i) {
-      const int t0 = static_cast<int>(i / hts) * kRlTok, h0 = static_cast<int>(i % hts) * kRlCols;
-      uint8_t* buf = io + ib * kRlIo + hf * kRlBox + q * 4096 + lane * 128;
-      bool got = true;
-      if (P.has_in) {
-        got = mbar_wait_bounded(&B.io_full[ib], ib_phase, B.abort_flag, kWaitLimitNs);
-      } else {
-        if (lane == 0) bulk_wait_group_read<kRlIos - 1>();    // this buffer's last store has been read out
-        __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0 && P.has_in) {                  // dx_in runs ahead of the products by up to four tiles
+      uint32_t ib = 0, ib_phase = 0;
+      int hi_t = h_lo, t0 = t_lo;
+      bool aborted = false;
+      for (int64_t i = lo; i < hi; ++i) {
+        if (!mbar_wait_bounded(&B.io_empty[ib], ib_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
+          fail();
+          aborted = true;
+          break;
+        }
+        mbar_arrive_expect_tx(&B.io_full[ib], kRlIo);
+        for (int h = 0; h < 2; ++h)
+          tma_load_2d(io + ib * kRlIo + h * kRlBox, tmIn, hi_t * kRlCols + 64 * h, t0, &B.io_full[ib]);
+        if (++ib == kRlIos) {
+          ib = 0;
+          ib_phase ^= 1;
+        }
+        if (++hi_t == hts) {
+          hi_t = 0;
+          t0 += kRlTok;
+        }
       }
+      if (aborted) {
+        const uint64_t w0 = globaltimer_ns();
+        while (globaltimer_ns() - w0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp >= 4) {
+    // Two groups of eight warps take turns at the tiles (group a: accumulator a).
+    // Rows 32 q .., columns 64 hf ..: 32 rows of 128 bytes of an io buffer belong to this warp
+    const int q = warp & 3, hf = ((warp - 4) >> 2) & 1, acc = (warp - 4) >> 3;
+    uint32_t acc_phase = 0, ib = acc, ib_phase = 0;
+    int t0 = t_lo, hi_t = h_lo + acc;
+    for (int64_t i = lo + acc; i < hi; i += 2, hi_t += 2) {
+      while (hi_t >= hts) {
+        hi_t -= hts;
+        t0 += kRlTok;
+      }
+      const int h0 = hi_t * kRlCols;
+      uint8_t* buf = io + ib * kRlIo + hf * kRlBox + q * 4096 + lane * 128;
+      bool got = mbar_wait_bounded(P.has_in ? &B.io_full[ib] : &B.io_empty[ib], P.has_in ? ib_phase : ib_phase ^ 1,
+                                   B.abort_flag, kWaitLimitNs);
       got = mbar_wait_bounded(&B.tfull[acc], acc_phase, B.abort_flag, kWaitLimitNs) && got;
       got = __all_sync(0xffffffffu, got);
       if (!got) {
@@ -437,15 +490,13 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
         if (t0 + q * 32 < P.T)
           tma_store_2d(tmOut, io + ib * kRlIo + hf * kRlBox + q * 4096, h0 + 64 * hf, t0 + q * 32);
         bulk_commit_group();
-        if (P.has_in) {
-          bulk_wait_group_read<0>();
-          mbar_arrive(&B.io_empty[ib]);
-        }
+        bulk_wait_group_read<0>();                // the store has left the buffer
+        mbar_arrive(&B.io_empty[ib]);
       }
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
-      if (++ib == kRlIos) {
-        ib = 0;
+      acc_phase ^= 1;
+      ib += 2;
+      if (ib >= kRlIos) {
+        ib -= kRlIos;
         ib_phase ^= 1;
       }
     }
@@ -455,7 +506,8 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
 }
 
 __global__ void __launch_bounds__(kRlThreads, 1)
-    router_linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
+    router_linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmGs,
+                         const __grid_constant__ CUtensorMap tmG,
                          const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmIn,
                          const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ RlArgs P) {
   extern __shared__ uint8_t raw[];
@@ -477,6 +529,15 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   B.never_set = B.abort_flag + 1;
   B.last = B.abort_flag + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(c < P.n_dw ? &tmGs : &tmG);
+    tma_prefetch_desc(c < P.n_dw ? &tmX : &tmW);
+    if (c >= P.n_dw) {
+      tma_prefetch_desc(&tmIn);
+      tma_prefetch_desc(&tmOut);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRlMaxStages; ++s) {
       mbar_init(&B.full[s], 1);
@@ -510,8 +571,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   dependency_wait();                              // the parts of G; whatever else the stream did before
-  const int c = blockIdx.x;
-  if (c < P.n_dw) rl_dw(P, &tmX, &tmG, sm, B, tmem, warp, lane, c);
+  if (c < P.n_dw) rl_dw(P, &tmX, &tmGs, sm, B, tmem, warp, lane, c);
   else rl_dx(P, &tmG, &tmW, &tmIn, &tmOut, sm, B, tmem, warp, lane, c - P.n_dw);
   tc_fence_before();
   __syncthreads();
@@ -569,8 +629,30 @@ __global__ void __launch_bounds__(256) router_split_kernel(const float* __restri
 
 constexpr int kRlMostDw = 1024;                   // partials are sized for this many dW CTAs at most
 
+// dW CTAs of `sms`: the number that lets both products end together, a whole
+// number of them per unit while there are fewer units than SMs (the CTAs of
+// one range of tokens then go through its rows side by side).  Joining a
+// unit's partials takes about 14 k cycles, what an SM moves 400 KB in.
+int rl_share(int sms, int units, int64_t blocks, int64_t block_cost, int64_t tiles, int64_t tile_cost) {
+  const int64_t most = blocks < kRlMostDw ? blocks : kRlMostDw;
+  const int step = units < sms ? units : 1;
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int n = step; n < sms || n == step; n += step) {
+    const int64_t dx = sms > n ? sms - n : 1;
+    const int64_t cost_dw = (blocks + n - 1) / n * block_cost + (n > units ? 400000 : 100000);
+    const int64_t cost_dx = (tiles + dx - 1) / dx * tile_cost;
+    const int64_t cost = cost_dw > cost_dx ? cost_dw : cost_dx;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return static_cast<int>(best < most ? best : most);
+}
+
 struct RlPlan {
-  int eg, groups, tb, units;
+  int eg, groups, tb, tiles_t, units;
   int64_t parts, part, count, bytes;
 };
 
@@ -578,7 +660,8 @@ RlPlan rl_plan(int T, int H, int E) {
   RlPlan p{};
   p.groups = (E + kRlGroup - 1) / kRlGroup;
   p.eg = p.groups > 1 ? kRlGroup : (E + 15) / 16 * 16;
-  p.tb = (T + kRlTok - 1) / kRlTok;
+  p.tb = (T + kRlStep - 1) / kRlStep;
+  p.tiles_t = (T + kRlTok - 1) / kRlTok;
   p.units = H / kRlCols * p.groups;
   const int64_t blocks = static_cast<int64_t>(p.units) * p.tb;
   api::Carver w;
@@ -620,33 +703,30 @@ extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router
   a.eg = p.eg;
   a.groups = p.groups;
   a.tb = p.tb;
+  a.tiles_t = p.tiles_t;
   a.units = p.units;
   a.g_boxes = (3 * p.eg + 63) / 64;
-  a.stage_bytes = (2 + a.g_boxes) * kRlBox;
+  a.stage_bytes = (2 + a.g_boxes) * kRlSmallBox;
   a.stages = kRlRing / a.stage_bytes < kRlMaxStages ? kRlRing / a.stage_bytes : kRlMaxStages;
   a.has_in = dx_in != nullptr;
   a.part = api::at<float>(workspace, p.part);
   a.status = dev_status;
   a.count = api::at<int32_t>(workspace, p.count);
   a.dw = dw_router;
-  // CTAs by the bytes each product moves through an SM: x and three parts of G a block; dx_in, dx, W_r and two
-  // parts of G (kept along the columns up to 64 experts) a tile
+  // Bytes each product moves through an SM: x and three parts of G a block; dx_in, dx, W_r and two parts of G
+  // (kept along the columns up to 64 experts) a tile.
   const int sms = device_sms();
   const int hts = H / kRlCols;
-  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tb) * hts;
+  const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tiles_t) * hts;
   const int64_t g2 = static_cast<int64_t>((2 * p.eg + 63) / 64) * kRlBox;
-  const int64_t dw_cost = blocks * a.stage_bytes;
-  const int64_t dx_cost = tiles * ((dx_in ? 2 : 1) * kRlIo + p.groups * (p.eg * 256ll) + (p.groups > 1 ? p.groups * g2 : g2 / hts));
-  int64_t n_dw = (sms * dw_cost + (dw_cost + dx_cost) / 2) / (dw_cost + dx_cost);
-  if (n_dw > sms - 1) n_dw = sms - 1;
-  if (n_dw > kRlMostDw) n_dw = kRlMostDw;
-  if (n_dw < 1) n_dw = 1;
-  a.n_dw = static_cast<int>(n_dw < blocks ? n_dw : blocks);
+  const int64_t tile_cost = (dx_in ? 2 : 1) * kRlIo + p.groups * (p.eg * 256ll) + (p.groups > 1 ? p.groups * g2 : g2 / hts);
+  a.n_dw = rl_share(sms, p.units, blocks, a.stage_bytes, tiles, tile_cost);
   const int64_t n_dx = sms > a.n_dw ? sms - a.n_dw : 1;
   a.n_dx = static_cast<int>(n_dx < tiles ? n_dx : tiles);
 
-  CUtensorMap mx, mg, mw, mi, mo;
-  if (!tma_map_bf16(&mx, x, H, T, kRlTok) || !tma_map_bf16(&mg, parts, 3ll * p.groups * p.eg, T, kRlTok) ||
+  CUtensorMap mx, mgs, mg, mw, mi, mo;
+  if (!tma_map_bf16(&mx, x, H, T, kRlStep) || !tma_map_bf16(&mgs, parts, 3ll * p.groups * p.eg, T, kRlStep) ||
+      !tma_map_bf16(&mg, parts, 3ll * p.groups * p.eg, T, kRlTok) ||
       !tma_map_bf16(&mw, w_router, H, E, static_cast<uint32_t>(p.eg)) ||
       !tma_map_bf16(&mi, dx_in ? dx_in : dx, H, T, kRlTok) || !tma_map_bf16(&mo, dx, H, T, 32))
     return MXG_ERR_CUDA;
@@ -657,5 +737,5 @@ extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router
   MXG_TRY(cudaGetLastError());
   MXG_TRY(allow_smem(router_linear_kernel, kRlSmem));
   return api::cuda_status(launch_after(router_linear_kernel, dim3(static_cast<unsigned>(a.n_dw + a.n_dx)),
-                                       dim3(kRlThreads), kRlSmem, s, mx, mg, mw, mi, mo, a));
+                                       dim3(kRlThreads), kRlSmem, s, mx, mgs, mg, mw, mi, mo, a));
 }

@@ -64,6 +64,21 @@ def test_router_linear_bwd(T, H, E, with_dx):
     _check(dx, dw, x, w, dx0 if with_dx else None, g)
 
 
+@pytest.mark.parametrize("T,H,E", [(12000, 2048, 8), (9000, 1024, 64)])
+def test_many_tiles_per_sm(T, H, E):
+    """Every SM goes round its buffers several times; the second call repeats the first bit for bit."""
+    m = require_gpu()
+    x, w, dx0, g = _inputs(T, H, E)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    xd, wd, gd, dd = x.cuda(), w.cuda(), torch.from_numpy(g).cuda(), dx0.cuda()
+    dx, dw = m.mxg_router_linear_bwd(xd, wd, gd, dd, status)
+    for _ in range(20):
+        dx2, dw2 = m.mxg_router_linear_bwd(xd, wd, gd, dd, status)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    assert int(status.item()) == 0
+    _check(dx, dw, x, w, dx0, g)
+
+
 def test_in_place_repeatable_and_on_another_stream():
     m = require_gpu()
     x, w, dx0, g = _inputs(3001, 512, 12)
