@@ -18,7 +18,7 @@
 // contiguous (K-major) or across it (MN-major), so no transposed copy is kept.
 // A and B are symmetric: only their tiles on and above the diagonal are
 // computed and stored, and a block below it is read as the transpose of the
-// one above (see ns_transposed).
+// one above (see ns_mn_stages).
 //
 // Number format.  Operands are fp16: X, A and B are bounded (|X|_F = 1 at the
 // start, singular values at most ~1.2 afterwards), so the eleven-bit
@@ -293,8 +293,8 @@ struct NsArgs {
   int app_m, app_n;                       // row and column tiles of X
   float alpha[3], alpha_last;             // each product's factor on the accumulators
   float beta, diag;                       // POLY: + beta A + diag I
-  const __half* ap;                       // A, [batch (x 2)][m][lda], lda a multiple of 16
-  int64_t lda;
+  uint16_t *xp[2], *ap, *bp;              // X, A, B; rows ldx and lda apart (multiples of 16), low parts low_x, low_a on
+  int64_t ldx, lda, low_x, low_a;
   uint16_t* update;                       // bf16 [batch][rows][cols], nullable
   const uint16_t* w_in;
   uint16_t* w_out;                        // nullable: w_in * w_keep - lr * value
@@ -379,11 +379,11 @@ __device__ __forceinline__ bool ns_wait_done(const NsArgs& P, const NsTile& tc, 
   }
 }
 
-// Whether the 64 contraction elements from k0 of operand rows row0 .. are read
-// MN-major: below the diagonal a symmetric matrix holds nothing, and the block
-// (rows, k) is the transpose of (k, rows).
-__device__ __forceinline__ bool ns_transposed(int form, int row0, int k0) {
-  return form == NS_MN || (form == NS_SYM && k0 / kNsSym < row0 / kNsSym);
+// How many stages of 64 contraction elements of operand rows row0 .. are read
+// MN-major, from the first on: below the diagonal a symmetric matrix holds
+// nothing, and the block (rows, k) is the transpose of (k, rows).
+__device__ __forceinline__ int ns_mn_stages(int form, int row0) {
+  return form == NS_MN ? INT_MAX : form == NS_SYM ? row0 / kNsSym * (kNsSym / kNsK) : 0;
 }
 
 template <bool PEER>
@@ -395,10 +395,6 @@ __device__ __forceinline__ void ns_load(uint8_t* dst, const CUtensorMap* map, bo
     if (PEER) tma_load_3d_pair(dst + h * kNsBoxBytes, map, x, y, b, peer_bar);
     else tma_load_3d(dst + h * kNsBoxBytes, map, x, y, b, bar);
   }
-}
-
-__device__ __forceinline__ uint64_t ns_desc(const uint8_t* op, bool mn) {
-  return smem_desc(smem_u32(op), mn ? kNsBoxBytes : 0, 1024, kLayoutSwizzle128B);
 }
 
 // 64 columns of a row, zero past the matrix's edge (whole 32-byte pieces: rows
@@ -436,6 +432,13 @@ __device__ __forceinline__ void ns_store_box(const uint32_t (&h)[32], uint8_t* b
   }
 }
 
+// The same by plain stores, 32 bytes at a time (rows are padded to 16).
+__device__ __forceinline__ void ns_store_direct(const uint32_t (&h)[32], uint16_t* dst, bool in, int col, int n) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (in && col + 16 * j < n) st_global_v8(dst + 16 * j, h + 8 * j);
+}
+
 // One 32 x 32 block of the last product to a bf16 matrix whose rows may start
 // at any even address: staged in fp32 (rows of 33 words) and written row by
 // row, 32 lanes side by side.
@@ -468,24 +471,35 @@ enum NsKind { NS_STORE,                   // alpha acc to fp16
               NS_WEIGHTS,                 // w_in * w_keep - lr alpha acc to bf16
               NS_BY_ROWS };               // update and / or weights by plain stores
 
-// Reads the 64 columns from TMEM at taddr, lets release() run once they are in
-// registers, and stores them (row0, col: of D; any: the block is not wholly
-// outside it).
-template <int KIND, bool SPLIT, typename F>
-__device__ __forceinline__ void ns_epilogue(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* boxes,
-                                            uint32_t& flip, const CUtensorMap* dst, int row0, int col, int b, bool any,
-                                            int lane, F release) {
+// Where 64 columns of a tile go: by TMA through shared-memory boxes, or (DIRECT)
+// by plain stores to rows `ld` apart of a matrix [rows][cols], low parts `low`
+// elements further on.
+struct NsDst {
+  const CUtensorMap* map;
+  uint16_t* p;
+  int rows, cols;
+  int64_t ld, low;
+};
+
+// Requests the addend, lets ready() wait for the accumulator, reads the 64
+// columns from TMEM at taddr, lets release() run once they are in registers,
+// and stores them (row0, col: of D; any: the block is not wholly outside it).
+template <int KIND, bool SPLIT, bool DIRECT, typename W, typename F>
+__device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* boxes,
+                                            uint32_t& flip, const NsDst& dst, int row0, int col, int b, bool any,
+                                            int lane, W ready, F release) {
   constexpr int ADD = KIND == NS_POLYNOMIAL || KIND == NS_WEIGHTS ? 32 : 1;
   uint32_t w[ADD], wl[SPLIT && KIND == NS_POLYNOMIAL ? 32 : 1];
   if constexpr (KIND == NS_POLYNOMIAL) {
     const bool in = row0 + lane < P.m;
     const int64_t off = (static_cast<int64_t>(b) * P.m + row0 + lane) * P.lda + col;
     ns_load_row(P.ap, off, in, col, P.m, w);
-    if constexpr (SPLIT) ns_load_row(P.ap + static_cast<int64_t>(P.batch) * P.m * P.lda, off, in, col, P.m, wl);
+    if constexpr (SPLIT) ns_load_row(P.ap + P.low_a, off, in, col, P.m, wl);
   }
   if constexpr (KIND == NS_WEIGHTS)
     ns_load_row(P.w_in, (static_cast<int64_t>(b) * P.rows + row0 + lane) * P.cols + col, row0 + lane < P.rows, col,
                 P.cols, w);
+  if (!ready()) return false;
   uint32_t h[32], l[SPLIT ? 32 : 1];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -530,16 +544,23 @@ __device__ __forceinline__ void ns_epilogue(const NsArgs& P, float alpha, uint32
       }
     }
   }
+  constexpr bool LOW = SPLIT && (KIND == NS_STORE || KIND == NS_POLYNOMIAL);
   if constexpr (KIND != NS_BY_ROWS) {
-    if (any) {
-      ns_store_box(h, boxes + flip * kNsOut, dst, row0, col, b, lane);
+    if constexpr (DIRECT) {
+      const bool in = row0 + lane < dst.rows;
+      uint16_t* p = dst.p + (static_cast<int64_t>(b) * dst.rows + row0 + lane) * dst.ld + col;
+      ns_store_direct(h, p, in, col, dst.cols);
+      if constexpr (LOW) ns_store_direct(l, p + dst.low, in, col, dst.cols);
+    } else if (any) {
+      ns_store_box(h, boxes + flip * kNsOut, dst.map, row0, col, b, lane);
       flip ^= 1;
-      if constexpr (SPLIT && (KIND == NS_STORE || KIND == NS_POLYNOMIAL)) {
-        ns_store_box(l, boxes + flip * kNsOut, dst, row0, col, b + P.batch, lane);
+      if constexpr (LOW) {
+        ns_store_box(l, boxes + flip * kNsOut, dst.map, row0, col, b + P.batch, lane);
         flip ^= 1;
       }
     }
   }
+  return true;
 }
 
 // ROWS: the last product leaves by plain stores (rows that TMA cannot address,
@@ -624,6 +645,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           break;
         }
         fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
+        const int pstages = ns_mn_stages(o.p_form, prow), qstages = ns_mn_stages(o.q_form, qrow);
         for (int kp = 0, kb = 0, part = 0; kp < parts * o.nk; ++kp) {
           const int pz = tc.b + (SPLIT && part == 1 ? P.batch : 0), qz = tc.b + (SPLIT && part == 0 ? P.batch : 0);
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
@@ -634,7 +656,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           uint8_t* sP = sm + stage * kNsStageBytes;
           uint8_t* sQ = sP + kNsOpBytes;
           const int k0 = kb * kNsK;
-          const bool pmn = ns_transposed(o.p_form, prow, k0), qmn = ns_transposed(o.q_form, qrow, k0);
+          const bool pmn = kb < pstages, qmn = kb < qstages;
           if (!PAIR || rank == 0) {
             mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);     // both CTAs' bytes
             ns_load<false>(sP, o.p, pmn, prow, k0, pz, &full[stage], 0u);
@@ -663,6 +685,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool aborted = false;
       int64_t done = 0;
+      const uint64_t desc0 = smem_desc(smem_u32(sm), kNsBoxBytes, 1024, kLayoutSwizzle128B);
       for (int64_t t = tile0; t < total && !aborted; t += tstep) {
         const NsTile tc = ns_tile<PAIR>(P, t);
         const bool got = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)
@@ -674,6 +697,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         tc_fence_after();
         const uint32_t d_t = tmem + acc * BN;
         const NsOperands o = ns_operands(P, tc);
+        // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
+        const int pmn = ns_mn_stages(o.p_form, tc.ti * TM), qmn = ns_mn_stages(o.q_form, tc.tj * BN);
         for (int kp = 0, kb = 0; kp < parts * o.nk; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
@@ -683,13 +708,11 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             break;
           }
           tc_fence_after();
-          // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
-          const bool pmn = ns_transposed(o.p_form, tc.ti * TM, kb * kNsK);
-          const bool qmn = ns_transposed(o.q_form, tc.tj * BN, kb * kNsK);
-          const uint8_t* sP = sm + stage * kNsStageBytes;
-          const uint64_t pd = ns_desc(sP, pmn), qd = ns_desc(sP + kNsOpBytes, qmn);
-          const uint32_t pstep = pmn ? 2048 >> 4 : 32 >> 4, qstep = qmn ? 2048 >> 4 : 32 >> 4;
-          const uint32_t id = idesc_f16(TM, BN) | (pmn ? kIdescAMn : 0u) | (qmn ? kIdescBMn : 0u);
+          // one thread issues everything: few instructions between the waits (the leading offset only matters
+          // MN-major)
+          const uint64_t pd = desc0 + stage * (kNsStageBytes >> 4), qd = pd + (kNsOpBytes >> 4);
+          const uint32_t pstep = kb < pmn ? 2048 >> 4 : 32 >> 4, qstep = kb < qmn ? 2048 >> 4 : 32 >> 4;
+          const uint32_t id = idesc_f16(TM, BN) | (kb < pmn ? kIdescAMn : 0u) | (kb < qmn ? kIdescBMn : 0u);
 #pragma unroll
           for (uint32_t k = 0; k < kNsK / 16; ++k)
             mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kp | k) != 0 ? 1u : 0u);
@@ -734,20 +757,19 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       bool got = true;
       if (tc.op == NS_POLY) {
         if (lane == 0) got = ns_wait_done(P, tc, abort_flag);
-        __syncwarp();
+        got = __all_sync(0xffffffffu, got);
       }
-      got = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs) && got;
-      got = __all_sync(0xffffffffu, got);
-      if (!got) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
 #pragma unroll 1
-      for (int c = 0; c < BOXES; ++c) {
+      for (int c = 0; c < BOXES && got; ++c) {
         const int col = col0 + 64 * c;
         const bool any = row0 < dm && col < dn;
+        auto ready = [&]() {              // before the first columns: the accumulator is complete
+          if (c != 0) return true;
+          const bool in = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs));
+          tc_fence_after();
+          return in;
+        };
         auto release = [&]() {            // after the last columns: the accumulator may be overwritten
           if (c != BOXES - 1) return;
           tc_fence_before();
@@ -761,25 +783,41 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           }
         };
         const uint32_t ta = tb + 64 * c;
+        const NsDst da{&P.as, P.ap, P.m, P.m, P.lda, P.low_a}, db{&P.bs, P.bp, P.m, P.m, P.lda, P.low_a},
+            dx{&P.xs[(tc.step & 1) ^ 1], P.xp[(tc.step & 1) ^ 1], P.rows, P.cols, P.ldx, P.low_x},
+            out{&P.out, P.w_out != nullptr ? P.w_out : P.update, P.rows, P.cols, P.cols, 0};
         if (tc.op == NS_GRAM)
-          ns_epilogue<NS_STORE, SPLIT>(P, P.alpha[NS_GRAM], ta, box, flip, &P.as, row0, col, tc.b, any, lane, release);
+          got = ns_epilogue<NS_STORE, SPLIT, !PAIR>(P, P.alpha[NS_GRAM], ta, box, flip, da, row0, col, tc.b, any, lane,
+                                                    ready, release);
         else if (tc.op == NS_POLY)
-          ns_epilogue<NS_POLYNOMIAL, SPLIT>(P, P.alpha[NS_POLY], ta, box, flip, &P.bs, row0, col, tc.b, any, lane,
-                                            release);
+          got = ns_epilogue<NS_POLYNOMIAL, SPLIT, !PAIR>(P, P.alpha[NS_POLY], ta, box, flip, db, row0, col, tc.b, any,
+                                                         lane, ready, release);
         else if (!last)
-          ns_epilogue<NS_STORE, SPLIT>(P, P.alpha[NS_APPLY], ta, box, flip, &P.xs[(tc.step & 1) ^ 1], row0, col, tc.b,
-                                       any, lane, release);
+          got = ns_epilogue<NS_STORE, SPLIT, !PAIR>(P, P.alpha[NS_APPLY], ta, box, flip, dx, row0, col, tc.b, any, lane,
+                                                    ready, release);
         else if (ROWS)
-          ns_epilogue<NS_BY_ROWS, SPLIT>(P, P.alpha_last, ta, box, flip, nullptr, row0, col, tc.b, any, lane, release);
+          got = ns_epilogue<NS_BY_ROWS, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
+                                                      ready, release);
         else if (P.w_out != nullptr)
-          ns_epilogue<NS_WEIGHTS, SPLIT>(P, P.alpha_last, ta, box, flip, &P.out, row0, col, tc.b, any, lane, release);
+          got = ns_epilogue<NS_WEIGHTS, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
+                                                      ready, release);
         else
-          ns_epilogue<NS_UPDATE, SPLIT>(P, P.alpha_last, ta, box, flip, &P.out, row0, col, tc.b, any, lane, release);
+          got = ns_epilogue<NS_UPDATE, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
+                                                     ready, release);
       }
-      if (!last && lane == 0) {
-        bulk_wait_group<0>();             // the stores are in memory,
-        fence_proxy_async_global();
-        red_release_gpu_add(P.done + tc.b, 1);
+      if (!got) {
+        if (lane == 0) fail();
+        break;
+      }
+      if (!last) {
+        __syncwarp();                     // plain stores: the warp's, before the release below
+        if (lane == 0) {
+          if (PAIR) {                     // TMA stores: in memory,
+            bulk_wait_group<0>();
+            fence_proxy_async_global();
+          }
+          red_release_gpu_add(P.done + tc.b, 1);
+        }
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
@@ -972,8 +1010,14 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.alpha_last = static_cast<float>(std::ldexp(static_cast<double>(a->scale), -kExpA - ex));
   n.beta = a->b;
   n.diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
-  n.ap = am;
+  n.xp[0] = reinterpret_cast<uint16_t*>(x[0]);
+  n.xp[1] = reinterpret_cast<uint16_t*>(x[1]);
+  n.ap = reinterpret_cast<uint16_t*>(am);
+  n.bp = reinterpret_cast<uint16_t*>(bm);
+  n.ldx = p.ldx;
   n.lda = p.lda;
+  n.low_x = static_cast<int64_t>(a->batch) * a->rows * p.ldx;
+  n.low_a = static_cast<int64_t>(a->batch) * p.m * p.lda;
   n.update = a->update;
   n.w_in = a->w_in;
   n.w_out = a->w_out;
