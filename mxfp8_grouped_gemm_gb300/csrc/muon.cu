@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // ------------------------------------------------------------------ products
 // D = P Q^T over fp16 operands, tiles of 128 x 128 on one SM or 256 x 256 on a
 // CTA pair (cta_group::2, each SM holding its 128 rows of both operands).
-// Warp 0 issues TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run the
-// epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
+// Warps 0 and 2 issue TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run
+// the epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
 // columns.  The accumulator is double-buffered in TMEM.
 //
 // One launch runs all products of all steps: the tiles of the whole run form
@@ -273,6 +273,8 @@ constexpr int kNsCtrl = 1024;
 constexpr int kNsSmem = 1024 + kNsStages * kNsStageBytes + 8 * kNsWarpOut + kNsCtrl;
 constexpr int kNsSym = 256;               // a symmetric matrix is stored in full within diagonal blocks of this size
 static_assert(kNsSmem <= 232448, "shared memory budget");
+constexpr int kNsALow = 2 * kNsOpBytes;   // FUSED: A's low part behind its high part (128 x 128), in the store boxes' place
+static_assert(2 * kNsALow <= 8 * kNsWarpOut, "A in two parts");
 static_assert(32 * 33 * 4 <= kNsWarpOut, "unaligned outputs stage 32 x 32 fp32 values");
 
 // How an operand lies in memory.
@@ -316,18 +318,21 @@ __host__ __device__ __forceinline__ int ns_first(int ti) {
 }
 
 // Tile t of the whole run: step by step, product by product, matrix by matrix.
-template <bool PAIR>
+// FUSED: A and B are one tile, computed together under NS_GRAM.
+template <bool PAIR, bool FUSED>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   constexpr int kArrive = PAIR ? 16 : 8;  // epilogue warps of a tile
+  constexpr int kSyms = FUSED ? 1 : 2;    // products before the last
   NsTile r;
   const int app = P.app_m * P.app_n;
   const int64_t sym_all = static_cast<int64_t>(P.sym_tiles) * P.batch;
-  const int64_t per_step = 2 * sym_all + static_cast<int64_t>(app) * P.batch;
+  const int64_t per_step = kSyms * sym_all + static_cast<int64_t>(app) * P.batch;
   r.step = static_cast<int>(t / per_step);
   int64_t l = t - r.step * per_step;
-  r.op = l < sym_all ? NS_GRAM : l < 2 * sym_all ? NS_POLY : NS_APPLY;
-  l -= r.op * sym_all;
-  r.need = kArrive * (r.step * (2 * P.sym_tiles + app) + r.op * P.sym_tiles);
+  const int before = l < sym_all ? 0 : l < kSyms * sym_all ? 1 : kSyms;       // products of the step
+  r.op = before == kSyms ? NS_APPLY : before;
+  l -= before * sym_all;
+  r.need = kArrive * (r.step * (kSyms * P.sym_tiles + app) + before * P.sym_tiles);
   if (r.op != NS_APPLY) {
     r.b = static_cast<int>(l / P.sym_tiles);
     int i = static_cast<int>(l - static_cast<int64_t>(r.b) * P.sym_tiles);
@@ -484,13 +489,13 @@ struct NsDst {
 // Requests the addend, lets ready() wait for the accumulator, reads the 64
 // columns from TMEM at taddr, lets release() run once they are in registers,
 // and stores them (row0, col: of D; any: the block is not wholly outside it).
-template <int KIND, bool SPLIT, bool DIRECT, typename W, typename F>
+// KEPT: the polynomial's A is already in w (and wl), zero outside the matrix.
+template <int KIND, bool SPLIT, bool DIRECT, bool KEPT, typename W, typename F>
 __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* boxes,
                                             uint32_t& flip, const NsDst& dst, int row0, int col, int b, bool any,
-                                            int lane, W ready, F release) {
-  constexpr int ADD = KIND == NS_POLYNOMIAL || KIND == NS_WEIGHTS ? 32 : 1;
-  uint32_t w[ADD], wl[SPLIT && KIND == NS_POLYNOMIAL ? 32 : 1];
-  if constexpr (KIND == NS_POLYNOMIAL) {
+                                            int lane, uint32_t (&w)[32], uint32_t (&wl)[SPLIT ? 32 : 1], W ready,
+                                            F release) {
+  if constexpr (KIND == NS_POLYNOMIAL && !KEPT) {
     const bool in = row0 + lane < P.m;
     const int64_t off = (static_cast<int64_t>(b) * P.m + row0 + lane) * P.lda + col;
     ns_load_row(P.ap, off, in, col, P.m, w);
@@ -563,9 +568,46 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32
   return true;
 }
 
+// FUSED: 32 rows x 64 columns of A to registers (h, low parts l) and to shared
+// memory as an operand: two boxes of 128 rows x 64 columns, 128-byte swizzle.
+// Whatever lies outside the matrix becomes zero, since it is contracted over.
+template <bool SPLIT>
+__device__ __forceinline__ void ns_keep_a(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* abuf, int row, int col,
+                                          uint32_t (&h)[32], uint32_t (&l)[SPLIT ? 32 : 1]) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + 32 * half, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = col + 32 * half + 2 * i;
+      const float x = row < P.m && c < P.m ? alpha * __uint_as_float(r[2 * i]) : 0.f;
+      const float y = row < P.m && c + 1 < P.m ? alpha * __uint_as_float(r[2 * i + 1]) : 0.f;
+      if constexpr (SPLIT) {
+        h[16 * half + i] = split_half2(x, y, l[16 * half + i]);
+      } else {
+        const __half2 v = __floats2half2_rn(x, y);
+        h[16 * half + i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+  }
+  uint8_t* dst = abuf + (col >> 6) * kNsOpBytes + row * 128;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint8_t* p = dst + ((j ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(p) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+    if constexpr (SPLIT)
+      *reinterpret_cast<uint4*>(p + kNsALow) = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+  }
+  fence_proxy_async_smem();
+}
+
 // ROWS: the last product leaves by plain stores (rows that TMA cannot address,
 // or both outputs at once).  SPLIT: operands in two fp16 parts.
-template <bool PAIR, bool ROWS, bool SPLIT>
+// FUSED: a short side of at most 128 makes A and B a single tile: B is computed
+// from the A in shared memory, without a trip to global memory between them.
+template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsArgs P) {
   constexpr int CG = PAIR ? 2 : 1;
   constexpr int BN = PAIR ? 256 : 128;    // columns of a tile (and accumulator columns)
@@ -578,7 +620,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   uint64_t* tfull = empty + kNsStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drained = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* a_ready = drained + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_ready + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_set = abort_flag + 1;
   uint32_t* landing = tmem_slot + 4;      // rank 1's release stores (pair)
@@ -597,6 +640,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       mbar_init(&tempty[a], PAIR ? 9 : 8);
     }
     mbar_init(drained, 1);
+    mbar_init(a_ready, 8);
     *abort_flag = 0;
     *never_set = 0;
     fence_barrier_init();
@@ -621,7 +665,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
   const int64_t tstep = PAIR ? gridDim.x / 2 : gridDim.x;
-  const int64_t total = static_cast<int64_t>(P.steps) * P.batch * (2 * P.sym_tiles + P.app_m * P.app_n);
+  const int64_t total = static_cast<int64_t>(P.steps) * P.batch * ((FUSED ? 1 : 2) * P.sym_tiles + P.app_m * P.app_n);
   // in parts: first (high, low), (low, high), then (high, high)
   constexpr int parts = SPLIT ? 3 : 1;
   auto fail = [&]() {
@@ -629,41 +673,39 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     *abort_flag = 1;
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
+    // warp 0 loads P, warp 2 Q: one thread takes ~150 cycles per box, and the
+    // boxes of a small product are its critical path
     if (lane == 0) {
+      const bool second = warp == 2;
       uint32_t stage = 0, phase = 0;
       bool aborted = false;
       const uint32_t full0 = PAIR ? map_to_rank(smem_u32(full), 0) : 0u;
       for (int64_t t = tile0; t < total && !aborted; t += tstep) {
-        const NsTile tc = ns_tile<PAIR>(P, t);
-        const int prow = tc.ti * TM + static_cast<int>(rank) * kNsRows;
-        const int qrow = tc.tj * BN + static_cast<int>(rank) * kNsRows;
+        const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
         const NsOperands o = ns_operands(P, tc);
+        const int row = (second ? tc.tj * BN : tc.ti * TM) + static_cast<int>(rank) * kNsRows;
+        const int mn_stages = ns_mn_stages(second ? o.q_form : o.p_form, row);
+        const CUtensorMap* map = second ? o.q : o.p;
         if (!ns_wait_done(P, tc, abort_flag)) {
           fail();
           aborted = true;
           break;
         }
         fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
-        const int pstages = ns_mn_stages(o.p_form, prow), qstages = ns_mn_stages(o.q_form, qrow);
         for (int kp = 0, kb = 0, part = 0; kp < parts * o.nk; ++kp) {
-          const int pz = tc.b + (SPLIT && part == 1 ? P.batch : 0), qz = tc.b + (SPLIT && part == 0 ? P.batch : 0);
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
             break;
           }
-          uint8_t* sP = sm + stage * kNsStageBytes;
-          uint8_t* sQ = sP + kNsOpBytes;
-          const int k0 = kb * kNsK;
-          const bool pmn = kb < pstages, qmn = kb < qstages;
+          uint8_t* dst = sm + stage * kNsStageBytes + (second ? kNsOpBytes : 0);
+          const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
           if (!PAIR || rank == 0) {
-            mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);     // both CTAs' bytes
-            ns_load<false>(sP, o.p, pmn, prow, k0, pz, &full[stage], 0u);
-            ns_load<false>(sQ, o.q, qmn, qrow, k0, qz, &full[stage], 0u);
+            if (!second) mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);      // all bytes of both CTAs
+            ns_load<false>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
           } else {
-            ns_load<true>(sP, o.p, pmn, prow, k0, pz, nullptr, full0 + stage * 8);
-            ns_load<true>(sQ, o.q, qmn, qrow, k0, qz, nullptr, full0 + stage * 8);
+            ns_load<true>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
           }
           if (++stage == kNsStages) {
             stage = 0;
@@ -682,12 +724,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, a_phase = 0;
       bool aborted = false;
       int64_t done = 0;
       const uint64_t desc0 = smem_desc(smem_u32(sm), kNsBoxBytes, 1024, kLayoutSwizzle128B);
       for (int64_t t = tile0; t < total && !aborted; t += tstep) {
-        const NsTile tc = ns_tile<PAIR>(P, t);
+        const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
         const bool got = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)
                               : mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs);
         if (!got) {
@@ -729,6 +771,29 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         ++done;
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
+        if (FUSED && tc.op == NS_GRAM) {
+          // A A^T from the A that the epilogue has put into shared memory, into the other accumulator
+          if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs) ||
+              !mbar_wait_bounded(a_ready, a_phase, abort_flag, kWaitLimitNs)) {
+            fail();
+            break;
+          }
+          a_phase ^= 1;
+          tc_fence_after();
+          const uint64_t ad = smem_desc(smem_u32(boxes), 0, 1024, kLayoutSwizzle128B);
+          const uint32_t d2 = tmem + acc * BN;
+          for (int part = 0; part < parts; ++part) {
+            const uint64_t pa = ad + (part == 1 ? kNsALow >> 4 : 0), qa = ad + (SPLIT && part == 0 ? kNsALow >> 4 : 0);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+              const uint32_t off = ((k >> 2) * kNsOpBytes + (k & 3) * 32) >> 4;
+              mma_bf16<CG>(d2, pa + off, qa + off, idesc_f16(TM, BN), (part | k) != 0 ? 1u : 0u);
+            }
+          }
+          mma_commit<CG>(&tfull[acc]);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
       }
       // rank 1's release stores of the last two tiles have landed here before this CTA exits
       if (PAIR && done > 1) mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, never_set, kWaitLimitNs);
@@ -748,7 +813,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
     uint32_t acc = 0, acc_phase = 0, flip = 0;
     for (int64_t t = tile0; t < total; t += tstep) {
-      const NsTile tc = ns_tile<PAIR>(P, t);
+      const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
       const bool last = tc.op == NS_APPLY && tc.step + 1 == P.steps;
       const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
       const int col0 = tc.tj * BN + hf * COLS;
@@ -758,6 +823,23 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       if (tc.op == NS_POLY) {
         if (lane == 0) got = ns_wait_done(P, tc, abort_flag);
         got = __all_sync(0xffffffffu, got);
+      }
+      uint32_t w[32], wl[SPLIT ? 32 : 1];
+      if (FUSED && tc.op == NS_GRAM) {
+        got = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs));
+        tc_fence_after();
+        if (got) {
+          ns_keep_a<SPLIT>(P, P.alpha[NS_GRAM], tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS,
+                           boxes, q * 32 + lane, hf * COLS, w, wl);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&tempty[acc]);
+            mbar_arrive(a_ready);
+          }
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
       }
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
 #pragma unroll 1
@@ -786,24 +868,24 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const NsDst da{&P.as, P.ap, P.m, P.m, P.lda, P.low_a}, db{&P.bs, P.bp, P.m, P.m, P.lda, P.low_a},
             dx{&P.xs[(tc.step & 1) ^ 1], P.xp[(tc.step & 1) ^ 1], P.rows, P.cols, P.ldx, P.low_x},
             out{&P.out, P.w_out != nullptr ? P.w_out : P.update, P.rows, P.cols, P.cols, 0};
-        if (tc.op == NS_GRAM)
-          got = ns_epilogue<NS_STORE, SPLIT, !PAIR>(P, P.alpha[NS_GRAM], ta, box, flip, da, row0, col, tc.b, any, lane,
-                                                    ready, release);
-        else if (tc.op == NS_POLY)
-          got = ns_epilogue<NS_POLYNOMIAL, SPLIT, !PAIR>(P, P.alpha[NS_POLY], ta, box, flip, db, row0, col, tc.b, any,
-                                                         lane, ready, release);
+        if (!FUSED && tc.op == NS_GRAM)
+          got = ns_epilogue<NS_STORE, SPLIT, !PAIR, false>(P, P.alpha[NS_GRAM], ta, box, flip, da, row0, col, tc.b, any,
+                                                           lane, w, wl, ready, release);
+        else if (FUSED ? tc.op == NS_GRAM : tc.op == NS_POLY)
+          got = ns_epilogue<NS_POLYNOMIAL, SPLIT, !PAIR, FUSED>(P, P.alpha[NS_POLY], ta, box, flip, db, row0, col, tc.b,
+                                                                any, lane, w, wl, ready, release);
         else if (!last)
-          got = ns_epilogue<NS_STORE, SPLIT, !PAIR>(P, P.alpha[NS_APPLY], ta, box, flip, dx, row0, col, tc.b, any, lane,
-                                                    ready, release);
+          got = ns_epilogue<NS_STORE, SPLIT, !PAIR, false>(P, P.alpha[NS_APPLY], ta, box, flip, dx, row0, col, tc.b,
+                                                           any, lane, w, wl, ready, release);
         else if (ROWS)
-          got = ns_epilogue<NS_BY_ROWS, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
-                                                      ready, release);
+          got = ns_epilogue<NS_BY_ROWS, SPLIT, !PAIR, false>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any,
+                                                             lane, w, wl, ready, release);
         else if (P.w_out != nullptr)
-          got = ns_epilogue<NS_WEIGHTS, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
-                                                      ready, release);
+          got = ns_epilogue<NS_WEIGHTS, SPLIT, !PAIR, false>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any,
+                                                             lane, w, wl, ready, release);
         else
-          got = ns_epilogue<NS_UPDATE, SPLIT, !PAIR>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any, lane,
-                                                     ready, release);
+          got = ns_epilogue<NS_UPDATE, SPLIT, !PAIR, false>(P, P.alpha_last, ta, box, flip, out, row0, col, tc.b, any,
+                                                            lane, w, wl, ready, release);
       }
       if (!got) {
         if (lane == 0) fail();
@@ -835,13 +917,13 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
 
 // --------------------------------------------------------------------- host
 // CTAs (or pairs) of a kernel that the device holds at once.
-template <bool PAIR, bool ROWS, bool SPLIT>
+template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
 int ns_resident() {
   static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < 64 && known[dev].load() > 0) return known[dev].load();
-  auto kern = ns_kernel<PAIR, ROWS, SPLIT>;
+  auto kern = ns_kernel<PAIR, ROWS, SPLIT, FUSED>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess) return 0;
   int n = 0;
   if (PAIR) {
@@ -865,7 +947,7 @@ int ns_resident() {
   return n;
 }
 
-template <bool PAIR, bool ROWS, bool SPLIT>
+template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
 cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
   constexpr int W = PAIR ? 256 : 128;
   a.app_m = (a.rows + W - 1) / W;
@@ -874,7 +956,7 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
   a.sym_tiles = 0;
   for (int i = 0; i < t; ++i) a.sym_tiles += t - ns_first<PAIR>(i);
   const int64_t most = static_cast<int64_t>(a.app_m) * a.app_n * a.batch;     // of any product
-  const int64_t units = ns_resident<PAIR, ROWS, SPLIT>();
+  const int64_t units = ns_resident<PAIR, ROWS, SPLIT, FUSED>();
   if (units <= 0) return cudaErrorCooperativeLaunchTooLarge;
   const int64_t n = most < units ? most : units;
   cudaLaunchConfig_t cfg = {};
@@ -891,7 +973,7 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, ns_kernel<PAIR, ROWS, SPLIT>, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ns_kernel<PAIR, ROWS, SPLIT, FUSED>, a);
   count_launch();
   return err != cudaSuccess ? err : cudaGetLastError();
 }
@@ -909,7 +991,7 @@ struct NsPlan {
 // directions over noise, the error of the bf16 update against an exact run
 // (its own rounding alone is 1.66e-3): one part 3.1e-3 at 8 x 8, 2.4e-3 at
 // 16 x 2000, 2.2e-3 from 64 x 64 to 256 x 256; two parts 1.67e-3.
-constexpr int kNsSplitMost = 64;          // not above 128: pairs do not split
+constexpr int kNsSplitMost = 64;          // not above 128: only single tiles of A split
 
 NsPlan ns_plan(int batch, int rows, int cols) {
   NsPlan p{};
@@ -1042,8 +1124,13 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   // fills only one of the two SMs, the smaller tiles keep more SMs busy
   const int64_t t256 = static_cast<int64_t>((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
   cudaError_t err;
-  if (t256 >= device_sms() / 2 && p.m > 128) err = by_rows ? launch_ns<true, true, false>(n, s) : launch_ns<true, false, false>(n, s);
-  else if (p.split) err = by_rows ? launch_ns<false, true, true>(n, s) : launch_ns<false, false, true>(n, s);
-  else err = by_rows ? launch_ns<false, true, false>(n, s) : launch_ns<false, false, false>(n, s);
+  if (t256 >= device_sms() / 2 && p.m > 128)
+    err = by_rows ? launch_ns<true, true, false, false>(n, s) : launch_ns<true, false, false, false>(n, s);
+  else if (p.m > 128)
+    err = by_rows ? launch_ns<false, true, false, false>(n, s) : launch_ns<false, false, false, false>(n, s);
+  else if (p.split)
+    err = by_rows ? launch_ns<false, true, true, true>(n, s) : launch_ns<false, false, true, true>(n, s);
+  else
+    err = by_rows ? launch_ns<false, true, false, true>(n, s) : launch_ns<false, false, false, true>(n, s);
   return api::cuda_status(err);
 }
