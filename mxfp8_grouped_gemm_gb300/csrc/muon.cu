@@ -260,6 +260,12 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // apart; a K = 16 step is 32 bytes).  MN-major: box h holds the 64 contraction
 // rows of operand rows 64 h .. (leading offset 8192 between them, 8-row groups
 // 1024 bytes apart; a K = 16 step is 16 rows, 2048 bytes).
+//
+// FUSED (a short side of at most 128): A is one tile, so both operands of
+// X X^T are the same 128 rows.  They are loaded once, and a stage holds 128
+// contraction elements instead of 64 of each operand.  SPLIT (at most 64):
+// the 128 rows are the high and the low parts, so one product yields all
+// pairs of parts, and A = (high, high) + (high, low) + (low, high).
 constexpr int kNsThreads = 384;
 constexpr int kNsK = 64;                  // contraction elements per stage
 constexpr int kNsRows = 128;              // rows of each operand per SM and stage
@@ -273,8 +279,12 @@ constexpr int kNsCtrl = 1024;
 constexpr int kNsSmem = 1024 + kNsStages * kNsStageBytes + 8 * kNsWarpOut + kNsCtrl;
 constexpr int kNsSym = 256;               // a symmetric matrix is stored in full within diagonal blocks of this size
 static_assert(kNsSmem <= 232448, "shared memory budget");
-constexpr int kNsALow = 2 * kNsOpBytes;   // FUSED: A's low part behind its high part (128 x 128), in the store boxes' place
-static_assert(2 * kNsALow <= 8 * kNsWarpOut, "A in two parts");
+// FUSED, in the store boxes' place: A as an operand (128 x 128; SPLIT: 64 columns
+// of its high part, then of its low part, then the two 64 x 64 fp32 blocks that
+// are added to the third)
+constexpr int kNsALow = kNsOpBytes;
+constexpr int kNsSwap = 2 * kNsOpBytes;
+static_assert(kNsSwap + 2 * 64 * 64 * 4 <= 8 * kNsWarpOut, "A and the blocks added to it");
 static_assert(32 * 33 * 4 <= kNsWarpOut, "unaligned outputs stage 32 x 32 fp32 values");
 
 // How an operand lies in memory.
@@ -568,28 +578,34 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32
   return true;
 }
 
-// FUSED: 32 rows x 64 columns of A to registers (h, low parts l) and to shared
-// memory as an operand: two boxes of 128 rows x 64 columns, 128-byte swizzle.
-// Whatever lies outside the matrix becomes zero, since it is contracted over.
-template <bool SPLIT>
-__device__ __forceinline__ void ns_keep_a(const NsArgs& P, float alpha, uint32_t taddr, uint8_t* abuf, int row, int col,
-                                          uint32_t (&h)[32], uint32_t (&l)[SPLIT ? 32 : 1]) {
+// FUSED: this lane's row of 32 rows x 64 columns of the accumulator, scaled.
+__device__ __forceinline__ void ns_read64(float alpha, uint32_t taddr, float (&v)[64]) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t r[32];
     tmem_ld_32x32b_x32(taddr + 32 * half, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int c = col + 32 * half + 2 * i;
-      const float x = row < P.m && c < P.m ? alpha * __uint_as_float(r[2 * i]) : 0.f;
-      const float y = row < P.m && c + 1 < P.m ? alpha * __uint_as_float(r[2 * i + 1]) : 0.f;
-      if constexpr (SPLIT) {
-        h[16 * half + i] = split_half2(x, y, l[16 * half + i]);
-      } else {
-        const __half2 v = __floats2half2_rn(x, y);
-        h[16 * half + i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
+    for (int i = 0; i < 32; ++i) v[32 * half + i] = alpha * __uint_as_float(r[i]);
+  }
+}
+
+// FUSED: 64 values of a row of A (columns col ..) to registers (h, low parts l)
+// and to shared memory as an operand: boxes of 64 columns, 128-byte swizzle.
+// Whatever lies outside the matrix becomes zero, since it is contracted over.
+template <bool SPLIT>
+__device__ __forceinline__ void ns_keep_a(const NsArgs& P, const float (&v)[64], uint8_t* abuf, int row, int col,
+                                          uint32_t (&h)[32], uint32_t (&l)[SPLIT ? 32 : 1]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int c = col + 2 * i;
+    const float x = row < P.m && c < P.m ? v[2 * i] : 0.f;
+    const float y = row < P.m && c + 1 < P.m ? v[2 * i + 1] : 0.f;
+    if constexpr (SPLIT) {
+      h[i] = split_half2(x, y, l[i]);
+    } else {
+      const __half2 p = __floats2half2_rn(x, y);
+      h[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
   }
   uint8_t* dst = abuf + (col >> 6) * kNsOpBytes + row * 128;
@@ -601,6 +617,15 @@ __device__ __forceinline__ void ns_keep_a(const NsArgs& P, float alpha, uint32_t
       *reinterpret_cast<uint4*>(p + kNsALow) = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
   }
   fence_proxy_async_smem();
+}
+
+// Joins the eight epilogue warps, bounded like every wait; false: some warp gave up.
+__device__ __forceinline__ bool ns_join(uint64_t* bar, uint32_t& phase, volatile int* abort, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  const bool ok = mbar_wait_bounded(bar, phase, abort, kWaitLimitNs);
+  phase ^= 1;
+  return __all_sync(0xffffffffu, ok);
 }
 
 // ROWS: the last product leaves by plain stores (rows that TMA cannot address,
@@ -621,7 +646,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   uint64_t* tempty = tfull + 2;
   uint64_t* drained = tempty + 2;
   uint64_t* a_ready = drained + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_ready + 1);
+  uint64_t* join = a_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(join + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_set = abort_flag + 1;
   uint32_t* landing = tmem_slot + 4;      // rank 1's release stores (pair)
@@ -641,6 +667,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     }
     mbar_init(drained, 1);
     mbar_init(a_ready, 8);
+    mbar_init(join, 8);
     *abort_flag = 0;
     *never_set = 0;
     fence_barrier_init();
@@ -687,25 +714,35 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const int row = (second ? tc.tj * BN : tc.ti * TM) + static_cast<int>(rank) * kNsRows;
         const int mn_stages = ns_mn_stages(second ? o.q_form : o.p_form, row);
         const CUtensorMap* map = second ? o.q : o.p;
+        const bool shared = FUSED && tc.op == NS_GRAM;
+        const int stages = shared ? (o.nk + 1) / 2 : parts * o.nk;
         if (!ns_wait_done(P, tc, abort_flag)) {
           fail();
           aborted = true;
           break;
         }
         fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
-        for (int kp = 0, kb = 0, part = 0; kp < parts * o.nk; ++kp) {
+        for (int kp = 0, kb = 0, part = 0; kp < stages; ++kp) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
             break;
           }
           uint8_t* dst = sm + stage * kNsStageBytes + (second ? kNsOpBytes : 0);
-          const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
-          if (!PAIR || rank == 0) {
-            if (!second) mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);      // all bytes of both CTAs
-            ns_load<false>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
+          if (!second && (!PAIR || rank == 0)) mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);    // all bytes of both CTAs
+          if (shared) {
+            // rows 0 .. 127, or the high and low parts of rows 0 .. 63, of the stage's first or second 64 elements
+            const int k0 = (2 * kp + second) * kNsK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = SPLIT ? 0 : 64 * h;
+              tma_load_3d(dst + h * kNsBoxBytes, map, mn_stages ? r : k0, mn_stages ? k0 : r, tc.b + (SPLIT && h ? P.batch : 0),
+                          &full[stage]);
+            }
           } else {
-            ns_load<true>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
+            const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
+            if (!PAIR || rank == 0) ns_load<false>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
+            else ns_load<true>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
           }
           if (++stage == kNsStages) {
             stage = 0;
@@ -741,7 +778,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const NsOperands o = ns_operands(P, tc);
         // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
         const int pmn = ns_mn_stages(o.p_form, tc.ti * TM), qmn = ns_mn_stages(o.q_form, tc.tj * BN);
-        for (int kp = 0, kb = 0; kp < parts * o.nk; ++kp) {
+        const bool shared = FUSED && tc.op == NS_GRAM;
+        const int stages = shared ? (o.nk + 1) / 2 : parts * o.nk;
+        for (int kp = 0, kb = 0; kp < stages; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
           if (!in) {
@@ -752,12 +791,18 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           tc_fence_after();
           // one thread issues everything: few instructions between the waits (the leading offset only matters
           // MN-major)
-          const uint64_t pd = desc0 + stage * (kNsStageBytes >> 4), qd = pd + (kNsOpBytes >> 4);
+          const uint64_t pd = desc0 + stage * (kNsStageBytes >> 4);
+          const uint64_t qd = shared ? pd : pd + (kNsOpBytes >> 4);
           const uint32_t pstep = kb < pmn ? 2048 >> 4 : 32 >> 4, qstep = kb < qmn ? 2048 >> 4 : 32 >> 4;
           const uint32_t id = idesc_f16(TM, BN) | (kb < pmn ? kIdescAMn : 0u) | (kb < qmn ? kIdescBMn : 0u);
 #pragma unroll
           for (uint32_t k = 0; k < kNsK / 16; ++k)
             mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kp | k) != 0 ? 1u : 0u);
+          if (shared) {                   // the stage's second 64 contraction elements
+            const uint64_t sd = pd + (kNsOpBytes >> 4);
+#pragma unroll
+            for (uint32_t k = 0; k < kNsK / 16; ++k) mma_bf16<CG>(d_t, sd + k * pstep, sd + k * pstep, id, 1u);
+          }
           mma_commit<CG>(&empty[stage]);
           if (++kb == o.nk) kb = 0;
           if (++stage == kNsStages) {
@@ -782,12 +827,18 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           tc_fence_after();
           const uint64_t ad = smem_desc(smem_u32(boxes), 0, 1024, kLayoutSwizzle128B);
           const uint32_t d2 = tmem + acc * BN;
-          for (int part = 0; part < parts; ++part) {
-            const uint64_t pa = ad + (part == 1 ? kNsALow >> 4 : 0), qa = ad + (SPLIT && part == 0 ? kNsALow >> 4 : 0);
+          if constexpr (SPLIT) {          // 64 x 64: (high, low), (low, high), (high, high)
+            for (int part = 0; part < 3; ++part) {
+              const uint64_t pa = ad + (part == 1 ? kNsALow >> 4 : 0), qa = ad + (part == 0 ? kNsALow >> 4 : 0);
+#pragma unroll
+              for (uint32_t k = 0; k < 4; ++k)
+                mma_bf16<CG>(d2, pa + 2 * k, qa + 2 * k, idesc_f16(TM, 64), (part | k) != 0 ? 1u : 0u);
+            }
+          } else {
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
               const uint32_t off = ((k >> 2) * kNsOpBytes + (k & 3) * 32) >> 4;
-              mma_bf16<CG>(d2, pa + off, qa + off, idesc_f16(TM, BN), (part | k) != 0 ? 1u : 0u);
+              mma_bf16<CG>(d2, ad + off, ad + off, idesc_f16(TM, BN), k != 0 ? 1u : 0u);
             }
           }
           mma_commit<CG>(&tfull[acc]);
@@ -811,7 +862,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
-    uint32_t acc = 0, acc_phase = 0, flip = 0;
+    uint32_t acc = 0, acc_phase = 0, flip = 0, join_phase = 0;
     for (int64_t t = tile0; t < total; t += tstep) {
       const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
       const bool last = tc.op == NS_APPLY && tc.step + 1 == P.steps;
@@ -829,16 +880,31 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         got = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs));
         tc_fence_after();
         if (got) {
-          ns_keep_a<SPLIT>(P, P.alpha[NS_GRAM], tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS,
-                           boxes, q * 32 + lane, hf * COLS, w, wl);
+          float v[64];
+          ns_read64(P.alpha[NS_GRAM], tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS, v);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&tempty[acc]);
-            mbar_arrive(a_ready);
-          }
+          if (lane == 0) mbar_arrive(&tempty[acc]);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
+          const int row = q * 32 + lane;
+          if constexpr (SPLIT) {
+            // (high, low) and (low, high) to the warps that hold (high, high); value c of row r at (c + r) % 64
+            float* swap = reinterpret_cast<float*>(boxes + kNsSwap) + (q < 2 ? 0 : 64 * 64) + (row & 63) * 64;
+            if ((q < 2) == (hf == 1))
+#pragma unroll
+              for (int i = 0; i < 64; ++i) swap[(i + row) & 63] = v[i];
+            got = ns_join(join, join_phase, abort_flag, lane);
+            if (got && q < 2 && hf == 0) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] += swap[(i + row) & 63] + swap[64 * 64 + ((i + row) & 63)];
+              ns_keep_a<SPLIT>(P, v, boxes, row, 0, w, wl);
+            }
+          } else {
+            ns_keep_a<SPLIT>(P, v, boxes, row, hf * COLS, w, wl);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(a_ready);
         }
       }
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
