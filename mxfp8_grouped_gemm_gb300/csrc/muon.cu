@@ -31,6 +31,7 @@
 // Sums are fp32 (tensor-core accumulators); momentum and norms are fp32/fp64.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -131,7 +132,7 @@ __device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) 
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
                                                              int32_t* __restrict__ done) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) done[blockIdx.y] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) done[blockIdx.y] = done[gridDim.y + blockIdx.y] = 0;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
   SumSq s{0.f, 0.f, 0.f};
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
@@ -301,7 +302,8 @@ struct NsArgs {
   int rows, cols, m;                      // X [rows][cols], m the short side
   int tall;                               // rows > cols
   int batch, steps;
-  int sym_tiles;                          // tiles of A (and of B) of one matrix
+  int sym_tiles;                          // tiles of A (and of B) of one matrix; FUSED: CTAs that share A's contraction
+  float* a_parts;                         // FUSED, sym_tiles > 1: their sums [batch][sym_tiles][side][side]
   int app_m, app_n;                       // row and column tiles of X
   float alpha[3], alpha_last;             // each product's factor on the accumulators
   float beta, diag;                       // POLY: + beta A + diag I
@@ -312,11 +314,13 @@ struct NsArgs {
   uint16_t* w_out;                        // nullable: w_in * w_keep - lr * value
   float w_keep, lr;
   int32_t* done;                          // [batch]: epilogue warps that have stored their part of a tile
+  int32_t* shares;                        // [batch]: FUSED, CTAs that have left their sum
   int32_t* status;
 };
 
 struct NsTile {
   int step, op, b, ti, tj;
+  int share;                              // FUSED, NS_GRAM: which part of the contraction
   int need;                               // done[b] once every earlier product of the matrix is stored
 };
 
@@ -328,7 +332,8 @@ __host__ __device__ __forceinline__ int ns_first(int ti) {
 }
 
 // Tile t of the whole run: step by step, product by product, matrix by matrix.
-// FUSED: A and B are one tile, computed together under NS_GRAM.
+// FUSED: A and B are one tile, computed together under NS_GRAM by sym_tiles
+// CTAs, of which one finishes it.
 template <bool PAIR, bool FUSED>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   constexpr int kArrive = PAIR ? 16 : 8;  // epilogue warps of a tile
@@ -342,12 +347,18 @@ __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
   const int before = l < sym_all ? 0 : l < kSyms * sym_all ? 1 : kSyms;       // products of the step
   r.op = before == kSyms ? NS_APPLY : before;
   l -= before * sym_all;
-  r.need = kArrive * (r.step * (kSyms * P.sym_tiles + app) + before * P.sym_tiles);
+  const int syms = FUSED ? 1 : P.sym_tiles;                                   // tiles that are stored
+  r.need = kArrive * (r.step * (kSyms * syms + app) + before * syms);
+  r.share = 0;
   if (r.op != NS_APPLY) {
     r.b = static_cast<int>(l / P.sym_tiles);
     int i = static_cast<int>(l - static_cast<int64_t>(r.b) * P.sym_tiles);
     const int tiles = P.tall ? P.app_n : P.app_m;      // of the short side
     r.ti = 0;
+    if (FUSED) {
+      r.share = i;
+      i = 0;
+    }
     while (i >= tiles - ns_first<PAIR>(r.ti)) {
       i -= tiles - ns_first<PAIR>(r.ti);
       ++r.ti;
@@ -380,6 +391,11 @@ __device__ __forceinline__ NsOperands ns_operands(const NsArgs& P, const NsTile&
   if (tc.op == NS_POLY) return {&P.a, &P.a, NS_SYM, NS_SYM, short_k};
   if (P.tall) return {x, &P.b, NS_K, NS_SYM, short_k};
   return {&P.b, x, NS_SYM, NS_MN, short_k};
+}
+
+// FUSED: first stage (of 128 contraction elements) of a share of A.
+__device__ __forceinline__ int ns_share_begin(const NsArgs& P, const NsOperands& o, int share) {
+  return (o.nk + 1) / 2 * share / P.sym_tiles;
 }
 
 // Waits until the products before tile tc of its matrix are in memory.
@@ -650,6 +666,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(join + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_set = abort_flag + 1;
+  volatile int* finishes = abort_flag + 2;          // FUSED: this CTA has the whole A
   uint32_t* landing = tmem_slot + 4;      // rank 1's release stores (pair)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -670,6 +687,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
     mbar_init(join, 8);
     *abort_flag = 0;
     *never_set = 0;
+    *finishes = 1;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -715,14 +733,15 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const int mn_stages = ns_mn_stages(second ? o.q_form : o.p_form, row);
         const CUtensorMap* map = second ? o.q : o.p;
         const bool shared = FUSED && tc.op == NS_GRAM;
-        const int stages = shared ? (o.nk + 1) / 2 : parts * o.nk;
+        const int first = shared ? ns_share_begin(P, o, tc.share) : 0;
+        const int stages = shared ? ns_share_begin(P, o, tc.share + 1) : parts * o.nk;
         if (!ns_wait_done(P, tc, abort_flag)) {
           fail();
           aborted = true;
           break;
         }
         fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
-        for (int kp = 0, kb = 0, part = 0; kp < stages; ++kp) {
+        for (int kp = first, kb = 0, part = 0; kp < stages; ++kp) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
@@ -779,8 +798,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
         const int pmn = ns_mn_stages(o.p_form, tc.ti * TM), qmn = ns_mn_stages(o.q_form, tc.tj * BN);
         const bool shared = FUSED && tc.op == NS_GRAM;
-        const int stages = shared ? (o.nk + 1) / 2 : parts * o.nk;
-        for (int kp = 0, kb = 0; kp < stages; ++kp) {
+        const int first = shared ? ns_share_begin(P, o, tc.share) : 0;
+        const int stages = shared ? ns_share_begin(P, o, tc.share + 1) : parts * o.nk;
+        for (int kp = first, kb = 0; kp < stages; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
           if (!in) {
@@ -797,7 +817,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           const uint32_t id = idesc_f16(TM, BN) | (kb < pmn ? kIdescAMn : 0u) | (kb < qmn ? kIdescBMn : 0u);
 #pragma unroll
           for (uint32_t k = 0; k < kNsK / 16; ++k)
-            mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, (kp | k) != 0 ? 1u : 0u);
+            mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, kp != first || k != 0 ? 1u : 0u);
           if (shared) {                   // the stage's second 64 contraction elements
             const uint64_t sd = pd + (kNsOpBytes >> 4);
 #pragma unroll
@@ -818,12 +838,16 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         if (acc == 0) acc_phase ^= 1;
         if (FUSED && tc.op == NS_GRAM) {
           // A A^T from the A that the epilogue has put into shared memory, into the other accumulator
-          if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs) ||
-              !mbar_wait_bounded(a_ready, a_phase, abort_flag, kWaitLimitNs)) {
+          if (!mbar_wait_bounded(a_ready, a_phase, abort_flag, kWaitLimitNs)) {
             fail();
             break;
           }
           a_phase ^= 1;
+          if (*finishes == 0) continue;   // another CTA finishes this A
+          if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)) {
+            fail();
+            break;
+          }
           tc_fence_after();
           const uint64_t ad = smem_desc(smem_u32(boxes), 0, 1024, kLayoutSwizzle128B);
           const uint32_t d2 = tmem + acc * BN;
@@ -876,6 +900,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         got = __all_sync(0xffffffffu, got);
       }
       uint32_t w[32], wl[SPLIT ? 32 : 1];
+      bool mine = true;                   // this CTA finishes the tile
       if (FUSED && tc.op == NS_GRAM) {
         got = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs));
         tc_fence_after();
@@ -887,29 +912,94 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           if (lane == 0) mbar_arrive(&tempty[acc]);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
-          const int row = q * 32 + lane;
+          const int row = q * 32 + lane, ca = SPLIT ? 0 : hf * COLS;
+          const bool holds = !SPLIT || (q < 2 && hf == 0);      // this warp's values are A's
           if constexpr (SPLIT) {
-            // (high, low) and (low, high) to the warps that hold (high, high); value c of row r at (c + r) % 64
-            float* swap = reinterpret_cast<float*>(boxes + kNsSwap) + (q < 2 ? 0 : 64 * 64) + (row & 63) * 64;
+            // (high, low) and (low, high) to the warps that hold (high, high); 16-byte piece j of row r at
+            // j ^ (r % 16), free of bank conflicts
+            float4* swap = reinterpret_cast<float4*>(boxes + kNsSwap) + (q < 2 ? 0 : 64 * 16) + (row & 63) * 16;
+            const int sw = row & 15;
             if ((q < 2) == (hf == 1))
 #pragma unroll
-              for (int i = 0; i < 64; ++i) swap[(i + row) & 63] = v[i];
+              for (int j = 0; j < 16; ++j)
+                if (4 * j < P.m) swap[j ^ sw] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             got = ns_join(join, join_phase, abort_flag, lane);
-            if (got && q < 2 && hf == 0) {
+            if (got && holds)
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] += swap[(i + row) & 63] + swap[64 * 64 + ((i + row) & 63)];
-              ns_keep_a<SPLIT>(P, v, boxes, row, 0, w, wl);
-            }
-          } else {
-            ns_keep_a<SPLIT>(P, v, boxes, row, hf * COLS, w, wl);
+              for (int j = 0; j < 16; ++j)
+                if (4 * j < P.m) {
+                  const float4 x = swap[j ^ sw], y = swap[64 * 16 + (j ^ sw)];
+                  v[4 * j] += x.x + y.x;
+                  v[4 * j + 1] += x.y + y.y;
+                  v[4 * j + 2] += x.z + y.z;
+                  v[4 * j + 3] += x.w + y.w;
+                }
           }
+          if (P.sym_tiles > 1 && got) {
+            // A share of the sum; the CTA that leaves the last one adds them up in order.  128 x 128: column by
+            // column, 32 rows side by side; SPLIT: row by row, only the few columns inside the matrix (measured,
+            // five steps: 2 x 8000 x 100 by columns 125 us, by rows 139; 15 x 1894 x 15 126 and 106).
+            constexpr int SIDE = SPLIT ? 64 : 128;
+            float* base = P.a_parts + static_cast<int64_t>(tc.b) * P.sym_tiles * SIDE * SIDE +
+                          (SPLIT ? row * SIDE : ca * SIDE + row);
+            const int live = holds && row < P.m ? P.m : 0;             // SPLIT: columns
+            float* dst = base + tc.share * SIDE * SIDE;
+            if constexpr (SPLIT) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (8 * j < live) st_global_v8(dst + 8 * j, reinterpret_cast<const uint32_t*>(v) + 8 * j);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) dst[i * SIDE] = v[i];
+            }
+            __threadfence();
+            got = ns_join(join, join_phase, abort_flag, lane);
+            if (got && warp == 4 && lane == 0)
+              *finishes = (atomicAdd(P.shares + tc.b, 1) + 1) % P.sym_tiles == 0;
+            got = got && ns_join(join, join_phase, abort_flag, lane);
+            mine = got && *finishes != 0;
+            if (mine && holds) {
+              __threadfence();
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] = 0.f;
+#pragma unroll
+              for (int c0 = 0; c0 < 64; c0 += 32) {    // 32 columns of two shares requested together
+                if (SPLIT && c0 >= live) continue;
+                for (int k = 0; k < P.sym_tiles; k += 2) {
+                  const float* src = base + k * SIDE * SIDE + c0 * (SPLIT ? 1 : SIDE);
+                  const float* nxt = k + 1 < P.sym_tiles ? src + SIDE * SIDE : src;
+                  uint32_t x[32], y[32];
+                  if constexpr (SPLIT) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                      const int c = c0 + j < live ? j : 0;             // columns past the matrix repeat the first ones
+                      ld_global_cg_v8(src + c, x + j);
+                      ld_global_cg_v8(nxt + c, y + j);
+                    }
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                      x[i] = __float_as_uint(__ldcg(src + i * SIDE));
+                      y[i] = __float_as_uint(__ldcg(nxt + i * SIDE));
+                    }
+                  }
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    v[c0 + i] += __uint_as_float(x[i]);
+                    if (k + 1 < P.sym_tiles) v[c0 + i] += __uint_as_float(y[i]);
+                  }
+                }
+              }
+            }
+          }
+          if (mine && got && holds) ns_keep_a<SPLIT>(P, v, boxes, row, ca, w, wl);
           __syncwarp();
           if (lane == 0) mbar_arrive(a_ready);
         }
       }
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
 #pragma unroll 1
-      for (int c = 0; c < BOXES && got; ++c) {
+      for (int c = 0; c < BOXES && got && mine; ++c) {
         const int col = col0 + 64 * c;
         const bool any = row0 < dm && col < dn;
         auto ready = [&]() {              // before the first columns: the accumulator is complete
@@ -957,6 +1047,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         if (lane == 0) fail();
         break;
       }
+      if (!mine) continue;                // another CTA finishes this A
       if (!last) {
         __syncwarp();                     // plain stores: the warp's, before the release below
         if (lane == 0) {
@@ -1019,9 +1110,12 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
   a.app_m = (a.rows + W - 1) / W;
   a.app_n = (a.cols + W - 1) / W;
   const int t = a.tall ? a.app_n : a.app_m;
-  a.sym_tiles = 0;
-  for (int i = 0; i < t; ++i) a.sym_tiles += t - ns_first<PAIR>(i);
-  const int64_t most = static_cast<int64_t>(a.app_m) * a.app_n * a.batch;     // of any product
+  if (!FUSED) {
+    a.sym_tiles = 0;
+    for (int i = 0; i < t; ++i) a.sym_tiles += t - ns_first<PAIR>(i);
+  }
+  // the largest product's tiles: X's, unless A's contraction is shared out
+  const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.app_m * a.app_n, FUSED ? a.sym_tiles : 0);
   const int64_t units = ns_resident<PAIR, ROWS, SPLIT, FUSED>();
   if (units <= 0) return cudaErrorCooperativeLaunchTooLarge;
   const int64_t n = most < units ? most : units;
@@ -1047,9 +1141,10 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
 struct NsPlan {
   int m, n, tall;                         // short and long side; tall: the matrix is [n][m]
   int split;
+  int shares;                             // CTAs that share the contraction of a single-tile A
   int64_t ldx, lda;                       // row lengths of X and of A and B, padded to 16
   int chunks;                             // partial sums of squares per matrix
-  int64_t part, done, x0, x1, a, b, bytes;
+  int64_t part, done, x0, x1, a, b, a_parts, bytes;
 };
 
 // A short side up to this is computed in two fp16 parts (high and low, three
@@ -1058,6 +1153,25 @@ struct NsPlan {
 // (its own rounding alone is 1.66e-3): one part 3.1e-3 at 8 x 8, 2.4e-3 at
 // 16 x 2000, 2.2e-3 from 64 x 64 to 256 x 256; two parts 1.67e-3.
 constexpr int kNsSplitMost = 64;          // not above 128: only single tiles of A split
+
+// CTAs that share the contraction n of a single-tile A while SMs are idle: a
+// stage of 128 elements takes about 550 cycles; leaving and joining the sums
+// about 3500 and, per CTA, what it takes to read 64 x 64 (split) or 128 x 128
+// fp32 values.
+int ns_shares(int batch, int m, int n, int split) {
+  if (m > 128) return 1;
+  const int stages = (n + 2 * kNsK - 1) / (2 * kNsK);
+  const int most = std::min(std::min(device_sms() / batch, stages), 16);
+  int best = 1, best_cost = stages * 550;
+  for (int s = 2; s <= most; ++s) {
+    const int cost = (stages + s - 1) / s * 550 + 3500 + s * (split ? 400 : 1300);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
 
 NsPlan ns_plan(int batch, int rows, int cols) {
   NsPlan p{};
@@ -1073,13 +1187,15 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   api::Carver w;
   p.split = p.m <= kNsSplitMost;
   p.part = w.take(8ll * batch * p.chunks);
-  p.done = w.take(4ll * batch);
+  p.shares = ns_shares(batch, p.m, p.n, p.split);
+  p.done = w.take(8ll * batch);           // and the shares' counters
   const int64_t one = p.split ? 4 : 2;    // bytes of an element
   const int64_t xb = one * batch * rows * p.ldx, ab = one * batch * p.m * p.lda;
   p.x0 = w.take(xb);
   p.x1 = w.take(xb);
   p.a = w.take(ab);
   p.b = w.take(ab);
+  p.a_parts = w.take(p.shares > 1 ? (p.split ? 4ll * 64 * 64 : 4ll * 128 * 128) * batch * p.shares : 0);
   p.bytes = w.off;
   return p;
 }
@@ -1172,6 +1288,9 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
   n.lr = a->lr;
   n.done = done;
+  n.shares = done + a->batch;
+  n.sym_tiles = p.shares;
+  n.a_parts = api::at<float>(a->workspace, p.a_parts);
   n.status = a->dev_status;
   const int64_t mats = static_cast<int64_t>(a->batch) * (p.split ? 2 : 1);
   bool ok = true;
