@@ -198,6 +198,8 @@ def _check(fn: str, code: int):
 def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor") -> int | None:
     if t is None:
         return None
+    if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if not t.is_contiguous():
@@ -210,7 +212,7 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor") -> int | None
 def _stream(stream) -> int | None:
     if stream is None:
         # the handle itself: building a Stream object costs more than a kernel launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
