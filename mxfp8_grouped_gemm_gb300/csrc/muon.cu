@@ -37,94 +37,12 @@
 #include <cmath>
 
 #include "api_common.h"
-#include "common.cuh"
 #include "kernels.h"
+#include "muon.cuh"
 #include "ptx.cuh"
 
 namespace mxg {
 namespace {
-
-constexpr int kExpA = 12;                 // A and B are stored times 2^12
-
-// ------------------------------------------------------------------ momentum
-// Sum of squares that neither overflows nor underflows for any fp32 input:
-// magnitudes below 2^-30 and from 2^46 are squared after scaling by a power of
-// two (NaN compares false and stays in the middle sum).
-struct SumSq {
-  float lo, mid, hi;
-  __device__ __forceinline__ void add(float v) {
-    const float m = fabsf(v);
-    if (m < 9.31322574615478515625e-10f) {             // 2^-30
-      const float t = v * 18446744073709551616.f;      // 2^64
-      lo = fmaf(t, t, lo);
-    } else if (m >= 70368744177664.f) {                // 2^46
-      const float t = v * 8.271806125530276749e-25f;   // 2^-80
-      hi = fmaf(t, t, hi);
-    } else {
-      mid = fmaf(v, v, mid);
-    }
-  }
-  __device__ __forceinline__ double total() const {
-    return static_cast<double>(lo) * 2.938735877055718770e-39 + static_cast<double>(mid) +
-           static_cast<double>(hi) * 1.461501637330902918e48;   // 2^-128, 2^160
-  }
-};
-
-constexpr int kMoThreads = 256;
-constexpr int kMoVec = 8;                 // elements a thread takes at once
-
-struct MomentumArgs {
-  const void* grad;                       // bf16 or fp32 [batch][rows][cols]
-  int grad_f32;
-  const float* mom_in;                    // nullable
-  float* mom_out;                         // nullable
-  float mu;
-  int nesterov;
-  int64_t per;                            // elements of a matrix
-};
-
-template <bool VEC>
-__device__ __forceinline__ void load_f32(const float* p, int64_t i, int n, float (&v)[kMoVec]) {
-  if constexpr (VEC) {
-    uint32_t w[8];
-    ld_global_v8(p + i, w);
-#pragma unroll
-    for (int j = 0; j < kMoVec; ++j) v[j] = __uint_as_float(w[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kMoVec; ++j) v[j] = j < n ? p[i + j] : 0.f;
-  }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void load_grad(const MomentumArgs& P, int64_t i, int n, float (&v)[kMoVec]) {
-  if (P.grad_f32) {
-    load_f32<VEC>(static_cast<const float*>(P.grad), i, n, v);
-  } else {
-    const uint16_t* g = static_cast<const uint16_t*>(P.grad) + i;
-    if constexpr (VEC) {
-      const uint4 q = *reinterpret_cast<const uint4*>(g);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) v[j] = j < n ? bf16_bits_to_float(g[j]) : 0.f;
-    }
-  }
-}
-
-// Two values as fp16 (returned) and what the rounding left, as fp16 too.
-__device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // New momentum and the sum of squares of u: one partial per block; the
 // products' counters are cleared.  VEC: every matrix starts on a 32-byte
@@ -138,30 +56,9 @@ __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, in
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
        i += static_cast<int64_t>(chunks) * kMoThreads * kMoVec) {
     const int n = static_cast<int>(P.per - i < kMoVec ? P.per - i : kMoVec);
-    float g[kMoVec], m[kMoVec];
-    load_grad<VEC>(P, base + i, n, g);
-    if (P.mom_in != nullptr) {
-      load_f32<VEC>(P.mom_in, base + i, n, m);
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) m[j] = fmaf(P.mu, m[j], g[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) m[j] = g[j];
-    }
-    if (P.mom_out != nullptr) {
-      if constexpr (VEC) {
-        st_global_v8(P.mom_out + base + i, reinterpret_cast<const uint32_t*>(m));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kMoVec; ++j)
-          if (j < n) P.mom_out[base + i + j] = m[j];
-      }
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) s.add(P.nesterov ? fmaf(P.mu, m[j], g[j]) : m[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) s.add(g[j]);
-    }
+    float u[kMoVec];
+    step_momentum<VEC>(P, base + i, n, u);
+    s.add8(u);
   }
   double t = s.total();
 #pragma unroll
@@ -195,20 +92,9 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
   if (threadIdx.x == 0) {
     n2 = 0.0;
     for (int i = 0; i < kMoThreads / 32; ++i) n2 += s_w[i];
-    // u / |u| 2^ex as three factors, so no intermediate leaves fp32's range
-    const double norm = sqrt(n2);
-    if (norm == 0.0) {
-      s_f[0] = s_f[1] = s_f[2] = 0.f;
-    } else if (isfinite(norm)) {
-      const int e = ilogb(norm);
-      const int h = (ex - e) / 2;
-      s_f[0] = scalbnf(1.f, h);
-      s_f[1] = scalbnf(1.f, ex - e - h);
-      s_f[2] = static_cast<float>(1.0 / scalbn(norm, -e));
-    } else {
-      s_f[0] = s_f[1] = 1.f;
-      s_f[2] = static_cast<float>(1.0 / norm);
-    }
+    float f[3];
+    norm_factors(n2, ex, f);
+    for (int i = 0; i < 3; ++i) s_f[i] = f[i];
   }
   __syncthreads();
   const float f0 = s_f[0], f1 = s_f[1], f2 = s_f[2];
@@ -221,13 +107,7 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
     const int n = min(kMoVec, cols - c);
     const int64_t i = b * P.per + r * cols + c;
     float u[kMoVec];
-    if (P.mom_out == nullptr || P.nesterov) load_grad<VEC>(P, i, n, u);
-    if (P.mom_out != nullptr) {
-      float m[kMoVec];
-      load_f32<VEC>(P.mom_out, i, n, m);
-#pragma unroll
-      for (int j = 0; j < kMoVec; ++j) u[j] = P.nesterov ? fmaf(P.mu, m[j], u[j]) : m[j];
-    }
+    momentum_u<VEC>(P, i, n, u);
     uint32_t h[kMoVec / 2], l[kMoVec / 2];
 #pragma unroll
     for (int j = 0; j < kMoVec / 2; ++j) h[j] = split_half2(u[2 * j] * f0 * f1 * f2, u[2 * j + 1] * f0 * f1 * f2, l[j]);
@@ -1236,16 +1116,43 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   if (a->workspace_bytes < static_cast<uint64_t>(p.bytes)) return MXG_ERR_WORKSPACE;
   api::NvtxRange nvtx("mxg.muon_update");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int ex = 0;                             // 2^ex ~ sqrt(n)
+  while ((1ll << (2 * ex)) < p.n) ++ex;
+  // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex);  B 2^12 = a 2^12 I + b (A 2^12) + c 2^-12 (A 2^12)(A 2^12);
+  // X' 2^ex = 2^-12 (B 2^12)(X 2^ex), the last one scale X'
+  const float alpha[3] = {static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex)),
+                          static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA)),
+                          static_cast<float>(std::ldexp(1.0, -kExpA))};
+  const float alpha_last = static_cast<float>(std::ldexp(static_cast<double>(a->scale), -kExpA - ex));
+  const float diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
+  const float w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
+  const int64_t per = static_cast<int64_t>(a->rows) * a->cols;
+  const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
+  if (p.m <= 128 && p.n <= kResidentMost) {
+    ResidentArgs r{};
+    r.mo = mo;
+    r.batch = a->batch;
+    r.rows = a->rows;
+    r.cols = a->cols;
+    r.steps = a->steps;
+    r.ex = ex;
+    for (int i = 0; i < 3; ++i) r.alpha[i] = alpha[i];
+    r.alpha_last = alpha_last;
+    r.beta = a->b;
+    r.diag = diag;
+    r.update = a->update;
+    r.w_in = a->w_in;
+    r.w_out = a->w_out;
+    r.w_keep = w_keep;
+    r.lr = a->lr;
+    r.status = a->dev_status;
+    return api::cuda_status(launch_muon_resident(r, p.split, s));
+  }
   double* part = api::at<double>(a->workspace, p.part);
   int32_t* done = api::at<int32_t>(a->workspace, p.done);
   __half* x[2] = {api::at<__half>(a->workspace, p.x0), api::at<__half>(a->workspace, p.x1)};
   __half* am = api::at<__half>(a->workspace, p.a);
   __half* bm = api::at<__half>(a->workspace, p.b);
-  int ex = 0;                             // 2^ex ~ sqrt(n)
-  while ((1ll << (2 * ex)) < p.n) ++ex;
-
-  const int64_t per = static_cast<int64_t>(a->rows) * a->cols;
-  const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
   const unsigned nb = static_cast<unsigned>(a->batch);
   // 32-byte loads where every matrix (and, for the cast, every row) starts on 32 bytes of each buffer
   const dim3 mgrid(static_cast<unsigned>(p.chunks), nb);
@@ -1266,14 +1173,10 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.tall = p.tall;
   n.batch = a->batch;
   n.steps = a->steps;
-  // A 2^12 = (X 2^ex)(X 2^ex)^T 2^(12 - 2 ex);  B 2^12 = a 2^12 I + b (A 2^12) + c 2^-12 (A 2^12)(A 2^12);
-  // X' 2^ex = 2^-12 (B 2^12)(X 2^ex), the last one scale X'
-  n.alpha[NS_GRAM] = static_cast<float>(std::ldexp(1.0, kExpA - 2 * ex));
-  n.alpha[NS_POLY] = static_cast<float>(std::ldexp(static_cast<double>(a->c), -kExpA));
-  n.alpha[NS_APPLY] = static_cast<float>(std::ldexp(1.0, -kExpA));
-  n.alpha_last = static_cast<float>(std::ldexp(static_cast<double>(a->scale), -kExpA - ex));
+  for (int i = 0; i < 3; ++i) n.alpha[i] = alpha[i];
+  n.alpha_last = alpha_last;
   n.beta = a->b;
-  n.diag = static_cast<float>(std::ldexp(static_cast<double>(a->a), kExpA));
+  n.diag = diag;
   n.xp[0] = reinterpret_cast<uint16_t*>(x[0]);
   n.xp[1] = reinterpret_cast<uint16_t*>(x[1]);
   n.ap = reinterpret_cast<uint16_t*>(am);
@@ -1285,7 +1188,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.update = a->update;
   n.w_in = a->w_in;
   n.w_out = a->w_out;
-  n.w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
+  n.w_keep = w_keep;
   n.lr = a->lr;
   n.done = done;
   n.shares = done + a->batch;
