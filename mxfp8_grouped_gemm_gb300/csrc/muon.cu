@@ -1128,7 +1128,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   const float w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
   const int64_t per = static_cast<int64_t>(a->rows) * a->cols;
   const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
-  if (p.m <= 128 && p.n <= kResidentMost) {
+  if (const int cluster = resident_cluster(a->batch, p.m, p.n, p.split)) {
     ResidentArgs r{};
     r.mo = mo;
     r.batch = a->batch;
@@ -1146,7 +1146,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
     r.w_keep = w_keep;
     r.lr = a->lr;
     r.status = a->dev_status;
-    return api::cuda_status(launch_muon_resident(r, p.split, s));
+    return api::cuda_status(launch_muon_resident(r, cluster, p.split, s));
   }
   double* part = api::at<double>(a->workspace, p.part);
   int32_t* done = api::at<int32_t>(a->workspace, p.done);

@@ -182,6 +182,8 @@ struct ResidentArgs {
   // set by the launcher
   int m, n, tall, slice;                  // short and long side; columns of the long side per CTA
 };
-cudaError_t launch_muon_resident(ResidentArgs a, bool split, cudaStream_t s);
+// CTAs that should take a matrix (short side m, long side n), 0: the tiled kernel is faster, or it does not fit.
+int resident_cluster(int batch, int m, int n, bool split);
+cudaError_t launch_muon_resident(ResidentArgs a, int cluster, bool split, cudaStream_t s);
 
 }  // namespace mxg

@@ -575,12 +575,28 @@ cudaError_t launch(const ResidentArgs& a, int C, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_muon_resident(ResidentArgs a, bool split, cudaStream_t s) {
+// Measured (five steps, us): more CTAs per matrix than its size needs pay off
+// while SMs are idle, 1 x 64 x 512 64 (one CTA) 50 (two) 38 (eight), 2 x 128 x
+// 1024 80 (two) 54 (eight), except up to 256 columns of more than 64 rows: 4 x
+// 128 x 256 41 (one) 46 (four), where the 128 x 128 sums cost more than they
+// spare.  Those sums also make clusters that need several turns slower than
+// the tiled kernel: 16 x 100 x 3000 183 against 139, 64 x 128 x 4096 499
+// against 405; 64 x 64 x 2048 is 152 against 243.
+int resident_cluster(int batch, int m, int n, bool split) {
+  if (m > 128 || n > kResidentMost) return 0;
+  const int sms = device_sms();
+  int C = 1;
+  while (C * kRsSlice < n) C *= 2;
+  if (!split && C > 1 && 2 * batch * C > sms) return 0;
+  if (split || n > 256)
+    while (C < kRsCluster && C * 64 < n && 2 * batch * C <= sms) C *= 2;
+  return C;
+}
+
+cudaError_t launch_muon_resident(ResidentArgs a, int C, bool split, cudaStream_t s) {
   a.tall = a.rows > a.cols;
   a.m = a.tall ? a.cols : a.rows;
   a.n = a.tall ? a.rows : a.cols;
-  int C = 1;
-  while (C * kRsSlice < a.n) C *= 2;
   a.slice = ((a.n + C - 1) / C + 63) / 64 * 64;
   return split ? launch<true>(a, C, s) : launch<false>(a, C, s);
 }
