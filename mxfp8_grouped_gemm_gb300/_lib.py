@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -288,6 +289,39 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+class _ScratchCache(threading.local):
+    """Small scratch kept per thread, device and stream: making and dropping a tensor takes longer than a launch.
+    Calls of one thread on one stream follow one another, so they can share it."""
+    BYTES = 1 << 20
+
+    def __init__(self):
+        self.kept = {}
+
+    def get(self, device, handle):
+        key = (device.index, handle)
+        t = self.kept.get(key)
+        if t is None:
+            t = self.kept[key] = torch.empty(self.BYTES, dtype=torch.uint8, device=device)
+        return t
+
+
+_scratch_cache = _ScratchCache()
+
+
+def _call_with_scratch(name: str, call, bytes_of, workspace, device, stream):
+    """call(pointer, bytes, stream handle) -> status, with the caller's workspace, the kept scratch, or, where that is
+    too small, the stream is not the current one or a graph is being captured, memory of its own."""
+    handle = _stream(stream)
+    if workspace is None and stream is None and not torch.cuda.is_current_stream_capturing():
+        t = _scratch_cache.get(device, handle)
+        status = call(t.data_ptr(), _ScratchCache.BYTES, handle)
+        if status != 5:                                # MXG_ERR_WORKSPACE: nothing was launched
+            return _check(name, status)
+    if workspace is None:
+        workspace = _empty(max(bytes_of(), 32), torch.uint8, device, stream)
+    _check(name, call(_ptr(workspace, None, "workspace"), workspace.numel(), handle))
+
+
 def _shape(t: torch.Tensor | None, shape: tuple, name: str):
     if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
@@ -321,13 +355,13 @@ def mxg_balance_loss_fwd(logits, ids, coef: float, dev_status, token_mask=None, 
     _shape(counts, (E,), "counts")
     _shape(prob_sums, (E,), "prob_sums")
     _shape(n_tokens, (1,), "n_tokens")
-    if workspace is None:
-        workspace = _empty(max(mxg_balance_loss_workspace_bytes(T, E), 32), torch.uint8, dev, stream)
-    _check("mxg_balance_loss_fwd", lib().mxg_balance_loss_fwd(
-        _ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _mask_ptr(token_mask, T), T, E, k, coef,
-        _ptr(loss, torch.float32, "loss"), _ptr(counts, torch.int32, "counts"),
-        _ptr(prob_sums, torch.float32, "prob_sums"), _ptr(n_tokens, torch.int32, "n_tokens"), _ptr(workspace),
-        workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    args = (_ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _mask_ptr(token_mask, T), T, E, k, coef,
+            _ptr(loss, torch.float32, "loss"), _ptr(counts, torch.int32, "counts"),
+            _ptr(prob_sums, torch.float32, "prob_sums"), _ptr(n_tokens, torch.int32, "n_tokens"))
+    status = _ptr(dev_status, torch.int32, "dev_status")
+    _call_with_scratch("mxg_balance_loss_fwd",
+                       lambda ws, n, s: lib().mxg_balance_loss_fwd(*args, ws, n, status, s),
+                       lambda: mxg_balance_loss_workspace_bytes(T, E), workspace, dev, stream)
     return loss, counts, prob_sums, n_tokens
 
 
@@ -370,13 +404,13 @@ def mxg_router_linear_bwd(x, w_router, dlogits, dx_in, dev_status, dx=None, dw_r
     _shape(dx_in, (T, H), "dx_in")
     _shape(dx, (T, H), "dx")
     _shape(dw_router, (E, H), "dw_router")
-    if workspace is None:
-        workspace = _empty(max(mxg_router_linear_bwd_workspace_bytes(T, H, E), 32), torch.uint8, dev, stream)
-    _check("mxg_router_linear_bwd", lib().mxg_router_linear_bwd(
-        _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.bfloat16, "w_router"),
-        _ptr(dlogits, torch.float32, "dlogits"), _ptr(dx_in, torch.bfloat16, "dx_in"), T, H, E,
-        _ptr(dx, torch.bfloat16, "dx"), _ptr(dw_router, torch.float32, "dw_router"), _ptr(workspace),
-        workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    args = (_ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.bfloat16, "w_router"),
+            _ptr(dlogits, torch.float32, "dlogits"), _ptr(dx_in, torch.bfloat16, "dx_in"), T, H, E,
+            _ptr(dx, torch.bfloat16, "dx"), _ptr(dw_router, torch.float32, "dw_router"))
+    status = _ptr(dev_status, torch.int32, "dev_status")
+    _call_with_scratch("mxg_router_linear_bwd",
+                       lambda ws, n, s: lib().mxg_router_linear_bwd(*args, ws, n, status, s),
+                       lambda: mxg_router_linear_bwd_workspace_bytes(T, H, E), workspace, dev, stream)
     return dx, dw_router
 
 
@@ -411,8 +445,6 @@ def mxg_muon_update(grad, dev_status, momentum=None, momentum_out=None, mu: floa
     for name, t in (("momentum", momentum), ("momentum_out", momentum_out), ("update", update), ("weights", weights),
                     ("weights_out", weights_out)):
         _shape(t, shape, name)
-    if workspace is None:
-        workspace = _empty(max(mxg_muon_workspace_bytes(batch, rows, cols), 32), torch.uint8, dev, stream)
     a, b, c = coefficients
     args = MuonArgs(batch=batch, rows=rows, cols=cols, grad_f32=int(grad.dtype == torch.float32),
                     grad=_ptr(grad, None, "grad"), momentum_in=_ptr(momentum, torch.float32, "momentum"),
@@ -420,9 +452,14 @@ def mxg_muon_update(grad, dev_status, momentum=None, momentum_out=None, mu: floa
                     steps=steps, a=a, b=b, c=c, scale=scale, update=_ptr(update, torch.bfloat16, "update"),
                     w_in=_ptr(weights, torch.bfloat16, "weights"),
                     w_out=_ptr(weights_out, torch.bfloat16, "weights_out"), lr=lr, weight_decay=weight_decay,
-                    workspace=_ptr(workspace), workspace_bytes=workspace.numel(),
                     dev_status=_ptr(dev_status, torch.int32, "dev_status"))
-    _check("mxg_muon_update", lib().mxg_muon_update(ctypes.byref(args), _stream(stream)))
+
+    def call(ws, n, s):
+        args.workspace, args.workspace_bytes = ws, n
+        return lib().mxg_muon_update(ctypes.byref(args), s)
+
+    _call_with_scratch("mxg_muon_update", call, lambda: mxg_muon_workspace_bytes(batch, rows, cols), workspace, dev,
+                       stream)
     return update if weights is None else weights_out
 
 

@@ -1021,6 +1021,7 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
 struct NsPlan {
   int m, n, tall;                         // short and long side; tall: the matrix is [n][m]
   int split;
+  int cluster;                            // CTAs per matrix that stays on the chip, 0: tiled
   int shares;                             // CTAs that share the contraction of a single-tile A
   int64_t ldx, lda;                       // row lengths of X and of A and B, padded to 16
   int chunks;                             // partial sums of squares per matrix
@@ -1066,6 +1067,11 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   p.chunks = static_cast<int>(c < most ? c : most);
   api::Carver w;
   p.split = p.m <= kNsSplitMost;
+  p.cluster = resident_cluster(batch, p.m, p.n, p.split);
+  if (p.cluster != 0) {                   // nothing of it leaves the chip
+    p.bytes = api::kAlign;
+    return p;
+  }
   p.part = w.take(8ll * batch * p.chunks);
   p.shares = ns_shares(batch, p.m, p.n, p.split);
   p.done = w.take(8ll * batch);           // and the shares' counters
@@ -1128,7 +1134,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   const float w_keep = static_cast<float>(1.0 - static_cast<double>(a->lr) * a->weight_decay);
   const int64_t per = static_cast<int64_t>(a->rows) * a->cols;
   const MomentumArgs mo{a->grad, a->grad_f32, a->momentum_in, a->momentum_out, a->mu, a->nesterov, per};
-  if (const int cluster = resident_cluster(a->batch, p.m, p.n, p.split)) {
+  if (p.cluster != 0) {
     ResidentArgs r{};
     r.mo = mo;
     r.batch = a->batch;
@@ -1146,7 +1152,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
     r.w_keep = w_keep;
     r.lr = a->lr;
     r.status = a->dev_status;
-    return api::cuda_status(launch_muon_resident(r, cluster, p.split, s));
+    return api::cuda_status(launch_muon_resident(r, p.cluster, p.split, s));
   }
   double* part = api::at<double>(a->workspace, p.part);
   int32_t* done = api::at<int32_t>(a->workspace, p.done);
