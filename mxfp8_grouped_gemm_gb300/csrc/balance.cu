@@ -198,53 +198,69 @@ __global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
     }
   }
   if (gridDim.x > 1) {
-    if (threadIdx.x == 0) part_tokens[blockIdx.x] = s_tok;
+    if (threadIdx.x == 0) {
+      part_tokens[blockIdx.x] = s_tok;
+      if (blockIdx.x == 0) part_tokens[kBlMaxBlocks] = 0;      // the finish's ticket
+    }
     return;
   }
   __syncthreads();
   balance_finish(s_sum[0], s_cnt, s_tok, s_term, E, k, coef, loss, counts, prob_sums, n_tokens);
 }
 
-// The partials: 1024 / W threads share an expert (W: E rounded up to a power of
-// two, at least 32), each adding every (1024 / W)-th block in order, then their
-// sums in order.
+// The partials, 32 experts a block: 32 threads share an expert, each adding
+// every 32nd block in order, then their sums in order.  The block that is last
+// to have its experts' sums in memory (ticket, zero before) takes the loss.
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const float* __restrict__ part,
                                                              const int32_t* __restrict__ part_counts,
                                                              const int32_t* __restrict__ part_tokens, int nblk, int E,
-                                                             int W, int k, float coef, float* __restrict__ loss,
-                                                             int32_t* __restrict__ counts,
+                                                             int k, float coef, int32_t* __restrict__ ticket,
+                                                             float* __restrict__ loss, int32_t* __restrict__ counts,
                                                              float* __restrict__ prob_sums,
                                                              int32_t* __restrict__ n_tokens) {
   __shared__ float s_sum[1024];
   __shared__ int s_cnt[1024];
   __shared__ float s_term[8];
-  __shared__ int s_n;
+  __shared__ int s_n, s_last;
   if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
   dependency_wait();
-  const int e = threadIdx.x % W, r = threadIdx.x / W, R = 1024 / W;
+  const int el = threadIdx.x & 31, e = blockIdx.x * 32 + el, r = threadIdx.x >> 5;
   float s = 0.f;
   int c = 0;
   if (e < E) {
-#pragma unroll 8
-    for (int b = r; b < nblk; b += R) {
-      s += part[static_cast<int64_t>(b) * E + e];
-      c += part_counts[static_cast<int64_t>(b) * E + e];
+#pragma unroll
+    for (int i = 0; i < (kBlMaxBlocks + 31) / 32; ++i) {
+      const int b = r + 32 * i;
+      if (b < nblk) {
+        s += part[static_cast<int64_t>(b) * E + e];
+        c += part_counts[static_cast<int64_t>(b) * E + e];
+      }
     }
   }
   s_sum[threadIdx.x] = s;
   s_cnt[threadIdx.x] = c;
   int n = threadIdx.x < nblk ? part_tokens[threadIdx.x] : 0;
   n = __reduce_add_sync(0xffffffffu, n);
-  if ((threadIdx.x & 31) == 0 && n != 0) atomicAdd(&s_n, n);
+  if (el == 0 && n != 0) atomicAdd(&s_n, n);
   __syncthreads();
-  if (r == 0) {
-    for (int i = 1; i < R; ++i) {
-      s += s_sum[i * W + e];
-      c += s_cnt[i * W + e];
+  if (r == 0 && e < E) {
+    for (int i = 1; i < 32; ++i) {
+      s += s_sum[i * 32 + el];
+      c += s_cnt[i * 32 + el];
     }
-    s_sum[e] = s;                        // this thread's own slots
-    s_cnt[e] = c;
+    prob_sums[e] = s;
+    counts[e] = c;
+    __threadfence();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  if (threadIdx.x < E) {
+    s_sum[threadIdx.x] = __ldcg(prob_sums + threadIdx.x);
+    s_cnt[threadIdx.x] = __ldcg(counts + threadIdx.x);
   }
   __syncthreads();
   balance_finish(s_sum, s_cnt, s_n, s_term, E, k, coef, loss, counts, prob_sums, n_tokens);
@@ -385,7 +401,7 @@ using namespace mxg;
 
 extern "C" size_t mxg_balance_loss_workspace_bytes(int T, int E) {
   if (T <= 0 || E <= 0 || E > 256) return 0;
-  return static_cast<size_t>(2 * part_floats(T, E) + api::align_up(4ll * kBlMaxBlocks, api::kAlign));
+  return static_cast<size_t>(2 * part_floats(T, E) + api::align_up(4ll * (kBlMaxBlocks + 1), api::kAlign));
 }
 
 extern "C" int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, const uint8_t* token_mask, int T, int E,
@@ -412,10 +428,9 @@ extern "C" int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, con
   count_launch();
   MXG_TRY(cudaGetLastError());
   if (nblk == 1) return MXG_OK;
-  int W = 32;
-  while (W < E) W *= 2;
-  MXG_TRY(launch_after(balance_finish_kernel, dim3(1), dim3(1024), 0, s, part, part_counts, part_tokens, nblk, E, W, k,
-                       coef, loss, counts, prob_sums, n_tokens));
+  MXG_TRY(launch_after(balance_finish_kernel, dim3(static_cast<unsigned>((E + 31) / 32)), dim3(1024), 0, s, part,
+                       part_counts, part_tokens, nblk, E, k, coef, part_tokens + kBlMaxBlocks, loss, counts, prob_sums,
+                       n_tokens));
   return MXG_OK;
 }
 
