@@ -17,7 +17,12 @@
 // at a time and every lane keeps its experts' sums in registers.  Where E is a
 // multiple of four (VEC) a lane's experts are two 16-byte pieces of the row.
 // Both passes are bound by the logits stream, and below a megabyte or so by
-// the latency of the launch and of one trip to memory.
+// the latency of the launch and of one trip to memory.  Where the stream is
+// long, the forward's 130 or so instructions a token and warp (of 32 logits x 8:
+// expf, the shuffles of a maximum and of a sum) take 7 us of issue for 65536 x
+// 256 beside 10 us of reads, and do not hide fully: its first pass takes 15 us
+// without the softmax and 20 with it (a launch alone is 4 of them).  Fetching the
+// next tokens ahead of the softmax changes nothing (32 warps an SM do that).
 #include <climits>
 #include <cmath>
 
@@ -33,6 +38,7 @@ constexpr int kBlVals = 8;               // experts per lane
 constexpr int kBlFwdThreads = 1024;
 constexpr int kBlFwdWarps = kBlFwdThreads / 32;
 constexpr int kBlMaxBlocks = 152;        // partial sums of the forward: one block per SM
+constexpr int kBlFinBlocks = 8;          // of 32 experts
 constexpr int kBlBwdThreads = 256;
 constexpr int kBlBwdWarps = kBlBwdThreads / 32;
 
@@ -97,6 +103,12 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ row, int E
   }
 }
 
+// Expert's share of the loss (before coef E).
+__device__ __forceinline__ float balance_term(float prob_sum, int count, int k, int n) {
+  const float nf = static_cast<float>(n);
+  return n > 0 ? (static_cast<float>(count) / (static_cast<float>(k) * nf)) * (prob_sum / nf) : 0.f;
+}
+
 // The counts and the loss from s_sum / s_cnt / n (whole block, at least 256
 // threads; the sums and counts of all experts are in shared memory).
 __device__ __forceinline__ void balance_finish(const float* s_sum, const int* s_cnt, int n, float* s_term, int E,
@@ -104,12 +116,11 @@ __device__ __forceinline__ void balance_finish(const float* s_sum, const int* s_
                                                int32_t* n_tokens) {
   const int e = threadIdx.x;
   if (e < 256) {
-    const float nf = static_cast<float>(n);
     float term = 0.f;
     if (e < E) {
       prob_sums[e] = s_sum[e];
       counts[e] = s_cnt[e];
-      if (n > 0) term = (static_cast<float>(s_cnt[e]) / (static_cast<float>(k) * nf)) * (s_sum[e] / nf);
+      term = balance_term(s_sum[e], s_cnt[e], k, n);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
@@ -198,10 +209,7 @@ __global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
     }
   }
   if (gridDim.x > 1) {
-    if (threadIdx.x == 0) {
-      part_tokens[blockIdx.x] = s_tok;
-      if (blockIdx.x == 0) part_tokens[kBlMaxBlocks] = 0;      // the finish's ticket
-    }
+    if (threadIdx.x == 0) part_tokens[blockIdx.x] = s_tok;
     return;
   }
   __syncthreads();
@@ -209,21 +217,21 @@ __global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
 }
 
 // The partials, 32 experts a block: 32 threads share an expert, each adding
-// every 32nd block in order, then their sums in order.  The block that is last
-// to have its experts' sums in memory (ticket, zero before) takes the loss.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const float* __restrict__ part,
-                                                             const int32_t* __restrict__ part_counts,
-                                                             const int32_t* __restrict__ part_tokens, int nblk, int E,
-                                                             int k, float coef, int32_t* __restrict__ ticket,
-                                                             float* __restrict__ loss, int32_t* __restrict__ counts,
-                                                             float* __restrict__ prob_sums,
-                                                             int32_t* __restrict__ n_tokens) {
+// every 32nd block in order, then their sums in order.  The eight blocks are one
+// cluster and each hands its experts' share of the loss to block 0 through
+// shared memory: 65536 x 256, both passes, 23.0 us; with a ticket in global
+// memory, the last block reading all sums again, 25.2; by a single block 29.
+__global__ void __cluster_dims__(kBlFinBlocks, 1, 1) __launch_bounds__(1024)
+balance_finish_kernel(const float* __restrict__ part, const int32_t* __restrict__ part_counts,
+                      const int32_t* __restrict__ part_tokens, int nblk, int E, int k, float coef,
+                      float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob_sums,
+                      int32_t* __restrict__ n_tokens) {
   __shared__ float s_sum[1024];
   __shared__ int s_cnt[1024];
-  __shared__ float s_term[8];
-  __shared__ int s_n, s_last;
+  __shared__ float s_term[kBlFinBlocks];  // block 0's: every block's share
+  __shared__ int s_n;
   if (threadIdx.x == 0) s_n = 0;
-  __syncthreads();
+  cluster_sync();                         // block 0 is there to be written to
   dependency_wait();
   const int el = threadIdx.x & 31, e = blockIdx.x * 32 + el, r = threadIdx.x >> 5;
   float s = 0.f;
@@ -244,26 +252,28 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const float* __res
   n = __reduce_add_sync(0xffffffffu, n);
   if (el == 0 && n != 0) atomicAdd(&s_n, n);
   __syncthreads();
-  if (r == 0 && e < E) {
-    for (int i = 1; i < 32; ++i) {
-      s += s_sum[i * 32 + el];
-      c += s_cnt[i * 32 + el];
+  if (r == 0) {
+    float term = 0.f;
+    if (e < E) {
+      for (int i = 1; i < 32; ++i) {
+        s += s_sum[i * 32 + el];
+        c += s_cnt[i * 32 + el];
+      }
+      prob_sums[e] = s;
+      counts[e] = c;
+      term = balance_term(s, c, k, s_n);
     }
-    prob_sums[e] = s;
-    counts[e] = c;
-    __threadfence();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+    if (el == 0) st_shared_cluster_f32(map_to_rank(smem_u32(&s_term[blockIdx.x]), 0), term);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(ticket, 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  if (threadIdx.x < E) {
-    s_sum[threadIdx.x] = __ldcg(prob_sums + threadIdx.x);
-    s_cnt[threadIdx.x] = __ldcg(counts + threadIdx.x);
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    float t = 0.f;
+    for (int i = 0; i < kBlFinBlocks; ++i) t += s_term[i];
+    *loss = coef * static_cast<float>(E) * t;
+    *n_tokens = s_n;
   }
-  __syncthreads();
-  balance_finish(s_sum, s_cnt, s_n, s_term, E, k, coef, loss, counts, prob_sums, n_tokens);
 }
 
 template <int LPT, bool VEC>
@@ -401,7 +411,7 @@ using namespace mxg;
 
 extern "C" size_t mxg_balance_loss_workspace_bytes(int T, int E) {
   if (T <= 0 || E <= 0 || E > 256) return 0;
-  return static_cast<size_t>(2 * part_floats(T, E) + api::align_up(4ll * (kBlMaxBlocks + 1), api::kAlign));
+  return static_cast<size_t>(2 * part_floats(T, E) + api::align_up(4ll * kBlMaxBlocks, api::kAlign));
 }
 
 extern "C" int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, const uint8_t* token_mask, int T, int E,
@@ -428,9 +438,8 @@ extern "C" int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, con
   count_launch();
   MXG_TRY(cudaGetLastError());
   if (nblk == 1) return MXG_OK;
-  MXG_TRY(launch_after(balance_finish_kernel, dim3(static_cast<unsigned>((E + 31) / 32)), dim3(1024), 0, s, part,
-                       part_counts, part_tokens, nblk, E, k, coef, part_tokens + kBlMaxBlocks, loss, counts, prob_sums,
-                       n_tokens));
+  MXG_TRY(launch_after(balance_finish_kernel, dim3(kBlFinBlocks), dim3(1024), 0, s, part, part_counts, part_tokens,
+                       nblk, E, k, coef, loss, counts, prob_sums, n_tokens));
   return MXG_OK;
 }
 
