@@ -18,11 +18,14 @@
 // multiple of four (VEC) a lane's experts are two 16-byte pieces of the row.
 // Both passes are bound by the logits stream, and below a megabyte or so by
 // the latency of the launch and of one trip to memory.  Where the stream is
-// long, the forward's 130 or so instructions a token and warp (of 32 logits x 8:
-// expf, the shuffles of a maximum and of a sum) take 7 us of issue for 65536 x
-// 256 beside 10 us of reads, and do not hide fully: its first pass takes 15 us
-// without the softmax and 20 with it (a launch alone is 4 of them).  Fetching the
-// next tokens ahead of the softmax changes nothing (32 warps an SM do that).
+// long the forward's instructions count beside it (65536 x 256: 10 us of reads;
+// the softmax's arithmetic is some 130 instructions a warp and token), so it
+// steps pointers instead of multiplying 64-bit indices, takes a full warp's
+// maximum in one instruction and its own exponential and reciprocal: 23.0 ->
+// 18.9 us with the finish.  Fetching the next tokens ahead of the softmax
+// changes nothing (32 warps an SM do that).  Measured, launch included: forward
+// 65536 x 256 18.9 us (3.6 TB/s), 77 x 5 6.2; backward 8192 x 64 with the
+// route's gradient 9.3 us, 30011 x 60 9.3 (an empty kernel's graph: about 6).
 #include <climits>
 #include <cmath>
 
@@ -56,6 +59,22 @@ __device__ __forceinline__ int value_of(int e) {
   return VEC ? ((e >> 2) / LPT) * 4 + (e & 3) : e / LPT;
 }
 
+// e^d for d <= 0 (NaN stays; e^-200 and less are 0, as -inf): 2 to the power of
+// d log2 e, the product taken in two pieces y + lo since a power magnifies y's
+// rounding by y, and 2^lo = 1 + lo ln 2 for the tiny piece.  Within 2 ulp
+// (2^-22.5 of ex2 and one rounding), with fewer instructions than expf, which
+// has to serve all arguments.
+__device__ __forceinline__ float exp_neg(float d) {
+  constexpr double kLog2e = 1.4426950408889634;
+  constexpr float kHi = static_cast<float>(kLog2e), kLo = static_cast<float>(kLog2e - kHi);
+  float e;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(-200.f));
+  const float y = d * kHi;
+  const float lo = fmaf(d, kLo, fmaf(d, kHi, -y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+  return fmaf(e, lo * 0.693147181f, e);
+}
+
 // The group's softmax of one token: z[i] = logit of expert lane_in_group + LPT i
 // (-inf past E) becomes the probability.  A row without a finite logit gives
 // zeros; NaN (or +inf, as inf - inf) gives NaN in the whole row.
@@ -64,18 +83,21 @@ __device__ __forceinline__ void group_softmax(float (&z)[kBlVals]) {
   float top = z[0];
 #pragma unroll
   for (int i = 1; i < kBlVals; ++i) top = fmaxf(top, z[i]);
+  if constexpr (LPT == 32) {
+    asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(top));     // skips NaN like fmaxf
+  } else {
 #pragma unroll
-  for (int off = LPT / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (top == -INFINITY) top = 0.f;       // fmaxf skips NaN: a row of NaN and -inf keeps its NaN below
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kBlVals; ++i) {
-    z[i] = expf(z[i] - top);
-    sum += z[i];
+    for (int off = LPT / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   }
+  if (top == -INFINITY) top = 0.f;       // fmaxf skips NaN: a row of NaN and -inf keeps its NaN below
+#pragma unroll
+  for (int i = 0; i < kBlVals; ++i) z[i] = exp_neg(z[i] - top);
+  float sum = ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
 #pragma unroll
   for (int off = LPT / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  float inv;                             // of 1 <= sum <= 256, within 1 ulp
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sum));
+  if (sum == 0.f) inv = 0.f;
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) z[i] *= inv;
 }
@@ -159,26 +181,30 @@ __global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) acc[i] = 0.f;
   int tokens = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlFwdWarps * TPW;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlFwdWarps + warp) * TPW; t0 < T; t0 += 2 * step) {
+  // T k fits 31 bits, so token numbers (up to T + two steps) fit 32; the pointers step along
+  const uint32_t step = gridDim.x * kBlFwdWarps * TPW, end = static_cast<uint32_t>(T);
+  uint32_t t = (blockIdx.x * kBlFwdWarps + warp) * TPW + grp;
+  const float* row = logits + static_cast<int64_t>(t) * E;
+  const int32_t* id = ids + static_cast<int64_t>(t) * k + gl;
+  const int64_t row_step = static_cast<int64_t>(step) * E, id_step = static_cast<int64_t>(step) * k;
+  for (; t - grp < end; t += 2 * step, row += 2 * row_step, id += 2 * id_step) {
     // two tokens per group in flight
     float z[2][kBlVals];
     bool live[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t t = t0 + u * step + grp;
-      live[u] = t < T && (mask == nullptr || mask[t] != 0);
-      load_logits<LPT, VEC>(logits + t * E, E, gl, live[u], z[u]);
+      live[u] = t + u * step < end && (mask == nullptr || mask[t + u * step] != 0);
+      load_logits<LPT, VEC>(row + u * row_step, E, gl, live[u], z[u]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t t = t0 + u * step + grp;
       if (live[u]) {
         tokens += gl == 0;
         for (int j = gl; j < k; j += LPT) {
-          const int e = ids[t * k + j];
-          if (e < 0 || e >= E) report(status, MXG_ERR_EXPERT_ID);
+          const int e = id[u * id_step + j - gl];
+          if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) report(status, MXG_ERR_EXPERT_ID);
           else atomicAdd(&s_cnt[e], 1);
+          if (LPT == 32) break;          // k is at most 32
         }
       }
       __syncwarp();
@@ -219,8 +245,8 @@ __global__ void __launch_bounds__(kBlFwdThreads) balance_partial_kernel(
 // The partials, 32 experts a block: 32 threads share an expert, each adding
 // every 32nd block in order, then their sums in order.  The eight blocks are one
 // cluster and each hands its experts' share of the loss to block 0 through
-// shared memory: 65536 x 256, both passes, 23.0 us; with a ticket in global
-// memory, the last block reading all sums again, 25.2; by a single block 29.
+// shared memory.  (With a ticket in global memory instead, the last block
+// reading all sums again, 65536 x 256 took 2.2 us more; by a single block 6.)
 __global__ void __cluster_dims__(kBlFinBlocks, 1, 1) __launch_bounds__(1024)
 balance_finish_kernel(const float* __restrict__ part, const int32_t* __restrict__ part_counts,
                       const int32_t* __restrict__ part_tokens, int nblk, int E, int k, float coef,
@@ -285,12 +311,14 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
   constexpr int TPW = 32 / LPT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kBlBwdWarps * TPW;
-  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBlBwdWarps + warp) * TPW;
+  const uint32_t step = gridDim.x * kBlBwdWarps * TPW, end = static_cast<uint32_t>(T);
+  uint32_t t = (blockIdx.x * kBlBwdWarps + warp) * TPW + grp;
+  const int64_t row_step = static_cast<int64_t>(step) * E;
+  int64_t row = static_cast<int64_t>(t) * E;
   // the first logits are on their way while the counts arrive
-  bool in = t0 + grp < T, live = in && (mask == nullptr || mask[t0 + grp] != 0);
+  bool in = t < end, live = in && (mask == nullptr || mask[t] != 0);
   float z[kBlVals];
-  load_logits<LPT, VEC>(logits + (t0 + grp) * E, E, gl, live, z);
+  load_logits<LPT, VEC>(logits + row, E, gl, live, z);
   int cnt[kBlVals];
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) {
@@ -305,8 +333,7 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
   float dev[kBlVals];
 #pragma unroll
   for (int i = 0; i < kBlVals; ++i) dev[i] = static_cast<float>(static_cast<int64_t>(E) * cnt[i] - kn) * inv;
-  while (t0 < T) {
-    const int64_t t = t0 + grp;
+  while (t - grp < end) {
     group_softmax<LPT>(z);
     float mean = 0.f;
 #pragma unroll
@@ -317,25 +344,28 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < kBlVals; ++i) d[i] = live ? up * z[i] * (dev[i] - mean) : 0.f;
     const bool here = in;
-    t0 += step;
-    in = t0 + grp < T;
-    live = in && (mask == nullptr || mask[t0 + grp] != 0);
-    if (t0 < T) load_logits<LPT, VEC>(logits + (t0 + grp) * E, E, gl, live, z);
+    const int64_t pick = static_cast<int64_t>(t) * k;
+    float* dst = dlogits + row;
+    t += step;
+    row += row_step;
+    in = t < end;
+    live = in && (mask == nullptr || mask[t] != 0);
+    load_logits<LPT, VEC>(logits + row, E, gl, live, z);
     if (probs != nullptr) {
       // the route's gradient at the chosen experts: q_j (dq_j - sum_i q_i dq_i)
       float inner = 0.f;
       for (int j = gl; j < k; j += LPT)
-        if (here) inner = fmaf(probs[t * k + j], dprobs[t * k + j], inner);
+        if (here) inner = fmaf(probs[pick + j], dprobs[pick + j], inner);
 #pragma unroll
       for (int off = LPT / 2; off > 0; off >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, off);
       if (here) {
         for (int j = 0; j < k; ++j) {
-          const int e = ids[t * k + j];
+          const int e = ids[pick + j];
           if (e < 0 || e >= E) {
             if (gl == 0) report(status, MXG_ERR_EXPERT_ID);
           } else if (lane_of<LPT, VEC>(e) == gl) {
-            const float q = probs[t * k + j];
-            const float g = q * (dprobs[t * k + j] - inner);
+            const float q = probs[pick + j];
+            const float g = q * (dprobs[pick + j] - inner);
             const int v = value_of<LPT, VEC>(e);
 #pragma unroll
             for (int i = 0; i < kBlVals; ++i)
@@ -346,18 +376,17 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
       __syncwarp();
     }
     if (here) {
-      float* row = dlogits + t * E;
       if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < kBlVals; i += 4) {
           const int e = expert_of<LPT, VEC>(gl, i);
-          if (e < E) *reinterpret_cast<float4*>(row + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          if (e < E) *reinterpret_cast<float4*>(dst + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kBlVals; ++i) {
           const int e = expert_of<LPT, VEC>(gl, i);
-          if (e < E) row[e] = d[i];
+          if (e < E) dst[e] = d[i];
         }
       }
     }

@@ -141,6 +141,19 @@ def test_balanced_router_has_no_cancellation():
     assert np.linalg.norm(g - ref) <= 2e-6 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("T,E", [(9, 2), (300, 4), (4096, 32)])
+def test_every_expert_chosen_has_no_gradient(T, E):
+    """k = E: every f is 1 / E whatever the router does, the loss is coef and its gradient exactly zero."""
+    m = require_gpu()
+    z, ids, mask, _ = _inputs(T, E, E, True, 0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, counts, _, n = m.mxg_balance_loss_fwd(_dev(z), _dev(ids), 0.5, status, token_mask=_dev(mask))
+    g = m.mxg_balance_loss_bwd(_dev(z), counts, n, E, 0.5, status, token_mask=_dev(mask))
+    assert not g.any()
+    # the sums of a token's p: each within _p_rel of exact; T n-term additions in blocks and a few products
+    assert abs(float(loss.item()) - 0.5) <= 0.5 * (_p_rel(z) + 100 * U)
+
+
 def test_masked_and_infinite_rows():
     m = require_gpu()
     z, ids, _, _ = _inputs(64, 12, 3, False, 0)
