@@ -44,13 +44,19 @@
 namespace mxg {
 namespace {
 
+// The products' counters lie a cache line apart: waiting CTAs read them without
+// pause, and side by side the matrices slowed each other down (60 x 200 x 200,
+// 128-wide tiles: 148 us, 103 apart; 20 x 300 x 300 121 and 96).
+constexpr int kNsLine = 32;
+
 // New momentum and the sum of squares of u: one partial per block; the
 // products' counters are cleared.  VEC: every matrix starts on a 32-byte
 // boundary of each buffer.
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
                                                              int32_t* __restrict__ done) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) done[blockIdx.y] = done[gridDim.y + blockIdx.y] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    done[blockIdx.y * kNsLine] = done[(gridDim.y + blockIdx.y) * kNsLine] = 0;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
   SumSq s{0.f, 0.f, 0.f};
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
@@ -280,7 +286,7 @@ __device__ __forceinline__ int ns_share_begin(const NsArgs& P, const NsOperands&
 
 // Waits until the products before tile tc of its matrix are in memory.
 __device__ __forceinline__ bool ns_wait_done(const NsArgs& P, const NsTile& tc, volatile int* abort) {
-  const int32_t* c = P.done + tc.b;
+  const int32_t* c = P.done + tc.b * kNsLine;
   if (ld_acquire_gpu(c) >= tc.need) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -835,7 +841,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             __threadfence();
             got = ns_join(join, join_phase, abort_flag, lane);
             if (got && warp == 4 && lane == 0)
-              *finishes = (atomicAdd(P.shares + tc.b, 1) + 1) % P.sym_tiles == 0;
+              *finishes = (atomicAdd(P.shares + tc.b * kNsLine, 1) + 1) % P.sym_tiles == 0;
             got = got && ns_join(join, join_phase, abort_flag, lane);
             mine = got && *finishes != 0;
             if (mine && holds) {
@@ -935,7 +941,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             bulk_wait_group<0>();
             fence_proxy_async_global();
           }
-          red_release_gpu_add(P.done + tc.b, 1);
+          red_release_gpu_add(P.done + tc.b * kNsLine, 1);
         }
       }
       acc ^= 1;
@@ -1074,7 +1080,7 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   }
   p.part = w.take(8ll * batch * p.chunks);
   p.shares = ns_shares(batch, p.m, p.n, p.split);
-  p.done = w.take(8ll * batch);           // and the shares' counters
+  p.done = w.take(8ll * batch * kNsLine);           // and the shares' counters
   const int64_t one = p.split ? 4 : 2;    // bytes of an element
   const int64_t xb = one * batch * rows * p.ldx, ab = one * batch * p.m * p.lda;
   p.x0 = w.take(xb);
@@ -1197,7 +1203,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.w_keep = w_keep;
   n.lr = a->lr;
   n.done = done;
-  n.shares = done + a->batch;
+  n.shares = done + a->batch * kNsLine;
   n.sym_tiles = p.shares;
   n.a_parts = api::at<float>(a->workspace, p.a_parts);
   n.status = a->dev_status;
