@@ -54,9 +54,9 @@ constexpr int kNsLine = 32;
 // boundary of each buffer.
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
-                                                             int32_t* __restrict__ done) {
-  if (blockIdx.x == 0 && threadIdx.x == 0)
-    done[blockIdx.y * kNsLine] = done[(gridDim.y + blockIdx.y) * kNsLine] = 0;
+                                                             int32_t* __restrict__ done, int n_done) {
+  if (blockIdx.x == 0)
+    for (int i = blockIdx.y * kMoThreads + threadIdx.x; i < n_done; i += gridDim.y * kMoThreads) done[i] = 0;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
   SumSq s{0.f, 0.f, 0.f};
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
@@ -125,8 +125,9 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 }
 
 // ------------------------------------------------------------------ products
-// D = P Q^T over fp16 operands, tiles of 128 x 128 on one SM or 256 x 256 on a
-// CTA pair (cta_group::2, each SM holding its 128 rows of both operands).
+// D = P Q^T over fp16 operands, tiles of 128 x 64 or 128 x 128 on one SM or 256
+// x 256 on a CTA pair (cta_group::2, each SM holding its 128 rows of both
+// operands).
 // Warps 0 and 2 issue TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run
 // the epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
 // columns.  The accumulator is double-buffered in TMEM.
@@ -147,6 +148,10 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // apart; a K = 16 step is 32 bytes).  MN-major: box h holds the 64 contraction
 // rows of operand rows 64 h .. (leading offset 8192 between them, 8-row groups
 // 1024 bytes apart; a K = 16 step is 16 rows, 2048 bytes).
+//
+// X X^T has the fewest tiles and the longest contraction.  Where SMs would be
+// idle, several CTAs share a tile's contraction: each leaves its fp32 sums in
+// global memory, and the one that is last to do so adds them up in order.
 //
 // FUSED (a short side of at most 128): A is one tile, so both operands of
 // X X^T are the same 128 rows.  They are loaded once, and a stage holds 128
@@ -189,7 +194,9 @@ struct NsArgs {
   int tall;                               // rows > cols
   int batch, steps;
   int sym_tiles;                          // tiles of A (and of B) of one matrix; FUSED: CTAs that share A's contraction
-  float* a_parts;                         // FUSED, sym_tiles > 1: their sums [batch][sym_tiles][side][side]
+  int splits;                             // not FUSED: CTAs (pairs) that share the contraction of a tile of A
+  float* a_parts;                         // FUSED, sym_tiles > 1: their sums [batch][sym_tiles][side][side];
+                                          // splits > 1: [batch][sym_tiles][pair's CTA][splits][128 x BN]
   int app_m, app_n;                       // row and column tiles of X
   float alpha[3], alpha_last;             // each product's factor on the accumulators
   float beta, diag;                       // POLY: + beta A + diag I
@@ -200,56 +207,65 @@ struct NsArgs {
   uint16_t* w_out;                        // nullable: w_in * w_keep - lr * value
   float w_keep, lr;
   int32_t* done;                          // [batch]: epilogue warps that have stored their part of a tile
-  int32_t* shares;                        // [batch]: FUSED, CTAs that have left their sum
+  int32_t* shares;                        // [batch] (splits: [batch][sym_tiles][pair's CTA]): CTAs that have left their sum
   int32_t* status;
 };
 
 struct NsTile {
   int step, op, b, ti, tj;
-  int share;                              // FUSED, NS_GRAM: which part of the contraction
+  int share;                              // NS_GRAM: which part of the contraction
+  int tile;                               // NS_GRAM, splits: which tile of A, of all matrices
   int need;                               // done[b] once every earlier product of the matrix is stored
 };
 
-// First column tile of row tile ti of a symmetric matrix: tiles of 128 fill
-// the diagonal blocks of kNsSym as well.
-template <bool PAIR>
+// First column tile of row tile ti of a symmetric matrix: small tiles fill the
+// diagonal blocks of kNsSym as well.
+template <int TM, int BN>
 __host__ __device__ __forceinline__ int ns_first(int ti) {
-  return PAIR ? ti : ti & ~1;
+  return ti * TM / kNsSym * (kNsSym / BN);
 }
 
 // Tile t of the whole run: step by step, product by product, matrix by matrix.
 // FUSED: A and B are one tile, computed together under NS_GRAM by sym_tiles
 // CTAs, of which one finishes it.
-template <bool PAIR, bool FUSED>
+template <int TM, int BN, bool FUSED>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs& P, int64_t t) {
-  constexpr int kArrive = PAIR ? 16 : 8;  // epilogue warps of a tile
+  constexpr int kArrive = TM / 16;        // epilogue warps of a tile (BN = 64: half as many, that count twice)
   constexpr int kSyms = FUSED ? 1 : 2;    // products before the last
   NsTile r;
   const int app = P.app_m * P.app_n;
   const int64_t sym_all = static_cast<int64_t>(P.sym_tiles) * P.batch;
-  const int64_t per_step = kSyms * sym_all + static_cast<int64_t>(app) * P.batch;
+  const int splits = FUSED ? 1 : P.splits;
+  const int64_t extra = (splits - 1) * sym_all;                               // tiles of A that others share
+  const int64_t per_step = extra + kSyms * sym_all + static_cast<int64_t>(app) * P.batch;
   r.step = static_cast<int>(t / per_step);
-  int64_t l = t - r.step * per_step;
+  int64_t l = t - r.step * per_step - extra;
   const int before = l < sym_all ? 0 : l < kSyms * sym_all ? 1 : kSyms;       // products of the step
   r.op = before == kSyms ? NS_APPLY : before;
+  r.share = r.tile = 0;
+  if (splits > 1 && before == 0) {
+    l += extra;
+    r.tile = static_cast<int>(l / splits);
+    r.share = static_cast<int>(l - static_cast<int64_t>(r.tile) * splits);
+    l = r.tile;
+  }
   l -= before * sym_all;
   const int syms = FUSED ? 1 : P.sym_tiles;                                   // tiles that are stored
   r.need = kArrive * (r.step * (kSyms * syms + app) + before * syms);
-  r.share = 0;
   if (r.op != NS_APPLY) {
     r.b = static_cast<int>(l / P.sym_tiles);
     int i = static_cast<int>(l - static_cast<int64_t>(r.b) * P.sym_tiles);
-    const int tiles = P.tall ? P.app_n : P.app_m;      // of the short side
+    const int tiles = (P.m + BN - 1) / BN;
     r.ti = 0;
     if (FUSED) {
       r.share = i;
       i = 0;
     }
-    while (i >= tiles - ns_first<PAIR>(r.ti)) {
-      i -= tiles - ns_first<PAIR>(r.ti);
+    while (i >= tiles - ns_first<TM, BN>(r.ti)) {
+      i -= tiles - ns_first<TM, BN>(r.ti);
       ++r.ti;
     }
-    r.tj = ns_first<PAIR>(r.ti) + i;
+    r.tj = ns_first<TM, BN>(r.ti) + i;
   } else {
     // the short side's tiles vary fastest: B stays in L2, X streams
     r.b = static_cast<int>(l / app);
@@ -279,9 +295,10 @@ __device__ __forceinline__ NsOperands ns_operands(const NsArgs& P, const NsTile&
   return {&P.b, x, NS_SYM, NS_MN, short_k};
 }
 
-// FUSED: first stage (of 128 contraction elements) of a share of A.
+// First stage of a share of A: of sym_tiles (FUSED, stages of 128 contraction elements) or of splits.
+template <bool FUSED>
 __device__ __forceinline__ int ns_share_begin(const NsArgs& P, const NsOperands& o, int share) {
-  return (o.nk + 1) / 2 * share / P.sym_tiles;
+  return FUSED ? (o.nk + 1) / 2 * share / P.sym_tiles : o.nk * share / P.splits;
 }
 
 // Waits until the products before tile tc of its matrix are in memory.
@@ -303,11 +320,11 @@ __device__ __forceinline__ int ns_mn_stages(int form, int row0) {
   return form == NS_MN ? INT_MAX : form == NS_SYM ? row0 / kNsSym * (kNsSym / kNsK) : 0;
 }
 
-template <bool PEER>
+template <bool PEER, int BOXES>
 __device__ __forceinline__ void ns_load(uint8_t* dst, const CUtensorMap* map, bool mn, int row0, int k0, int b,
                                         uint64_t* bar, uint32_t peer_bar) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < BOXES; ++h) {
     const int x = mn ? row0 + 64 * h : k0, y = mn ? k0 : row0 + 64 * h;
     if (PEER) tma_load_3d_pair(dst + h * kNsBoxBytes, map, x, y, b, peer_bar);
     else tma_load_3d(dst + h * kNsBoxBytes, map, x, y, b, bar);
@@ -349,10 +366,11 @@ __device__ __forceinline__ void ns_store_box(const uint32_t (&h)[32], uint8_t* b
   }
 }
 
-// The same by plain stores, 32 bytes at a time (rows are padded to 16).
+// The same (or 32 columns) by plain stores, 32 bytes at a time (rows are padded to 16).
+template <int HALVES = 2>
 __device__ __forceinline__ void ns_store_direct(const uint32_t (&h)[32], uint16_t* dst, bool in, int col, int n) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 2 * HALVES; ++j)
     if (in && col + 16 * j < n) st_global_v8(dst + 16 * j, h + 8 * j);
 }
 
@@ -534,11 +552,17 @@ __device__ __forceinline__ bool ns_join(uint64_t* bar, uint32_t& phase, volatile
 // or both outputs at once).  SPLIT: operands in two fp16 parts.
 // FUSED: a short side of at most 128 makes A and B a single tile: B is computed
 // from the A in shared memory, without a trip to global memory between them.
-template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
+// BN: columns of a tile (and of an accumulator); 256 on a CTA pair.  64: four of
+// the epilogue warps store a tile (eight with half the columns each, and so
+// twice the releases, measured 4 to 8 us slower over five steps).
+template <int BN, bool ROWS, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant__ NsArgs P) {
+  constexpr bool PAIR = BN == 256;
   constexpr int CG = PAIR ? 2 : 1;
-  constexpr int BN = PAIR ? 256 : 128;    // columns of a tile (and accumulator columns)
   constexpr int TM = PAIR ? 256 : 128;    // rows of a tile, both CTAs
+  constexpr int COLS = BN == 64 ? 64 : BN / 2;                    // columns of an epilogue warp
+  constexpr int kStage = kNsOpBytes + (BN == 64 ? kNsBoxBytes : kNsOpBytes);      // bytes that a CTA loads
+  static_assert((BN == 64 || BN == 128 || BN == 256) && (!FUSED || BN == 128), "tiles");
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* boxes = sm + kNsStages * kNsStageBytes;
@@ -596,7 +620,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
   const uint32_t tmem = *tmem_slot;
   const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x;
   const int64_t tstep = PAIR ? gridDim.x / 2 : gridDim.x;
-  const int64_t total = static_cast<int64_t>(P.steps) * P.batch * ((FUSED ? 1 : 2) * P.sym_tiles + P.app_m * P.app_n);
+  const int64_t total = static_cast<int64_t>(P.steps) * P.batch *
+                        ((FUSED ? 1 : 1 + P.splits) * P.sym_tiles + P.app_m * P.app_n);
   // in parts: first (high, low), (low, high), then (high, high)
   constexpr int parts = SPLIT ? 3 : 1;
   auto fail = [&]() {
@@ -613,28 +638,29 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       bool aborted = false;
       const uint32_t full0 = PAIR ? map_to_rank(smem_u32(full), 0) : 0u;
       for (int64_t t = tile0; t < total && !aborted; t += tstep) {
-        const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
+        const NsTile tc = ns_tile<TM, BN, FUSED>(P, t);
         const NsOperands o = ns_operands(P, tc);
         const int row = (second ? tc.tj * BN : tc.ti * TM) + static_cast<int>(rank) * kNsRows;
         const int mn_stages = ns_mn_stages(second ? o.q_form : o.p_form, row);
         const CUtensorMap* map = second ? o.q : o.p;
         const bool shared = FUSED && tc.op == NS_GRAM;
-        const int first = shared ? ns_share_begin(P, o, tc.share) : 0;
-        const int stages = shared ? ns_share_begin(P, o, tc.share + 1) : parts * o.nk;
+        const bool part_of = shared || (!FUSED && tc.op == NS_GRAM && P.splits > 1);
+        const int first = part_of ? ns_share_begin<FUSED>(P, o, tc.share) : 0;
+        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * o.nk;
         if (!ns_wait_done(P, tc, abort_flag)) {
           fail();
           aborted = true;
           break;
         }
         fence_proxy_async_global();       // the counts were acquired; the loads are the async proxy's
-        for (int kp = first, kb = 0, part = 0; kp < stages; ++kp) {
+        for (int kp = first, kb = shared ? 0 : first, part = 0; kp < stages; ++kp) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
             break;
           }
           uint8_t* dst = sm + stage * kNsStageBytes + (second ? kNsOpBytes : 0);
-          if (!second && (!PAIR || rank == 0)) mbar_arrive_expect_tx(&full[stage], CG * kNsStageBytes);    // all bytes of both CTAs
+          if (!second && (!PAIR || rank == 0)) mbar_arrive_expect_tx(&full[stage], CG * kStage);    // all bytes of both CTAs
           if (shared) {
             // rows 0 .. 127, or the high and low parts of rows 0 .. 63, of the stage's first or second 64 elements
             const int k0 = (2 * kp + second) * kNsK;
@@ -646,8 +672,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             }
           } else {
             const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
-            if (!PAIR || rank == 0) ns_load<false>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
-            else ns_load<true>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
+            if (BN == 64 && second) ns_load<false, 1>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
+            else if (!PAIR || rank == 0) ns_load<false, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
+            else ns_load<true, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
           }
           if (++stage == kNsStages) {
             stage = 0;
@@ -671,7 +698,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       int64_t done = 0;
       const uint64_t desc0 = smem_desc(smem_u32(sm), kNsBoxBytes, 1024, kLayoutSwizzle128B);
       for (int64_t t = tile0; t < total && !aborted; t += tstep) {
-        const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
+        const NsTile tc = ns_tile<TM, BN, FUSED>(P, t);
         const bool got = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)
                               : mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs);
         if (!got) {
@@ -684,9 +711,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         // a tile's rows lie in one block of kNsSym, so the pair's CTAs agree on the form
         const int pmn = ns_mn_stages(o.p_form, tc.ti * TM), qmn = ns_mn_stages(o.q_form, tc.tj * BN);
         const bool shared = FUSED && tc.op == NS_GRAM;
-        const int first = shared ? ns_share_begin(P, o, tc.share) : 0;
-        const int stages = shared ? ns_share_begin(P, o, tc.share + 1) : parts * o.nk;
-        for (int kp = first, kb = 0; kp < stages; ++kp) {
+        const bool part_of = shared || (!FUSED && tc.op == NS_GRAM && P.splits > 1);
+        const int first = part_of ? ns_share_begin<FUSED>(P, o, tc.share) : 0;
+        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * o.nk;
+        for (int kp = first, kb = shared ? 0 : first; kp < stages; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
           if (!in) {
@@ -767,21 +795,30 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       mbar_wait_bounded(drained, 0, never_set, kWaitLimitNs);
     }
   } else if (warp >= 4) {
-    constexpr int COLS = BN / 2;
     constexpr int BOXES = COLS / 64;
     const int q = warp & 3;
     const int hf = (warp - 4) >> 2;
     uint8_t* box = boxes + (warp - 4) * kNsWarpOut;
     uint32_t acc = 0, acc_phase = 0, flip = 0, join_phase = 0;
+    auto free_accumulator = [&]() {       // it has been read and may be overwritten
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR && rank == 1)
+          st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u, map_to_rank(smem_u32(&tempty[acc]), 0));
+        else
+          mbar_arrive(&tempty[acc]);
+      }
+    };
     for (int64_t t = tile0; t < total; t += tstep) {
-      const NsTile tc = ns_tile<PAIR, FUSED>(P, t);
+      const NsTile tc = ns_tile<TM, BN, FUSED>(P, t);
       const bool last = tc.op == NS_APPLY && tc.step + 1 == P.steps;
       const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
       const int col0 = tc.tj * BN + hf * COLS;
       const int dm = tc.op == NS_APPLY ? P.rows : P.m, dn = tc.op == NS_APPLY ? P.cols : P.m;   // of D
       // A is read by plain loads here, so this warp, too, waits for it
       bool got = true;
-      if (tc.op == NS_POLY) {
+      if (tc.op == NS_POLY && (BN != 64 || hf == 0)) {
         if (lane == 0) got = ns_wait_done(P, tc, abort_flag);
         got = __all_sync(0xffffffffu, got);
       }
@@ -883,7 +920,90 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           if (lane == 0) mbar_arrive(a_ready);
         }
       }
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * COLS;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + hf * (BN / 2);
+      if (!FUSED && tc.op == NS_GRAM && P.splits > 1) {
+        // A share of the sum of a tile: half the columns of this lane's row, in pieces of 16 bytes with the lanes
+        // side by side.  The CTA that leaves the last share of its 128 rows adds them up in order and stores them.
+        constexpr int kChunks = BN / 64;                               // of 32 columns
+        constexpr int kPiece = 128 * 4, kShare = 128 * BN;             // floats
+        got = __all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs));
+        tc_fence_after();
+        if (got) {
+          const int64_t sum = static_cast<int64_t>(tc.tile) * CG + rank;
+          float* base = P.a_parts + sum * P.splits * kShare + hf * (BN / 8) * kPiece + (q * 32 + lane) * 4;
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tb + 32 * c, r);
+            tmem_ld_wait();
+            float* dst = base + tc.share * kShare + c * 8 * kPiece;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(dst + j * kPiece) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+          }
+          free_accumulator();
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+          __threadfence();
+          got = ns_join(join, join_phase, abort_flag, lane);
+          if (got && warp == 4 && lane == 0)
+            *finishes = (atomicAdd(P.shares + sum * kNsLine, 1) + 1) % P.splits == 0;
+          got = got && ns_join(join, join_phase, abort_flag, lane);
+          if (got && *finishes != 0) {
+            __threadfence();
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              const float* src = base + c * 8 * kPiece;
+              for (int k = 0; k < P.splits; k += 2) {                  // two shares requested together
+                float4 x[2][8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    x[u][j] = __ldcg(reinterpret_cast<const float4*>(src + min(k + u, P.splits - 1) * kShare + j * kPiece));
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                  if (k + u < P.splits)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                      v[4 * j] += x[u][j].x;
+                      v[4 * j + 1] += x[u][j].y;
+                      v[4 * j + 2] += x[u][j].z;
+                      v[4 * j + 3] += x[u][j].w;
+                    }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __half2 h = __floats2half2_rn(P.alpha[NS_GRAM] * v[2 * i], P.alpha[NS_GRAM] * v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              const int col = tc.tj * BN + hf * (BN / 2) + 32 * c;
+              ns_store_direct<1>(w, P.ap + (static_cast<int64_t>(tc.b) * P.m + row0 + lane) * P.lda + col,
+                                 row0 + lane < P.m, col, P.m);
+            }
+            __syncwarp();
+            if (lane == 0) red_release_gpu_add(P.done + tc.b * kNsLine, 1);
+          }
+        }
+        if (!got) {
+          if (lane == 0) fail();
+          break;
+        }
+        continue;
+      }
+      if (BN == 64 && hf == 1) {          // the other four warps store this tile
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs))) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        continue;
+      }
 #pragma unroll 1
       for (int c = 0; c < BOXES && got && mine; ++c) {
         const int col = col0 + 64 * c;
@@ -894,17 +1014,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           tc_fence_after();
           return in;
         };
-        auto release = [&]() {            // after the last columns: the accumulator may be overwritten
-          if (c != BOXES - 1) return;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR && rank == 1)
-              st_async_complete_tx(map_to_rank(smem_u32(&landing[warp - 4]), 0), 1u,
-                                   map_to_rank(smem_u32(&tempty[acc]), 0));
-            else
-              mbar_arrive(&tempty[acc]);
-          }
+        auto release = [&]() {            // after the last columns
+          if (c == BOXES - 1) free_accumulator();
         };
         const uint32_t ta = tb + 64 * c;
         const NsDst da{&P.as, P.ap, P.m, P.m, P.lda, P.low_a}, db{&P.bs, P.bp, P.m, P.m, P.lda, P.low_a},
@@ -941,7 +1052,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             bulk_wait_group<0>();
             fence_proxy_async_global();
           }
-          red_release_gpu_add(P.done + tc.b * kNsLine, 1);
+          red_release_gpu_add(P.done + tc.b * kNsLine, BN == 64 ? 2 : 1);
         }
       }
       acc ^= 1;
@@ -960,13 +1071,14 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
 
 // --------------------------------------------------------------------- host
 // CTAs (or pairs) of a kernel that the device holds at once.
-template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
+template <int BN, bool ROWS, bool SPLIT, bool FUSED>
 int ns_resident() {
+  constexpr bool PAIR = BN == 256;
   static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < 64 && known[dev].load() > 0) return known[dev].load();
-  auto kern = ns_kernel<PAIR, ROWS, SPLIT, FUSED>;
+  auto kern = ns_kernel<BN, ROWS, SPLIT, FUSED>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess) return 0;
   int n = 0;
   if (PAIR) {
@@ -990,19 +1102,15 @@ int ns_resident() {
   return n;
 }
 
-template <bool PAIR, bool ROWS, bool SPLIT, bool FUSED>
+template <int BN, bool ROWS, bool SPLIT, bool FUSED>
 cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
-  constexpr int W = PAIR ? 256 : 128;
-  a.app_m = (a.rows + W - 1) / W;
-  a.app_n = (a.cols + W - 1) / W;
-  const int t = a.tall ? a.app_n : a.app_m;
-  if (!FUSED) {
-    a.sym_tiles = 0;
-    for (int i = 0; i < t; ++i) a.sym_tiles += t - ns_first<PAIR>(i);
-  }
+  constexpr bool PAIR = BN == 256;
+  constexpr int TM = PAIR ? 256 : 128;
+  a.app_m = (a.rows + TM - 1) / TM;
+  a.app_n = (a.cols + BN - 1) / BN;
   // the largest product's tiles: X's, unless A's contraction is shared out
-  const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.app_m * a.app_n, FUSED ? a.sym_tiles : 0);
-  const int64_t units = ns_resident<PAIR, ROWS, SPLIT, FUSED>();
+  const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.app_m * a.app_n, a.sym_tiles * a.splits);
+  const int64_t units = ns_resident<BN, ROWS, SPLIT, FUSED>();
   if (units <= 0) return cudaErrorCooperativeLaunchTooLarge;
   const int64_t n = most < units ? most : units;
   cudaLaunchConfig_t cfg = {};
@@ -1019,7 +1127,7 @@ cudaError_t launch_ns(NsArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, ns_kernel<PAIR, ROWS, SPLIT, FUSED>, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ns_kernel<BN, ROWS, SPLIT, FUSED>, a);
   count_launch();
   return err != cudaSuccess ? err : cudaGetLastError();
 }
@@ -1028,7 +1136,10 @@ struct NsPlan {
   int m, n, tall;                         // short and long side; tall: the matrix is [n][m]
   int split;
   int cluster;                            // CTAs per matrix that stays on the chip, 0: tiled
-  int shares;                             // CTAs that share the contraction of a single-tile A
+  int bn;                                 // columns of a tile
+  int sym_tiles;                          // tiles of A; of a single-tile A the CTAs that share its contraction
+  int splits;                             // CTAs that share the contraction of a tile of A
+  int n_done;                             // counters
   int64_t ldx, lda;                       // row lengths of X and of A and B, padded to 16
   int chunks;                             // partial sums of squares per matrix
   int64_t part, done, x0, x1, a, b, a_parts, bytes;
@@ -1060,6 +1171,52 @@ int ns_shares(int batch, int m, int n, int split) {
   return best;
 }
 
+// Tiles of a symmetric m x m matrix that are computed.
+template <int TM, int BN>
+int ns_sym_tiles(int m) {
+  const int tm = (m + TM - 1) / TM, tn = (m + BN - 1) / BN;
+  int n = 0;
+  for (int i = 0; i < tm; ++i) n += tn - ns_first<TM, BN>(i);
+  return n;
+}
+
+// Cycles of a step with tiles of TM x BN, fitted to timings of some forty shapes
+// with each kind of tile: a product takes 3000 until its first stage is there
+// (the count of the one before, the first loads), then per tile of the busiest
+// SM its stages (550 cycles, a pair's 600) and its epilogue (up to the release
+// of the next product).  SMs without a tile of A can share its contraction
+// instead: each of `splits` CTAs leaves its sums, and the last one reads them
+// all.  Five steps with 64 / 128 / 256 columns, microseconds, the rule's choice
+// within 7 % of the best one everywhere:
+//   8 x 256 x 256    68  77  93      1 x 8192 x 700   276 235 273
+//   1 x 1300 x 1300 196 173 189      60 x 200 x 200   136 104 113
+//   100 x 256 x 256 203 140 127      1 x 8192 x 2000 1242 716 544
+// and not shared / shared: 1 x 200 x 3000 (64) 128 / 95, 1 x 6000 x 140 (64)
+// 193 / 102, 1 x 3000 x 1000 (128) 251 / 217, 2 x 1000 x 8000 (256) 430 / 368.
+template <int TM, int BN>
+double ns_step_cost(int batch, int rows, int cols, int* splits) {
+  constexpr bool PAIR = BN == 256;
+  const double units = PAIR ? device_sms() / 2 : device_sms();
+  const double stage = PAIR ? 600 : 550, epilogue = PAIR ? 7000 : BN == 128 ? 3200 : 2000;
+  const int m = std::min(rows, cols), n = std::max(rows, cols);
+  const int long_k = (n + kNsK - 1) / kNsK, short_k = (m + kNsK - 1) / kNsK;
+  const double a = static_cast<double>(batch) * ns_sym_tiles<TM, BN>(m);
+  const double x = static_cast<double>(batch) * ((rows + TM - 1) / TM) * ((cols + BN - 1) / BN);
+  auto product = [&](double tiles, int stages) { return 3000 + std::max(1.0, tiles / units) * (stages * stage + epilogue); };
+  const double others = product(a, short_k) + product(x, short_k);
+  double gram = product(a, long_k);
+  *splits = 1;
+  const int most = static_cast<int>(std::min({units / a, static_cast<double>(long_k), 16.0}));
+  for (int s = 2; s <= most; ++s) {
+    const double c = product(1, (long_k + s - 1) / s) + (PAIR ? 6000 + 2000 * s : BN == 128 ? 4500 + 1300 * s : 3700 + 750 * s);
+    if (c < gram) {
+      gram = c;
+      *splits = s;
+    }
+  }
+  return gram + others;
+}
+
 NsPlan ns_plan(int batch, int rows, int cols) {
   NsPlan p{};
   p.tall = rows > cols;
@@ -1079,15 +1236,36 @@ NsPlan ns_plan(int batch, int rows, int cols) {
     return p;
   }
   p.part = w.take(8ll * batch * p.chunks);
-  p.shares = ns_shares(batch, p.m, p.n, p.split);
-  p.done = w.take(8ll * batch * kNsLine);           // and the shares' counters
+  p.splits = 1;
+  if (p.m <= 128) {
+    p.bn = 128;
+    p.sym_tiles = ns_shares(batch, p.m, p.n, p.split);
+  } else {
+    // 64, 128 (one SM) or 256 columns (a pair; half the operand bytes per product of the others)
+    int splits[3];
+    const double c64 = ns_step_cost<128, 64>(batch, rows, cols, &splits[0]);
+    const double c128 = ns_step_cost<128, 128>(batch, rows, cols, &splits[1]);
+    const double c256 = ns_step_cost<256, 256>(batch, rows, cols, &splits[2]);
+    const int best = c64 <= c128 && c64 <= c256 ? 0 : c128 <= c256 ? 1 : 2;
+    p.bn = 64 << best;
+    p.splits = splits[best];
+    p.sym_tiles = best == 0   ? ns_sym_tiles<128, 64>(p.m)
+                  : best == 1 ? ns_sym_tiles<128, 128>(p.m)
+                              : ns_sym_tiles<256, 256>(p.m);
+  }
+  const int ctas = p.bn == 256 ? 2 : 1;   // of a tile
+  p.n_done = batch * (p.splits > 1 ? 1 + ctas * p.sym_tiles : 2) * kNsLine;
+  p.done = w.take(4ll * p.n_done);        // and the shares' counters
   const int64_t one = p.split ? 4 : 2;    // bytes of an element
   const int64_t xb = one * batch * rows * p.ldx, ab = one * batch * p.m * p.lda;
   p.x0 = w.take(xb);
   p.x1 = w.take(xb);
   p.a = w.take(ab);
   p.b = w.take(ab);
-  p.a_parts = w.take(p.shares > 1 ? (p.split ? 4ll * 64 * 64 : 4ll * 128 * 128) * batch * p.shares : 0);
+  // the shares of the sums of A
+  p.a_parts = w.take(p.splits > 1 ? 4ll * 128 * p.bn * ctas * batch * p.sym_tiles * p.splits
+                     : p.m <= 128 && p.sym_tiles > 1 ? (p.split ? 4ll * 64 * 64 : 4ll * 128 * 128) * batch * p.sym_tiles
+                                                     : 0);
   p.bytes = w.off;
   return p;
 }
@@ -1168,8 +1346,8 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   const unsigned nb = static_cast<unsigned>(a->batch);
   // 32-byte loads where every matrix (and, for the cast, every row) starts on 32 bytes of each buffer
   const dim3 mgrid(static_cast<unsigned>(p.chunks), nb);
-  if (per % 16 == 0) momentum_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done);
-  else momentum_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done);
+  if (per % 16 == 0) momentum_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done, p.n_done);
+  else momentum_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done, p.n_done);
   count_launch();
   const int64_t lo_off = p.split ? static_cast<int64_t>(a->batch) * a->rows * p.ldx : 0;
   if (a->cols % 16 == 0)
@@ -1204,7 +1382,8 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.lr = a->lr;
   n.done = done;
   n.shares = done + a->batch * kNsLine;
-  n.sym_tiles = p.shares;
+  n.sym_tiles = p.sym_tiles;
+  n.splits = p.splits;
   n.a_parts = api::at<float>(a->workspace, p.a_parts);
   n.status = a->dev_status;
   const int64_t mats = static_cast<int64_t>(a->batch) * (p.split ? 2 : 1);
@@ -1220,17 +1399,16 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   if (!by_rows)
     ok = ok && tma_map_b16_3d(&n.out, a->w_out ? a->w_out : a->update, a->cols, a->rows, a->batch, a->cols, 32);
   if (!ok) return MXG_ERR_CUDA;
-  // a pair's 256 x 256 tiles read half as much per product; with fewer of them than pairs, or a short side that
-  // fills only one of the two SMs, the smaller tiles keep more SMs busy
-  const int64_t t256 = static_cast<int64_t>((a->rows + 255) / 256) * ((a->cols + 255) / 256) * a->batch;
   cudaError_t err;
-  if (t256 >= device_sms() / 2 && p.m > 128)
-    err = by_rows ? launch_ns<true, true, false, false>(n, s) : launch_ns<true, false, false, false>(n, s);
+  if (p.bn == 256)
+    err = by_rows ? launch_ns<256, true, false, false>(n, s) : launch_ns<256, false, false, false>(n, s);
+  else if (p.bn == 64)
+    err = by_rows ? launch_ns<64, true, false, false>(n, s) : launch_ns<64, false, false, false>(n, s);
   else if (p.m > 128)
-    err = by_rows ? launch_ns<false, true, false, false>(n, s) : launch_ns<false, false, false, false>(n, s);
+    err = by_rows ? launch_ns<128, true, false, false>(n, s) : launch_ns<128, false, false, false>(n, s);
   else if (p.split)
-    err = by_rows ? launch_ns<false, true, true, true>(n, s) : launch_ns<false, false, true, true>(n, s);
+    err = by_rows ? launch_ns<128, true, true, true>(n, s) : launch_ns<128, false, true, true>(n, s);
   else
-    err = by_rows ? launch_ns<false, true, false, true>(n, s) : launch_ns<false, false, false, true>(n, s);
+    err = by_rows ? launch_ns<128, true, false, true>(n, s) : launch_ns<128, false, false, true>(n, s);
   return api::cuda_status(err);
 }

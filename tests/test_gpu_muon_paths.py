@@ -51,6 +51,29 @@ def test_forms(batch, m, n, tall):
     assert torch.equal(upd, again)
 
 
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("batch,m,n", [
+    (1, 130, 3001),             # tiles of 64 columns, every one's contraction shared; odd rows
+    (2, 600, 2000),             # of 128, shared
+    (8, 400, 4000),             # of 256 on pairs, shared
+    (8, 399, 4001),
+    (20, 300, 300),             # of 128, not shared
+    (70, 200, 200),             # of 256 on pairs, not shared, one tile each
+])
+def test_many_matrices_and_long_ones(batch, m, n, tall):
+    """The forms that need many or long matrices; the oracle on the first and the last one."""
+    mx = require_gpu()
+    rows, cols = (n, m) if tall else (m, n)
+    g = torch.from_numpy(_grad(batch, rows, cols, 7 * m + n)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    upd = mx.mxg_muon_update(g, status, scale=0.7)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    ends = sorted({0, batch - 1})
+    _close(upd[ends], _orth(g[ends].double().cpu().numpy(), 0.7))
+    assert torch.equal(upd, mx.mxg_muon_update(g, status, scale=0.7))
+
+
 @pytest.mark.parametrize("rows,cols", [(48, 96), (96, 48), (100, 5000), (200, 304), (304, 200), (201, 303)])
 def test_update_and_weights_together(rows, cols):
     """Both outputs of one call are what each gives alone."""
