@@ -26,9 +26,14 @@
 //      grows at every seam), and the CTA that brings a unit's count of partials
 //      to its end adds them up in order.  No CTA waits for another.
 //  dx: 128 tokens x 128 hidden columns a tile, K = 64 experts x 2 parts a step
-//      (W_r read across).  Up to 64 experts, G stays while the CTA goes along
-//      the tokens' columns.  dx_in comes by TMA into the buffer that the result
-//      leaves from.
+//      (W_r read across).  G stays while the CTA goes along the tokens'
+//      columns.  dx_in comes by TMA into the buffer that the result leaves from.
+//
+// Measured, both launches (T x H x E, with dx_in): 16384 x 4096 x 8 71 us (5.7
+// TB/s: HBM), 8191 x 2048 x 64 28.4 us (3.6 TB/s), 8192 x 2048 x 128 39 us,
+// without dx_in 5003 x 1024 x 256 28 us.  7 us are the launches and the split;
+// beyond 64 experts the products count (a tile's MMAs take 135 cycles each, a
+// block of dW 900), and joining the partials of dW about 7 us.
 #include <climits>
 
 #include "api_common.h"
@@ -51,17 +56,32 @@ constexpr int kRlFlush = 4;                       // dW blocks per accumulator (
 constexpr int kRlRing = 229376;                   // bytes of all rings
 constexpr int kRlG = 2 * kRlBox;                  // dx: high and mid of a group for 128 tokens
 constexpr int kRlW = kRlGroup * 256;              // dx: 64 experts x 128 columns of W_r
-constexpr int kRlOps = 2;                         // of each
+constexpr int kRlGs = 4;                          // dx: most slots for G
 constexpr int kRlIo = 2 * kRlBox;                 // dx: one tile of dx_in / dx
-constexpr int kRlIos = 4;                         // even: a buffer always serves the same group of epilogue warps
+constexpr int kRlIos = 4;                         // most; even: a buffer always serves the same group of epilogue warps
 constexpr int kRlMaxStages = 8;
 constexpr int kRlSmem = 1024 + kRlRing + 1024;
-static_assert(kRlOps * (kRlG + kRlW) + kRlIos * kRlIo <= kRlRing, "dx rings");
 static_assert(kRlSmem <= 232448, "shared memory budget");
 // The two epilogue groups take turns at the tiles.  With an odd number of
 // buffers a group would see only every second phase of a buffer's barrier, and
 // a parity wait cannot tell the phase it waits for from the one before last.
 static_assert(kRlIos % 2 == 0, "each buffer belongs to one epilogue group");
+
+// dx: what shared memory holds.  One group: G of two ranges of tokens, two
+// blocks of W_r, four output buffers.  More: G of one range, all groups, two
+// output buffers, and as many blocks of W_r as fit.
+struct RlDx {
+  int gs, ws, ios;
+};
+__host__ __device__ constexpr RlDx rl_dx_slots(int groups) {
+  return groups == 1 ? RlDx{2, 2, 4} : RlDx{groups, (kRlRing - groups * kRlG - 2 * kRlIo) / kRlW, 2};
+}
+constexpr bool rl_dx_fits(int groups) {
+  const RlDx d = rl_dx_slots(groups);
+  return d.gs <= kRlGs && d.gs % groups == 0 && d.ws >= 2 && d.ws <= kRlMaxStages && d.ios <= kRlIos && d.ios % 2 == 0 &&
+         d.gs * kRlG + d.ws * kRlW + d.ios * kRlIo <= kRlRing;
+}
+static_assert(rl_dx_fits(1) && rl_dx_fits(2) && rl_dx_fits(3) && rl_dx_fits(4), "dx rings");
 
 struct RlArgs {
   int T, H, E;
@@ -304,10 +324,10 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
   const int64_t all = static_cast<int64_t>(P.tiles_t) * hts;
   const int64_t lo = rl_cut(all, c, P.n_dx), hi = rl_cut(all, c + 1, P.n_dx);
   const int t_lo = static_cast<int>(lo / hts) * kRlTok, h_lo = static_cast<int>(lo % hts);
-  uint8_t* wr = sm + kRlOps * kRlG;
-  uint8_t* io = wr + kRlOps * kRlW;
+  const RlDx slots = rl_dx_slots(P.groups);
+  uint8_t* wr = sm + slots.gs * kRlG;
+  uint8_t* io = wr + slots.ws * kRlW;
   const int g_boxes = (2 * P.eg + 63) / 64;       // high and mid of the group
-  const bool keep = P.groups == 1;                // G serves all tiles of its tokens
   auto fail = [&]() {
     report(P.status, MXG_ERR_TIMEOUT);
     *B.abort_flag = 1;
@@ -320,7 +340,7 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
       for (int64_t i = lo; i < hi && !aborted; ++i) {
         const int h0 = hi_t * kRlCols;
         for (int g = 0; g < P.groups; ++g) {
-          if (!keep || i == lo || hi_t == 0) {
+          if (i == lo || hi_t == 0) {             // G serves all tiles of its tokens
             if (!mbar_wait_bounded(&B.g_empty[gs], g_phase ^ 1, B.abort_flag, kWaitLimitNs)) {
               fail();
               aborted = true;
@@ -329,8 +349,10 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
             mbar_arrive_expect_tx(&B.g_full[gs], static_cast<uint32_t>(g_boxes * kRlBox));
             for (int h = 0; h < g_boxes; ++h)
               tma_load_2d(sm + gs * kRlG + h * kRlBox, tmG, g * 3 * P.eg + 64 * h, t0, &B.g_full[gs]);
-            gs ^= 1;
-            if (gs == 0) g_phase ^= 1;
+            if (++gs == static_cast<uint32_t>(slots.gs)) {
+              gs = 0;
+              g_phase ^= 1;
+            }
           }
           if (!mbar_wait_bounded(&B.empty[stage], phase ^ 1, B.abort_flag, kWaitLimitNs)) {
             fail();
@@ -341,8 +363,10 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
           mbar_arrive_expect_tx(&B.full[stage], static_cast<uint32_t>(2 * w_box));
           for (int h = 0; h < 2; ++h)
             tma_load_2d(wr + stage * kRlW + h * w_box, tmW, h0 + 64 * h, g * P.eg, &B.full[stage]);
-          stage ^= 1;
-          if (stage == 0) phase ^= 1;
+          if (++stage == static_cast<uint32_t>(slots.ws)) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
         if (++hi_t == hts) {
           hi_t = 0;
@@ -367,9 +391,8 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
           break;
         }
         uint32_t on = 0;
-        for (int g = 0; g < P.groups; ++g) {
-          if ((!keep || i == lo || hi_t == 0) &&
-              !mbar_wait_bounded(&B.g_full[gs], g_phase, B.abort_flag, kWaitLimitNs)) {
+        for (int g = 0; g < P.groups; ++g) {      // slot gs + g: the slots hold whole sets of groups
+          if ((i == lo || hi_t == 0) && !mbar_wait_bounded(&B.g_full[gs + g], g_phase, B.abort_flag, kWaitLimitNs)) {
             fail();
             aborted = true;
             break;
@@ -380,7 +403,7 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
             break;
           }
           tc_fence_after();
-          const uint64_t gd = smem_desc(smem_u32(sm + gs * kRlG), 0, 1024, kLayoutSwizzle128B);
+          const uint64_t gd = smem_desc(smem_u32(sm + (gs + g) * kRlG), 0, 1024, kLayoutSwizzle128B);
           const uint64_t wd = smem_desc(smem_u32(wr + stage * kRlW), P.eg * 128, 1024, kLayoutSwizzle128B);
           for (int part = 1; part >= 0; --part)
             for (int k = 0; k < P.eg / 16; ++k) {
@@ -389,15 +412,20 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
               on = 1;
             }
           mma_commit<1>(&B.empty[stage]);
-          stage ^= 1;
-          if (stage == 0) phase ^= 1;
-          if (!keep || hi_t == hts - 1) {         // the last use of this G
-            mma_commit<1>(&B.g_empty[gs]);
-            gs ^= 1;
-            if (gs == 0) g_phase ^= 1;
+          if (++stage == static_cast<uint32_t>(slots.ws)) {
+            stage = 0;
+            phase ^= 1;
           }
+          if (hi_t == hts - 1) mma_commit<1>(&B.g_empty[gs + g]);      // the last use of this G
         }
         if (aborted) break;
+        if (hi_t == hts - 1) {
+          gs += P.groups;
+          if (gs == static_cast<uint32_t>(slots.gs)) {
+            gs = 0;
+            g_phase ^= 1;
+          }
+        }
         mma_commit<1>(&B.tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
@@ -419,7 +447,7 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
         mbar_arrive_expect_tx(&B.io_full[ib], kRlIo);
         for (int h = 0; h < 2; ++h)
           tma_load_2d(io + ib * kRlIo + h * kRlBox, tmIn, hi_t * kRlCols + 64 * h, t0, &B.io_full[ib]);
-        if (++ib == kRlIos) {
+        if (++ib == static_cast<uint32_t>(slots.ios)) {
           ib = 0;
           ib_phase ^= 1;
         }
@@ -495,8 +523,8 @@ __device__ void rl_dx(const RlArgs& P, const CUtensorMap* tmG, const CUtensorMap
       }
       acc_phase ^= 1;
       ib += 2;
-      if (ib >= kRlIos) {
-        ib -= kRlIos;
+      if (ib >= static_cast<uint32_t>(slots.ios)) {
+        ib -= slots.ios;
         ib_phase ^= 1;
       }
     }
@@ -521,8 +549,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
   B.io_full = B.tempty + 2;
   B.io_empty = B.io_full + kRlIos;
   B.g_full = B.io_empty + kRlIos;
-  B.g_empty = B.g_full + kRlOps;
-  B.drained = B.g_empty + kRlOps;
+  B.g_empty = B.g_full + kRlGs;
+  B.drained = B.g_empty + kRlGs;
   B.join = B.drained + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(B.join + 1);
   B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -551,7 +579,7 @@ __global__ void __launch_bounds__(kRlThreads, 1)
       mbar_init(&B.io_full[i], 1);
       mbar_init(&B.io_empty[i], 8);
     }
-    for (int i = 0; i < kRlOps; ++i) {
+    for (int i = 0; i < kRlGs; ++i) {
       mbar_init(&B.g_full[i], 1);
       mbar_init(&B.g_empty[i], 1);
     }
@@ -629,26 +657,30 @@ __global__ void __launch_bounds__(256) router_split_kernel(const float* __restri
 
 constexpr int kRlMostDw = 1024;                   // partials are sized for this many dW CTAs at most
 
-// dW CTAs of `sms`: the number that lets both products end together, a whole
-// number of them per unit while there are fewer units than SMs (the CTAs of
-// one range of tokens then go through its rows side by side).  Joining a
-// unit's partials takes about 14 k cycles, what an SM moves 400 KB in.
-int rl_share(int sms, int units, int64_t blocks, int64_t block_cost, int64_t tiles, int64_t tile_cost) {
+// dW CTAs of `sms`: the number that lets both products end together.  In cycles,
+// from timings of each product alone and of both with 48 to 112 CTAs for dW: a
+// block of tokens takes 500 and its bytes at 100 a cycle, joining a unit's
+// partials 14000 (17000 unless the CTAs of one range of tokens go through its
+// rows side by side, 3500 where every CTA has whole units), a tile 1000 and 135
+// per MMA but at least 1950, its first operands 4000.  The choice is within 7 %
+// of the best multiple of eight at eleven shapes; shared out by bytes alone it
+// was up to 25 % off (4096 x 4096 x 192: 58.5 us, now 49.6).
+int rl_share(int sms, int units, int64_t blocks, int stage_bytes, int64_t tiles, int mmas) {
   const int64_t most = blocks < kRlMostDw ? blocks : kRlMostDw;
-  const int step = units < sms ? units : 1;
+  const int64_t block = 500 + stage_bytes / 100, tile = mmas < 8 ? 1950 : 1000 + 135 * mmas;
   int best = 1;
   int64_t best_cost = INT64_MAX;
-  for (int n = step; n < sms || n == step; n += step) {
+  for (int n = 1; n <= most && (n < sms || n == 1); n = n < 8 ? 2 * n : n + 8) {
     const int64_t dx = sms > n ? sms - n : 1;
-    const int64_t cost_dw = (blocks + n - 1) / n * block_cost + (n > units ? 400000 : 100000);
-    const int64_t cost_dx = (tiles + dx - 1) / dx * tile_cost;
+    const int64_t cost_dw = (blocks + n - 1) / n * block + (units % n == 0 ? 3500 : n % units == 0 ? 14000 : 17000);
+    const int64_t cost_dx = (tiles + dx - 1) / dx * tile + 4000;
     const int64_t cost = cost_dw > cost_dx ? cost_dw : cost_dx;
     if (cost < best_cost) {
       best_cost = cost;
       best = n;
     }
   }
-  return static_cast<int>(best < most ? best : most);
+  return best;
 }
 
 struct RlPlan {
@@ -713,14 +745,10 @@ extern "C" int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router
   a.status = dev_status;
   a.count = api::at<int32_t>(workspace, p.count);
   a.dw = dw_router;
-  // Bytes each product moves through an SM: x and three parts of G a block; dx_in, dx, W_r and two parts of G
-  // (kept along the columns up to 64 experts) a tile.
   const int sms = device_sms();
   const int hts = H / kRlCols;
   const int64_t blocks = static_cast<int64_t>(p.units) * p.tb, tiles = static_cast<int64_t>(p.tiles_t) * hts;
-  const int64_t g2 = static_cast<int64_t>((2 * p.eg + 63) / 64) * kRlBox;
-  const int64_t tile_cost = (dx_in ? 2 : 1) * kRlIo + p.groups * (p.eg * 256ll) + (p.groups > 1 ? p.groups * g2 : g2 / hts);
-  a.n_dw = rl_share(sms, p.units, blocks, a.stage_bytes, tiles, tile_cost);
+  a.n_dw = rl_share(sms, p.units, blocks, a.stage_bytes, tiles, p.groups * p.eg / 8);
   const int64_t n_dx = sms > a.n_dw ? sms - a.n_dw : 1;
   a.n_dx = static_cast<int>(n_dx < tiles ? n_dx : tiles);
 

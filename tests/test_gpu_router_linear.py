@@ -79,6 +79,27 @@ def test_many_tiles_per_sm(T, H, E):
     _check(dx, dw, x, w, dx0, g)
 
 
+@pytest.mark.parametrize("with_dx", [True, False])
+@pytest.mark.parametrize("T,H,E", [
+    (30000, 128, 100),          # one tile of columns: new tokens at every tile
+    (20001, 256, 256),          # two, all groups' gradients replaced after them
+    (12000, 640, 150),          # three groups, an odd number of tiles of columns
+    (9001, 1024, 70),           # two groups, of which the second is nearly empty
+])
+def test_groups_of_experts_over_many_tiles(T, H, E, with_dx):
+    """More than 64 experts: their gradients stay while an SM goes along the columns, and are replaced at the end."""
+    m = require_gpu()
+    x, w, dx0, g = _inputs(T, H, E)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    xd, wd, gd, dd = x.cuda(), w.cuda(), torch.from_numpy(g).cuda(), dx0.cuda() if with_dx else None
+    dx, dw = m.mxg_router_linear_bwd(xd, wd, gd, dd, status)
+    for _ in range(10):
+        dx2, dw2 = m.mxg_router_linear_bwd(xd, wd, gd, dd, status)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    assert int(status.item()) == 0
+    _check(dx, dw, x, w, dx0 if with_dx else None, g)
+
+
 def test_in_place_repeatable_and_on_another_stream():
     m = require_gpu()
     x, w, dx0, g = _inputs(3001, 512, 12)
