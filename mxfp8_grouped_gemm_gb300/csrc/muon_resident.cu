@@ -20,6 +20,7 @@
 //
 // Latency bounds it: a step is a chain of three products of 1-2 k cycles and
 // the passes between them.
+#include <atomic>
 #include <climits>
 
 #include "kernels.h"
@@ -573,23 +574,53 @@ cudaError_t launch(const ResidentArgs& a, int C, cudaStream_t s) {
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// Clusters of C CTAs that the device holds at once (asked once; a cluster lies
+// within one part of the chip, so 152 SMs hold 76 of two, but 36 of four and 15
+// of eight).
+int clusters_at_once(int C) {
+  static std::atomic<int> known[64][4];
+  const int log = C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return device_sms() / C;
+  if (dev < 64 && (n = known[dev][log].load()) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(C));
+  cfg.blockDim = dim3(kRsThreads);
+  cfg.dynamicSmemBytes = kRsSmem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = muon_resident_kernel<true>;
+  if (allow_smem(kern, kRsSmem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess ||
+      n <= 0) {
+    cudaGetLastError();
+    return device_sms() / C;
+  }
+  if (dev < 64) known[dev][log].store(n);
+  return n;
+}
+
 }  // namespace
 
 // Measured (five steps, us): more CTAs per matrix than its size needs pay off
-// while SMs are idle, 1 x 64 x 512 64 (one CTA) 50 (two) 38 (eight), 2 x 128 x
-// 1024 80 (two) 54 (eight), except up to 256 columns of more than 64 rows: 4 x
-// 128 x 256 41 (one) 46 (four), where the 128 x 128 sums cost more than they
-// spare.  Those sums also make clusters that need several turns slower than
-// the tiled kernel: 16 x 100 x 3000 183 against 139, 64 x 128 x 4096 499
-// against 405; 64 x 64 x 2048 is 152 against 243.
+// while the device holds all clusters at once, 1 x 64 x 512 64 (one CTA) 50 (two)
+// 38 (eight), 2 x 128 x 1024 80 (two) 54 (eight), 19 x 64 x 1024 52 (four) 79
+// (eight, in turns), except up to 256 columns of more than 64 rows: 4 x 128 x 256
+// 41 (one) 46 (four), where the 128 x 128 sums cost more than they spare.  Those
+// sums also make clusters that need several turns slower than the tiled kernel:
+// 16 x 100 x 3000 183 against 132, 64 x 128 x 4096 499 against 405 (in one turn
+// 30 x 128 x 2000 92 against 133); 64 x 64 x 2048 is 150 against 232.
 int resident_cluster(int batch, int m, int n, bool split) {
   if (m > 128 || n > kResidentMost) return 0;
-  const int sms = device_sms();
   int C = 1;
   while (C * kRsSlice < n) C *= 2;
-  if (!split && C > 1 && 2 * batch * C > sms) return 0;
+  if (!split && C > 1 && batch > clusters_at_once(C)) return 0;
   if (split || n > 256)
-    while (C < kRsCluster && C * 64 < n && 2 * batch * C <= sms) C *= 2;
+    while (C < kRsCluster && C * 64 < n && batch <= clusters_at_once(2 * C)) C *= 2;
   return C;
 }
 

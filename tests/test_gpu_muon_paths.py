@@ -59,6 +59,9 @@ def test_forms(batch, m, n, tall):
     (8, 399, 4001),
     (20, 300, 300),             # of 128, not shared
     (70, 200, 200),             # of 256 on pairs, not shared, one tile each
+    (30, 128, 2000),            # on the chip, clusters of four
+    (19, 64, 1024),             # the same, where eight would not fit at once
+    (38, 100, 1000),            # clusters of two
 ])
 def test_many_matrices_and_long_ones(batch, m, n, tall):
     """The forms that need many or long matrices; the oracle on the first and the last one."""
