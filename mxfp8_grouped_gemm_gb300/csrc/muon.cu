@@ -51,7 +51,8 @@ constexpr int kNsLine = 32;
 
 // New momentum and the sum of squares of u: one partial per block; the
 // products' counters are cleared.  VEC: every matrix starts on a 32-byte
-// boundary of each buffer.
+// boundary of each buffer.  HBM bounds it: 64 x 2048 x 1024 with bf16 gradients
+// 210 us, 6.4 TB/s.
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
                                                              int32_t* __restrict__ done, int n_done) {
@@ -81,7 +82,9 @@ __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, in
 
 // X0 = u / |u|_F 2^ex in fp16, rows ld apart.  A block takes whole rows; its
 // first act is the matrix's norm from the partials (the same sum, in the same
-// order, in every block).
+// order, in every block).  It reads the gradient and the new momentum again:
+// 64 x 2048 x 1024 156 us, 6.9 TB/s.  (u cannot be written in fp16 before its
+// norm is known, and in fp32 it costs more bytes.)
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int chunks, const double* __restrict__ part,
                                                          int ex, int rows, int cols, __half* __restrict__ x,
@@ -131,6 +134,16 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // Warps 0 and 2 issue TMA, warp 1 owns TMEM and issues the MMAs, warps 4-11 run
 // the epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half of the tile's
 // columns.  The accumulator is double-buffered in TMEM.
+//
+// What bounds them: long contractions the tensor cores and the power cap (1 x
+// 28672 x 4096, X X^T 1.66-1.81 PFLOP/s, all five steps 1.55), a pair's tiles of
+// K = 1024 what an SM takes in (57 bytes a cycle; the MMAs alone need 8.2 k
+// cycles a tile, with their loads 11-13 k; 64 x 2048 x 1024 1.9 ms for five
+// steps, 1.35 PFLOP/s), small and middling matrices the hand-over from product
+// to product: 1.0 k cycles to see the count, 1.3 k for the first loads, 0.7 k
+// from the last MMA to the epilogue, 1.2 k there, 1.8 k for the release (3 x 1001
+// x 333: 97 us, 15 products).  TMA boxes instead of plain stores for the small
+// tiles are 1-8 % slower there, a sixth stage or a third loading warp no faster.
 //
 // One launch runs all products of all steps: the tiles of the whole run form
 // one list that the CTAs (or pairs) deal out in turn, so a product's last

@@ -19,7 +19,9 @@
 // A = (high, high) + (high, low) + (low, high).
 //
 // Latency bounds it: a step is a chain of three products of 1-2 k cycles and
-// the passes between them.
+// the passes between them.  4 x 128 x 256, five steps: 41 us, of 78 k cycles 12 k
+// for the momentum, 4 k for the norm and 10 k for X0 (57 us tiled); 20 x 64 x 512
+// 41 us (84), 5 x 128 x 4096 88 us (115).
 #include <atomic>
 #include <climits>
 
