@@ -50,22 +50,34 @@ namespace {
 constexpr int kNsLine = 32;
 
 // New momentum and the sum of squares of u: one partial per block; the
-// products' counters are cleared.  VEC: every matrix starts on a 32-byte
-// boundary of each buffer.  HBM bounds it: 64 x 2048 x 1024 with bf16 gradients
-// 210 us, 6.4 TB/s.
-template <bool VEC>
+// products' counters are cleared.  Groups of eight elements are counted from the
+// start of the whole batch, so that they lie on 32 bytes of every buffer
+// whatever the size of a matrix; what is left of a matrix at its two ends goes
+// to its first block, one element a thread.  HBM bounds it: 64 x 2048 x 1024 with
+// bf16 gradients 210 us, 6.4 TB/s.
 __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, int chunks, double* __restrict__ part,
                                                              int32_t* __restrict__ done, int n_done) {
   if (blockIdx.x == 0)
     for (int i = blockIdx.y * kMoThreads + threadIdx.x; i < n_done; i += gridDim.y * kMoThreads) done[i] = 0;
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * P.per;
+  const int64_t start = static_cast<int64_t>(blockIdx.y) * P.per, end = start + P.per;
+  const int64_t lo = (start + kMoVec - 1) / kMoVec * kMoVec;                   // the whole groups are [lo, hi)
+  const int64_t hi = end / kMoVec * kMoVec > lo ? end / kMoVec * kMoVec : lo;
   SumSq s{0.f, 0.f, 0.f};
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < P.per;
+  for (int64_t i = lo + (static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x) * kMoVec; i < hi;
        i += static_cast<int64_t>(chunks) * kMoThreads * kMoVec) {
-    const int n = static_cast<int>(P.per - i < kMoVec ? P.per - i : kMoVec);
     float u[kMoVec];
-    step_momentum<VEC>(P, base + i, n, u);
+    step_momentum<true>(P, i, kMoVec, u);
     s.add8(u);
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 2 * kMoVec) {
+    const int64_t i = threadIdx.x < kMoVec ? start + threadIdx.x : hi + threadIdx.x - kMoVec;
+    if (threadIdx.x < kMoVec ? i < lo && i < end : i < end) {
+      float u[kMoVec];
+      step_momentum<false>(P, i, 1, u);
+#pragma unroll
+      for (int j = 1; j < kMoVec; ++j) u[j] = 0.f;
+      s.add8(u);
+    }
   }
   double t = s.total();
 #pragma unroll
@@ -80,11 +92,14 @@ __global__ void __launch_bounds__(kMoThreads) momentum_kernel(MomentumArgs P, in
   }
 }
 
-// X0 = u / |u|_F 2^ex in fp16, rows ld apart.  A block takes whole rows; its
-// first act is the matrix's norm from the partials (the same sum, in the same
-// order, in every block).  It reads the gradient and the new momentum again:
-// 64 x 2048 x 1024 156 us, 6.9 TB/s.  (u cannot be written in fp16 before its
-// norm is known, and in fp32 it costs more bytes.)
+// X0 = u / |u|_F 2^ex in fp16, rows ld apart.  A block's first act is the
+// matrix's norm from the partials (the same sum, in the same order, in every
+// block).  VEC: rows of whole groups of eight elements, which lie on 32 bytes of
+// every buffer.  Otherwise 32 lanes take 32 elements side by side, eight in
+// flight, and step through rows and columns (groups along the rows were 2-4 %
+// of the whole update slower, 40 x 511 x 770 340 us against 325).  It reads the
+// gradient and the new momentum again: 64 x 2048 x 1024 156 us, 6.9 TB/s.  (u cannot be written in fp16
+// before its norm is known, and in fp32 it costs more bytes.)
 template <bool VEC>
 __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int chunks, const double* __restrict__ part,
                                                          int ex, int rows, int cols, __half* __restrict__ x,
@@ -107,16 +122,46 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
   }
   __syncthreads();
   const float f0 = s_f[0], f1 = s_f[1], f2 = s_f[2];
-  const int groups = (cols + kMoVec - 1) / kMoVec;          // of a row
+  if constexpr (!VEC) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kMoThreads;
+    const int64_t dr = stride / cols;
+    const int dc = static_cast<int>(stride - dr * cols);
+    int64_t e = static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x;
+    int64_t r = e / cols;
+    int c = static_cast<int>(e - r * cols);
+    const int64_t per = P.per;
+    __half* dst = x + static_cast<int64_t>(b) * rows * ld;
+    while (e < per) {
+      float u[kMoVec];
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) u[j] = e + j * stride < per ? momentum_u1(P, b * per + e + j * stride) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kMoVec; ++j) {
+        if (e < per) {
+          const float v = u[j] * f0 * f1 * f2;
+          const __half h = __float2half_rn(v);
+          dst[r * ld + c] = h;
+          if (lo_off != 0) dst[r * ld + c + lo_off] = __float2half_rn(v - __half2float(h));
+        }
+        e += stride;
+        r += dr;
+        c += dc;
+        if (c >= cols) {
+          c -= cols;
+          ++r;
+        }
+      }
+    }
+    return;
+  }
+  const int groups = cols / kMoVec;                         // of a row
   const int64_t total = static_cast<int64_t>(rows) * groups;
   for (int64_t gi = static_cast<int64_t>(blockIdx.x) * kMoThreads + threadIdx.x; gi < total;
        gi += static_cast<int64_t>(gridDim.x) * kMoThreads) {
     const int64_t r = gi / groups;
     const int c = static_cast<int>(gi - r * groups) * kMoVec;
-    const int n = min(kMoVec, cols - c);
-    const int64_t i = b * P.per + r * cols + c;
     float u[kMoVec];
-    momentum_u<VEC>(P, i, n, u);
+    momentum_u8(P, b * P.per + r * cols + c, u);
     uint32_t h[kMoVec / 2], l[kMoVec / 2];
 #pragma unroll
     for (int j = 0; j < kMoVec / 2; ++j) h[j] = split_half2(u[2 * j] * f0 * f1 * f2, u[2 * j + 1] * f0 * f1 * f2, l[j]);
@@ -1357,13 +1402,11 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   __half* am = api::at<__half>(a->workspace, p.a);
   __half* bm = api::at<__half>(a->workspace, p.b);
   const unsigned nb = static_cast<unsigned>(a->batch);
-  // 32-byte loads where every matrix (and, for the cast, every row) starts on 32 bytes of each buffer
   const dim3 mgrid(static_cast<unsigned>(p.chunks), nb);
-  if (per % 16 == 0) momentum_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done, p.n_done);
-  else momentum_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done, p.n_done);
+  momentum_kernel<<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, done, p.n_done);
   count_launch();
   const int64_t lo_off = p.split ? static_cast<int64_t>(a->batch) * a->rows * p.ldx : 0;
-  if (a->cols % 16 == 0)
+  if (a->cols % kMoVec == 0)
     cast_kernel<true><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x[0], p.ldx, lo_off);
   else cast_kernel<false><<<mgrid, kMoThreads, 0, s>>>(mo, p.chunks, part, ex, a->rows, a->cols, x[0], p.ldx, lo_off);
   count_launch();

@@ -134,16 +134,21 @@ __device__ __forceinline__ void step_momentum(const MomentumArgs& P, int64_t i, 
   for (int j = 0; j < kMoVec; ++j) u[j] = P.nesterov ? fmaf(P.mu, m[j], u[j]) : m[j];
 }
 
-// u of eight elements from the new momentum.
-template <bool VEC>
-__device__ __forceinline__ void momentum_u(const MomentumArgs& P, int64_t i, int n, float (&u)[kMoVec]) {
-  if (P.mom_out == nullptr || P.nesterov) load_grad<VEC>(P, i, n, u);
+// u of eight elements (on 32 bytes of every buffer), and of one, from the new momentum.
+__device__ __forceinline__ void momentum_u8(const MomentumArgs& P, int64_t i, float (&u)[kMoVec]) {
+  if (P.mom_out == nullptr || P.nesterov) load_grad<true>(P, i, kMoVec, u);
   if (P.mom_out != nullptr) {
     float m[kMoVec];
-    load_f32<VEC>(P.mom_out, i, n, m);
+    load_f32<true>(P.mom_out, i, kMoVec, m);
 #pragma unroll
     for (int j = 0; j < kMoVec; ++j) u[j] = P.nesterov ? fmaf(P.mu, m[j], u[j]) : m[j];
   }
+}
+__device__ __forceinline__ float momentum_u1(const MomentumArgs& P, int64_t i) {
+  const float g = P.grad_f32 ? static_cast<const float*>(P.grad)[i]
+                             : bf16_bits_to_float(static_cast<const uint16_t*>(P.grad)[i]);
+  if (P.mom_out == nullptr) return g;
+  return P.nesterov ? fmaf(P.mu, P.mom_out[i], g) : P.mom_out[i];
 }
 
 // u / |u| 2^ex is u times these three factors, in this order, so that no
