@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
       const NsTile tc = ns_tile<TM, BN, FUSED>(P, t);
       const bool last = tc.op == NS_APPLY && tc.step + 1 == P.steps;
       const int row0 = tc.ti * TM + static_cast<int>(rank) * kNsRows + q * 32;
-      const int col0 = tc.tj * BN + hf * COLS;
+      const int col0 = tc.tj * BN + (SPLIT && P.tall && tc.op == NS_APPLY ? 0 : hf * COLS);
       const int dm = tc.op == NS_APPLY ? P.rows : P.m, dn = tc.op == NS_APPLY ? P.cols : P.m;   // of D
       // A is read by plain loads here, so this warp, too, waits for it
       bool got = true;
@@ -1052,7 +1052,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         }
         continue;
       }
-      if (BN == 64 && hf == 1) {          // the other four warps store this tile
+      // SPLIT: half of the tile of X' lies outside the matrix.  Rows past 63 leave two of four quadrants idle; in a tall
+      // matrix the columns past 63 do, and the two groups of four warps take turns at the tiles instead.
+      const bool halved = SPLIT && tc.op == NS_APPLY;
+      const bool turns = halved && P.tall;
+      if ((BN == 64 && hf == 1) || (halved && (P.tall ? acc != static_cast<uint32_t>(hf) : q >= 2))) {
+        // other warps store this tile
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, kWaitLimitNs))) {
           if (lane == 0) fail();
           break;
@@ -1062,6 +1067,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         if (acc == 0) acc_phase ^= 1;
         continue;
       }
+      const uint32_t tq = turns ? tb - hf * COLS : tb;
 #pragma unroll 1
       for (int c = 0; c < BOXES && got && mine; ++c) {
         const int col = col0 + 64 * c;
@@ -1075,7 +1081,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         auto release = [&]() {            // after the last columns
           if (c == BOXES - 1) free_accumulator();
         };
-        const uint32_t ta = tb + 64 * c;
+        const uint32_t ta = tq + 64 * c;
         const NsDst da{&P.as, P.ap, P.m, P.m, P.lda, P.low_a}, db{&P.bs, P.bp, P.m, P.m, P.lda, P.low_a},
             dx{&P.xs[(tc.step & 1) ^ 1], P.xp[(tc.step & 1) ^ 1], P.rows, P.cols, P.ldx, P.low_x},
             out{&P.out, P.w_out != nullptr ? P.w_out : P.update, P.rows, P.cols, P.cols, 0};
@@ -1110,7 +1116,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             bulk_wait_group<0>();
             fence_proxy_async_global();
           }
-          red_release_gpu_add(P.done + tc.b * kNsLine, BN == 64 ? 2 : 1);
+          red_release_gpu_add(P.done + tc.b * kNsLine, BN == 64 || halved ? 2 : 1);
         }
       }
       acc ^= 1;
