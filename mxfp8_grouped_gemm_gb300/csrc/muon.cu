@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const int row = (second ? tc.tj * BN : tc.ti * TM) + static_cast<int>(rank) * kNsRows;
         const int mn_stages = ns_mn_stages(second ? o.q_form : o.p_form, row);
         const CUtensorMap* map = second ? o.q : o.p;
+        const bool halved = SPLIT && tc.op == NS_APPLY;      // B: at most 64 rows
         const bool shared = FUSED && tc.op == NS_GRAM;
         const bool part_of = shared || (!FUSED && tc.op == NS_GRAM && P.splits > 1);
         const int first = part_of ? ns_share_begin<FUSED>(P, o, tc.share) : 0;
@@ -718,7 +719,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             break;
           }
           uint8_t* dst = sm + stage * kNsStageBytes + (second ? kNsOpBytes : 0);
-          if (!second && (!PAIR || rank == 0)) mbar_arrive_expect_tx(&full[stage], CG * kStage);    // all bytes of both CTAs
+          if (!second && (!PAIR || rank == 0))
+            mbar_arrive_expect_tx(&full[stage], CG * (halved ? kStage - kNsBoxBytes : kStage));   // all bytes of both CTAs
           if (shared) {
             // rows 0 .. 127, or the high and low parts of rows 0 .. 63, of the stage's first or second 64 elements
             const int k0 = (2 * kp + second) * kNsK;
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
             }
           } else {
             const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
-            if (BN == 64 && second) ns_load<false, 1>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
+            if ((BN == 64 && second) || (halved && second == (P.tall != 0))) ns_load<false, 1>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
             else if (!PAIR || rank == 0) ns_load<false, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
             else ns_load<true, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
           }
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
           const uint64_t pd = desc0 + stage * (kNsStageBytes >> 4);
           const uint64_t qd = shared ? pd : pd + (kNsOpBytes >> 4);
           const uint32_t pstep = kb < pmn ? 2048 >> 4 : 32 >> 4, qstep = kb < qmn ? 2048 >> 4 : 32 >> 4;
-          const uint32_t id = idesc_f16(TM, BN) | (kb < pmn ? kIdescAMn : 0u) | (kb < qmn ? kIdescBMn : 0u);
+          const uint32_t id = idesc_f16(TM, SPLIT && tc.op == NS_APPLY && P.tall ? 64 : BN) | (kb < pmn ? kIdescAMn : 0u) | (kb < qmn ? kIdescBMn : 0u);
 #pragma unroll
           for (uint32_t k = 0; k < kNsK / 16; ++k)
             mma_bf16<CG>(d_t, pd + k * pstep, qd + k * qstep, id, kp != first || k != 0 ? 1u : 0u);
