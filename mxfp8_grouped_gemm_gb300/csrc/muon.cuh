@@ -173,7 +173,7 @@ __device__ __forceinline__ void norm_factors(double n2, int ex, float (&f)[3]) {
 
 // The whole update of matrices that stay on the chip (muon_resident.cu):
 // short side at most 128, long side at most kResidentMost.
-constexpr int kResidentMost = 4096;
+constexpr int kResidentMost = 8192;
 struct ResidentArgs {
   MomentumArgs mo;
   int batch, rows, cols, steps;

@@ -1,8 +1,8 @@
 // The orthogonalised momentum update of small matrices, on the chip from the
 // gradient to the update (see muon.cu for the mathematics and the number
-// format): short side M at most 128, long side N at most 4096.
+// format): short side M at most 128, long side N at most 8192.
 //
-// A cluster of 1, 2, 4 or 8 CTAs takes a matrix; each keeps its share of the
+// A cluster of 1, 2, 4, 8 or 16 CTAs takes a matrix; each keeps its share of the
 // long side (up to 512 columns) of X in shared memory for the whole run, as
 // rows of the short side: boxes of 128 rows x 64 columns, 128-byte swizzle.
 // The same bytes serve as an operand of both products over X:
@@ -21,7 +21,7 @@
 // Latency bounds it: a step is a chain of three products of 1-2 k cycles and
 // the passes between them.  4 x 128 x 256, five steps: 41 us, of 78 k cycles 12 k
 // for the momentum, 4 k for the norm and 10 k for X0 (57 us tiled); 20 x 64 x 512
-// 41 us (84), 5 x 128 x 4096 88 us (115).
+// 41 us (84), 5 x 128 x 4096 90 us (115), 2 x 48 x 8192 on sixteen CTAs 74 (124).
 #include <atomic>
 #include <climits>
 
@@ -34,7 +34,7 @@ namespace {
 constexpr int kRsWarps = 8;                       // warps that compute; one more issues the MMAs
 constexpr int kRsThreads = 32 * (kRsWarps + 1);
 constexpr int kRsSlice = 512;                     // columns of the long side per CTA, at most
-constexpr int kRsCluster = 8;
+constexpr int kRsCluster = 16;                    // more than eight: by opt-in
 static_assert(kRsSlice * kRsCluster == kResidentMost, "largest long side");
 constexpr int kRsBox = 128 * 128;                 // 128 rows x 64 fp16
 constexpr int kRsX = kRsSlice / 64 * kRsBox;
@@ -51,7 +51,7 @@ __device__ __forceinline__ int swz(int j, int r) { return (j ^ (r & 7)) << 4; }
 // in every CTA: CTA k adds up its share of the rows in rank order and stores
 // them everywhere.  Only that CTA reads those rows of the others, so they can
 // be overwritten at once.  All threads of all CTAs.
-template <int SIDE>
+template <int SIDE, int MOST>
 __device__ __forceinline__ void cluster_sum(uint8_t* part, int C, uint32_t rank, int tid) {
   cluster_sync();
   if (tid < 32 * kRsWarps) {
@@ -61,21 +61,25 @@ __device__ __forceinline__ void cluster_sum(uint8_t* part, int C, uint32_t rank,
     for (int i = tid; i < SIDE / C * PIECES; i += 32 * kRsWarps) {
       const int row = r0 + i / PIECES;
       const uint32_t at = base + row * SIDE * 4 + swz(i % PIECES, row);
-      float4 v[kRsCluster];
+      float4 s;
 #pragma unroll
-      for (int k = 0; k < kRsCluster; ++k)
-        if (k < C) v[k] = ld_shared_cluster_v4(map_to_rank(at, k));
-      float4 s = v[0];
+      for (int k0 = 0; k0 < MOST; k0 += 8) {        // eight requested together
+        float4 v[8];
 #pragma unroll
-      for (int k = 1; k < kRsCluster; ++k)
-        if (k < C) {
-          s.x += v[k].x;
-          s.y += v[k].y;
-          s.z += v[k].z;
-          s.w += v[k].w;
-        }
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < C) v[k] = ld_shared_cluster_v4(map_to_rank(at, k0 + k));
+        if (k0 == 0) s = v[0];
 #pragma unroll
-      for (int k = 0; k < kRsCluster; ++k)
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k > 0 && k0 + k < C) {
+            s.x += v[k].x;
+            s.y += v[k].y;
+            s.z += v[k].z;
+            s.w += v[k].w;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < MOST; ++k)
         if (k < C) st_shared_cluster_v4(map_to_rank(at, k), s);
     }
   }
@@ -264,7 +268,8 @@ __device__ __forceinline__ void x0_pass(const MomentumArgs& P, const Items& I, i
   }
 }
 
-template <bool SPLIT>
+// MOST: CTAs of a cluster (8 or 16: the sums of sixteen need registers that cost the others 2 %).
+template <bool SPLIT, int MOST>
 __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __grid_constant__ ResidentArgs P, int C) {
   extern __shared__ uint8_t raw[];
   uint8_t* xs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __gr
           p[0] = make_float4(x.x + (y.x + z.x), x.y + (y.y + z.y), x.z + (y.z + z.z), x.w + (y.w + z.w));
         }
     }
-    if (C > 1) cluster_sum<SPLIT ? 64 : 128>(part, C, rank, tid);
+    if (C > 1) cluster_sum<SPLIT ? 64 : 128, MOST>(part, C, rank, tid);
     if (warp < kRsWarps) {
       if constexpr (SPLIT) {
         // (C = 1: the thread's own sums; else the cluster's, behind its barrier)
@@ -554,10 +559,11 @@ __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __gr
   if (warp == kRsWarps) tmem_dealloc<1>(tmem, 512);
 }
 
-template <bool SPLIT>
+template <bool SPLIT, int MOST>
 cudaError_t launch(const ResidentArgs& a, int C, cudaStream_t s) {
-  auto kern = muon_resident_kernel<SPLIT>;
+  auto kern = muon_resident_kernel<SPLIT, MOST>;
   cudaError_t err = allow_smem(kern, kRsSmem);
+  if (err == cudaSuccess && MOST > 8) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -580,11 +586,12 @@ cudaError_t launch(const ResidentArgs& a, int C, cudaStream_t s) {
 // within one part of the chip, so 152 SMs hold 76 of two, but 36 of four and 15
 // of eight).
 int clusters_at_once(int C) {
-  static std::atomic<int> known[64][4];
-  const int log = C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3;
+  static std::atomic<int> known[64][5];   // one more than the answer
+  int log = 0;
+  while (1 << log < C) ++log;
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return device_sms() / C;
-  if (dev < 64 && (n = known[dev][log].load()) > 0) return n;
+  if (dev < 64 && (n = known[dev][log].load()) > 0) return n - 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(C));
@@ -596,13 +603,14 @@ int clusters_at_once(int C) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = muon_resident_kernel<true>;
-  if (allow_smem(kern, kRsSmem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess ||
-      n <= 0) {
+  auto kern = C > 8 ? muon_resident_kernel<true, kRsCluster> : muon_resident_kernel<true, 8>;
+  if (allow_smem(kern, kRsSmem) != cudaSuccess ||
+      (C > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    return device_sms() / C;
+    return C > 8 ? 0 : device_sms() / C;
   }
-  if (dev < 64) known[dev][log].store(n);
+  if (dev < 64) known[dev][log].store(n + 1);
   return n;
 }
 
@@ -615,14 +623,16 @@ int clusters_at_once(int C) {
 // 41 (one) 46 (four), where the 128 x 128 sums cost more than they spare.  Those
 // sums also make clusters that need several turns slower than the tiled kernel:
 // 16 x 100 x 3000 183 against 132, 64 x 128 x 4096 499 against 405 (in one turn
-// 30 x 128 x 2000 92 against 133); 64 x 64 x 2048 is 150 against 232.
+// 30 x 128 x 2000 92 against 133); 64 x 64 x 2048 is 150 against 232.  Sixteen
+// CTAs, of which the device holds seven clusters, only where eight are too few
+// (6 x 128 x 6000 91 against 129) and in one turn.
 int resident_cluster(int batch, int m, int n, bool split) {
   if (m > 128 || n > kResidentMost) return 0;
   int C = 1;
   while (C * kRsSlice < n) C *= 2;
-  if (!split && C > 1 && batch > clusters_at_once(C)) return 0;
+  if (C > 8 ? batch > clusters_at_once(C) : !split && C > 1 && batch > clusters_at_once(C)) return 0;
   if (split || n > 256)
-    while (C < kRsCluster && C * 64 < n && batch <= clusters_at_once(2 * C)) C *= 2;
+    while (C < 8 && C * 64 < n && batch <= clusters_at_once(2 * C)) C *= 2;
   return C;
 }
 
@@ -631,7 +641,8 @@ cudaError_t launch_muon_resident(ResidentArgs a, int C, bool split, cudaStream_t
   a.m = a.tall ? a.cols : a.rows;
   a.n = a.tall ? a.rows : a.cols;
   a.slice = ((a.n + C - 1) / C + 63) / 64 * 64;
-  return split ? launch<true>(a, C, s) : launch<false>(a, C, s);
+  if (C > 8) return split ? launch<true, kRsCluster>(a, C, s) : launch<false, kRsCluster>(a, C, s);
+  return split ? launch<true, 8>(a, C, s) : launch<false, 8>(a, C, s);
 }
 
 }  // namespace mxg

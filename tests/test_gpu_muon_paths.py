@@ -62,6 +62,12 @@ def test_forms(batch, m, n, tall):
     (30, 128, 2000),            # on the chip, clusters of four
     (19, 64, 1024),             # the same, where eight would not fit at once
     (38, 100, 1000),            # clusters of two
+    (3, 48, 8192),              # clusters of sixteen, high and low parts
+    (2, 101, 5001),             # the same with one part, the last CTAs without columns
+    (9, 60, 4500),              # too many of them to stay on the chip
+    (9, 100, 4500),
+    (1, 40, 8200),              # too long for it
+    (1, 100, 9001),
 ])
 def test_many_matrices_and_long_ones(batch, m, n, tall):
     """The forms that need many or long matrices; the oracle on the first and the last one."""
