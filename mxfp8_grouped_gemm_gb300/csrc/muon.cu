@@ -264,6 +264,7 @@ struct NsArgs {
   const uint16_t* w_in;
   uint16_t* w_out;                        // nullable: w_in * w_keep - lr * value
   float w_keep, lr;
+  int b_low;                              // FUSED, not SPLIT: B has a low part
   int32_t* done;                          // [batch]: epilogue warps that have stored their part of a tile
   int32_t* shares;                        // [batch] (splits: [batch][sym_tiles][pair's CTA]): CTAs that have left their sum
   int32_t* status;
@@ -493,7 +494,9 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32
     ns_load_row(P.w_in, (static_cast<int64_t>(b) * P.rows + row0 + lane) * P.cols + col, row0 + lane < P.rows, col,
                 P.cols, w);
   if (!ready()) return false;
-  uint32_t h[32], l[SPLIT ? 32 : 1];
+  // KEPT and one part of A: B may have a low part all the same
+  constexpr bool B_LOW = KIND == NS_POLYNOMIAL && KEPT && !SPLIT;
+  uint32_t h[32], l[SPLIT || B_LOW ? 32 : 1];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t r[32];
@@ -528,7 +531,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32
         }
         if constexpr (KIND == NS_UPDATE || KIND == NS_WEIGHTS) {
           h[j] = pack_bf16x2(x, y);
-        } else if constexpr (SPLIT) {
+        } else if constexpr (SPLIT || B_LOW) {
           h[j] = split_half2(x, y, l[j]);
         } else {
           const __half2 v = __floats2half2_rn(x, y);
@@ -544,6 +547,8 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& P, float alpha, uint32
       uint16_t* p = dst.p + (static_cast<int64_t>(b) * dst.rows + row0 + lane) * dst.ld + col;
       ns_store_direct(h, p, in, col, dst.cols);
       if constexpr (LOW) ns_store_direct(l, p + dst.low, in, col, dst.cols);
+      if constexpr (B_LOW)
+        if (P.b_low) ns_store_direct(l, p + dst.low, in, col, dst.cols);
     } else if (any) {
       ns_store_box(h, boxes + flip * kNsOut, dst.map, row0, col, b, lane);
       flip ^= 1;
@@ -682,6 +687,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
                         ((FUSED ? 1 : 1 + P.splits) * P.sym_tiles + P.app_m * P.app_n);
   // in parts: first (high, low), (low, high), then (high, high)
   constexpr int parts = SPLIT ? 3 : 1;
+  const bool b_parts = FUSED && !SPLIT && P.b_low;      // X' = (B's low part) X + (its high part) X
   auto fail = [&]() {
     report(P.status, MXG_ERR_TIMEOUT);
     *abort_flag = 1;
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const bool shared = FUSED && tc.op == NS_GRAM;
         const bool part_of = shared || (!FUSED && tc.op == NS_GRAM && P.splits > 1);
         const int first = part_of ? ns_share_begin<FUSED>(P, o, tc.share) : 0;
-        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * o.nk;
+        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * (b_parts && tc.op == NS_APPLY ? 2 : 1) * o.nk;
         if (!ns_wait_done(P, tc, abort_flag)) {
           fail();
           aborted = true;
@@ -731,7 +737,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
                           &full[stage]);
             }
           } else {
-            const int z = tc.b + (SPLIT && part == (second ? 0 : 1) ? P.batch : 0);
+            const bool low = SPLIT ? part == (second ? 0 : 1) : b_parts && part == 0 && second == (P.tall != 0);
+            const int z = tc.b + (low ? P.batch : 0);
             if ((BN == 64 && second) || (halved && second == (P.tall != 0))) ns_load<false, 1>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
             else if (!PAIR || rank == 0) ns_load<false, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, &full[stage], 0u);
             else ns_load<true, 2>(dst, map, kb < mn_stages, row, kb * kNsK, z, nullptr, full0 + stage * 8);
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_kernel(const __grid_constant
         const bool shared = FUSED && tc.op == NS_GRAM;
         const bool part_of = shared || (!FUSED && tc.op == NS_GRAM && P.splits > 1);
         const int first = part_of ? ns_share_begin<FUSED>(P, o, tc.share) : 0;
-        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * o.nk;
+        const int stages = part_of ? ns_share_begin<FUSED>(P, o, tc.share + 1) : parts * (b_parts && tc.op == NS_APPLY ? 2 : 1) * o.nk;
         for (int kp = first, kb = shared ? 0 : first; kp < stages; ++kp) {
           const bool in = PAIR ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, kWaitLimitNs)
                                : mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
@@ -1327,7 +1334,7 @@ NsPlan ns_plan(int batch, int rows, int cols) {
   p.x0 = w.take(xb);
   p.x1 = w.take(xb);
   p.a = w.take(ab);
-  p.b = w.take(ab);
+  p.b = w.take(p.m <= 128 && !p.split && muon_b_low(p.m, p.n) ? 2 * ab : ab);
   // the shares of the sums of A
   p.a_parts = w.take(p.splits > 1 ? 4ll * 128 * p.bn * ctas * batch * p.sym_tiles * p.splits
                      : p.m <= 128 && p.sym_tiles > 1 ? (p.split ? 4ll * 64 * 64 : 4ll * 128 * 128) * batch * p.sym_tiles
@@ -1448,16 +1455,18 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   n.shares = done + a->batch * kNsLine;
   n.sym_tiles = p.sym_tiles;
   n.splits = p.splits;
+  n.b_low = p.m <= 128 && !p.split && muon_b_low(p.m, p.n);
   n.a_parts = api::at<float>(a->workspace, p.a_parts);
   n.status = a->dev_status;
   const int64_t mats = static_cast<int64_t>(a->batch) * (p.split ? 2 : 1);
+  const int64_t b_mats = n.b_low ? 2ll * a->batch : mats;
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     ok = ok && tma_map_b16_3d(&n.x[i], x[i], a->cols, a->rows, mats, p.ldx, 64);
     ok = ok && tma_map_b16_3d(&n.xs[i], x[i], a->cols, a->rows, mats, p.ldx, 32);
   }
   ok = ok && tma_map_b16_3d(&n.a, am, p.m, p.m, mats, p.lda, 64) && tma_map_b16_3d(&n.as, am, p.m, p.m, mats, p.lda, 32);
-  ok = ok && tma_map_b16_3d(&n.b, bm, p.m, p.m, mats, p.lda, 64) && tma_map_b16_3d(&n.bs, bm, p.m, p.m, mats, p.lda, 32);
+  ok = ok && tma_map_b16_3d(&n.b, bm, p.m, p.m, b_mats, p.lda, 64) && tma_map_b16_3d(&n.bs, bm, p.m, p.m, b_mats, p.lda, 32);
   // whole 32-byte pieces of the caller's rows, one output
   const bool by_rows = a->cols % 16 != 0 || (a->w_out && a->update);
   if (!by_rows)

@@ -151,6 +151,15 @@ __device__ __forceinline__ float momentum_u1(const MomentumArgs& P, int64_t i) {
   return P.nesterov ? fmaf(P.mu, P.mom_out[i], g) : P.mom_out[i];
 }
 
+// Whether B has a low part too (short side m of 65 to 128, long side n).  B's
+// rounding is the largest error of an update from a few strong directions over
+// noise (simulated, 96 x 3000: 1.8e-3 of X from B, 1.1e-3 from A, 0.7e-3 from X;
+// the bf16 result's own rounding 1.66e-3).  Measured, times that rounding, one
+// part and two: 96 x 958 1.49 1.24, 90 x 6000 1.70 1.28, 80 x 3000 1.61 1.30, but
+// 128 x 6000 1.36 1.18 and 96 x 300 1.35 1.19, where one part is enough (two cost
+// 8-10 % of the time).
+__host__ __device__ constexpr bool muon_b_low(int m, int n) { return m < 120 && n > 512; }
+
 // u / |u| 2^ex is u times these three factors, in this order, so that no
 // intermediate leaves fp32's range; n2 = |u|^2.
 __device__ __forceinline__ void norm_factors(double n2, int ex, float (&f)[3]) {

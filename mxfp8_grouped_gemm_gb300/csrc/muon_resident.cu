@@ -18,6 +18,8 @@
 // fp16 parts; one product yields all pairs of parts, and
 // A = (high, high) + (high, low) + (low, high).
 //
+// Otherwise A and X have one part, and B one or two (see muon_b_low).
+//
 // Latency bounds it: a step is a chain of three products of 1-2 k cycles and
 // the passes between them.  4 x 128 x 256, five steps: 41 us, of 78 k cycles 12 k
 // for the momentum, 4 k for the norm and 10 k for X0 (57 us tiled); 20 x 64 x 512
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __gr
   const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
   const uint64_t xd = smem_desc(smem_u32(xs), 0, 1024, kLayoutSwizzle128B);            // K-major
   const uint64_t xm = smem_desc(smem_u32(xs), kRsBox, 1024, kLayoutSwizzle128B);       // MN-major
+  const bool b_low = !SPLIT && muon_b_low(P.m, P.n);
   const uint64_t ad = smem_desc(smem_u32(ab), 0, 1024, kLayoutSwizzle128B);
   const int ksteps = (P.m + 15) / 16;
   uint32_t phase = 0;
@@ -489,15 +492,18 @@ __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __gr
           uint4* p = reinterpret_cast<uint4*>(ab + hf * kRsBox + row * 128 + swz(j, row));
           const uint4 a4 = *p;                               // the A that was multiplied: eleven bits, as the product saw it
           const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-          uint32_t o[4];
+          uint32_t o[4], l[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 af = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
             const int c = hf * 64 + 8 * j + 2 * i;
-            o[i] = half2_bits(fmaf(P.beta, af.x, v[8 * j + 2 * i]) + (row < P.m && row == c ? P.diag : 0.f),
-                              fmaf(P.beta, af.y, v[8 * j + 2 * i + 1]) + (row < P.m && row == c + 1 ? P.diag : 0.f));
+            o[i] = split_half2(fmaf(P.beta, af.x, v[8 * j + 2 * i]) + (row < P.m && row == c ? P.diag : 0.f),
+                               fmaf(P.beta, af.y, v[8 * j + 2 * i + 1]) + (row < P.m && row == c + 1 ? P.diag : 0.f), l[i]);
           }
           *p = make_uint4(o[0], o[1], o[2], o[3]);
+          // B's low part, where the sums were
+          if (b_low)
+            *reinterpret_cast<uint4*>(part + hf * kRsBox + row * 128 + swz(j, row)) = make_uint4(l[0], l[1], l[2], l[3]);
         }
       }
     }
@@ -512,14 +518,15 @@ __global__ void __launch_bounds__(kRsThreads, 1) muon_resident_kernel(const __gr
         for (int c = 0; c < P.slice; c += 256) {
           const uint32_t id = idesc_f16(128, min(256, P.slice - c)) | kIdescBMn;
           const uint64_t qb = xm + (c / 64 * kRsBox >> 4);
-          for (int p = 0; p < (SPLIT ? 3 : 1); ++p) {
-            const uint64_t pa = ad + (SPLIT && p == 1 ? kRsBox >> 4 : 0);
+          const int p0 = SPLIT || b_low ? 0 : 1;
+          for (int p = p0; p < (SPLIT ? 3 : 2); ++p) {      // one part of X: B's low part, then its high part
+            const uint64_t pa = SPLIT ? ad + (p == 1 ? kRsBox >> 4 : 0) : p == 0 ? ad + (kRsAb >> 4) : ad;
             const uint64_t qa = qb + (SPLIT && p == 0 ? 64 * 128 >> 4 : 0);            // low parts: rows 64 ..
 #pragma unroll
             for (int k = 0; k < (SPLIT ? 4 : 8); ++k)
               if (k < ksteps)
                 mma_bf16<1>(tmem + c, pa + (((k >> 2) * kRsBox + (k & 3) * 32) >> 4), qa + k * (2048 >> 4), id,
-                            (p | k) != 0 ? 1u : 0u);
+                            p != p0 || k != 0 ? 1u : 0u);
           }
         }
         mma_commit<1>(bar);

@@ -83,6 +83,22 @@ def test_many_matrices_and_long_ones(batch, m, n, tall):
     assert torch.equal(upd, mx.mxg_muon_update(g, status, scale=0.7))
 
 
+@pytest.mark.parametrize("batch,m,n", [(3, 90, 6000), (2, 96, 3000), (1, 80, 9000), (40, 100, 700)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_few_strong_directions(batch, m, n, tall):
+    """Short sides of 65 to 119, where B's rounding would be the largest error: with B in two parts the update's own
+    rounding (1.66e-3), A's (1.1e-3 of the result) and X's (0.7e-3) are left, 2.1e-3 together; with a tenth of margin."""
+    mx = require_gpu()
+    rows, cols = (n, m) if tall else (m, n)
+    g = torch.from_numpy(_grad(batch, rows, cols, 9 * m + n)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    upd = mx.mxg_muon_update(g, status)
+    ends = sorted({0, batch - 1})
+    got, ref = np_(upd[ends]).astype(np.float64), _orth(g[ends].double().cpu().numpy())
+    assert int(status.item()) == 0
+    assert np.linalg.norm(got - ref) <= 2.3e-3 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("rows,cols", [(48, 96), (96, 48), (100, 5000), (200, 304), (304, 200), (201, 303)])
 def test_update_and_weights_together(rows, cols):
     """Both outputs of one call are what each gives alone."""
