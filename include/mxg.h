@@ -221,6 +221,8 @@ int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router, const flo
  * stays in its own.
  * Pointers are 32-byte aligned; momentum_out may be momentum_in and w_out may
  * be w_in, other buffers do not overlap.
+ * The workspace query is for the current device (its SM count decides which
+ * form runs).  The tiled form launches its products cooperatively.
  * Requires batch <= 65535, rows and cols <= 2^21, batch * max(rows, cols) < 2^31 - 256. */
 typedef struct {
   int32_t batch, rows, cols;
