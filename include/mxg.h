@@ -244,6 +244,12 @@ typedef struct {
   int32_t* dev_status;
 } mxg_muon_args;
 size_t mxg_muon_workspace_bytes(int batch, int rows, int cols);
+/* The form that these sizes take on the current device, to form[4]:
+ *   [0] CTAs of the cluster that keeps a matrix on the chip, 0: tiled products
+ *   [1] tiled: columns of a tile (64, 128; 256: a pair of SMs), else 0
+ *   [2] tiled: CTAs (pairs) that share the contraction of a tile of X X^T, else 0
+ *   [3] fp16 parts of X (2 for a short side up to 64) */
+int mxg_muon_form(int batch, int rows, int cols, int32_t* form);
 int mxg_muon_update(const mxg_muon_args* args, void* stream);
 
 /* ----------------------------------------------------------------------------

@@ -14,6 +14,6 @@ from ._lib import (  # noqa: F401
     mxg_router_fwd_permute, mxg_grouped_mlp_fwd_grouped_mx,
     mxg_balance_loss_bwd, mxg_balance_loss_fwd, mxg_balance_loss_workspace_bytes,
     mxg_router_linear_bwd, mxg_router_linear_bwd_workspace_bytes,
-    MUON_COEFFICIENTS, MuonArgs, mxg_muon_update, mxg_muon_workspace_bytes,
+    MUON_COEFFICIENTS, MuonArgs, mxg_muon_form, mxg_muon_update, mxg_muon_workspace_bytes,
 )
 from .layer import GroupedExperts, GroupedMLP  # noqa: F401

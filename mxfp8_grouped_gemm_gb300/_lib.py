@@ -42,6 +42,7 @@ EXPORTS = [
     "mxg_router_fwd_permute", "mxg_grouped_mlp_fwd_grouped_mx",
     "mxg_balance_loss_workspace_bytes", "mxg_balance_loss_fwd", "mxg_balance_loss_bwd",
     "mxg_router_linear_bwd_workspace_bytes", "mxg_router_linear_bwd", "mxg_muon_workspace_bytes", "mxg_muon_update",
+    "mxg_muon_form",
 ]
 
 FWD_STAGES = ["permute", "quant_weights", "quant_x", "gate_up", "down", "combine"]
@@ -177,6 +178,7 @@ def lib() -> ctypes.CDLL:
         "mxg_router_linear_bwd_workspace_bytes": (SZ, [I32, I32, I32]),
         "mxg_router_linear_bwd": (I32, [P, P, P, P, I32, I32, I32, P, P, P, SZ, P, P]),
         "mxg_muon_workspace_bytes": (SZ, [I32, I32, I32]),
+        "mxg_muon_form": (I32, [I32, I32, I32, ctypes.POINTER(I32)]),
         "mxg_muon_update": (I32, [ctypes.POINTER(MuonArgs), P]),
     }
     for name, (res, args) in sig.items():
@@ -416,6 +418,14 @@ def mxg_router_linear_bwd(x, w_router, dlogits, dx_in, dev_status, dx=None, dw_r
 
 def mxg_muon_workspace_bytes(batch, rows, cols) -> int:
     return int(lib().mxg_muon_workspace_bytes(batch, rows, cols))
+
+
+def mxg_muon_form(batch, rows, cols) -> dict:
+    """The form that an update of these sizes takes on the current device: `cluster` CTAs keep a matrix on the chip, or,
+    where that is 0, products in tiles of `tile` columns, `shares` CTAs to a tile of X X^T; X in `parts` fp16 numbers."""
+    form = (ctypes.c_int * 4)()
+    _check("mxg_muon_form", lib().mxg_muon_form(batch, rows, cols, form))
+    return dict(zip(("cluster", "tile", "shares", "parts"), form))
 
 
 MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)

@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 // 1024 bytes apart; a K = 16 step is 16 rows, 2048 bytes).
 //
 // X X^T has the fewest tiles and the longest contraction.  Where SMs would be
-// idle, several CTAs share a tile's contraction: each leaves its fp32 sums in
-// global memory, and the one that is last to do so adds them up in order.
+// idle, or the contraction is too long for one accumulator (kNsLongest), several
+// CTAs share it: each leaves its fp32 sums in global memory, and the one that is
+// last to do so adds them up in order.
 //
 // FUSED (a short side of at most 128): A is one tile, so both operands of
 // X X^T are the same 128 rows.  They are loaded once, and a stage holds 128
@@ -1225,6 +1226,20 @@ struct NsPlan {
 // 16 x 2000, 2.2e-3 from 64 x 64 to 256 x 256; two parts 1.67e-3.
 constexpr int kNsSplitMost = 64;          // not above 128: only single tiles of A split
 
+// The longest contraction of X X^T that one accumulator takes.  The tensor cores
+// cut their running sums, by about 1.5e-8 of the result per instruction (16
+// elements), and the diagonal of X X^T is a sum of squares: all of it is cut the
+// same way, and the quintic's steps magnify the bias of A by up to 30 in X.
+// Measured in one accumulator, 4 x n, the result's gain 1 + g: g = 1.8e-3 at n =
+// 65536, 2.4e-3 at 131072, 1.0e-2 at 524288, 3.7e-2 at 2097152; longer sides are
+// therefore added up in fp32 from shares, whether SMs are idle or not.  Where A is
+// one tile a share costs little: 4 x n then has g at most 5e-4 at any n (152 x 4 x
+// 131072 15.0 -> 15.3 ms, 152 x 4 x 2097152 233 -> 285).  With more tiles there are
+// more, smaller singular values, whose first steps hardly see A (130 x 131072 in
+// one accumulator 1.1e-3, in two 4e-4 at the same time).
+constexpr int kNsLongestOne = 16384;      // A one tile
+constexpr int kNsLongest = 65536;
+
 // CTAs that share the contraction n of a single-tile A while SMs are idle: a
 // stage of 128 elements takes about 550 cycles; leaving and joining the sums
 // about 3500 and, per CTA, what it takes to read 64 x 64 (split) or 128 x 128
@@ -1232,9 +1247,10 @@ constexpr int kNsSplitMost = 64;          // not above 128: only single tiles of
 int ns_shares(int batch, int m, int n, int split) {
   if (m > 128) return 1;
   const int stages = (n + 2 * kNsK - 1) / (2 * kNsK);
-  const int most = std::min(std::min(device_sms() / batch, stages), 16);
-  int best = 1, best_cost = stages * 550;
-  for (int s = 2; s <= most; ++s) {
+  const int least = (n + kNsLongestOne - 1) / kNsLongestOne;
+  const int most = std::max(least, std::min(std::min(device_sms() / batch, stages), 16));
+  int best = 1, best_cost = least > 1 ? INT_MAX : stages * 550;
+  for (int s = std::max(least, 2); s <= most; ++s) {
     const int cost = (stages + s - 1) / s * 550 + 3500 + s * (split ? 400 : 1300);
     if (cost < best_cost) {
       best_cost = cost;
@@ -1277,11 +1293,12 @@ double ns_step_cost(int batch, int rows, int cols, int* splits) {
   const double x = static_cast<double>(batch) * ((rows + TM - 1) / TM) * ((cols + BN - 1) / BN);
   auto product = [&](double tiles, int stages) { return 3000 + std::max(1.0, tiles / units) * (stages * stage + epilogue); };
   const double others = product(a, short_k) + product(x, short_k);
-  double gram = product(a, long_k);
+  const int least = (n + kNsLongest - 1) / kNsLongest;
+  double gram = least > 1 ? HUGE_VAL : product(a, long_k);
   *splits = 1;
-  const int most = static_cast<int>(std::min({units / a, static_cast<double>(long_k), 16.0}));
-  for (int s = 2; s <= most; ++s) {
-    const double c = product(1, (long_k + s - 1) / s) + (PAIR ? 6000 + 2000 * s : BN == 128 ? 4500 + 1300 * s : 3700 + 750 * s);
+  const int most = std::max(least, static_cast<int>(std::min({units / a, static_cast<double>(long_k), 16.0})));
+  for (int s = std::max(least, 2); s <= most; ++s) {
+    const double c = product(a * s, (long_k + s - 1) / s) + (PAIR ? 6000 + 2000 * s : BN == 128 ? 4500 + 1300 * s : 3700 + 750 * s);
     if (c < gram) {
       gram = c;
       *splits = s;
@@ -1362,6 +1379,17 @@ using namespace mxg;
 extern "C" size_t mxg_muon_workspace_bytes(int batch, int rows, int cols) {
   if (muon_shape(batch, rows, cols) != MXG_OK) return 0;
   return static_cast<size_t>(ns_plan(batch, rows, cols).bytes);
+}
+
+extern "C" int mxg_muon_form(int batch, int rows, int cols, int32_t* form) {
+  if (!form) return MXG_ERR_ARG;
+  if (const int err = muon_shape(batch, rows, cols)) return err;
+  const NsPlan p = ns_plan(batch, rows, cols);
+  form[0] = p.cluster;
+  form[1] = p.bn;
+  form[2] = p.cluster != 0 ? 0 : p.m <= 128 ? p.sym_tiles : p.splits;
+  form[3] = p.split ? 2 : 1;
+  return MXG_OK;
 }
 
 extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
