@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kRlThreads, 1)
 
 // G in three bf16 parts: parts[t][group][part][eg], zero past E.  Each part
 // takes the next eight significant bits (cut, so that the parts add up to g
-// exactly and none overflows); an infinity or NaN stays in the first.
+// exactly and none overflows); an infinity or NaN stays in the first, a NaN with
+// the quiet bit set, since the bits that are cut off may be all that it has.
 __global__ void __launch_bounds__(256) router_split_kernel(const float* __restrict__ g, int T, int E, int eg,
                                                           int groups, uint16_t* __restrict__ parts, int units,
                                                           int32_t* __restrict__ count) {
@@ -641,6 +642,7 @@ __global__ void __launch_bounds__(256) router_split_kernel(const float* __restri
   for (int i = 0; i < 4; ++i) {
     p[0][i] = v[i] >> 16;
     p[1][i] = p[2][i] = 0u;
+    if ((v[i] & 0x7fffffffu) > 0x7f800000u) p[0][i] |= 0x40u;
     if ((v[i] & 0x7f800000u) != 0x7f800000u) {
       const float r = __uint_as_float(v[i]) - __uint_as_float(v[i] & 0xffff0000u);
       const uint32_t b = __float_as_uint(r) & 0xffff0000u;
