@@ -161,7 +161,8 @@ int mxg_router_bwd(const uint16_t* x, const uint16_t* w_router, const int32_t* i
  *   logits      fp32 [T][E]; -inf switches an expert off for the token (a row
  *               of -inf has p = 0); NaN and +inf give NaN
  *   ids         int32 [T][k], the route (mxg_route_topk, mxg_router_fwd)
- *   token_mask  nullable uint8 [T]: 0 = the token (padding) does not count
+ *   token_mask  nullable uint8 [T]: 0 = the token (padding) does not count and
+ *               its ids are not read
  *   loss        fp32 [1] out;  counts int32 [E] out: c_e
  *   prob_sums   fp32 [E] out: P_e;  n_tokens int32 [1] out: n
  *   workspace   >= mxg_balance_loss_workspace_bytes(T, E) bytes
@@ -186,7 +187,12 @@ int mxg_balance_loss_fwd(const float* logits, const int32_t* ids, const uint8_t*
  *   dloss                 nullable fp32 [1]: the loss's own gradient (1 if null)
  *   ids, probs, dprobs    all three or none: int32, fp32, fp32 [T][k]
  *   dlogits               fp32 [T][E] out
- * Requirements and reporting as mxg_balance_loss_fwd. */
+ * The route's part is added for tokens that token_mask drops as well: where
+ * such a token has a route, its dprobs are zero if its output carries no
+ * gradient.  Ids outside [0, E) add nothing; they are reported as
+ * MXG_ERR_EXPERT_ID on tokens that count.  A token that token_mask drops may have
+ * no route at all: all its ids out of range, its probs and dprobs arbitrary.
+ * Requirements as mxg_balance_loss_fwd. */
 int mxg_balance_loss_bwd(const float* logits, const uint8_t* token_mask, const int32_t* counts,
                          const int32_t* n_tokens, int T, int E, int k, float coef, const float* dloss,
                          const int32_t* ids, const float* probs, const float* dprobs, float* dlogits,

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
     float d[kBlVals];
 #pragma unroll
     for (int i = 0; i < kBlVals; ++i) d[i] = live ? up * z[i] * (dev[i] - mean) : 0.f;
-    const bool here = in;
+    const bool here = in, kept = live;
     const int64_t pick = static_cast<int64_t>(t) * k;
     float* dst = dlogits + row;
     t += step;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kBlBwdThreads) balance_bwd_kernel(
         for (int j = 0; j < k; ++j) {
           const int e = ids[pick + j];
           if (e < 0 || e >= E) {
-            if (gl == 0) report(status, MXG_ERR_EXPERT_ID);
+            if (gl == 0 && kept) report(status, MXG_ERR_EXPERT_ID);      // a dropped token may have no route
           } else if (lane_of<LPT, VEC>(e) == gl) {
             const float q = probs[pick + j];
             const float g = q * (dprobs[pick + j] - inner);
