@@ -222,8 +222,9 @@ int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router, const flo
  *   update = scale X                                  (bf16, rounded once)
  *   w_out  = w_in (1 - lr weight_decay) - lr scale X  (bf16, rounded once)
  * The products take fp16 operands scaled by powers of two and add up in fp32;
- * a, b, c must keep the singular values of X within about 2 (3.4445, -4.7750,
- * 2.0315 keep them below 1.3).  Matrices are independent: a NaN or infinity
+ * a, b, c must keep the singular values of X within about 2 and, on them, the
+ * polynomial a + b s^2 + c s^4 within 15.99, where B overflows (3.4445, -4.7750,
+ * 2.0315 keep them below 1.3, and within 3.45); |a| >= 15.99 is refused.  Matrices are independent: a NaN or infinity
  * stays in its own.
  * Pointers are 32-byte aligned; momentum_out may be momentum_in and w_out may
  * be w_in, other buffers do not overlap.

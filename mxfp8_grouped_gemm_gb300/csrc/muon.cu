@@ -1398,6 +1398,7 @@ extern "C" int mxg_muon_update(const mxg_muon_args* a, void* stream) {
   if ((a->w_in != nullptr) != (a->w_out != nullptr)) return MXG_ERR_ARG;
   if (!a->update && !a->w_out) return MXG_ERR_ARG;
   if (a->steps < 1 || a->steps > 64) return MXG_ERR_ARG;
+  if (!(std::fabs(a->a) < kMostA)) return MXG_ERR_ARG;
   if (const int err = muon_shape(a->batch, a->rows, a->cols)) return err;
   if (!api::aligned32(a->grad) || !api::aligned32(a->momentum_in) || !api::aligned32(a->momentum_out) ||
       !api::aligned32(a->update) || !api::aligned32(a->w_in) || !api::aligned32(a->w_out) ||

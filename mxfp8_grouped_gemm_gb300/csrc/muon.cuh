@@ -23,6 +23,7 @@ struct MomentumArgs {
 namespace {
 
 constexpr int kExpA = 12;                 // A and B are stored times 2^12
+constexpr float kMostA = 15.99f;          // a 2^12 is B's diagonal for small singular values: fp16 ends at 65504
 
 // ------------------------------------------------------------------ momentum
 // Sum of squares that neither overflows nor underflows for any fp32 input:
