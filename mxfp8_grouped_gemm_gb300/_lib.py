@@ -293,8 +293,10 @@ def _empty(shape, dtype, device, stream):
 
 class _ScratchCache(threading.local):
     """Small scratch kept per thread, device and stream: making and dropping a tensor takes longer than a launch.
-    Calls of one thread on one stream follow one another, so they can share it."""
+    Calls of one thread on one stream follow one another, so they can share it.  A stream is known by its handle, as
+    in torch's allocator: one that is not torch's is destroyed only after its work has ended."""
     BYTES = 1 << 20
+    MOST = 64                              # as many streams; the oldest makes room (its memory goes to its stream's pool)
 
     def __init__(self):
         self.kept = {}
@@ -303,6 +305,8 @@ class _ScratchCache(threading.local):
         key = (device.index, handle)
         t = self.kept.get(key)
         if t is None:
+            if len(self.kept) >= self.MOST:
+                del self.kept[next(iter(self.kept))]
             t = self.kept[key] = torch.empty(self.BYTES, dtype=torch.uint8, device=device)
         return t
 
