@@ -44,14 +44,20 @@ class MoETraining:
                             weights=weight, lr=self.lr, weight_decay=self.weight_decay)
 
     def step(self, x, target, token_mask=None):
-        """One step on x, target bf16 [T, H] -> (mean squared error, balance loss, tokens per expert), on the device."""
+        """One step on x, target bf16 [T, H] -> (mean squared error, balance loss, tokens per expert), on the device.
+        Tokens that token_mask drops (padding) count in neither loss."""
         layer, k = self.layer, self.k
         logits, ids, probs = mxg.mxg_router_fwd(x, self.w_router, k)
         balance, counts, _, n = mxg.mxg_balance_loss_fwd(logits, ids, self.coef, self.status, token_mask=token_mask)
         y, _ = layer.forward(x, ids, probs, self.w_gate_up, self.w_down)
         err = y.float() - target.float()
-        mse = err.square().mean()
-        dx, dw_gate_up, dw_down, dprobs = layer.backward((err * (2.0 / err.numel())).bfloat16())
+        if token_mask is None:
+            mse, dy = err.square().mean(), err * (2.0 / err.numel())
+        else:
+            err = err.masked_fill(token_mask[:, None] == 0, 0.0)
+            per = 1.0 / (n.clamp(min=1) * err.shape[1])
+            mse, dy = err.square().sum() * per[0], err * (2.0 * per)
+        dx, dw_gate_up, dw_down, dprobs = layer.backward(dy.bfloat16())
         # the route's gradient and the balance loss's, on all logits; then through the router's linear layer
         dlogits = mxg.mxg_balance_loss_bwd(logits, counts, n, k, self.coef, self.status, token_mask=token_mask,
                                            route=(ids, probs, dprobs))
