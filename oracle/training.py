@@ -78,3 +78,45 @@ def orthogonalise(u, steps, coefficients):
         s = x @ x.T
         x = a * x + (b * s + c * (s @ s)) @ x
     return x.T if tall else x
+
+
+def _fp16_parts(v, scale, parts):
+    """v as the sum of one or two fp16 numbers held times `scale`."""
+    out, rest = [], np.asarray(v, np.float64) * scale
+    for _ in range(parts):
+        h = rest.astype(np.float16).astype(np.float64)
+        out.append(h / scale)
+        rest = rest - h
+    return out
+
+
+def bf16_round(v):
+    """Nearest bf16 value (ties to even) of each finite element."""
+    u = np.ascontiguousarray(v, np.float32).view(np.uint32)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) & np.uint32(0xFFFF0000)).view(np.float32).astype(np.float64)
+
+
+def orthogonalise_in_fp16(u, steps, coefficients, x_parts, b_parts, lost=None):
+    """`orthogonalise` in the GPU's number format, all else in 64 bits: X and A in x_parts fp16 numbers, B in b_parts
+    (X times the power of two next to sqrt(long side), A and B times 2^12), low parts multiplied by high ones only,
+    the result rounded to bf16.  It tells what of an update's error is the format's own.  lost = (product, i, j) leaves
+    out part i of its first operand times part j of its second, for tests of what a bound can see."""
+    a, b, c = coefficients
+    x = u / np.sqrt((u * u).sum())
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    sx = 1
+    while sx * sx < x.shape[1]:
+        sx *= 2
+
+    def product(name, p, q):
+        return sum(p[i] @ q[j] for i in range(len(p)) for j in range(len(q)) if i + j < 2 and (name, i, j) != lost)
+
+    xp = _fp16_parts(x, sx, x_parts)
+    for _ in range(steps):
+        ap = _fp16_parts(product("A", xp, [v.T for v in xp]), 4096.0, x_parts)
+        bp = _fp16_parts(a * np.eye(x.shape[0]) + b * sum(ap) + c * product("B", ap, ap), 4096.0, b_parts)
+        x = product("X", bp, xp)
+        xp = _fp16_parts(x, sx, x_parts)
+    return bf16_round(x.T if tall else x)
