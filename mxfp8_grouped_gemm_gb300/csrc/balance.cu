@@ -59,11 +59,12 @@ __device__ __forceinline__ int value_of(int e) {
   return VEC ? ((e >> 2) / LPT) * 4 + (e & 3) : e / LPT;
 }
 
-// e^d for d <= 0 (NaN stays; e^-200 and less are 0, as -inf): 2 to the power of
-// d log2 e, the product taken in two pieces y + lo since a power magnifies y's
-// rounding by y, and 2^lo = 1 + lo ln 2 for the tiny piece.  Within 2 ulp
-// (2^-22.5 of ex2 and one rounding), with fewer instructions than expf, which
-// has to serve all arguments.
+// e^d for d <= 0 (NaN stays): 2 to the power of d log2 e, the product taken in
+// two pieces y + lo since a power magnifies y's rounding by y, and 2^lo = 1 + lo
+// ln 2 for the tiny piece.  The relative error is below 2^-22 (ex2's 2^-22.5 and
+// one rounding).  What is below fp32's normal numbers (d < -87.33) becomes zero,
+// and so arguments can be kept above -200, where -inf would make lo NaN.  Fewer
+// instructions than expf, which has to serve all arguments.
 __device__ __forceinline__ float exp_neg(float d) {
   constexpr double kLog2e = 1.4426950408889634;
   constexpr float kHi = static_cast<float>(kLog2e), kLo = static_cast<float>(kLog2e - kHi);
