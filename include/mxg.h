@@ -221,11 +221,18 @@ int mxg_router_linear_bwd(const uint16_t* x, const uint16_t* w_router, const flo
  *          A = X X^T,  X <- a X + (b A + c A A) X     (X^T X for a tall matrix)
  *   update = scale X                                  (bf16, rounded once)
  *   w_out  = w_in (1 - lr weight_decay) - lr scale X  (bf16, rounded once)
- * The products take fp16 operands scaled by powers of two and add up in fp32;
+ * The products take fp16 operands scaled by powers of two and add up in fp32.
+ * For a short side up to 64 they are held in two fp16 parts, and the update is
+ * the exact one but for its own rounding (1.7e-3 of its norm).  Above that in
+ * one (B in two for 65 to 119 with a long side over 512), and the error is 2.0
+ * to 2.5e-3 where the singular values of u are of one size, but more where they
+ * fall off: the rounding of X fills directions that are nearly empty, and the
+ * steps multiply those by up to a^steps (485).  512 x 1024: singular values 1/i
+ * 4e-3, 1/i^2 2e-2, rank 64 2e-2, rank 8 4e-2, rank 1 1.5e-1.
  * a, b, c must keep the singular values of X within about 2 and, on them, the
  * polynomial a + b s^2 + c s^4 within 15.99, where B overflows (3.4445, -4.7750,
- * 2.0315 keep them below 1.3, and within 3.45); |a| >= 15.99 is refused.  Matrices are independent: a NaN or infinity
- * stays in its own.
+ * 2.0315 keep them below 1.3, and within 3.45); |a| >= 15.99 is refused.
+ * Matrices are independent: a NaN or infinity stays in its own.
  * Pointers are 32-byte aligned; momentum_out may be momentum_in and w_out may
  * be w_in, other buffers do not overlap.
  * The workspace query is for the current device (its SM count decides which

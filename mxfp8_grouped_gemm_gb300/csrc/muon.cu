@@ -28,6 +28,13 @@
 //   A 2^12, B 2^12          (entries at most ~1.5 and ~5).
 // Folding a I into B rounds a + B_ii to eleven bits, an error of the size of
 // X's own rounding, and spares the last product a second read of X.
+// One part serves gradients whose singular values are of one size (2.0-2.5e-3 of
+// the update, 1.66e-3 of it bf16's rounding).  Directions that are nearly empty
+// fill with X0's rounding, 1.7e-4 of its norm, and are multiplied by up to a^5 =
+// 485: 0.15 of a rank-1 update, 0.04 at rank 8, 4e-3 for singular values 1 / i.
+// Two parts of X in the first three steps would take 6 products more than the 15
+// (of m x m x n) of a long matrix; up to 64 rows, where a tile has room for both
+// parts, all operands have two and only the result's rounding is left.
 // Sums are fp32 (tensor-core accumulators); momentum and norms are fp32/fp64.
 #include <cuda_fp16.h>
 
@@ -182,9 +189,9 @@ __global__ void __launch_bounds__(kMoThreads) cast_kernel(MomentumArgs P, int ch
 //
 // What bounds them: long contractions the tensor cores and the power cap (1 x
 // 28672 x 4096, X X^T 1.66-1.81 PFLOP/s, all five steps 1.55), a pair's tiles of
-// K = 1024 what an SM takes in (57 bytes a cycle; the MMAs alone need 8.2 k
-// cycles a tile, with their loads 11-13 k; 64 x 2048 x 1024 1.9 ms for five
-// steps, 1.35 PFLOP/s), small and middling matrices the hand-over from product
+// K = 1024 the refill of stages that MMAs hold while they read them (40-48 bytes a
+// cycle and SM, 64 at the full rate: the MMAs alone need 8.2 k cycles a tile, with
+// their loads 11-13 k; 64 x 2048 x 1024 1.9 ms for five steps, 1.35 PFLOP/s), small and middling matrices the hand-over from product
 // to product: 1.0 k cycles to see the count, 1.3 k for the first loads, 0.7 k
 // from the last MMA to the epilogue, 1.2 k there, 1.8 k for the release (3 x 1001
 // x 333: 97 us, 15 products).  TMA boxes instead of plain stores for the small

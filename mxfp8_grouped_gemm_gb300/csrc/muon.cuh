@@ -158,7 +158,9 @@ __device__ __forceinline__ float momentum_u1(const MomentumArgs& P, int64_t i) {
 // the bf16 result's own rounding 1.66e-3).  Measured, times that rounding, one
 // part and two: 96 x 958 1.49 1.24, 90 x 6000 1.70 1.28, 80 x 3000 1.61 1.30, but
 // 128 x 6000 1.36 1.18 and 96 x 300 1.35 1.19, where one part is enough (two cost
-// 8-10 % of the time).
+// 8-10 % of the time).  At the edges, one part and (past them) two: 80 x 512 1.48,
+// 80 x 513 1.21; 112 x 512 1.35, 112 x 513 1.17; 120 x 513 1.33, 119 x 513 1.16; 120 x
+// 6000 1.38, 119 x 6000 1.18.
 __host__ __device__ constexpr bool muon_b_low(int m, int n) { return m < 120 && n > 512; }
 
 // u / |u| 2^ex is u times these three factors, in this order, so that no

@@ -627,7 +627,13 @@ int clusters_at_once(int C) {
 // while the device holds all clusters at once, 1 x 64 x 512 64 (one CTA) 50 (two)
 // 38 (eight), 2 x 128 x 1024 80 (two) 54 (eight), 19 x 64 x 1024 52 (four) 79
 // (eight, in turns), except up to 256 columns of more than 64 rows: 4 x 128 x 256
-// 41 (one) 46 (four), where the 128 x 128 sums cost more than they spare.  Those
+// 41 (one) 46 (four), where the 128 x 128 sums cost more than they spare.  Around
+// that edge, one / two / four / eight CTAs (the same for 1 and 4 matrices):
+//   72 x 256 35 46 45 49    96 x 256 39 47 45 50    128 x 256 41 48 47 50
+//   72 x 257 45 54 52 52    96 x 257 48 58 52 52    128 x 257 54 60 56 52
+//   72 x 400 50 54 48 49    96 x 400 52 56 49 49    128 x 400 58 60 51 50
+//   72 x 512 54 54 49 50    96 x 512 58 56 49 50    128 x 512 64 60 52 50
+// so eight cost up to 13 % just past 256 columns of fewer than 128 rows.  Those
 // sums also make clusters that need several turns slower than the tiled kernel:
 // 16 x 100 x 3000 183 against 132, 64 x 128 x 4096 499 against 405 (in one turn
 // 30 x 128 x 2000 92 against 133); 64 x 64 x 2048 is 150 against 232.  Sixteen
