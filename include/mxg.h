@@ -267,6 +267,141 @@ int mxg_muon_form(int batch, int rows, int cols, int32_t* form);
 int mxg_muon_update(const mxg_muon_args* args, void* stream);
 
 /* ----------------------------------------------------------------------------
+ * Routing by scores.  [Grouped] Fig. 1 routes by the largest logits; this is an
+ * addition for layers that route by scores, with a bias that balances the load.
+ * With z a token's logits and s = softmax(z) over all E experts, or sigmoid(z):
+ *   choice  c = s + bias.  The E experts are `groups` groups of consecutive ones;
+ *           a group's score is the sum of its two largest c (group_top 2) or its
+ *           largest (1).  The top_groups best groups take part (ties to the
+ *           lower group), and in them the k largest c (ties to the lower id).
+ *           Without a bias, and without sums over groups, the order is that of
+ *           the logits.
+ *   weights probs[t][j] = scale s_j, or, with renormalize, scale s_j / (sum of
+ *           the k chosen s; 0 if that is 0).  The bias takes no part in them.
+ * The ids are those of scores in 64 bits, whatever fp32 would round.  An expert
+ * with z = -inf (or NaN, or a bias of -inf) is off: it ranks behind all others,
+ * by id, and adds nothing to its group's score (a group with none left ranks
+ * last); where fewer than k are left, experts that are off fill the route, with
+ * weight 0 where z = -inf.  In a softmax a NaN or +inf makes the weights NaN
+ * (renormalised ones where it is among the chosen), and all experts off where
+ * scores are ranked.
+ *   logits      fp32 [T][E] (device);  bias nullable fp32 [E]
+ *   score       MXG_SCORE_SOFTMAX or MXG_SCORE_SIGMOID
+ *   ids, probs  int32, fp32 [T][k] out, in descending order of c
+ * Requires 1 <= k <= E <= 256, k <= 32, E % groups == 0, k <= top_groups * E /
+ * groups, group_top <= E / groups (where groups > 1), scale > 0. */
+enum { MXG_SCORE_SOFTMAX = 0, MXG_SCORE_SIGMOID = 1 };
+int mxg_route_scores_fwd(const float* logits, const float* bias, int T, int E, int k, int score, int groups,
+                         int top_groups, int group_top, int renormalize, float scale, int32_t* ids, float* probs,
+                         void* stream);
+
+/* Gradient of the weights of mxg_route_scores_fwd (the choice carries none), as
+ * one dense matrix for mxg_router_linear_bwd.  With p, dp a token's probs and
+ * dprobs and S = sum_i p_i dp_i, dlogits is dlogits_in plus, at the chosen experts,
+ *   p_j (dp_j - S / scale)  (renormalize)  or  p_j dp_j,
+ *   times 1 - sigmoid(z_j)  (MXG_SCORE_SIGMOID),
+ * and, for a softmax that is not renormalised, minus softmax(z)[e] S everywhere.
+ *   logits, ids, probs   the forward's;  dprobs fp32 [T][k]
+ *   dlogits_in  nullable fp32 [T][E] (e.g. mxg_balance_loss_bwd's); may be dlogits
+ *   dlogits     fp32 [T][E] out
+ * Ids outside [0, E) add nothing at an expert and are reported as
+ * MXG_ERR_EXPERT_ID; an id that stands twice adds twice.  Requirements as
+ * mxg_route_scores_fwd. */
+int mxg_route_scores_bwd(const float* logits, const int32_t* ids, const float* probs, const float* dprobs,
+                         const float* dlogits_in, int T, int E, int k, int score, int renormalize, float scale,
+                         float* dlogits, int32_t* dev_status, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Residual addition and root-mean-square norm: the layer's input from the
+ * residual stream, in bf16 and (or only) as the row-wise MXFP8 rows that
+ * mxg_grouped_mlp_fwd_grouped_mx and expert-parallel dispatch take.  An
+ * addition: the pages start at the layer's input.
+ *   r = x + residual (x alone if null);  residual_out = r in the residual's type
+ *   rstd = 1 / sqrt(mean(r^2) + eps);  y = r rstd weight  (bf16, rounded once,
+ *   from the r that is not rounded)
+ *   q, s = y in MXFP8: what mxg_mxfp8_quantize writes for it, bit for bit
+ * All arithmetic is fp32; a row whose sum of squares passes fp32 gives rstd 0.
+ * y may be x and residual_out may be residual; other buffers do not overlap.
+ * Pointers are 32-byte aligned.
+ * Requires H % 8 == 0, H <= 16384; with q H % 128 == 0, and T % 128 == 0 in the
+ * MMA layout. */
+typedef struct {
+  int32_t T, H;
+  const uint16_t* x;          /* bf16 [T][H]                                             */
+  const void* residual;       /* nullable [T][H], bf16 or (residual_f32 1) fp32          */
+  void* residual_out;         /* nullable [T][H] out, the same type                      */
+  int32_t residual_f32;
+  int32_t weight_f32;
+  const void* weight;         /* [H], bf16 or (weight_f32 1) fp32                        */
+  float eps;                  /* >= 0                                                    */
+  int32_t layout;             /* of s: MXG_LAYOUT_CANONICAL or MXG_LAYOUT_MMA (R = T)    */
+  uint16_t* y;                /* bf16 [T][H] out; nullable with q                        */
+  uint8_t* q;                 /* nullable E4M3 codes [T][H] out, with s                  */
+  uint8_t* s;                 /* E8M0 scales out, T * H / 32 bytes                       */
+  float* rstd;                /* nullable fp32 [T] out, for the backward                 */
+} mxg_rms_norm_fwd_args;
+int mxg_rms_norm_fwd(const mxg_rms_norm_fwd_args* args, void* stream);
+
+/* Its backward.  With xh = r rstd and g = dy weight,
+ *   d = rstd (g - xh mean(g xh)) + dresidual
+ *   dx = d in bf16;  dresidual_out = d in fp32;  dweight = sum over rows of dy xh
+ * (fp32 arithmetic, fixed-order sums).  d is the gradient of x and of residual
+ * alike: where the residual stream is bf16, dx is both.
+ * dx may be dy or (bf16) dresidual, dresidual_out may be (fp32) dresidual; other
+ * buffers do not overlap.  Pointers are 32-byte aligned.
+ * Requires H % 8 == 0, H <= 16384. */
+typedef struct {
+  int32_t T, H;
+  const uint16_t* dy;         /* bf16 [T][H]                                             */
+  const void* r;              /* [T][H]: residual_out, or x; bf16 or (r_f32 1) fp32      */
+  int32_t r_f32;
+  int32_t weight_f32;
+  const void* weight;         /* [H] as in the forward                                   */
+  const float* rstd;          /* fp32 [T] from the forward                               */
+  const void* dresidual;      /* nullable [T][H], r's type: gradient of residual_out     */
+  uint16_t* dx;               /* bf16 [T][H] out                                         */
+  float* dresidual_out;       /* nullable fp32 [T][H] out, with r_f32                    */
+  float* dweight;             /* fp32 [H] out, overwritten                               */
+  void* workspace;            /* >= mxg_rms_norm_bwd_workspace_bytes(T, H) bytes         */
+  uint64_t workspace_bytes;
+} mxg_rms_norm_bwd_args;
+size_t mxg_rms_norm_bwd_workspace_bytes(int T, int H);
+int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Norm over all gradients, and clipping by it: between the backward calls and
+ * mxg_muon_update or any other update.  An addition: the pages stop at the
+ * gradients.
+ *   norm = sqrt(sum of g^2 over all tensors)
+ *   out  = g min(1, max_norm / norm)     (in g's type, rounded once)
+ * The tensors (bf16 and fp32 mixed) are a host array, read during the call only.
+ * Squares are added in fp32 within 32 elements and in fp64 beyond, in a fixed
+ * order; sums that leave fp32's range are taken in fp64 throughout, so norms of
+ * gradients of any finite size are right (written as infinity beyond fp32, while
+ * mxg_grad_clip's own factor still has its value).  An infinite norm clips to
+ * zero (an infinite element to NaN), one that is NaN makes every output NaN.
+ *   workspace  >= mxg_grad_norm_workspace_bytes(n) bytes
+ * mxg_grad_clip takes the norm itself and writes it to norm_out (nullable), or,
+ * given norm_in (fp32 [1], device; e.g. joined over ranks), scales by that and
+ * needs no workspace.  `in` and `out` of a tensor may be the same memory (left
+ * untouched where the factor is 1); other buffers do not overlap, and no tensor
+ * is listed twice as an output.  Tensors may have no elements and any
+ * element-aligned address (16-byte aligned ones move in 16-byte pieces).
+ * Requires n > 0, max_norm > 0, fewer than 2^31 pieces of 16384 elements. */
+typedef struct {
+  const void* in;
+  void* out;                  /* mxg_grad_clip only                                      */
+  int64_t numel;
+  int32_t f32;                /* 0: bf16, 1: fp32                                        */
+  int32_t reserved;           /* 0                                                       */
+} mxg_tensor;
+size_t mxg_grad_norm_workspace_bytes(int n);
+int mxg_grad_norm(const mxg_tensor* tensors, int n, float* norm, void* workspace, size_t workspace_bytes,
+                  void* stream);
+int mxg_grad_clip(const mxg_tensor* tensors, int n, float max_norm, const float* norm_in, float* norm_out,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------------------
  * Permute index: counting sort of the flat index f = t*k + j by expert id,
  * stable in f (bit-exact, deterministic).  [Grouped] "Grouping fragmented
  * expert workloads" (split_sizes: one token count per expert); [Overhead]

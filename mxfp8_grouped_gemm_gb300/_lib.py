@@ -42,7 +42,9 @@ EXPORTS = [
     "mxg_router_fwd_permute", "mxg_grouped_mlp_fwd_grouped_mx",
     "mxg_balance_loss_workspace_bytes", "mxg_balance_loss_fwd", "mxg_balance_loss_bwd",
     "mxg_router_linear_bwd_workspace_bytes", "mxg_router_linear_bwd", "mxg_muon_workspace_bytes", "mxg_muon_update",
-    "mxg_muon_form",
+    "mxg_muon_form", "mxg_route_scores_fwd", "mxg_route_scores_bwd", "mxg_rms_norm_fwd",
+    "mxg_rms_norm_bwd_workspace_bytes", "mxg_rms_norm_bwd", "mxg_grad_norm_workspace_bytes", "mxg_grad_norm",
+    "mxg_grad_clip",
 ]
 
 FWD_STAGES = ["permute", "quant_weights", "quant_x", "gate_up", "down", "combine"]
@@ -104,6 +106,26 @@ class MuonArgs(ctypes.Structure):
                 ("w_out", ctypes.c_void_p), ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
                 ("dev_status", ctypes.c_void_p)]
+
+
+class RmsNormFwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("residual_f32", ctypes.c_int32), ("weight_f32", ctypes.c_int32),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("layout", ctypes.c_int32),
+                ("y", ctypes.c_void_p), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class RmsNormBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dy", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("r_f32", ctypes.c_int32), ("weight_f32", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dresidual_out", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class TensorRef(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("f32", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -180,6 +202,14 @@ def lib() -> ctypes.CDLL:
         "mxg_muon_workspace_bytes": (SZ, [I32, I32, I32]),
         "mxg_muon_form": (I32, [I32, I32, I32, ctypes.POINTER(I32)]),
         "mxg_muon_update": (I32, [ctypes.POINTER(MuonArgs), P]),
+        "mxg_route_scores_fwd": (I32, [P, P, I32, I32, I32, I32, I32, I32, I32, I32, F32, P, P, P]),
+        "mxg_route_scores_bwd": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, P, P]),
+        "mxg_rms_norm_fwd": (I32, [ctypes.POINTER(RmsNormFwdArgs), P]),
+        "mxg_rms_norm_bwd_workspace_bytes": (SZ, [I32, I32]),
+        "mxg_rms_norm_bwd": (I32, [ctypes.POINTER(RmsNormBwdArgs), P]),
+        "mxg_grad_norm_workspace_bytes": (SZ, [I32]),
+        "mxg_grad_norm": (I32, [P, I32, P, P, SZ, P]),
+        "mxg_grad_clip": (I32, [P, I32, F32, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -475,6 +505,235 @@ def mxg_muon_update(grad, dev_status, momentum=None, momentum_out=None, mu: floa
     _call_with_scratch("mxg_muon_update", call, lambda: mxg_muon_workspace_bytes(batch, rows, cols), workspace, dev,
                        stream)
     return update if weights is None else weights_out
+
+
+MXG_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(name) -> int:
+    if name not in MXG_SCORE:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {name!r}")
+    return MXG_SCORE[name]
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {list(t.shape)}")
+    return t.shape
+
+
+def _here(**tensors):
+    """The library runs on the current device, so that is where its tensors have to be."""
+    dev = None
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda:
+            dev = torch._C._cuda_getDevice() if dev is None else dev
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def mxg_route_scores_fwd(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                         group_top: int = 2, renormalize: bool = True, scale: float = 1.0, ids=None, probs=None,
+                         stream=None):
+    """Routing by softmax or sigmoid scores of logits [T, E] -> (ids int32 [T, k], probs fp32 [T, k]).
+
+    bias (fp32 [E]) is added for the choice alone; of `groups` groups of experts the `top_groups` with the largest sums
+    of their group_top largest scores take part; the weights are the chosen scores, renormalised or not, times scale."""
+    T, E = _matrix(logits, "logits")
+    kind = _score(score)
+    ids = _empty((T, k), torch.int32, logits.device, stream) if ids is None else ids
+    probs = _empty((T, k), torch.float32, logits.device, stream) if probs is None else probs
+    _shape(bias, (E,), "bias")
+    _shape(ids, (T, k), "ids")
+    _shape(probs, (T, k), "probs")
+    _here(logits=logits, bias=bias, ids=ids, probs=probs)
+    _check("mxg_route_scores_fwd", lib().mxg_route_scores_fwd(
+        _ptr(logits, torch.float32, "logits"), _ptr(bias, torch.float32, "bias"), T, E, k, kind, groups,
+        top_groups, group_top, int(renormalize), scale, _ptr(ids, torch.int32, "ids"),
+        _ptr(probs, torch.float32, "probs"), _stream(stream)))
+    return ids, probs
+
+
+def mxg_route_scores_bwd(logits, ids, probs, dprobs, dev_status, score: str = "softmax", renormalize: bool = True,
+                         scale: float = 1.0, dlogits_in=None, dlogits=None, stream=None):
+    """Gradient of mxg_route_scores_fwd's weights on the logits, dense fp32 [T, E], added to dlogits_in if given (which
+    may be dlogits)."""
+    T, E = _matrix(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    kind = _score(score)
+    dlogits = _empty((T, E), torch.float32, logits.device, stream) if dlogits is None else dlogits
+    for name, t in (("ids", ids), ("probs", probs), ("dprobs", dprobs)):
+        _shape(t, (T, k), name)
+    _shape(dlogits_in, (T, E), "dlogits_in")
+    _shape(dlogits, (T, E), "dlogits")
+    _here(logits=logits, ids=ids, probs=probs, dprobs=dprobs, dlogits_in=dlogits_in, dlogits=dlogits,
+          dev_status=dev_status)
+    _check("mxg_route_scores_bwd", lib().mxg_route_scores_bwd(
+        _ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _ptr(probs, torch.float32, "probs"),
+        _ptr(dprobs, torch.float32, "dprobs"), _ptr(dlogits_in, torch.float32, "dlogits_in"), T, E, k, kind,
+        int(renormalize), scale, _ptr(dlogits, torch.float32, "dlogits"),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    return dlogits
+
+
+def _real(t: torch.Tensor | None, name: str):
+    if t is not None and t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def mxg_rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None, q=None, s=None, rstd=None,
+                     codes: bool = False, bf16: bool = True, layout: int = MXG_LAYOUT_CANONICAL, stream=None) -> dict:
+    """Residual addition and root-mean-square norm of x bf16 [T, H] -> {'y', 'rstd'}, with a residual 'residual' (the
+    sum, residual_out), with codes (or q and s given) 'q' uint8 [T, H] and 's' uint8 (T * H / 32 bytes, `layout`).
+
+    residual and weight are bf16 or fp32.  residual_out may be residual, y may be x.  bf16 False: codes alone, no y."""
+    T, H = _matrix(x, "x")
+    dev = x.device
+    if (q is None) != (s is None):
+        raise ValueError("q and s are given together")
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out needs residual")
+    _real(residual, "residual")
+    _real(weight, "weight")
+    if not bf16 and y is not None:
+        raise ValueError("y is given but bf16 is False")
+    y = _empty((T, H), torch.bfloat16, dev, stream) if y is None and bf16 else y
+    rstd = _empty(T, torch.float32, dev, stream) if rstd is None else rstd
+    if residual is not None and residual_out is None:
+        residual_out = _empty((T, H), residual.dtype, dev, stream)
+    if codes and q is None:
+        q = _empty((T, H), torch.uint8, dev, stream)
+        s = _empty((T, H // 32), torch.uint8, dev, stream)
+    _shape(weight, (H,), "weight")
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y), ("q", q)):
+        _shape(t, (T, H), name)
+    _shape(rstd, (T,), "rstd")
+    if s is not None and s.numel() != T * H // 32:
+        raise ValueError(f"s must have {T * H // 32} elements, got {s.numel()}")
+    _here(x=x, weight=weight, residual=residual, residual_out=residual_out, y=y, q=q, s=s, rstd=rstd)
+    args = RmsNormFwdArgs(T, H, _ptr(x, torch.bfloat16, "x"), _ptr(residual, None, "residual"),
+                          _ptr(residual_out, None if residual is None else residual.dtype, "residual_out"),
+                          int(residual is not None and residual.dtype == torch.float32),
+                          int(weight.dtype == torch.float32), _ptr(weight, None, "weight"), eps, layout,
+                          _ptr(y, torch.bfloat16, "y"), _ptr(q, torch.uint8, "q"), _ptr(s, torch.uint8, "s"),
+                          _ptr(rstd, torch.float32, "rstd"))
+    _check("mxg_rms_norm_fwd", lib().mxg_rms_norm_fwd(ctypes.byref(args), _stream(stream)))
+    out = {"rstd": rstd}
+    if y is not None:
+        out["y"] = y
+    if residual is not None:
+        out["residual"] = residual_out
+    if q is not None:
+        out["q"], out["s"] = q, s
+    return out
+
+
+def mxg_rms_norm_bwd_workspace_bytes(T, H) -> int:
+    return int(lib().mxg_rms_norm_bwd_workspace_bytes(T, H))
+
+
+def mxg_rms_norm_bwd(dy, r, weight, rstd, dresidual=None, dx=None, dresidual_out=None, dweight=None, workspace=None,
+                     stream=None):
+    """Backward of mxg_rms_norm_fwd for r = its 'residual' (or x, without one), bf16 or fp32 -> (dx bf16 [T, H],
+    dresidual_out fp32 [T, H] where r is fp32, else None, dweight fp32 [H]).
+
+    dresidual (r's type) is the gradient that reaches the sum from elsewhere.  With a bf16 residual, dx is the gradient
+    of x and of the residual alike.  dx may be dy or dresidual, dresidual_out may be dresidual."""
+    T, H = _matrix(dy, "dy")
+    dev = dy.device
+    _real(r, "r")
+    _real(weight, "weight")
+    f32 = r.dtype == torch.float32
+    if dresidual_out is not None and not f32:
+        raise ValueError("dresidual_out is for an fp32 residual: dx is the gradient of a bf16 one")
+    dx = _empty((T, H), torch.bfloat16, dev, stream) if dx is None else dx
+    if f32 and dresidual_out is None:
+        dresidual_out = _empty((T, H), torch.float32, dev, stream)
+    dweight = _empty(H, torch.float32, dev, stream) if dweight is None else dweight
+    for name, t in (("r", r), ("dresidual", dresidual), ("dx", dx), ("dresidual_out", dresidual_out)):
+        _shape(t, (T, H), name)
+    _shape(weight, (H,), "weight")
+    _shape(rstd, (T,), "rstd")
+    _shape(dweight, (H,), "dweight")
+    _here(dy=dy, r=r, weight=weight, rstd=rstd, dresidual=dresidual, dx=dx, dresidual_out=dresidual_out,
+          dweight=dweight, workspace=workspace)
+    args = RmsNormBwdArgs(T, H, _ptr(dy, torch.bfloat16, "dy"), _ptr(r, None, "r"), int(f32),
+                          int(weight.dtype == torch.float32), _ptr(weight, None, "weight"),
+                          _ptr(rstd, torch.float32, "rstd"), _ptr(dresidual, r.dtype, "dresidual"),
+                          _ptr(dx, torch.bfloat16, "dx"), _ptr(dresidual_out, torch.float32, "dresidual_out"),
+                          _ptr(dweight, torch.float32, "dweight"))
+
+    def call(ws, n, st):
+        args.workspace, args.workspace_bytes = ws, n
+        return lib().mxg_rms_norm_bwd(ctypes.byref(args), st)
+
+    _call_with_scratch("mxg_rms_norm_bwd", call, lambda: mxg_rms_norm_bwd_workspace_bytes(T, H), workspace, dev, stream)
+    return dx, dresidual_out, dweight
+
+
+def mxg_grad_norm_workspace_bytes(n) -> int:
+    return int(lib().mxg_grad_norm_workspace_bytes(n))
+
+
+def _tensor_refs(grads, out):
+    """The tensors as the library's table; out None: no outputs."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError("no gradients given")
+    if out is not None and len(out) != n:
+        raise ValueError(f"{n} gradients but {len(out)} outputs")
+    refs = (TensorRef * n)()
+    for i, t in enumerate(grads):
+        _real(t, f"grads[{i}]")
+        _here(grads=t)
+        r = refs[i]
+        r.ptr, r.numel, r.f32 = _ptr(t, None, f"grads[{i}]"), t.numel(), int(t.dtype == torch.float32)
+        if out is not None:
+            o = out[i]
+            if o is not t:
+                _shape(o, t.shape, f"out[{i}]")
+                _here(out=o)
+            r.out = _ptr(o, t.dtype, f"out[{i}]")
+    if out is not None:
+        used = [r.out for r in refs if r.numel]
+        if len(set(used)) != len(used):
+            raise ValueError("a tensor is listed twice as an output")
+    return refs, n
+
+
+def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """Norm over all tensors of a list (bf16, fp32; contiguous, any shapes) -> fp32 [1]."""
+    refs, n = _tensor_refs(grads, None)
+    dev = grads[0].device
+    norm = _empty(1, torch.float32, dev, stream) if norm is None else norm
+    _shape(norm, (1,), "norm")
+    _here(norm=norm, workspace=workspace)
+    to = _ptr(norm, torch.float32, "norm")
+    _call_with_scratch("mxg_grad_norm", lambda ws, b, st: lib().mxg_grad_norm(refs, n, to, ws, b, st),
+                       lambda: mxg_grad_norm_workspace_bytes(n), workspace, dev, stream)
+    return norm
+
+
+def mxg_grad_clip(grads, max_norm: float, out=None, norm=None, norm_out=None, workspace=None, stream=None):
+    """Gradients times min(1, max_norm / norm) -> (norm fp32 [1], outputs), into `out` (a list like grads) or, without
+    one, in place.  norm: fp32 [1] to clip by, e.g. joined over ranks; else the norm over grads is taken (norm_out)."""
+    if norm is not None and norm_out is not None:
+        raise ValueError("norm_out is for the norm that is taken here")
+    out = grads if out is None else out
+    refs, n = _tensor_refs(grads, out)
+    dev = grads[0].device
+    if norm is None and norm_out is None:
+        norm_out = _empty(1, torch.float32, dev, stream)
+    _shape(norm, (1,), "norm")
+    _shape(norm_out, (1,), "norm_out")
+    _here(norm=norm, norm_out=norm_out, workspace=workspace)
+    by, to = _ptr(norm, torch.float32, "norm"), _ptr(norm_out, torch.float32, "norm_out")
+    if by is not None:
+        _check("mxg_grad_clip", lib().mxg_grad_clip(refs, n, max_norm, by, None, None, 0, _stream(stream)))
+        return norm, out
+    _call_with_scratch("mxg_grad_clip", lambda ws, b, st: lib().mxg_grad_clip(refs, n, max_norm, None, to, ws, b, st),
+                       lambda: mxg_grad_norm_workspace_bytes(n), workspace, dev, stream)
+    return norm_out, out
 
 
 def mxg_route_permute(ids: torch.Tensor, E: int, dev_status: torch.Tensor, stream=None) -> dict:

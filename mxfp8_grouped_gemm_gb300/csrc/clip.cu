@@ -1,0 +1,326 @@
+// Norm over all gradients of a model, and clipping by it.
+//
+//   norm = sqrt(sum of g^2 over all tensors),  out = g min(1, max_norm / norm)
+//
+// The tensors are cut into chunks of kChunk elements, numbered through; the
+// tensor table is a kernel argument (a graph keeps its own copy, and nothing is
+// copied to the device).  A CTA takes chunks blockIdx, blockIdx + grid, ... and
+// writes the sum of their squares as one fp64 number; the numbers are added up
+// in order.  Both passes are bound by HBM.
+//
+// A chunk's squares are added in fp32.  Where that sum is not finite or so small
+// that squares may have vanished, the chunk is added again in fp64: gradients of
+// 1e30 and of 1e-30 have norms.
+#include <cmath>
+#include <cstring>
+
+#include "api_common.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mxg {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kPer = 32;                          // elements of a chunk per thread
+constexpr int kChunk = kThreads * kPer;
+constexpr int kMaxBlocks = 152 * 4;
+constexpr int kTable = 512;                       // tensors per launch
+
+struct Tensor {
+  const void* in;
+  void* out;
+  int64_t numel;
+  uint32_t first;                                 // number of its first chunk
+  uint32_t f32;
+};
+template <int N>
+struct Table {
+  Tensor t[N];
+  uint32_t n, chunks;
+};
+
+template <int N>
+__device__ __forceinline__ int tensor_of(const Table<N>& tab, uint32_t chunk) {
+  int lo = 0, hi = static_cast<int>(tab.n) - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab.t[mid].first <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float get(const void* p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
+}
+
+// The thread's elements of a chunk: kPer / 8 runs of eight; the last elements of
+// a tensor, and all of one whose memory does not start on 16 bytes, singly.
+template <typename F8, typename F1>
+__device__ __forceinline__ void for_chunk(bool wide, int64_t base, int64_t left, F8 f8, F1 f1) {
+  if (wide && left >= kChunk) {
+#pragma unroll
+    for (int i = 0; i < kPer / 8; ++i) f8(base + 8 * (threadIdx.x + i * kThreads));
+  } else {
+    const int n = static_cast<int>(left < kChunk ? left : kChunk), runs = wide ? n / 8 : 0;
+    for (int i = threadIdx.x; i < runs; i += kThreads) f8(base + 8 * i);
+    for (int i = 8 * runs + threadIdx.x; i < n; i += kThreads) f1(base + i);
+  }
+}
+
+__device__ __forceinline__ void load8(const void* p, bool f32, int64_t i, float (&v)[8]) {
+  if (f32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+// Block-wide sum in fp64, on every thread.
+__device__ __forceinline__ double block_sum(double v, double* s_sum) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += s_sum[i];
+  return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ Table<N> tab, double* part) {
+  __shared__ double s_sum[kThreads / 32];
+  launch_dependents();
+  double total = 0.0;
+  for (uint32_t c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
+    const Tensor& t = tab.t[tensor_of(tab, c)];
+    const bool f32 = t.f32 != 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(t.in) & 15u) == 0;
+    const int64_t base = static_cast<int64_t>(c - t.first) * kChunk, left = t.numel - base;
+    float sum = 0.f;
+    uint32_t any = 0;
+    for_chunk(
+        wide, base, left,
+        [&](int64_t i) {
+          float v[8];
+          load8(t.in, f32, i, v);
+          float q = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            q = fmaf(v[j], v[j], q);
+            any |= __float_as_uint(v[j]) << 1;
+          }
+          sum += q;
+        },
+        [&](int64_t i) {
+          const float v = get(t.in, f32, i);
+          sum = fmaf(v, v, sum);
+          any |= __float_as_uint(v) << 1;
+        });
+    // squares below 2^-126 lose digits, at most 32 x 2^-149 of a sum that is over 2^-100
+    if (any != 0 && !(sum > 0x1p-100f && sum < INFINITY)) {
+      double exact = 0.0;
+      const auto add = [&](int64_t i) {
+        const double v = get(t.in, f32, i);
+        exact = fma(v, v, exact);
+      };
+      for_chunk(
+          wide, base, left,
+          [&](int64_t i) {
+            for (int j = 0; j < 8; ++j) add(i + j);
+          },
+          add);
+      total += exact;
+    } else {
+      total += static_cast<double>(sum);
+    }
+  }
+  total = block_sum(total, s_sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = total;
+}
+
+// The norm from the partial sums, in a fixed order (the whole block gets it).
+__device__ __forceinline__ double norm_of(const double* part, int n, double* s_sum) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) v += part[i];
+  return sqrt(block_sum(v, s_sum));
+}
+
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int n, float* norm) {
+  __shared__ double s_sum[kThreads / 32];
+  dependency_wait();
+  const double v = norm_of(part, n, s_sum);
+  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+}
+
+// out = g coef.  The norm comes from the partial sums (part), or from the caller
+// (norm_in).
+template <int N>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<N> tab, const double* part, int nparts,
+                                                         const float* norm_in, float max_norm, float* norm_out) {
+  __shared__ double s_sum[kThreads / 32];
+  dependency_wait();
+  double norm;
+  if (part != nullptr) {
+    norm = norm_of(part, nparts, s_sum);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = static_cast<float>(norm);
+  } else {
+    norm = *norm_in;
+  }
+  // NaN makes everything NaN, infinity everything zero (and NaN what is infinite)
+  const float coef = norm <= max_norm ? 1.f : static_cast<float>(max_norm / norm);
+  for (uint32_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
+    const uint32_t c = tab.chunks - 1 - k;        // what was read last is still in L2
+    const Tensor& t = tab.t[tensor_of(tab, c)];
+    const bool f32 = t.f32 != 0;
+    if (coef == 1.f && t.in == t.out) continue;
+    const bool wide = ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
+    const int64_t base = static_cast<int64_t>(c - t.first) * kChunk, left = t.numel - base;
+    for_chunk(
+        wide, base, left,
+        [&](int64_t i) {
+          float v[8];
+          load8(t.in, f32, i, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= coef;
+          if (f32) {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(t.out) + i);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.out) + i) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                           pack_bf16x2(v[6], v[7]));
+          }
+        },
+        [&](int64_t i) {
+          const float v = get(t.in, f32, i) * coef;
+          if (f32) static_cast<float*>(t.out)[i] = v;
+          else static_cast<uint16_t*>(t.out)[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+        });
+  }
+}
+
+int check_tensors(const mxg_tensor* t, int n, bool out) {
+  if (!t || n <= 0) return MXG_ERR_ARG;
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].numel < 0 || (t[i].f32 != 0 && t[i].f32 != 1)) return MXG_ERR_ARG;
+    if (t[i].numel == 0) continue;
+    if (!t[i].in || (out && !t[i].out)) return MXG_ERR_ARG;
+    const uintptr_t size = t[i].f32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(t[i].in) % size != 0) return MXG_ERR_ALIGN;
+    if (out && reinterpret_cast<uintptr_t>(t[i].out) % size != 0) return MXG_ERR_ALIGN;
+    if (t[i].numel > (1ll << 45)) return MXG_ERR_SHAPE;
+    chunks += (t[i].numel + kChunk - 1) / kChunk;
+    if (chunks > INT32_MAX) return MXG_ERR_SHAPE;
+  }
+  return MXG_OK;
+}
+
+int blocks_of(uint32_t chunks) { return chunks < kMaxBlocks ? static_cast<int>(chunks) : kMaxBlocks; }
+
+// Calls f(table of up to N tensors) for every launch the tensors need; a small
+// set travels in a small argument.  Tensors without elements take no entry.
+template <typename F>
+cudaError_t for_tables(const mxg_tensor* t, int n, F f) {
+  int at = 0;
+  while (true) {
+    while (at < n && t[at].numel == 0) ++at;
+    if (at >= n) return cudaSuccess;
+    const auto fill = [&](auto& tab) {
+      tab.n = tab.chunks = 0;
+      constexpr uint32_t most = sizeof(tab.t) / sizeof(tab.t[0]);
+      for (; at < n && tab.n < most; ++at) {
+        if (t[at].numel == 0) continue;
+        tab.t[tab.n++] = Tensor{t[at].in, t[at].out, t[at].numel, tab.chunks, static_cast<uint32_t>(t[at].f32)};
+        tab.chunks += static_cast<uint32_t>((t[at].numel + kChunk - 1) / kChunk);
+      }
+    };
+    cudaError_t err;
+    if (n - at <= 16) {
+      Table<16> tab;
+      fill(tab);
+      err = f(tab);
+    } else {
+      static thread_local Table<kTable> tab;
+      fill(tab);
+      err = f(tab);
+    }
+    if (err != cudaSuccess) return err;
+  }
+}
+
+int table_count(int n) { return (n + kTable - 1) / kTable; }
+
+// The partial sums of all tensors; their number to *nparts.
+cudaError_t launch_square_sums(const mxg_tensor* t, int n, double* part, int* nparts, cudaStream_t s) {
+  *nparts = 0;
+  return for_tables(t, n, [&](const auto& tab) {
+    constexpr int N = sizeof(tab.t) / sizeof(tab.t[0]);
+    const int blocks = blocks_of(tab.chunks);
+    square_sum_kernel<N><<<blocks, kThreads, 0, s>>>(tab, part + *nparts);
+    count_launch();
+    *nparts += blocks;
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+}  // namespace mxg
+
+using namespace mxg;
+
+extern "C" size_t mxg_grad_norm_workspace_bytes(int n) {
+  return n <= 0 ? 0 : static_cast<size_t>(table_count(n)) * kMaxBlocks * sizeof(double);
+}
+
+extern "C" int mxg_grad_norm(const mxg_tensor* tensors, int n, float* norm, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (!norm || !workspace) return MXG_ERR_ARG;
+  if (const int err = check_tensors(tensors, n, false)) return err;
+  if (!api::aligned32(workspace) || !api::aligned32(norm)) return MXG_ERR_ALIGN;
+  if (workspace_bytes < mxg_grad_norm_workspace_bytes(n)) return MXG_ERR_WORKSPACE;
+  api::NvtxRange nvtx("mxg.grad_norm");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int nparts = 0;
+  double* part = static_cast<double*>(workspace);
+  MXG_TRY(launch_square_sums(tensors, n, part, &nparts, s));
+  MXG_TRY(launch_after(norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(part), nparts, norm));
+  return MXG_OK;
+}
+
+extern "C" int mxg_grad_clip(const mxg_tensor* tensors, int n, float max_norm, const float* norm_in, float* norm_out,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(max_norm > 0.f) || (!norm_in && !workspace) || (norm_in && norm_out)) return MXG_ERR_ARG;
+  if (const int err = check_tensors(tensors, n, true)) return err;
+  if (!api::aligned32(workspace) || !api::aligned32(norm_in) || !api::aligned32(norm_out)) return MXG_ERR_ALIGN;
+  if (!norm_in && workspace_bytes < mxg_grad_norm_workspace_bytes(n)) return MXG_ERR_WORKSPACE;
+  api::NvtxRange nvtx("mxg.grad_clip");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int nparts = 0;
+  double* part = static_cast<double*>(workspace);
+  if (!norm_in) MXG_TRY(launch_square_sums(tensors, n, part, &nparts, s));
+  bool told = norm_out == nullptr;
+  MXG_TRY(for_tables(tensors, n, [&](const auto& tab) {
+    constexpr int N = sizeof(tab.t) / sizeof(tab.t[0]);
+    float* to = told ? nullptr : norm_out;
+    told = true;
+    return launch_after(scale_kernel<N>, dim3(blocks_of(tab.chunks)), dim3(kThreads), 0, s, tab,
+                        static_cast<const double*>(norm_in ? nullptr : part), nparts, norm_in, max_norm, to);
+  }));
+  if (!told)                                      // no tensor has elements: the norm is zero
+    MXG_TRY(launch_after(norm_kernel, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(part), nparts, norm_out));
+  return MXG_OK;
+}

@@ -88,6 +88,22 @@ __device__ __forceinline__ float fp8_dequant(float amax) {
   return __uint_as_float(mx_scale_byte(__float_as_uint(amax) & 0x7fffffffu) << 23);
 }
 
+// Largest magnitude of packed bf16 pairs, as fp32 bits: max.xorsign.abs
+// keeps the larger magnitude of each lane pair (its sign bit, the XOR of the
+// operands' signs, is cleared at the end), one instruction per word.
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pair_max_bits(const uint32_t* w, int n) {
+  uint32_t m = w[0];
+#pragma unroll
+  for (int i = 1; i < n; ++i) m = absmax_bf16x2(m, w[i]);
+  m &= 0x7fff7fffu;
+  return max(m << 16, m & 0xffff0000u);
+}
+
 // Two fp32 -> two E4M3 codes (round to nearest even, saturate to +-448);
 // a in the low byte, b in the high byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {

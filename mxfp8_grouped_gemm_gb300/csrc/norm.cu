@@ -1,0 +1,379 @@
+// Residual addition with the root-mean-square norm that makes the layer's
+// input, in bf16 and (optionally) row-wise MXFP8, and its backward pass.
+//
+//   r = x + residual,  rstd = 1 / sqrt(mean(r^2) + eps),  y = r rstd w
+// and, with xh = r rstd, g = dy w,
+//   dr = rstd (g - xh mean(g xh)) + dresidual,   dw = sum over rows of dy xh.
+//
+// A row is read once and stays in registers between its sum and its output:
+// thread t of the row's threads holds the 16-byte chunks t, t + threads, ...
+// (8 values each, so four neighbouring lanes hold one MX block).  Rows of up to
+// 1024 values are handled by 8 to 32 lanes of a warp, several rows a CTA; wider
+// ones by a CTA of their own.  Both passes are bound by HBM.
+#include <cmath>
+
+#include "api_common.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mxg {
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kMaxH = 16384;
+constexpr int kRowThreads = 128;        // CTA of the rows that lanes of a warp share
+constexpr int kMaxThreads = 512;        // CTA of one wide row
+
+enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
+
+__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { *reinterpret_cast<uint4*>(p) = pack8(v); }
+
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int off = W / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Sum over the row's threads: LPR lanes of a warp, or (LPR 0) the whole CTA.
+// The CTA's form needs one barrier: successive rows use s_part in turn.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float (*s_part)[32], int parity) {
+  if constexpr (LPR != 0) {
+    return lanes_sum<LPR>(v);
+  } else {
+    v = lanes_sum<32>(v);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) s_part[parity][warp] = v;
+    __syncthreads();
+    return lanes_sum<32>(lane < static_cast<int>(blockDim.x >> 5) ? s_part[parity][lane] : 0.f);
+  }
+}
+
+struct NormFwdParams {
+  int T, H;
+  const uint16_t* x;
+  const void* residual;
+  void* residual_out;
+  const void* weight;
+  int w32;
+  float eps, inv_h;
+  uint16_t* y;
+  uint8_t* q;
+  uint8_t* s;
+  int layout;
+  float* rstd;
+};
+
+__device__ __forceinline__ void load_weight(const void* w, int w32, int col, float (&v)[8]) {
+  if (w32) load8(static_cast<const float*>(w) + col, v);
+  else load8(static_cast<const uint16_t*>(w) + col, v);
+}
+
+template <int LPR, int NCH, int RES>
+__global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_fwd_kernel(const NormFwdParams P) {
+  __shared__ float s_part[2][32];
+  const int threads = LPR != 0 ? LPR : static_cast<int>(blockDim.x);
+  const int th = LPR != 0 ? static_cast<int>(threadIdx.x) % LPR : static_cast<int>(threadIdx.x);
+  const int64_t row = LPR != 0 ? static_cast<int64_t>(blockIdx.x) * (kRowThreads / LPR) + threadIdx.x / LPR
+                               : static_cast<int64_t>(blockIdx.x);
+  const bool live = row < P.T;
+  const int n8 = P.H >> 3;
+  const int64_t base = row * P.H;
+  float r[NCH][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = th + i * threads;
+    const bool in = live && c < n8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+    if (in) {
+      load8(P.x + base + 8 * c, r[i]);
+      if constexpr (RES != RES_NONE) {
+        float a[8];
+        if constexpr (RES == RES_F32) load8(static_cast<const float*>(P.residual) + base + 8 * c, a);
+        else load8(static_cast<const uint16_t*>(P.residual) + base + 8 * c, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] += a[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NCH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(r[i][j], r[i][j], sum);
+  sum = row_sum<LPR>(sum, s_part, 0);
+  const float rstd = 1.f / sqrtf(fmaf(sum, P.inv_h, P.eps));
+  if (live && th == 0 && P.rstd != nullptr) P.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = th + i * threads;
+    const bool in = live && c < n8;
+    if (in) {
+      if constexpr (RES != RES_NONE) {
+        if (P.residual_out != nullptr) {
+          if constexpr (RES == RES_F32) store8(static_cast<float*>(P.residual_out) + base + 8 * c, r[i]);
+          else store8(static_cast<uint16_t*>(P.residual_out) + base + 8 * c, r[i]);
+        }
+      }
+      float w[8];
+      load_weight(P.weight, P.w32, 8 * c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * rstd * w[j];
+    }
+    const uint4 y = pack8(r[i]);
+    if (in && P.y != nullptr) *reinterpret_cast<uint4*>(P.y + base + 8 * c) = y;
+    if (P.q != nullptr) {
+      // the codes of the bf16 values, so that they are mxg_mxfp8_quantize's on y
+      const uint32_t words[4] = {y.x, y.y, y.z, y.w};
+      uint32_t amax = pair_max_bits(words, 4);
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const uint32_t sb = mx_scale_byte(amax);
+      const float inv = mx_inv_scale(sb);
+      float v[8];
+      unpack8(y, v);
+      const uint32_t lo = cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      const uint32_t hi = cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+      if (in) {
+        *reinterpret_cast<uint2*>(P.q + base + 8 * c) = make_uint2(lo, hi);
+        if ((c & 3) == 0) P.s[sf_offset(P.layout, row, c >> 2, P.T, P.H >> 5)] = static_cast<uint8_t>(sb);
+      }
+    }
+  }
+}
+
+struct NormBwdParams {
+  int T, H;
+  const uint16_t* dy;
+  const void* r;
+  const void* weight;
+  int w32;
+  const float* rstd;
+  float inv_h;
+  const void* dresidual;
+  uint16_t* dx;
+  float* dresidual_out;
+  float* part;            // [gridDim.x][H]; the result itself where the grid is one CTA
+};
+
+template <int LPR, int NCH, bool F32>
+__global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd_kernel(const NormBwdParams P) {
+  constexpr int kGroups = LPR != 0 ? kRowThreads / LPR : 1;     // rows at a time
+  __shared__ float s_part[2][32];
+  __shared__ float s_acc[LPR != 0 ? (kGroups - 1) * LPR * NCH * 8 : 1];
+  launch_dependents();
+  const int threads = LPR != 0 ? LPR : static_cast<int>(blockDim.x);
+  const int th = LPR != 0 ? static_cast<int>(threadIdx.x) % LPR : static_cast<int>(threadIdx.x);
+  const int group = LPR != 0 ? static_cast<int>(threadIdx.x) / LPR : 0;
+  const int n8 = P.H >> 3;
+  float acc[NCH][8];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  int parity = 0;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < P.T;
+       first += static_cast<int64_t>(gridDim.x) * kGroups, parity ^= 1) {
+    const int64_t row = first + group;
+    const bool live = row < P.T;
+    const int64_t base = row * P.H;
+    const float rstd = live ? P.rstd[row] : 0.f;
+    float xh[NCH][8], g[NCH][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = th + i * threads;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xh[i][j] = g[i][j] = 0.f;
+      if (live && c < n8) {
+        load8(P.dy + base + 8 * c, g[i]);
+        if constexpr (F32) load8(static_cast<const float*>(P.r) + base + 8 * c, xh[i]);
+        else load8(static_cast<const uint16_t*>(P.r) + base + 8 * c, xh[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = th + i * threads;
+      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < n8) load_weight(P.weight, P.w32, 8 * c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[i][j] *= rstd;
+        acc[i][j] = fmaf(g[i][j], xh[i][j], acc[i][j]);
+        g[i][j] *= w[j];
+        dot = fmaf(g[i][j], xh[i][j], dot);
+      }
+    }
+    const float mean = row_sum<LPR>(dot, s_part, parity) * P.inv_h;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = th + i * threads;
+      if (live && c < n8) {
+        float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (P.dresidual != nullptr) {
+          if constexpr (F32) load8(static_cast<const float*>(P.dresidual) + base + 8 * c, d);
+          else load8(static_cast<const uint16_t*>(P.dresidual) + base + 8 * c, d);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-xh[i][j], mean, g[i][j]), d[j]);
+        if (P.dx != nullptr) store8(P.dx + base + 8 * c, d);
+        if constexpr (F32) {
+          if (P.dresidual_out != nullptr) store8(P.dresidual_out + base + 8 * c, d);
+        }
+      }
+    }
+  }
+  // the row groups' sums in order
+  if constexpr (kGroups > 1) {
+    if (group != 0) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_acc[(((group - 1) * NCH + i) * 8 + j) * LPR + th] = acc[i][j];
+    }
+    __syncthreads();
+    if (group != 0) return;
+    for (int k = 0; k < kGroups - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] += s_acc[((k * NCH + i) * 8 + j) * LPR + th];
+  }
+  float* out = P.part + static_cast<int64_t>(blockIdx.x) * P.H;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = th + i * threads;
+    if (c < n8) store8(out + 8 * c, acc[i]);
+  }
+}
+
+// dweight: the CTAs' partial sums, eight threads to a column, in order.
+__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* __restrict__ part, int nblk, int H,
+                                                           float* __restrict__ dw) {
+  __shared__ float s_sum[8][32];
+  dependency_wait();
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < H)
+    for (int b = k; b < nblk; b += 8) v += part[static_cast<int64_t>(b) * H + col];
+  s_sum[k][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (k == 0 && col < H) {
+    for (int i = 1; i < 8; ++i) v += s_sum[i][threadIdx.x & 31];
+    dw[col] = v;
+  }
+}
+
+// Calls f(lanes per row or 0, chunks per thread) with the form of a width, as
+// compile-time numbers.
+template <typename F>
+void with_width(int H, F f) {
+  const int n8 = H / 8;
+  using std::integral_constant;
+  if (n8 <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (n8 <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (n8 <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (n8 <= 64) f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  else if (n8 <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  else f(integral_constant<int, 0>{}, integral_constant<int, 4>{});
+}
+
+int wide_threads(int H) { return (H / 8 + 4 * 32 - 1) / (4 * 32) * 32; }
+
+int rows_at_once(int H) { return H <= 64 ? 16 : H <= 128 ? 8 : H <= 1024 ? 4 : 1; }
+
+int bwd_blocks(int T, int H) {
+  const int64_t need = (static_cast<int64_t>(T) + rows_at_once(H) - 1) / rows_at_once(H);
+  const int64_t most = static_cast<int64_t>(kSms) * (H <= 4096 ? 4 : H <= 8192 ? 2 : 1);
+  return static_cast<int>(need < most ? need : most);
+}
+
+}  // namespace
+}  // namespace mxg
+
+using namespace mxg;
+
+extern "C" int mxg_rms_norm_fwd(const mxg_rms_norm_fwd_args* A, void* stream) {
+  if (!A || !A->x || !A->weight || (!A->y && !A->q)) return MXG_ERR_ARG;
+  if ((A->q == nullptr) != (A->s == nullptr) || (A->residual_out && !A->residual)) return MXG_ERR_ARG;
+  if (A->T <= 0 || A->H <= 0 || !(A->eps >= 0.f) || !std::isfinite(A->eps)) return MXG_ERR_ARG;
+  if (A->q && A->layout != MXG_LAYOUT_CANONICAL && A->layout != MXG_LAYOUT_MMA) return MXG_ERR_ARG;
+  if (A->H % 8 != 0 || A->H > kMaxH) return MXG_ERR_SHAPE;
+  if (A->q && (A->H % 128 != 0 || (A->layout == MXG_LAYOUT_MMA && A->T % 128 != 0))) return MXG_ERR_SHAPE;
+  if (!api::aligned32(A->x) || !api::aligned32(A->residual) || !api::aligned32(A->residual_out) ||
+      !api::aligned32(A->weight) || !api::aligned32(A->y) || !api::aligned32(A->q) || !api::aligned32(A->s) ||
+      !api::aligned32(A->rstd))
+    return MXG_ERR_ALIGN;
+  api::NvtxRange nvtx("mxg.rms_norm_fwd");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  NormFwdParams p{A->T, A->H, A->x, A->residual, A->residual_out, A->weight, A->weight_f32 != 0, A->eps,
+                  static_cast<float>(1.0 / A->H), A->y, A->q, A->s, A->layout, A->rstd};
+  const int rows = rows_at_once(A->H);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(A->T) + rows - 1) / rows);
+  with_width(A->H, [&](auto lpr, auto nch) {
+    const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H);
+    if (!A->residual) norm_fwd_kernel<lpr.value, nch.value, RES_NONE><<<grid, block, 0, st>>>(p);
+    else if (A->residual_f32) norm_fwd_kernel<lpr.value, nch.value, RES_F32><<<grid, block, 0, st>>>(p);
+    else norm_fwd_kernel<lpr.value, nch.value, RES_BF16><<<grid, block, 0, st>>>(p);
+  });
+  count_launch();
+  return api::cuda_status(cudaGetLastError());
+}
+
+extern "C" size_t mxg_rms_norm_bwd_workspace_bytes(int T, int H) {
+  if (T <= 0 || H <= 0 || H % 8 != 0 || H > kMaxH) return 0;
+  return static_cast<size_t>(4ll * bwd_blocks(T, H) * H);
+}
+
+extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
+  if (!A || !A->dy || !A->r || !A->weight || !A->rstd || !A->dx || !A->dweight || !A->workspace) return MXG_ERR_ARG;
+  if (A->T <= 0 || A->H <= 0) return MXG_ERR_ARG;
+  if (A->dresidual_out && !A->r_f32) return MXG_ERR_ARG;
+  if (A->H % 8 != 0 || A->H > kMaxH) return MXG_ERR_SHAPE;
+  if (!api::aligned32(A->dy) || !api::aligned32(A->r) || !api::aligned32(A->weight) || !api::aligned32(A->rstd) ||
+      !api::aligned32(A->dresidual) || !api::aligned32(A->dx) || !api::aligned32(A->dresidual_out) ||
+      !api::aligned32(A->dweight) || !api::aligned32(A->workspace))
+    return MXG_ERR_ALIGN;
+  if (A->workspace_bytes < mxg_rms_norm_bwd_workspace_bytes(A->T, A->H)) return MXG_ERR_WORKSPACE;
+  api::NvtxRange nvtx("mxg.rms_norm_bwd");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int nblk = bwd_blocks(A->T, A->H);
+  NormBwdParams p{A->T, A->H, A->dy, A->r, A->weight, A->weight_f32 != 0, A->rstd, static_cast<float>(1.0 / A->H),
+                  A->dresidual, A->dx, A->dresidual_out,
+                  nblk == 1 ? A->dweight : static_cast<float*>(A->workspace)};
+  with_width(A->H, [&](auto lpr, auto nch) {
+    const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H);
+    if (A->r_f32) norm_bwd_kernel<lpr.value, nch.value, true><<<nblk, block, 0, st>>>(p);
+    else norm_bwd_kernel<lpr.value, nch.value, false><<<nblk, block, 0, st>>>(p);
+  });
+  count_launch();
+  MXG_TRY(cudaGetLastError());
+  if (nblk == 1) return MXG_OK;
+  MXG_TRY(launch_after(norm_dweight_kernel, dim3((A->H + 31) / 32), dim3(256), 0, st, p.part, nblk, A->H, A->dweight));
+  return MXG_OK;
+}
