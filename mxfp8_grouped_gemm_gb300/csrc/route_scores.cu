@@ -45,7 +45,6 @@ struct RouteParams {
   int spread;           // else: lanes that scan a group together, a power of two
   int renorm;
   float scale;
-  int reps;             // tokens a lane group takes one after another
   int32_t* ids;
   float* probs;
 };
@@ -69,6 +68,29 @@ __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
   for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
   return v;
+}
+
+// The sigmoid of a weight: relative error at most 6 x 2^-24.
+__device__ __forceinline__ float sigmoid_of(float z) {
+  const float t = expf(-fabsf(z));
+  return (z >= 0.f ? 1.f : t) / (1.f + t);
+}
+
+// The weight of a chosen logit (-inf: 0), of a token whose choices lie in kp
+// neighbouring lanes.  A renormalised sigmoid's are taken relative to the largest
+// chosen, which keeps them from vanishing together.
+__device__ __forceinline__ float weight_of(const RouteParams& P, float z, int kp, float top, float inv) {
+  float low = z;
+  if (P.renorm)
+    for (int off = kp >> 1; off > 0; off >>= 1) low = fmaxf(low, __shfl_xor_sync(kAll, low, off));
+  float w;
+  if (z == -INFINITY) w = 0.f;
+  else if (P.score == SOFTMAX) w = expf(z - (P.renorm ? low : top));
+  else w = P.renorm && low < 0.f ? expf(z - low) / (1.f + expf(z)) : sigmoid_of(z);
+  if (!P.renorm) return w * (P.score == SOFTMAX ? P.scale * inv : P.scale);
+  float total = w;
+  for (int off = kp >> 1; off > 0; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
+  return total == 0.f ? 0.f : w * (P.scale / total);
 }
 
 // ------------------------------------------------------------------ 64 bits --
@@ -106,9 +128,9 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// The choice for one token by the whole warp, all in fp64: lane j gets the j-th id.
+// One token by the whole warp, its choice in fp64.
 template <bool SCORED>
-__device__ __noinline__ int route_exact(const RouteParams& P, int64_t t) {
+__device__ __noinline__ void route_exact(const RouteParams& P, int64_t t) {
   const int lane = threadIdx.x & 31;
   const float* row = P.logits + t * P.E;
   double c[kVals];
@@ -190,7 +212,20 @@ __device__ __noinline__ int route_exact(const RouteParams& P, int64_t t) {
     if (e / kVals == lane) there &= ~(1u << (e % kVals));
     if (lane == j) id = e;
   }
-  return id;
+  float inv = 1.f;
+  if (P.score == SOFTMAX && !P.renorm) {
+    float sum = 0.f;
+    top = lanes_max<32>(top);
+    if (top == -INFINITY) top = 0.f;
+    for (int e = lane; e < P.E; e += 32) sum += expf(row[e] - top);
+    sum = lanes_sum<32>(sum);
+    inv = sum == 0.f ? 0.f : 1.f / sum;
+  }
+  const float w = weight_of(P, lane < P.k ? row[id] : -INFINITY, 32, top, inv);
+  if (lane < P.k) {
+    P.ids[t * P.k + lane] = id;
+    P.probs[t * P.k + lane] = w;
+  }
 }
 
 // --------------------------------------------------------------------- fp32 --
@@ -206,12 +241,6 @@ __device__ __forceinline__ float rcp_fast(float d) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
-// The sigmoid of a weight: relative error at most 6 x 2^-24.
-__device__ __forceinline__ float sigmoid_of(float z) {
-  const float t = expf(-fabsf(z));
-  return (z >= 0.f ? 1.f : t) / (1.f + t);
-}
-
 // Descending.
 __device__ __forceinline__ void sort8(float (&h)[kVals]) {
   constexpr int net[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
@@ -229,8 +258,87 @@ __device__ __forceinline__ void top_two(float& a, float& b, float a2, float b2) 
   a = fmaxf(a, a2);
 }
 
-// LPT lanes per token.  SCORED: ranked by scores (with a bias, or sums over
-// groups), else by the logits, whose order is exact.
+struct Kept {
+  float worst, next;    // scores of the last group kept and of the best one left out
+  uint32_t experts;     // of the lane's eight, those in groups that are kept
+  bool close;           // groups of equal scores on both sides
+};
+
+// The best groups of any size, from a token's experts in shared memory.
+// `scratch`: `room` floats of shared memory of the token's own.
+template <int LPT>
+__device__ __forceinline__ Kept kept_groups(const RouteParams& P, const float* row_c, float* scratch, int room, int lane) {
+  const int gl = lane % LPT;
+  const unsigned mask = group_mask<LPT>(lane);
+  Kept out{-INFINITY, -INFINITY, 0u, false};
+  __syncwarp();
+  // entry x = gl + LPT r of the lanes' list: group x / spread, scanned with step `spread`
+  float score[kVals];
+  bool first[kVals];
+#pragma unroll
+  for (int r = 0; r < kVals; ++r) {
+    score[r] = -INFINITY;
+    first[r] = false;
+    if (r * LPT < P.groups * P.spread) {
+      const int x = gl + LPT * r, g = x / P.spread, sub = x % P.spread;
+      float a = -INFINITY, b = -INFINITY;
+      if (g < P.groups) {
+        for (int e = sub; e < P.size; e += P.spread) top_two(a, b, row_c[g * P.size + e], -INFINITY);
+      }
+      for (int off = 1; off < P.spread; off <<= 1) {
+        const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
+        top_two(a, b, a2, b2);
+      }
+      score[r] = P.group_top == 2 && b != -INFINITY ? a + b : a;
+      first[r] = g < P.groups && sub == 0;
+    }
+  }
+  float cur[kVals];
+#pragma unroll
+  for (int r = 0; r < kVals; ++r) cur[r] = score[r];
+  for (int m = 0; m <= P.top_groups; ++m) {
+    float best = cur[0];
+#pragma unroll
+    for (int r = 1; r < kVals; ++r) best = fmaxf(best, cur[r]);
+    out.next = lanes_max<LPT>(best);
+    if (m == P.top_groups) break;
+    out.worst = out.next;
+#pragma unroll
+    for (int r = 0; r < kVals; ++r)
+      if (cur[r] == out.worst) cur[r] = -INFINITY;
+  }
+  int kept = 0;
+#pragma unroll
+  for (int r = 0; r < kVals; ++r) kept += __popc(__ballot_sync(kAll, first[r] && score[r] >= out.worst) & mask);
+  out.close = kept != P.top_groups;
+  // the scores to shared memory, where every lane finds those of its experts
+  for (int lo = 0; lo < P.groups; lo += room) {
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kVals; ++r) {
+      const int g = (gl + LPT * r) / P.spread;
+      if (first[r] && g >= lo && g < lo + room) scratch[g - lo] = score[r];
+    }
+    __syncwarp();
+    for (int i = 0; i < kVals; ++i) {
+      const int e = gl * kVals + i, g = e / P.size;
+      if (e < P.E && g >= lo && g < lo + room && scratch[g - lo] >= out.worst) out.experts |= 1u << i;
+    }
+  }
+  __syncwarp();
+  return out;
+}
+
+// What ranks the experts: the logits, whose order is exact, or scores (with a
+// bias, or sums over groups).
+enum { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
+// Groups: all take part, each is a power of two of whole lanes, any size.
+enum { NO_GROUPS = 0, LANE_GROUPS = 1, ANY_GROUPS = 2 };
+
+// A warp takes NB tokens: first LPT lanes to a token rank its experts and pick k
+// heads, which leaves (value, lane) pairs in shared memory; then KP lanes to a
+// token, one to a choice, find the ids and make the weights (KP: k rounded up to
+// a power of two), so that this part's cost is shared by 32 / KP tokens.
 //
 // Error of a score, in units of 2^-24: a sigmoid s = 1 / (1 + t) moves by s (1 -
 // s) <= 1/4 of t's relative error, which is 1.5 |z| + 2.83 (|z| s (1 - s) <=
@@ -239,22 +347,23 @@ __device__ __forceinline__ void top_two(float& a, float& b, float a2, float b2) 
 // the sum by 30 of itself (the mean of |d| over a softmax of 256 is below 5.6; 13
 // additions), reciprocal and product 3: 37 of the largest score; relative to a
 // score, with |d| <= 88, 256.  c = s + bias adds a rounding of c.
-template <int LPT, bool SCORED, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RouteParams P) {
-  constexpr int TPW = 32 / LPT;
-  constexpr int SEL = 32 / LPT < kVals ? 32 / LPT : kVals;      // choices a lane keeps
+template <int LPT, int BY, int GROUPS>
+__global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_constant__ RouteParams P) {
+  constexpr bool SCORED = BY != BY_LOGIT;
+  constexpr int TPW = 32 / LPT;                                 // tokens at a time
+  constexpr int NB = TPW > 4 ? TPW : 4;                         // tokens of the warp
   constexpr int MOST = LPT * kVals < 32 ? LPT * kVals : 32;     // choices of a token
   constexpr float kU = 1.f / 16777216.f;                        // 2^-24
   constexpr float kTiny = 1e-37f;                               // below that scores have no relative error
-  __shared__ __align__(16) float s_c[kWarps][32 * kVals];
-  __shared__ __align__(8) float2 s_v[kWarps][TPW][MOST + 1];
+  __shared__ __align__(16) float s_c[kWarps][NB][LPT * kVals];  // what ranks a token's experts
+  __shared__ __align__(16) float s_h[kWarps][32 * kVals];       // the same, each lane's in descending order
+  // a token's choices; then the best value left out and whether to rank again; the softmax's maximum and 1 / sum
+  __shared__ __align__(8) float2 s_win[kWarps][NB][MOST + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
-  const unsigned mask = group_mask<LPT>(lane);
+  const unsigned mask = group_mask<LPT>(lane), ahead = mask & ((1u << lane) - 1u);
   const bool softmax = P.score == SOFTMAX;
   const bool ragged = P.E < LPT * kVals;
-  float* row_c = s_c[warp] + grp * LPT * kVals;
-  float2* win = s_v[warp][grp];
 
   float bias[kVals];
   float reach = 0.f;                                            // largest |bias|
@@ -269,13 +378,22 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RoutePa
     reach = lanes_max<LPT>(reach);
   }
 
-  int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * P.reps * TPW + grp;
-  for (int n = 0; n < P.reps; ++n, t += TPW) {
-    if (t - grp >= P.T) return;                                 // the whole warp
-    const bool in = t < P.T;
-    const float* row = P.logits + (in ? t : 0) * P.E;
+  // the warp's share of the tokens, NB at a time
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t end = (me + 1) * P.T / warps;
+#pragma unroll 1
+  for (int64_t t0 = me * P.T / warps; t0 < end; t0 += NB) {
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(NB), end - t0));
+  __syncwarp();                                                 // the last tokens' rows have been read
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += TPW) {
+    const int n = n0 + grp;
+    const bool in = n < ntok;
+    const float* row = P.logits + (t0 + (in ? n : 0)) * P.E;
+    float2* win = s_win[warp][n];
+    float* row_c = s_c[warp][n];
     float z[kVals];
-    if constexpr (VEC) {
+    if (P.E % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < kVals; i += 4) {
         const int e = gl * kVals + i;
@@ -292,10 +410,9 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RoutePa
     for (int i = 0; i < kVals; ++i) probe = fmaf(z[i], 0.f, probe);
     const bool odd = __any_sync(kAll, probe != probe);          // an infinity or a NaN among the warp's logits
 
-    // h: what ranks the experts
-    float h[kVals];
+    float h[kVals];                                             // what ranks the experts
     float top = 0.f, inv = 1.f;
-    if (softmax && (SCORED || !P.renorm)) {
+    if (BY == BY_SOFTMAX || (BY == BY_LOGIT && softmax && !P.renorm)) {
       top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kVals; ++i)
@@ -311,12 +428,11 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RoutePa
       sum = lanes_sum<LPT>(sum);
       inv = sum == 0.f ? 0.f : 1.f / sum;
     }
-    if constexpr (SCORED) {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) h[i] = (softmax ? h[i] * inv : rcp_fast(1.f + exp_fast(-z[i]))) + bias[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVals; ++i) h[i] = z[i];
+    for (int i = 0; i < kVals; ++i) {
+      if constexpr (BY == BY_LOGIT) h[i] = z[i];
+      else if constexpr (BY == BY_SIGMOID) h[i] = rcp_fast(1.f + exp_fast(-z[i])) + bias[i];
+      else h[i] = fmaf(h[i], inv, bias[i]);
     }
     if (odd) {
 #pragma unroll
@@ -328,19 +444,15 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RoutePa
       for (int i = 0; i < kVals; ++i)
         if (gl * kVals + i >= P.E) h[i] = -INFINITY;
     }
-    __syncwarp();                                               // the last token's rows have been read
 #pragma unroll
     for (int i = 0; i < kVals; i += 4)
       *reinterpret_cast<float4*>(row_c + gl * kVals + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     sort8(h);
-    // an absolute bound on the error of a score, and one relative to it (its size is at most |c| + reach)
-    const float abs_err = softmax ? 37.f * kU * inv : 4.1f * kU;
-    const float rel_err = softmax ? 256.f * kU : 138.f * kU;
     bool close = false;                                         // a decision that fp32 cannot take
 
-    if (P.top_groups < P.groups) {
+    if constexpr (GROUPS != NO_GROUPS) {
       float worst = -INFINITY, next;
-      if (P.lanes_of_group != 0) {
+      if constexpr (GROUPS == LANE_GROUPS) {
         float a = h[0], b = h[1];
         for (int off = 1; off < P.lanes_of_group; off <<= 1) {
           const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
@@ -353,188 +465,112 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const RoutePa
           if (cur == worst) cur = -INFINITY;
         }
         next = lanes_max<LPT>(cur);
-        const bool keep = score >= worst, first = gl % P.lanes_of_group == 0 && gl * kVals < P.E;
+        const bool keep = score >= worst, first = (gl & (P.lanes_of_group - 1)) == 0 && gl * kVals < P.E;
         if (__popc(__ballot_sync(kAll, keep && first) & mask) != P.top_groups) close = true;     // equal scores
-        if (!keep) {
-#pragma unroll
-          for (int i = 0; i < kVals; ++i) h[i] = -INFINITY;
-        }
+        if (!keep) h[0] = -INFINITY;                            // its lane is never picked
       } else {
-        __syncwarp();
-        // entry x = gl + LPT r of the lanes' list: group x / spread, scanned with step `spread`
-        float score[kVals];
-        bool first[kVals];
+        const Kept kept = kept_groups<LPT>(P, row_c, reinterpret_cast<float*>(win), 2 * (MOST + 2), lane);
+        worst = kept.worst;
+        next = kept.next;
+        close = kept.close;
 #pragma unroll
-        for (int r = 0; r < kVals; ++r) {
-          score[r] = -INFINITY;
-          first[r] = false;
-          if (r * LPT < P.groups * P.spread) {
-            const int x = gl + LPT * r, g = x / P.spread, sub = x % P.spread;
-            float a = -INFINITY, b = -INFINITY;
-            if (g < P.groups) {
-              for (int e = sub; e < P.size; e += P.spread) top_two(a, b, row_c[g * P.size + e], -INFINITY);
-            }
-            for (int off = 1; off < P.spread; off <<= 1) {
-              const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
-              top_two(a, b, a2, b2);
-            }
-            score[r] = P.group_top == 2 && b != -INFINITY ? a + b : a;
-            first[r] = g < P.groups && sub == 0;
-          }
-        }
-        float cur[kVals];
-#pragma unroll
-        for (int r = 0; r < kVals; ++r) cur[r] = score[r];
-        for (int m = 0; m <= P.top_groups; ++m) {
-          float best = cur[0];
-#pragma unroll
-          for (int r = 1; r < kVals; ++r) best = fmaxf(best, cur[r]);
-          next = lanes_max<LPT>(best);
-          if (m == P.top_groups) break;
-          worst = next;
-#pragma unroll
-          for (int r = 0; r < kVals; ++r)
-            if (cur[r] == worst) cur[r] = -INFINITY;
-        }
-        int kept = 0;
-#pragma unroll
-        for (int r = 0; r < kVals; ++r)
-          kept += __popc(__ballot_sync(kAll, first[r] && score[r] >= worst) & mask);
-        if (kept != P.top_groups) close = true;
-        // the scores to shared memory, where every lane finds those of its experts
-        float* s_score = reinterpret_cast<float*>(s_v[warp]);
-        const int per = TPW * (MOST + 1) * 2 / TPW;             // floats of a token
-        float own[kVals];
-        for (int lo = 0; lo < P.groups; lo += per) {
-          __syncwarp();
-#pragma unroll
-          for (int r = 0; r < kVals; ++r) {
-            const int g = (gl + LPT * r) / P.spread;
-            if (first[r] && g >= lo && g < lo + per) s_score[grp * per + g - lo] = score[r];
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < kVals; ++i) {
-            const int g = (gl * kVals + i) / P.size;
-            if (g >= lo && g < lo + per && g < P.groups) own[i] = s_score[grp * per + g - lo];
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) h[i] = gl * kVals + i < P.E && own[i] >= worst ? row_c[gl * kVals + i] : -INFINITY;
+        for (int i = 0; i < kVals; ++i) h[i] = (kept.experts >> i & 1u) ? row_c[gl * kVals + i] : -INFINITY;
         sort8(h);
       }
       if (worst == -INFINITY) close = true;                     // groups without an expert left
       if constexpr (SCORED) {
-        // two scores and the rounding of c twice and of the sum
-        const float err = 2.f * abs_err + 4.f * kU * (softmax ? inv + reach : 1.f + reach);
+        // two scores, the roundings of their c and that of the sum
+        const float err = BY == BY_SOFTMAX ? 2.f * 37.f * kU * inv + 4.f * kU * (inv + reach)
+                                           : 2.f * 4.1f * kU + 4.f * kU * (1.f + reach);
         if (!(worst - next > 2.f * err)) close = true;
       }
     }
 
-    // the rounds; with scores one more, which shows the best of the experts left out
-    __syncwarp();
-    for (int j = 0; j < P.k + (SCORED ? 1 : 0); ++j) {
-      const float best = lanes_max<LPT>(h[0]);
-      const int owner = __ffs(__ballot_sync(kAll, h[0] == best) & mask) - 1;
-      if (lane == owner) {
-        win[j] = make_float2(best, __int_as_float(gl));
+    // the rounds: the lowest lane with the largest head gives it, and takes its next from shared memory
+    float* list = s_h[warp] + lane * kVals;
 #pragma unroll
-        for (int i = 0; i + 1 < kVals; ++i) h[i] = h[i + 1];
-        h[kVals - 1] = -INFINITY;
+    for (int i = 0; i < kVals; i += 4)
+      *reinterpret_cast<float4*>(list + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+    float head = h[0];
+    const float* last = list + kVals - 1;
+    float2* to = win;
+#pragma unroll 2
+    for (int j = 0; j < P.k; ++j, ++to) {
+      const float best = lanes_max<LPT>(head);
+      const bool equal = head == best;
+      if ((__ballot_sync(kAll, equal) & ahead) == 0 && equal) {
+        *to = make_float2(best, __int_as_float(gl));
+        head = list == last ? -INFINITY : *++list;
       }
     }
-    __syncwarp();
-    int sel[SEL];
-#pragma unroll
-    for (int r = 0; r < SEL; ++r) {
-      const int j = gl + r * LPT;
-      sel[r] = 0;
-      if (j < P.k) {
-        const float v = win[j].x;
-        const int o = __float_as_int(win[j].y);
-        if (v == -INFINITY) close = true;                       // fewer than k experts are left
-        int skip = 0;
-        if constexpr (SCORED) {
-          const float w = win[j + 1].x;
-          const float size = fmaxf(fabsf(v), w == -INFINITY ? 0.f : fabsf(w)) + reach;
-          if (!(v - w > 2.f * (fminf(abs_err, rel_err * size) + kU * size) + kTiny)) close = true;
-        } else {
-          // equal logits of one lane, chosen one after another
-          while (skip < j && win[j - 1 - skip].x == v && __float_as_int(win[j - 1 - skip].y) == o) ++skip;
-        }
-        float c[kVals];
-#pragma unroll
-        for (int i = 0; i < kVals; i += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(row_c + o * kVals + i);
-          c[i] = q.x, c[i + 1] = q.y, c[i + 2] = q.z, c[i + 3] = q.w;
-        }
-        int idx = 0;
-        if constexpr (SCORED) {
-#pragma unroll
-          for (int i = kVals - 1; i >= 0; --i)
-            if (c[i] == v) idx = i;
-        } else {
-#pragma unroll
-          for (int i = kVals - 1; i >= 0; --i) {
-            int ahead = 0;
-#pragma unroll
-            for (int m = 0; m < i; ++m) ahead += c[m] == v;
-            if (c[i] == v && ahead == skip) idx = i;
-          }
-        }
-        sel[r] = o * kVals + idx;
-      }
+    const float left = SCORED ? lanes_max<LPT>(head) : -INFINITY;
+    if (gl == 0) {
+      win[P.k] = make_float2(left, close ? 1.f : 0.f);
+      win[P.k + 1] = make_float2(top, inv);
     }
-    unsigned again = __ballot_sync(kAll, in && close);
-    while (again != 0) {
-      const int l = __ffs(again) - 1;
-      again &= ~group_mask<LPT>(l);
-      const int id = route_exact<SCORED>(P, t - grp + l / LPT);
-#pragma unroll
-      for (int r = 0; r < SEL; ++r) {
-        const int e = __shfl_sync(kAll, id, gl + r * LPT);
-        if (grp == l / LPT && gl + r * LPT < P.k) sel[r] = e;
-      }
-    }
+  }
+  __syncwarp();
 
-    // weights; those of a renormalised sigmoid by the largest chosen, which keeps them from vanishing together
-    float w[SEL], zc[SEL];
-    float low = -INFINITY;
-#pragma unroll
-    for (int r = 0; r < SEL; ++r) {
-      zc[r] = gl + r * LPT < P.k ? row[sel[r]] : -INFINITY;
-      low = fmaxf(low, zc[r]);
+  int kp_log = 0;
+  while ((1 << kp_log) < P.k) ++kp_log;
+  const int kp = 1 << kp_log;
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += 32 >> kp_log) {
+    const int j = lane & (kp - 1), n = n0 + (lane >> kp_log);
+    const bool here = n < ntok && j < P.k;
+    const int nn = n < ntok ? n : 0, jj = here ? j : 0;
+    const float* row = P.logits + (t0 + nn) * P.E;
+    const float2* win = s_win[warp][nn];
+    const float v = win[jj].x, top = win[P.k + 1].x, inv = win[P.k + 1].y;
+    const int o = __float_as_int(win[jj].y);
+    bool close = win[P.k].y != 0.f || v == -INFINITY;           // or fewer than k experts are left
+    int skip = 0;
+    if constexpr (SCORED) {
+      // an absolute bound on the error of a score, and one relative to it (its size is at most |c| + reach)
+      const float abs_err = BY == BY_SOFTMAX ? 37.f * kU * inv : 4.1f * kU;
+      const float rel_err = BY == BY_SOFTMAX ? 256.f * kU : 138.f * kU;
+      const float w = win[jj + 1].x;
+      const float size = fmaxf(fabsf(v), w == -INFINITY ? 0.f : fabsf(w)) + reach;
+      if (!(v - w > 2.f * (fminf(abs_err, rel_err * size) + kU * size) + kTiny)) close = true;
+    } else {
+      // equal logits of one lane, chosen one after another
+      while (skip < jj && win[jj - 1 - skip].x == v && __float_as_int(win[jj - 1 - skip].y) == o) ++skip;
     }
-    if (P.renorm) low = lanes_max<LPT>(low);
-    float total = 0.f;
+    const float* row_c = s_c[warp][nn] + o * kVals;
+    float c[kVals];
 #pragma unroll
-    for (int r = 0; r < SEL; ++r) {
-      if (zc[r] == -INFINITY) {
-        w[r] = 0.f;
-      } else if (softmax) {
-        w[r] = expf(zc[r] - (P.renorm ? low : top));
-      } else {
-        w[r] = P.renorm && low < 0.f ? expf(zc[r] - low) / (1.f + expf(zc[r])) : sigmoid_of(zc[r]);
-      }
-      total += w[r];
+    for (int i = 0; i < kVals; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(row_c + i);
+      c[i] = q.x, c[i + 1] = q.y, c[i + 2] = q.z, c[i + 3] = q.w;
     }
-    float factor = P.scale;
-    if (P.renorm) {
-      total = lanes_sum<LPT>(total);
-      factor = total == 0.f ? 0.f : P.scale / total;
-    } else if (softmax) {
-      factor = P.scale * inv;
-    }
-    if (in) {
+    int idx = 0;
 #pragma unroll
-      for (int r = 0; r < SEL; ++r) {
-        const int j = gl + r * LPT;
-        if (j < P.k) {
-          P.ids[t * P.k + j] = sel[r];
-          P.probs[t * P.k + j] = w[r] * factor;
-        }
-      }
+    for (int i = kVals - 1; i >= 0; --i)
+      if (c[i] == v) idx = i;
+    if (!SCORED && skip != 0) {
+      for (idx = 0; idx < kVals - 1; ++idx)
+        if (row_c[idx] == v && skip-- == 0) break;
+    }
+    int sel = o * kVals + idx;
+    unsigned again = __ballot_sync(kAll, here && close);        // such a token's first id is -1 until below
+    again >>= lane & ~(kp - 1);
+    again &= kp == 32 ? kAll : (1u << kp) - 1u;
+
+    const float w = weight_of(P, here ? row[sel] : -INFINITY, kp, top, inv);
+    if (here) {
+      P.ids[(t0 + n) * P.k + j] = again != 0 ? -1 : sel;
+      P.probs[(t0 + n) * P.k + j] = w;
+    }
+  }
+  }
+  // the tokens that fp32 could not decide, in fp64
+  __syncwarp();
+  for (int64_t t1 = me * P.T / warps; t1 < end; t1 += 32) {
+    unsigned again = __ballot_sync(kAll, t1 + lane < end && P.ids[(t1 + lane) * P.k] < 0);
+    while (again != 0) {
+      const int64_t t = t1 + __ffs(again) - 1;
+      again &= again - 1;
+      route_exact<SCORED>(P, t);
     }
   }
 }
@@ -664,25 +700,30 @@ int lanes_per_token(int E) {
   return l;
 }
 
-// Calls f(lanes per token, 16-byte rows).
+// Calls f with the number as a compile-time one.
 template <typename F>
 void with_lanes(int E, F f) {
-  const auto vec = [&](auto l) {
-    if (E % 4 == 0) f(l, std::true_type{});
-    else f(l, std::false_type{});
-  };
   switch (lanes_per_token(E)) {
-    case 1: vec(std::integral_constant<int, 1>{}); break;
-    case 2: vec(std::integral_constant<int, 2>{}); break;
-    case 4: vec(std::integral_constant<int, 4>{}); break;
-    case 8: vec(std::integral_constant<int, 8>{}); break;
-    case 16: vec(std::integral_constant<int, 16>{}); break;
-    default: vec(std::integral_constant<int, 32>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 8: f(std::integral_constant<int, 8>{}); break;
+    case 16: f(std::integral_constant<int, 16>{}); break;
+    default: f(std::integral_constant<int, 32>{}); break;
+  }
+}
+template <typename F>
+void with_three(int n, F f) {
+  switch (n) {
+    case 0: f(std::integral_constant<int, 0>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    default: f(std::integral_constant<int, 2>{}); break;
   }
 }
 
-unsigned token_blocks(int T, int E, int reps) {
-  const int64_t per = static_cast<int64_t>(kWarps) * (32 / lanes_per_token(E)) * reps;
+// Blocks for T tokens, each warp taking what its lanes hold at once.
+unsigned token_blocks(int T, int E) {
+  const int64_t per = static_cast<int64_t>(kWarps) * (32 / lanes_per_token(E));
   return static_cast<unsigned>((T + per - 1) / per);
 }
 
@@ -712,18 +753,21 @@ extern "C" int mxg_route_scores_fwd(const float* logits, const float* bias, int 
     return MXG_ERR_ALIGN;
   api::NvtxRange nvtx("mxg.route_scores_fwd");
   const int lanes = lanes_per_token(E);
-  RouteParams p{logits, bias, T, E, k, score, groups, top_groups, group_top, size, 0, 1, renormalize != 0, scale, 1, ids,
+  RouteParams p{logits, bias, T, E, k, score, groups, top_groups, group_top, size, 0, 1, renormalize != 0, scale, ids,
                 probs};
   const int whole = size % kVals == 0 ? size / kVals : 0;
   if ((whole & (whole - 1)) == 0) p.lanes_of_group = whole;
   while (2 * p.spread * groups <= lanes) p.spread *= 2;
-  if (T >= 16384) p.reps = 4;
   const bool scored = bias != nullptr || (top_groups < groups && group_top == 2);
+  const int by = !scored ? BY_LOGIT : score == SIGMOID ? BY_SIGMOID : BY_SOFTMAX;
+  const int kind = top_groups == groups ? NO_GROUPS : p.lanes_of_group != 0 ? LANE_GROUPS : ANY_GROUPS;
+  // all that fit at once (four blocks an SM), fewer where a warp would get less than a set of tokens
+  const unsigned most = 4 * 152, need = token_blocks(T, E), grid = need < most ? need : most;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  with_lanes(E, [&](auto l, auto v) {
-    const unsigned grid = token_blocks(T, E, p.reps);
-    if (scored) route_scores_kernel<l.value, true, v.value><<<grid, kThreads, 0, st>>>(p);
-    else route_scores_kernel<l.value, false, v.value><<<grid, kThreads, 0, st>>>(p);
+  with_lanes(E, [&](auto l) {
+    with_three(by, [&](auto b) {
+      with_three(kind, [&](auto g) { route_scores_kernel<l.value, b.value, g.value><<<grid, kThreads, 0, st>>>(p); });
+    });
   });
   count_launch();
   return api::cuda_status(cudaGetLastError());
@@ -740,9 +784,10 @@ extern "C" int mxg_route_scores_bwd(const float* logits, const int32_t* ids, con
   api::NvtxRange nvtx("mxg.route_scores_bwd");
   const RouteBwdParams p{logits, ids,   probs, dprobs,           dlogits_in,   dlogits,   T,
                          E,      k,     score, renormalize != 0, 1.f / scale, dev_status};
-  with_lanes(E, [&](auto l, auto v) {
-    route_scores_bwd_kernel<l.value, v.value>
-        <<<token_blocks(T, E, 1), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  with_lanes(E, [&](auto l) {
+    if (E % 4 == 0) route_scores_bwd_kernel<l.value, true><<<token_blocks(T, E), kThreads, 0, st>>>(p);
+    else route_scores_bwd_kernel<l.value, false><<<token_blocks(T, E), kThreads, 0, st>>>(p);
   });
   count_launch();
   return api::cuda_status(cudaGetLastError());
