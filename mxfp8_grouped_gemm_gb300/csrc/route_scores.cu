@@ -23,6 +23,7 @@
 #include "api_common.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace mxg {
 namespace {
@@ -105,127 +106,10 @@ __device__ __forceinline__ double of_key(uint64_t k) {
   const int64_t b = static_cast<int64_t>(k);
   return __longlong_as_double(b ^ ((~b >> 63) | INT64_MIN));
 }
-
-// The warp's largest key (expert 8 lane + i) among those that `in` names, ties
-// to the lowest expert; every lane gets the expert.  0: none.
-__device__ __forceinline__ uint64_t warp_best(const uint64_t (&key)[kVals], uint32_t in, int lane, int* expert) {
-  uint64_t m = 0;
-  int idx = 0;
-#pragma unroll
-  for (int i = kVals - 1; i >= 0; --i) {
-    if ((in >> i & 1u) && key[i] >= m) m = key[i], idx = i;
-  }
-  const uint32_t hi = static_cast<uint32_t>(m >> 32), best_hi = __reduce_max_sync(kAll, hi);
-  const uint32_t lo = hi == best_hi ? static_cast<uint32_t>(m) : 0u, best_lo = __reduce_max_sync(kAll, lo);
-  const uint64_t best = static_cast<uint64_t>(best_hi) << 32 | best_lo;
-  const int owner = __ffs(__ballot_sync(kAll, m == best)) - 1;
-  *expert = __shfl_sync(kAll, lane * kVals + idx, owner);
-  return best;
-}
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
   return v;
-}
-
-// One token by the whole warp, its choice in fp64.
-template <bool SCORED>
-__device__ __noinline__ void route_exact(const RouteParams& P, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  const float* row = P.logits + t * P.E;
-  double c[kVals];
-  uint32_t there = 0, live = 0;
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kVals; ++i) {
-    const int e = lane * kVals + i;
-    const float z = e < P.E ? row[e] : -INFINITY;
-    if (e < P.E) there |= 1u << i;
-    if (z != -INFINITY) live |= 1u << i;               // a NaN is on, and its score NaN
-    c[i] = z;
-    top = fmaxf(top, z);
-  }
-  if constexpr (SCORED) {
-    top = lanes_max<32>(top);
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      const bool on = live >> i & 1u;
-      if (P.score == SIGMOID) c[i] = on ? 1.0 / (1.0 + exp(-c[i])) : 0.0;
-      else c[i] = on ? exp(c[i] - top) : 0.0;
-      sum += c[i];
-    }
-    if (P.score == SOFTMAX) {
-      sum = warp_sum(sum);
-#pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if (sum != 0.0) c[i] /= sum;
-    }
-    if (P.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if (there >> i & 1u) c[i] += static_cast<double>(P.bias[lane * kVals + i]);
-    }
-  }
-  uint64_t key[kVals];
-#pragma unroll
-  for (int i = 0; i < kVals; ++i) key[i] = key_of((live >> i & 1u) ? c[i] : -INFINITY);
-  if (P.top_groups < P.groups) {
-    uint64_t score[kVals];                             // of group 8 lane + i
-    uint32_t left = 0;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) score[i] = 0;
-    for (int g = 0; g < P.groups; ++g) {
-      uint32_t in = 0;
-#pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if (static_cast<unsigned>(lane * kVals + i - g * P.size) < static_cast<unsigned>(P.size)) in |= 1u << i;
-      int e;
-      double a = of_key(warp_best(key, in, lane, &e));
-      if (P.group_top == 2) {
-        if (e / kVals == lane) in &= ~(1u << (e % kVals));
-        const double b = of_key(warp_best(key, in, lane, &e));
-        if (b != -INFINITY) a += b;
-      }
-      if (g / kVals == lane) {
-        left |= 1u << (g % kVals);
-#pragma unroll
-        for (int i = 0; i < kVals; ++i)
-          if (i == g % kVals) score[i] = key_of(a);
-      }
-    }
-    uint32_t kept = 0;                                 // of the lane's own experts
-    for (int n = 0; n < P.top_groups; ++n) {
-      int g;
-      warp_best(score, left, lane, &g);
-      if (g / kVals == lane) left &= ~(1u << (g % kVals));
-#pragma unroll
-      for (int i = 0; i < kVals; ++i)
-        if (static_cast<unsigned>(lane * kVals + i - g * P.size) < static_cast<unsigned>(P.size)) kept |= 1u << i;
-    }
-    there &= kept;
-  }
-  int id = 0;                                          // k <= 32: lane j keeps the j-th choice
-  for (int j = 0; j < P.k; ++j) {
-    int e;
-    warp_best(key, there, lane, &e);
-    if (e / kVals == lane) there &= ~(1u << (e % kVals));
-    if (lane == j) id = e;
-  }
-  float inv = 1.f;
-  if (P.score == SOFTMAX && !P.renorm) {
-    float sum = 0.f;
-    top = lanes_max<32>(top);
-    if (top == -INFINITY) top = 0.f;
-    for (int e = lane; e < P.E; e += 32) sum += expf(row[e] - top);
-    sum = lanes_sum<32>(sum);
-    inv = sum == 0.f ? 0.f : 1.f / sum;
-  }
-  const float w = weight_of(P, lane < P.k ? row[id] : -INFINITY, 32, top, inv);
-  if (lane < P.k) {
-    P.ids[t * P.k + lane] = id;
-    P.probs[t * P.k + lane] = w;
-  }
 }
 
 // --------------------------------------------------------------------- fp32 --
@@ -241,6 +125,30 @@ __device__ __forceinline__ float rcp_fast(float d) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
+// A lane's list: eight and the -inf behind them, at a stride that keeps 16-byte
+// stores of neighbouring lanes in different banks.
+constexpr int kList = 12;
+
+// One round: of the lanes whose head is the largest (`best`), the one without
+// another `ahead` of it writes (best, its number) to `to` and takes its next, at
+// the `end` -inf again.
+// All by predicate: as a branch the round took 28 instructions, so it is 11.
+__device__ __forceinline__ void take(float& head, uint32_t& list, uint32_t end, uint32_t to, float best, int number,
+                                     unsigned ahead) {
+  asm volatile(
+      "{\n .reg .pred eq, p;\n .reg .b32 who;\n"
+      " setp.eq.f32 eq, %0, %3;\n"
+      " vote.sync.ballot.b32 who, eq, 0xffffffff;\n"
+      " and.b32 who, who, %5;\n"
+      " setp.eq.and.u32 p, who, 0, eq;\n"
+      " @p st.shared.v2.b32 [%2], {%6, %4};\n"
+      " @p add.u32 %1, %1, 4;\n @p min.u32 %1, %1, %7;\n"
+      " @p ld.shared.f32 %0, [%1];\n}"
+      : "+f"(head), "+r"(list)
+      : "r"(to), "f"(best), "r"(number), "r"(ahead), "r"(__float_as_uint(best)), "r"(end)
+      : "memory");
+}
+
 // Descending.
 __device__ __forceinline__ void sort8(float (&h)[kVals]) {
   constexpr int net[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
@@ -335,6 +243,237 @@ enum { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
 // Groups: all take part, each is a power of two of whole lanes, any size.
 enum { NO_GROUPS = 0, LANE_GROUPS = 1, ANY_GROUPS = 2 };
 
+// Absolute error of c in fp32, in units of 2^-24 (see below), for scores of at
+// most `most` (1, or the softmax's largest) and biases of at most `reach`.
+template <int BY>
+__device__ __forceinline__ float error_of(float most, float reach) {
+  constexpr float kU = 1.f / 16777216.f;
+  if constexpr (BY == BY_LOGIT) return 0.f;
+  else if constexpr (BY == BY_SIGMOID) return kU * (4.1f + 1.f + reach);
+  else return kU * (38.f * most + reach);
+}
+
+// The warp's largest key (expert 8 lane + i) among those that `in` names, ties
+// to the lowest expert; every lane gets the expert.  0: none.
+__device__ __forceinline__ uint64_t warp_best(const uint64_t (&key)[kVals], uint32_t in, int lane, int* expert) {
+  uint64_t m = 0;
+  int idx = 0;
+#pragma unroll
+  for (int i = kVals - 1; i >= 0; --i) {
+    if ((in >> i & 1u) && key[i] >= m) m = key[i], idx = i;
+  }
+  const uint32_t hi = static_cast<uint32_t>(m >> 32), best_hi = __reduce_max_sync(kAll, hi);
+  const uint32_t lo = hi == best_hi ? static_cast<uint32_t>(m) : 0u, best_lo = __reduce_max_sync(kAll, lo);
+  const uint64_t best = static_cast<uint64_t>(best_hi) << 32 | best_lo;
+  const int owner = __ffs(__ballot_sync(kAll, m == best)) - 1;
+  *expert = __shfl_sync(kAll, lane * kVals + idx, owner);
+  return best;
+}
+// One token by the whole warp, everything in fp64: the j-th choice to win[j].y.
+template <bool SCORED>
+__device__ __noinline__ void rank_all(const RouteParams& P, const float* row, float2* win) {
+  const int lane = threadIdx.x & 31;
+  double c[kVals];
+  uint32_t there = 0, live = 0;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) {
+    const int e = lane * kVals + i;
+    const float z = e < P.E ? row[e] : -INFINITY;
+    if (e < P.E) there |= 1u << i;
+    if (z != -INFINITY) live |= 1u << i;               // a NaN is on, and its score NaN
+    c[i] = z;
+    top = fmaxf(top, z);
+  }
+  if constexpr (SCORED) {
+    top = lanes_max<32>(top);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const bool on = live >> i & 1u;
+      if (P.score == SIGMOID) c[i] = on ? 1.0 / (1.0 + exp(-c[i])) : 0.0;
+      else c[i] = on ? exp(c[i] - top) : 0.0;
+      sum += c[i];
+    }
+    if (P.score == SOFTMAX) {
+      sum = warp_sum(sum);
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        if (sum != 0.0) c[i] /= sum;
+    }
+    if (P.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        if (there >> i & 1u) c[i] += static_cast<double>(P.bias[lane * kVals + i]);
+    }
+  }
+  uint64_t key[kVals];
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) key[i] = key_of((live >> i & 1u) ? c[i] : -INFINITY);
+  if (P.top_groups < P.groups) {
+    uint64_t score[kVals];                             // of group 8 lane + i
+    uint32_t left = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) score[i] = 0;
+    for (int g = 0; g < P.groups; ++g) {
+      uint32_t in = 0;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        if (static_cast<unsigned>(lane * kVals + i - g * P.size) < static_cast<unsigned>(P.size)) in |= 1u << i;
+      int e;
+      double a = of_key(warp_best(key, in, lane, &e));
+      if (P.group_top == 2) {
+        if (e / kVals == lane) in &= ~(1u << (e % kVals));
+        const double b = of_key(warp_best(key, in, lane, &e));
+        if (b != -INFINITY) a += b;
+      }
+      if (g / kVals == lane) {
+        left |= 1u << (g % kVals);
+#pragma unroll
+        for (int i = 0; i < kVals; ++i)
+          if (i == g % kVals) score[i] = key_of(a);
+      }
+    }
+    uint32_t kept = 0;                                 // of the lane's own experts
+    for (int n = 0; n < P.top_groups; ++n) {
+      int g;
+      warp_best(score, left, lane, &g);
+      if (g / kVals == lane) left &= ~(1u << (g % kVals));
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        if (static_cast<unsigned>(lane * kVals + i - g * P.size) < static_cast<unsigned>(P.size)) kept |= 1u << i;
+    }
+    there &= kept;
+  }
+  for (int j = 0; j < P.k; ++j) {
+    int e;
+    warp_best(key, there, lane, &e);
+    if (e / kVals == lane) there &= ~(1u << (e % kVals));
+    if (lane == j) win[j].y = __int_as_float(e);
+  }
+  __syncwarp();
+}
+
+// One token by the whole warp, its decisions in fp64: the j-th choice to
+// win[j].y.  fp32 scores and their error bound name the few experts that a
+// decision can hang on (a group's largest, and the k largest, with what lies
+// within the error of them); these are evaluated in fp64, one to a lane.  Where
+// they are more than lanes, or experts that are off have to fill the route, all
+// are ranked.  (All in fp64 for every such token cost 14 us of the 57 that
+// 65536 x 256 took: a few dozen tokens, but the last to finish.)
+//   row_c   fp32 c; -inf: off, NaN: its group does not take part
+//   kth     the k-th largest c, unless the groups are to be decided as well
+template <int BY, int GROUPS, int N>
+__device__ __noinline__ void rank_close(const RouteParams& P, const float* row, const float* row_c, float2* win,
+                                        uint8_t* list, float reach, float most, bool groups_close) {
+  const int lane = threadIdx.x & 31;
+  if (BY == BY_LOGIT || (GROUPS == ANY_GROUPS && groups_close)) return rank_all<BY != BY_LOGIT>(P, row, win);
+  float c[kVals];
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) c[i] = lane * kVals < N ? row_c[lane * kVals + i] : NAN;
+  const float slack = 2.1f * error_of<BY>(most, reach) + 1e-37f;
+  float top = 0.f;
+  double sum = 1.0;
+  if (BY == BY_SOFTMAX) {
+    top = -INFINITY;
+    for (int e = lane; e < P.E; e += 32) top = fmaxf(top, row[e]);
+    top = lanes_max<32>(top);
+    sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < P.E; e += 32) sum += exp(static_cast<double>(row[e]) - top);
+    sum = warp_sum(sum);
+  }
+  // The experts with c at least `from`: their number; lane n gets the n-th and its key.
+  int mine = 0;
+  uint64_t key = 0;
+  const auto evaluate = [&](float from) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const bool w = c[i] >= from && c[i] != -INFINITY;
+      const unsigned who = __ballot_sync(kAll, w);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (w && at < 32) list[at] = static_cast<uint8_t>(lane * kVals + i);
+      n += __popc(who);
+    }
+    __syncwarp();
+    if (n <= 32) {
+      mine = lane < n ? list[lane] : -1;
+      const double z = row[lane < n ? mine : 0];
+      const double x = exp(BY == BY_SIGMOID ? -z : z - top);
+      double v = BY == BY_SIGMOID ? 1.0 / (1.0 + x) : x / sum;
+      if (P.bias != nullptr && lane < n) v += static_cast<double>(P.bias[mine]);
+      key = lane < n ? key_of(v) : 0;
+    }
+    __syncwarp();
+    return n;
+  };
+  float kth = -INFINITY;
+  if (GROUPS == LANE_GROUPS && groups_close) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) top_two(a, b, c[i], -INFINITY);
+    for (int off = 1; off < P.lanes_of_group; off <<= 1) {
+      const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
+      top_two(a, b, a2, b2);
+    }
+    const int n = evaluate((P.group_top == 2 ? b : a) - slack);
+    if (n > 32) return rank_all<true>(P, row, win);
+    uint64_t best = 0, second = 0;                     // of group `lane`
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const uint64_t v = __shfl_sync(kAll, key, i);
+      if (__shfl_sync(kAll, mine, i) / P.size == lane) {
+        second = max(second, min(best, v));
+        best = max(best, v);
+      }
+    }
+    const uint64_t score = P.group_top == 2 && second != 0 ? key_of(of_key(best) + of_key(second)) : best;
+    int ahead = 0;
+#pragma unroll 1
+    for (int g = 0; g < P.groups; ++g) {
+      const uint64_t v = __shfl_sync(kAll, score, g);
+      ahead += v > score || (v == score && g < lane);
+    }
+    const unsigned kept = __ballot_sync(kAll, lane < P.groups && ahead < P.top_groups);
+    const bool in = lane / P.lanes_of_group < 32 && (kept >> (lane / P.lanes_of_group) & 1u);
+    int live = 0;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      if (!in) c[i] = NAN;
+      live += c[i] > -INFINITY;
+    }
+    if (static_cast<int>(__reduce_add_sync(kAll, live)) < P.k) return rank_all<true>(P, row, win);
+    float bound = INFINITY;                            // the k-th largest of what is left
+    for (int j = 0; j < P.k;) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        if (c[i] < bound) m = fmaxf(m, c[i]);
+      kth = bound = lanes_max<32>(m);
+      int equal = 0;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) equal += c[i] == bound;
+      j += static_cast<int>(__reduce_add_sync(kAll, equal));
+    }
+  } else {
+    kth = win[P.k - 1].x;
+    __syncwarp();
+  }
+  if (kth == -INFINITY) return rank_all<true>(P, row, win);
+  const int n = evaluate(kth - slack);
+  if (n > 32) return rank_all<true>(P, row, win);
+  int ahead = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const uint64_t v = __shfl_sync(kAll, key, i);
+    const int o = __shfl_sync(kAll, mine, i);
+    ahead += v > key || (v == key && o < mine);
+  }
+  if (lane < n && ahead < P.k) win[ahead].y = __int_as_float(mine);
+  __syncwarp();
+}
+
 // A warp takes NB tokens: first LPT lanes to a token rank its experts and pick k
 // heads, which leaves (value, lane) pairs in shared memory; then KP lanes to a
 // token, one to a choice, find the ids and make the weights (KP: k rounded up to
@@ -348,32 +487,40 @@ enum { NO_GROUPS = 0, LANE_GROUPS = 1, ANY_GROUPS = 2 };
 // additions), reciprocal and product 3: 37 of the largest score; relative to a
 // score, with |d| <= 88, 256.  c = s + bias adds a rounding of c.
 template <int LPT, int BY, int GROUPS>
-__global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_constant__ RouteParams P) {
+__global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_constant__ RouteParams P) {
   constexpr bool SCORED = BY != BY_LOGIT;
   constexpr int TPW = 32 / LPT;                                 // tokens at a time
   constexpr int NB = TPW > 4 ? TPW : 4;                         // tokens of the warp
   constexpr int MOST = LPT * kVals < 32 ? LPT * kVals : 32;     // choices of a token
   constexpr float kU = 1.f / 16777216.f;                        // 2^-24
   constexpr float kTiny = 1e-37f;                               // below that scores have no relative error
-  __shared__ __align__(16) float s_c[kWarps][NB][LPT * kVals];  // what ranks a token's experts
-  __shared__ __align__(16) float s_h[kWarps][32 * kVals];       // the same, each lane's in descending order
-  // a token's choices; then the best value left out and whether to rank again; the softmax's maximum and 1 / sum
-  __shared__ __align__(8) float2 s_win[kWarps][NB][MOST + 2];
+  struct __align__(16) Shared {
+    float c[NB][LPT * kVals];           // what ranks a token's experts
+    float h[32][kList];                 // the same, each lane's in descending order, then -inf
+    // a token's choices; then the best value left out and whether to rank again; the softmax's maximum and 1 / sum
+    float2 win[NB][MOST + 2];
+  };
+  __shared__ Shared s_all[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
   const unsigned mask = group_mask<LPT>(lane), ahead = mask & ((1u << lane) - 1u);
+  Shared& S = s_all[warp];
+  S.h[lane][kVals] = -INFINITY;
   const bool softmax = P.score == SOFTMAX;
   const bool ragged = P.E < LPT * kVals;
 
-  float bias[kVals];
+  __shared__ __align__(16) float s_bias[SCORED ? LPT * kVals : 4];
   float reach = 0.f;                                            // largest |bias|
   if constexpr (SCORED) {
+    for (int e = threadIdx.x; e < LPT * kVals; e += kThreads) {
+      float b = P.bias != nullptr && e < P.E ? P.bias[e] : 0.f;
+      s_bias[e] = b != b ? -INFINITY : b;
+    }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
-      const int e = gl * kVals + i;
-      bias[i] = P.bias != nullptr && e < P.E ? P.bias[e] : 0.f;
-      if (bias[i] != bias[i]) bias[i] = -INFINITY;
-      if (fabsf(bias[i]) < INFINITY) reach = fmaxf(reach, fabsf(bias[i]));
+      const float b = fabsf(s_bias[gl * kVals + i]);
+      if (b < INFINITY) reach = fmaxf(reach, b);
     }
     reach = lanes_max<LPT>(reach);
   }
@@ -381,18 +528,11 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
   // the warp's share of the tokens, NB at a time
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t end = (me + 1) * P.T / warps;
-#pragma unroll 1
-  for (int64_t t0 = me * P.T / warps; t0 < end; t0 += NB) {
-  const int ntok = static_cast<int>(min(static_cast<int64_t>(NB), end - t0));
-  __syncwarp();                                                 // the last tokens' rows have been read
-#pragma unroll 1
-  for (int n0 = 0; n0 < ntok; n0 += TPW) {
-    const int n = n0 + grp;
-    const bool in = n < ntok;
-    const float* row = P.logits + (t0 + (in ? n : 0)) * P.E;
-    float2* win = s_win[warp][n];
-    float* row_c = s_c[warp][n];
-    float z[kVals];
+  int64_t t0 = me * P.T / warps;
+  unsigned undecided = 0;                                       // tokens of the set that fp32 cannot decide
+  float z[kVals];
+  const auto load = [&](int64_t t) {                            // past the share: some token of it
+    const float* row = P.logits + min(t, end - 1) * P.E;
     if (P.E % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < kVals; i += 4) {
@@ -405,6 +545,19 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < kVals; ++i) z[i] = gl * kVals + i < P.E ? row[gl * kVals + i] : 0.f;
     }
+  };
+  if (t0 < end) load(t0 + grp);
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+  for (; t0 < end; t0 += NB) {
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(NB), end - t0));
+  __syncwarp();                                                 // the last tokens' rows have been read
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += TPW) {
+    const int n = n0 + grp;
+    float2* win = S.win[n];
+    float* row_c = S.c[n];
     float probe = 0.f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) probe = fmaf(z[i], 0.f, probe);
@@ -428,11 +581,18 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
       sum = lanes_sum<LPT>(sum);
       inv = sum == 0.f ? 0.f : 1.f / sum;
     }
+    if constexpr (BY == BY_LOGIT) {
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      if constexpr (BY == BY_LOGIT) h[i] = z[i];
-      else if constexpr (BY == BY_SIGMOID) h[i] = rcp_fast(1.f + exp_fast(-z[i])) + bias[i];
-      else h[i] = fmaf(h[i], inv, bias[i]);
+      for (int i = 0; i < kVals; ++i) h[i] = z[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(s_bias + gl * kVals + i);
+        const float bias[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int m = i; m < i + 4; ++m)
+          h[m] = BY == BY_SIGMOID ? rcp_fast(1.f + exp_fast(-z[m])) + bias[m - i] : fmaf(h[m], inv, bias[m - i]);
+      }
     }
     if (odd) {
 #pragma unroll
@@ -444,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
       for (int i = 0; i < kVals; ++i)
         if (gl * kVals + i >= P.E) h[i] = -INFINITY;
     }
+    load(t0 + n + TPW);                                         // on its way while this token is ranked
 #pragma unroll
     for (int i = 0; i < kVals; i += 4)
       *reinterpret_cast<float4*>(row_c + gl * kVals + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
@@ -452,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
 
     if constexpr (GROUPS != NO_GROUPS) {
       float worst = -INFINITY, next;
+      uint32_t out;                                             // of the lane's experts, those that take no part
       if constexpr (GROUPS == LANE_GROUPS) {
         float a = h[0], b = h[1];
         for (int off = 1; off < P.lanes_of_group; off <<= 1) {
@@ -460,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
         }
         const float score = P.group_top == 2 && b != -INFINITY ? a + b : a;
         float cur = score;
+#pragma unroll 4
         for (int r = 0; r < P.top_groups; ++r) {
           worst = lanes_max<LPT>(cur);
           if (cur == worst) cur = -INFINITY;
@@ -467,42 +630,47 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
         next = lanes_max<LPT>(cur);
         const bool keep = score >= worst, first = (gl & (P.lanes_of_group - 1)) == 0 && gl * kVals < P.E;
         if (__popc(__ballot_sync(kAll, keep && first) & mask) != P.top_groups) close = true;     // equal scores
+        out = keep ? 0u : 0xffu;
         if (!keep) h[0] = -INFINITY;                            // its lane is never picked
       } else {
         const Kept kept = kept_groups<LPT>(P, row_c, reinterpret_cast<float*>(win), 2 * (MOST + 2), lane);
         worst = kept.worst;
         next = kept.next;
         close = kept.close;
+        out = ~kept.experts;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) h[i] = (kept.experts >> i & 1u) ? row_c[gl * kVals + i] : -INFINITY;
         sort8(h);
       }
       if (worst == -INFINITY) close = true;                     // groups without an expert left
       if constexpr (SCORED) {
-        // two scores, the roundings of their c and that of the sum
-        const float err = BY == BY_SOFTMAX ? 2.f * 37.f * kU * inv + 4.f * kU * (inv + reach)
-                                           : 2.f * 4.1f * kU + 4.f * kU * (1.f + reach);
+        // two scores and the rounding of their sum
+        const float most = BY == BY_SOFTMAX ? inv : 1.f, err = 2.f * (error_of<BY>(most, reach) + kU * (most + reach));
         if (!(worst - next > 2.f * err)) close = true;
+        if (GROUPS == LANE_GROUPS && !close && out != 0) {
+#pragma unroll
+          for (int i = 0; i < kVals; i += 4)
+            *reinterpret_cast<float4*>(row_c + gl * kVals + i) = make_float4(NAN, NAN, NAN, NAN);
+        }
+        if (GROUPS == ANY_GROUPS && !close) {
+#pragma unroll
+          for (int i = 0; i < kVals; ++i)
+            if (out >> i & 1u) row_c[gl * kVals + i] = NAN;
+        }
       }
     }
 
     // the rounds: the lowest lane with the largest head gives it, and takes its next from shared memory
-    float* list = s_h[warp] + lane * kVals;
+    float* list = S.h[lane];
 #pragma unroll
     for (int i = 0; i < kVals; i += 4)
       *reinterpret_cast<float4*>(list + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     float head = h[0];
-    const float* last = list + kVals - 1;
-    float2* to = win;
-#pragma unroll 2
-    for (int j = 0; j < P.k; ++j, ++to) {
-      const float best = lanes_max<LPT>(head);
-      const bool equal = head == best;
-      if ((__ballot_sync(kAll, equal) & ahead) == 0 && equal) {
-        *to = make_float2(best, __int_as_float(gl));
-        head = list == last ? -INFINITY : *++list;
-      }
-    }
+    uint32_t at = smem_u32(list);
+    const uint32_t end_of_list = at + 4 * kVals;
+    const uint32_t to = smem_u32(win);
+#pragma unroll 4
+    for (int j = 0; j < P.k; ++j) take(head, at, end_of_list, to + 8 * j, lanes_max<LPT>(head), gl, ahead);
     const float left = SCORED ? lanes_max<LPT>(head) : -INFINITY;
     if (gl == 0) {
       win[P.k] = make_float2(left, close ? 1.f : 0.f);
@@ -520,10 +688,11 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
     const bool here = n < ntok && j < P.k;
     const int nn = n < ntok ? n : 0, jj = here ? j : 0;
     const float* row = P.logits + (t0 + nn) * P.E;
-    const float2* win = s_win[warp][nn];
+    const float2* win = S.win[nn];
     const float v = win[jj].x, top = win[P.k + 1].x, inv = win[P.k + 1].y;
     const int o = __float_as_int(win[jj].y);
-    bool close = win[P.k].y != 0.f || v == -INFINITY;           // or fewer than k experts are left
+    const bool groups_close = win[P.k].y != 0.f;
+    bool close = groups_close || v == -INFINITY;                // or fewer than k experts are left
     int skip = 0;
     if constexpr (SCORED) {
       // an absolute bound on the error of a score, and one relative to it (its size is at most |c| + reach)
@@ -536,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
       // equal logits of one lane, chosen one after another
       while (skip < jj && win[jj - 1 - skip].x == v && __float_as_int(win[jj - 1 - skip].y) == o) ++skip;
     }
-    const float* row_c = s_c[warp][nn] + o * kVals;
+    const float* row_c = S.c[nn] + o * kVals;
     float c[kVals];
 #pragma unroll
     for (int i = 0; i < kVals; i += 4) {
@@ -552,26 +721,38 @@ __global__ void __launch_bounds__(kThreads, 4) route_scores_kernel(const __grid_
         if (row_c[idx] == v && skip-- == 0) break;
     }
     int sel = o * kVals + idx;
-    unsigned again = __ballot_sync(kAll, here && close);        // such a token's first id is -1 until below
-    again >>= lane & ~(kp - 1);
-    again &= kp == 32 ? kAll : (1u << kp) - 1u;
-
+    unsigned who = __ballot_sync(kAll, here && close);
+    while (who != 0) {
+      const int place = (__ffs(who) - 1) >> kp_log;             // the token's among the 32 / kp
+      who &= ~((kp == 32 ? kAll : (1u << kp) - 1u) << (place << kp_log));
+      undecided |= 1u << (n0 + place);
+    }
     const float w = weight_of(P, here ? row[sel] : -INFINITY, kp, top, inv);
     if (here) {
-      P.ids[(t0 + n) * P.k + j] = again != 0 ? -1 : sel;
+      P.ids[(t0 + n) * P.k + j] = sel;
       P.probs[(t0 + n) * P.k + j] = w;
     }
   }
+  if (undecided != 0) break;
   }
-  // the tokens that fp32 could not decide, in fp64
-  __syncwarp();
-  for (int64_t t1 = me * P.T / warps; t1 < end; t1 += 32) {
-    unsigned again = __ballot_sync(kAll, t1 + lane < end && P.ids[(t1 + lane) * P.k] < 0);
-    while (again != 0) {
-      const int64_t t = t1 + __ffs(again) - 1;
-      again &= again - 1;
-      route_exact<SCORED>(P, t);
+  if (undecided == 0) return;
+  do {
+    const int n = __ffs(undecided) - 1;
+    undecided &= undecided - 1;
+    const float* row = P.logits + (t0 + n) * P.E;
+    float2* win = S.win[n];
+    __syncwarp();
+    const float2 stat = win[P.k + 1];
+    rank_close<BY, GROUPS, LPT * kVals>(P, row, S.c[n], win, reinterpret_cast<uint8_t*>(S.h), reach, stat.y,
+                                        win[P.k].y != 0.f);
+    const int sel = __float_as_int(win[lane < P.k ? lane : 0].y);
+    const float w = weight_of(P, lane < P.k ? row[sel] : -INFINITY, 32, stat.x, stat.y);
+    if (lane < P.k) {
+      P.ids[(t0 + n) * P.k + lane] = sel;
+      P.probs[(t0 + n) * P.k + lane] = w;
     }
+  } while (undecided != 0);
+  t0 += NB;
   }
 }
 
@@ -761,8 +942,8 @@ extern "C" int mxg_route_scores_fwd(const float* logits, const float* bias, int 
   const bool scored = bias != nullptr || (top_groups < groups && group_top == 2);
   const int by = !scored ? BY_LOGIT : score == SIGMOID ? BY_SIGMOID : BY_SOFTMAX;
   const int kind = top_groups == groups ? NO_GROUPS : p.lanes_of_group != 0 ? LANE_GROUPS : ANY_GROUPS;
-  // all that fit at once (four blocks an SM), fewer where a warp would get less than a set of tokens
-  const unsigned most = 4 * 152, need = token_blocks(T, E), grid = need < most ? need : most;
+  // all that fit at once (three blocks an SM), fewer where a warp would get less than a set of tokens
+  const unsigned most = 3 * 152, need = token_blocks(T, E), grid = need < most ? need : most;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   with_lanes(E, [&](auto l) {
     with_three(by, [&](auto b) {
