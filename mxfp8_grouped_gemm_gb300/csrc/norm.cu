@@ -181,28 +181,98 @@ struct NormBwdParams {
   float* part;            // [gridDim.x][H]; the result itself where the grid is one CTA
 };
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows that are copied into shared memory ahead of the one that is worked on: as
+// many as fit with the CTAs an SM runs (bwd_ctas); 16384 fp32 values are one.
+constexpr int rows_ahead(int lpr, int nch, bool f32) {
+  const bool widest = lpr == 0 && nch == 4;
+  return f32 ? (widest ? 0 : 1) : widest ? 1 : nch == 1 ? 2 : 3;
+}
+
+// A CTA takes rows blockIdx, + grid, ... and keeps the sums of its columns of
+// dweight in registers.  Every thread copies its own chunks of the next rows into
+// shared memory and reads them back itself, so that
+// kAhead rows are on their way without a register or a barrier for them.
 template <int LPR, int NCH, bool F32>
 __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd_kernel(const NormBwdParams P) {
   constexpr int kGroups = LPR != 0 ? kRowThreads / LPR : 1;     // rows at a time
+  constexpr int kAhead = rows_ahead(LPR, NCH, F32);
+  constexpr int kR = F32 ? 2 : 1;                               // 16-byte pieces of a chunk of r
+  constexpr int kPieces = NCH * (1 + 2 * kR);                   // of a thread's part of a row: dy, r, dresidual
+  extern __shared__ __align__(16) uint8_t s_rows[];             // [kAhead + 1][kPieces][threads] x 16 bytes
   __shared__ float s_part[2][32];
-  __shared__ float s_acc[LPR != 0 ? (kGroups - 1) * LPR * NCH * 8 : 1];
   launch_dependents();
   const int threads = LPR != 0 ? LPR : static_cast<int>(blockDim.x);
   const int th = LPR != 0 ? static_cast<int>(threadIdx.x) % LPR : static_cast<int>(threadIdx.x);
   const int group = LPR != 0 ? static_cast<int>(threadIdx.x) / LPR : 0;
   const int n8 = P.H >> 3;
-  float acc[NCH][8];
+  const uint32_t piece = blockDim.x * 16, stage_bytes = kPieces * piece;
+  const uint32_t slot0 = smem_u32(s_rows) + threadIdx.x * 16;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  const int rb = F32 ? 32 : 16;                                 // bytes of a chunk of r
+
+  const auto request = [&](int64_t row, uint32_t slot) {
+    if (row < P.T) {
+      const int64_t base = row * n8;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i)
+      for (int i = 0; i < NCH; ++i) {
+        const int c = th + i * threads;
+        if (c < n8) {
+          copy16(slot + i * piece, P.dy + (base + c) * 8);
+          const uint8_t* r = static_cast<const uint8_t*>(P.r) + (base + c) * rb;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  int parity = 0;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups; first < P.T;
-       first += static_cast<int64_t>(gridDim.x) * kGroups, parity ^= 1) {
-    const int64_t row = first + group;
+          for (int m = 0; m < kR; ++m) copy16(slot + (NCH + kR * i + m) * piece, r + 16 * m);
+          if (P.dresidual != nullptr) {
+            const uint8_t* d = static_cast<const uint8_t*>(P.dresidual) + (base + c) * rb;
+#pragma unroll
+            for (int m = 0; m < kR; ++m) copy16(slot + (NCH + kR * (NCH + i) + m) * piece, d + 16 * m);
+          }
+        }
+      }
+    }
+    copies_end();
+  };
+  const auto read = [&](uint32_t slot, int i, bool wide, float (&v)[8]) {      // piece(s) i of a slot
+    const uint8_t* p = s_rows + (slot - smem_u32(s_rows));
+    if (wide) {
+      const float4 a = *reinterpret_cast<const float4*>(p + i * piece);
+      const float4 b = *reinterpret_cast<const float4*>(p + (i + 1) * piece);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      unpack8(*reinterpret_cast<const uint4*>(p + i * piece), v);
+    }
+  };
+
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) request(row0 + a * step, slot0 + a * stage_bytes);
+  float acc[NCH][8], w[NCH][8];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = th + i * threads;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = w[i][j] = 0.f;
+    if (c < n8) load_weight(P.weight, P.w32, 8 * c, w[i]);
+  }
+  float rstd_next = row0 < P.T ? P.rstd[row0] : 0.f;
+  int parity = 0, stage = 0;
+  for (int64_t row = row0; row - group < P.T; row += step, parity ^= 1) {
     const bool live = row < P.T;
-    const int64_t base = row * P.H;
-    const float rstd = live ? P.rstd[row] : 0.f;
+    const float rstd = live ? rstd_next : 0.f;
+    if (row + step < P.T) rstd_next = P.rstd[row + step];
+    const int ahead = stage >= 1 ? stage - 1 : kAhead;          // the slot of the row before, which is free
+    request(row + kAhead * step, slot0 + ahead * stage_bytes);
+    copies_wait<kAhead>();
+    const uint32_t slot = slot0 + stage * stage_bytes;
+    stage = stage == kAhead ? 0 : stage + 1;
     float xh[NCH][8], g[NCH][8];
     float dot = 0.f;
 #pragma unroll
@@ -211,45 +281,39 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd
 #pragma unroll
       for (int j = 0; j < 8; ++j) xh[i][j] = g[i][j] = 0.f;
       if (live && c < n8) {
-        load8(P.dy + base + 8 * c, g[i]);
-        if constexpr (F32) load8(static_cast<const float*>(P.r) + base + 8 * c, xh[i]);
-        else load8(static_cast<const uint16_t*>(P.r) + base + 8 * c, xh[i]);
+        read(slot, i, false, g[i]);
+        read(slot, NCH + kR * i, F32, xh[i]);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = th + i * threads;
-      float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < n8) load_weight(P.weight, P.w32, 8 * c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xh[i][j] *= rstd;
         acc[i][j] = fmaf(g[i][j], xh[i][j], acc[i][j]);
-        g[i][j] *= w[j];
+        g[i][j] *= w[i][j];
         dot = fmaf(g[i][j], xh[i][j], dot);
       }
     }
     const float mean = row_sum<LPR>(dot, s_part, parity) * P.inv_h;
+    const int64_t base = row * n8;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = th + i * threads;
       if (live && c < n8) {
         float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (P.dresidual != nullptr) {
-          if constexpr (F32) load8(static_cast<const float*>(P.dresidual) + base + 8 * c, d);
-          else load8(static_cast<const uint16_t*>(P.dresidual) + base + 8 * c, d);
-        }
+        if (P.dresidual != nullptr) read(slot, NCH + kR * (NCH + i), F32, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-xh[i][j], mean, g[i][j]), d[j]);
-        if (P.dx != nullptr) store8(P.dx + base + 8 * c, d);
+        store8(P.dx + (base + c) * 8, d);
         if constexpr (F32) {
-          if (P.dresidual_out != nullptr) store8(P.dresidual_out + base + 8 * c, d);
+          if (P.dresidual_out != nullptr) store8(P.dresidual_out + (base + c) * 8, d);
         }
       }
     }
   }
+  copies_wait<0>();
   // the row groups' sums in order
   if constexpr (kGroups > 1) {
+    float* s_acc = reinterpret_cast<float*>(s_rows);
+    __syncthreads();
     if (group != 0) {
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
@@ -292,7 +356,7 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const float* __restri
 // Calls f(lanes per row or 0, chunks per thread) with the form of a width, as
 // compile-time numbers.
 template <typename F>
-void with_width(int H, F f) {
+void with_width(int H, int wide_chunks, F f) {
   const int n8 = H / 8;
   using std::integral_constant;
   if (n8 <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
@@ -300,16 +364,25 @@ void with_width(int H, F f) {
   else if (n8 <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (n8 <= 64) f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
   else if (n8 <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  else if (wide_chunks == 2) f(integral_constant<int, 0>{}, integral_constant<int, 2>{});
   else f(integral_constant<int, 0>{}, integral_constant<int, 4>{});
 }
 
-int wide_threads(int H) { return (H / 8 + 4 * 32 - 1) / (4 * 32) * 32; }
+int wide_threads(int H, int chunks) { return (H / 8 + chunks * 32 - 1) / (chunks * 32) * 32; }
 
 int rows_at_once(int H) { return H <= 64 ? 16 : H <= 128 ? 8 : H <= 1024 ? 4 : 1; }
 
+// The backward's chunks per thread of a wide row, its threads, and the shared
+// memory of its rows (in the widest case, fp32 streams).
+int bwd_chunks(int H) { return H <= 8192 ? 2 : 4; }
+int bwd_threads(int H) { return H <= 1024 ? kRowThreads : wide_threads(H, bwd_chunks(H)); }
+
+// CTAs of the backward: what fits on the SMs at once (their partial sums of
+// dweight are read again), at most one for each set of rows.
+int bwd_ctas(int H) { return H <= 256 ? 8 : H <= 512 ? 4 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1; }
 int bwd_blocks(int T, int H) {
   const int64_t need = (static_cast<int64_t>(T) + rows_at_once(H) - 1) / rows_at_once(H);
-  const int64_t most = static_cast<int64_t>(kSms) * (H <= 4096 ? 4 : H <= 8192 ? 2 : 1);
+  const int64_t most = static_cast<int64_t>(kSms) * bwd_ctas(H);
   return static_cast<int>(need < most ? need : most);
 }
 
@@ -335,8 +408,8 @@ extern "C" int mxg_rms_norm_fwd(const mxg_rms_norm_fwd_args* A, void* stream) {
                   static_cast<float>(1.0 / A->H), A->y, A->q, A->s, A->layout, A->rstd};
   const int rows = rows_at_once(A->H);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(A->T) + rows - 1) / rows);
-  with_width(A->H, [&](auto lpr, auto nch) {
-    const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H);
+  with_width(A->H, 4, [&](auto lpr, auto nch) {
+    const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H, nch.value);
     if (!A->residual) norm_fwd_kernel<lpr.value, nch.value, RES_NONE><<<grid, block, 0, st>>>(p);
     else if (A->residual_f32) norm_fwd_kernel<lpr.value, nch.value, RES_F32><<<grid, block, 0, st>>>(p);
     else norm_fwd_kernel<lpr.value, nch.value, RES_BF16><<<grid, block, 0, st>>>(p);
@@ -366,11 +439,18 @@ extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
   NormBwdParams p{A->T, A->H, A->dy, A->r, A->weight, A->weight_f32 != 0, A->rstd, static_cast<float>(1.0 / A->H),
                   A->dresidual, A->dx, A->dresidual_out,
                   nblk == 1 ? A->dweight : static_cast<float*>(A->workspace)};
-  with_width(A->H, [&](auto lpr, auto nch) {
-    const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H);
-    if (A->r_f32) norm_bwd_kernel<lpr.value, nch.value, true><<<nblk, block, 0, st>>>(p);
-    else norm_bwd_kernel<lpr.value, nch.value, false><<<nblk, block, 0, st>>>(p);
+  const int block = bwd_threads(A->H);
+  cudaError_t err = cudaSuccess;
+  with_width(A->H, bwd_chunks(A->H), [&](auto lpr, auto nch) {
+    const auto launch = [&](auto* kern, bool f32) {
+      const int smem = (rows_ahead(lpr.value, nch.value, f32) + 1) * nch.value * (f32 ? 5 : 3) * block * 16;
+      err = allow_smem(kern, 200 * 1024);
+      if (err == cudaSuccess) kern<<<nblk, block, smem, st>>>(p);
+    };
+    if (A->r_f32) launch(norm_bwd_kernel<lpr.value, nch.value, true>, true);
+    else launch(norm_bwd_kernel<lpr.value, nch.value, false>, false);
   });
+  MXG_TRY(err);
   count_launch();
   MXG_TRY(cudaGetLastError());
   if (nblk == 1) return MXG_OK;
