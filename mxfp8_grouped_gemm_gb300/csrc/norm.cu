@@ -181,8 +181,11 @@ struct NormBwdParams {
   float* part;            // [gridDim.x][H]; the result itself where the grid is one CTA
 };
 
+// L1: of values whose other half of a 32-byte sector is copied next.
+template <bool L1>
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  if constexpr (L1) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -190,24 +193,27 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows that are copied into shared memory ahead of the one that is worked on: as
-// many as fit with the CTAs an SM runs (bwd_ctas); 16384 fp32 values are one.
-constexpr int rows_ahead(int lpr, int nch, bool f32) {
+// Rows of a CTA (or of its lane groups) in shared memory: as many as fit with the
+// CTAs an SM runs (bwd_ctas); one of 16384 fp32 values.
+constexpr int row_slots(int lpr, int nch, bool f32) {
   const bool widest = lpr == 0 && nch == 4;
-  return f32 ? (widest ? 0 : 1) : widest ? 1 : nch == 1 ? 2 : 3;
+  return f32 ? (widest ? 1 : 2) : widest ? 2 : nch == 1 ? 3 : 4;
 }
 
 // A CTA takes rows blockIdx, + grid, ... and keeps the sums of its columns of
 // dweight in registers.  Every thread copies its own chunks of the next rows into
 // shared memory and reads them back itself, so that
-// kAhead rows are on their way without a register or a barrier for them.
+// kSlots rows are on their way without a register or a barrier for them: a slot
+// is filled again as soon as its row is in registers (kHold) or, where a thread
+// has too much of a row for that, once it has been read a second time.
 template <int LPR, int NCH, bool F32>
 __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd_kernel(const NormBwdParams P) {
   constexpr int kGroups = LPR != 0 ? kRowThreads / LPR : 1;     // rows at a time
-  constexpr int kAhead = rows_ahead(LPR, NCH, F32);
+  constexpr int kSlots = row_slots(LPR, NCH, F32);
+  constexpr bool kHold = LPR != 0 || NCH < 4;
   constexpr int kR = F32 ? 2 : 1;                               // 16-byte pieces of a chunk of r
   constexpr int kPieces = NCH * (1 + 2 * kR);                   // of a thread's part of a row: dy, r, dresidual
-  extern __shared__ __align__(16) uint8_t s_rows[];             // [kAhead + 1][kPieces][threads] x 16 bytes
+  extern __shared__ __align__(16) uint8_t s_rows[];             // [kSlots][kPieces][threads] x 16 bytes
   __shared__ float s_part[2][32];
   launch_dependents();
   const int threads = LPR != 0 ? LPR : static_cast<int>(blockDim.x);
@@ -227,14 +233,14 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd
       for (int i = 0; i < NCH; ++i) {
         const int c = th + i * threads;
         if (c < n8) {
-          copy16(slot + i * piece, P.dy + (base + c) * 8);
+          copy16<false>(slot + i * piece, P.dy + (base + c) * 8);
           const uint8_t* r = static_cast<const uint8_t*>(P.r) + (base + c) * rb;
 #pragma unroll
-          for (int m = 0; m < kR; ++m) copy16(slot + (NCH + kR * i + m) * piece, r + 16 * m);
+          for (int m = 0; m < kR; ++m) copy16<F32>(slot + (NCH + kR * i + m) * piece, r + 16 * m);
           if (P.dresidual != nullptr) {
             const uint8_t* d = static_cast<const uint8_t*>(P.dresidual) + (base + c) * rb;
 #pragma unroll
-            for (int m = 0; m < kR; ++m) copy16(slot + (NCH + kR * (NCH + i) + m) * piece, d + 16 * m);
+            for (int m = 0; m < kR; ++m) copy16<F32>(slot + (NCH + kR * (NCH + i) + m) * piece, d + 16 * m);
           }
         }
       }
@@ -253,14 +259,14 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd
   };
 
 #pragma unroll
-  for (int a = 0; a < kAhead; ++a) request(row0 + a * step, slot0 + a * stage_bytes);
-  float acc[NCH][8], w[NCH][8];
+  for (int a = 0; a < kSlots; ++a) request(row0 + a * step, slot0 + a * stage_bytes);
+  float acc[NCH][8], w[kHold ? NCH : 1][8];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = th + i * threads;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = w[i][j] = 0.f;
-    if (c < n8) load_weight(P.weight, P.w32, 8 * c, w[i]);
+    for (int j = 0; j < 8; ++j) acc[i][j] = w[kHold ? i : 0][j] = 0.f;
+    if (kHold && c < n8) load_weight(P.weight, P.w32, 8 * c, w[i]);
   }
   float rstd_next = row0 < P.T ? P.rstd[row0] : 0.f;
   int parity = 0, stage = 0;
@@ -268,45 +274,99 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd
     const bool live = row < P.T;
     const float rstd = live ? rstd_next : 0.f;
     if (row + step < P.T) rstd_next = P.rstd[row + step];
-    const int ahead = stage >= 1 ? stage - 1 : kAhead;          // the slot of the row before, which is free
-    request(row + kAhead * step, slot0 + ahead * stage_bytes);
-    copies_wait<kAhead>();
+    copies_wait<kSlots - 1>();
     const uint32_t slot = slot0 + stage * stage_bytes;
-    stage = stage == kAhead ? 0 : stage + 1;
-    float xh[NCH][8], g[NCH][8];
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
+    stage = stage == kSlots - 1 ? 0 : stage + 1;
+    // chunk i of the row: dy weight and r rstd
+    const auto load = [&](int i, float (&g)[8], float (&xh)[8]) {
       const int c = th + i * threads;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xh[i][j] = g[i][j] = 0.f;
+      for (int j = 0; j < 8; ++j) xh[j] = g[j] = 0.f;
       if (live && c < n8) {
-        read(slot, i, false, g[i]);
-        read(slot, NCH + kR * i, F32, xh[i]);
+        read(slot, i, false, g);
+        read(slot, NCH + kR * i, F32, xh);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
-        acc[i][j] = fmaf(g[i][j], xh[i][j], acc[i][j]);
-        g[i][j] *= w[i][j];
-        dot = fmaf(g[i][j], xh[i][j], dot);
-      }
-    }
-    const float mean = row_sum<LPR>(dot, s_part, parity) * P.inv_h;
-    const int64_t base = row * n8;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
+      for (int j = 0; j < 8; ++j) xh[j] *= rstd;
+    };
+    const auto finish = [&](int i, const float (&g)[8], const float (&xh)[8], const uint4 (&held)[kR], float mean) {
       const int c = th + i * threads;
       if (live && c < n8) {
-        float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (P.dresidual != nullptr) read(slot, NCH + kR * (NCH + i), F32, d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-xh[i][j], mean, g[i][j]), d[j]);
-        store8(P.dx + (base + c) * 8, d);
+        const int64_t at = (row * n8 + c) * 8;
+        float d[8];
         if constexpr (F32) {
-          if (P.dresidual_out != nullptr) store8(P.dresidual_out + (base + c) * 8, d);
+          const uint4 a = held[0], b = held[1];
+          const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = __uint_as_float(v[j]);
+        } else {
+          unpack8(held[0], d);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(-xh[j], mean, g[j]), d[j]);
+        store8(P.dx + at, d);
+        if constexpr (F32) {
+          if (P.dresidual_out != nullptr) store8(P.dresidual_out + at, d);
         }
       }
+    };
+    const auto hold = [&](int i, uint4 (&held)[kR]) {             // dresidual, as it came
+#pragma unroll
+      for (int m = 0; m < kR; ++m) {
+        held[m] = make_uint4(0, 0, 0, 0);
+        if (P.dresidual != nullptr && live && th + i * threads < n8)
+          held[m] = *reinterpret_cast<const uint4*>(s_rows + (slot - smem_u32(s_rows)) +
+                                                    (NCH + kR * (NCH + i) + m) * piece);
+      }
+    };
+    float dot = 0.f;
+    if constexpr (kHold) {
+      float xh[NCH][8], g[NCH][8];
+      uint4 held[NCH][kR];
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        load(i, g[i], xh[i]);
+        hold(i, held[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[i][j] = fmaf(g[i][j], xh[i][j], acc[i][j]);
+          g[i][j] *= w[i][j];
+          dot = fmaf(g[i][j], xh[i][j], dot);
+        }
+      }
+      const float mean = row_sum<LPR>(dot, s_part, parity) * P.inv_h;
+      __syncwarp();                                             // the slot has been read
+      request(row + kSlots * step, slot);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) finish(i, g[i], xh[i], held[i], mean);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        float xh[8], g[8];
+        load(i, g, xh);
+        const int c = th + i * threads;
+        if (c < n8) load_weight(P.weight, P.w32, 8 * c, w[0]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[i][j] = fmaf(g[j], xh[j], acc[i][j]);
+          dot = fmaf(g[j] * w[0][j], xh[j], dot);
+        }
+      }
+      const float mean = row_sum<LPR>(dot, s_part, parity) * P.inv_h;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        float xh[8], g[8];
+        uint4 held[kR];
+        load(i, g, xh);
+        hold(i, held);
+        const int c = th + i * threads;
+        if (c < n8) load_weight(P.weight, P.w32, 8 * c, w[0]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= w[0][j];
+        finish(i, g, xh, held, mean);
+      }
+      __syncwarp();
+      request(row + kSlots * step, slot);
     }
   }
   copies_wait<0>();
@@ -336,21 +396,21 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_bwd
   }
 }
 
-// dweight: the CTAs' partial sums, eight threads to a column, in order.
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const float* __restrict__ part, int nblk, int H,
-                                                           float* __restrict__ dw) {
-  __shared__ float s_sum[8][32];
+// dweight: the CTAs' partial sums, 32 threads to a column, in order.
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* __restrict__ part, int nblk, int H,
+                                                            float* __restrict__ dw) {
+  __shared__ float s_sum[32][33];
   dependency_wait();
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (col < H)
-    for (int b = k; b < nblk; b += 8) v += part[static_cast<int64_t>(b) * H + col];
-  s_sum[k][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (k == 0 && col < H) {
-    for (int i = 1; i < 8; ++i) v += s_sum[i][threadIdx.x & 31];
-    dw[col] = v;
+  if (col < H) {
+#pragma unroll 8
+    for (int b = k; b < nblk; b += 32) v += part[static_cast<int64_t>(b) * H + col];
   }
+  s_sum[k][lane] = v;
+  __syncthreads();
+  v = lanes_sum<32>(s_sum[lane][k]);
+  if (lane == 0 && blockIdx.x * 32 + k < H) dw[blockIdx.x * 32 + k] = v;
 }
 
 // Calls f(lanes per row or 0, chunks per thread) with the form of a width, as
@@ -443,7 +503,7 @@ extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
   cudaError_t err = cudaSuccess;
   with_width(A->H, bwd_chunks(A->H), [&](auto lpr, auto nch) {
     const auto launch = [&](auto* kern, bool f32) {
-      const int smem = (rows_ahead(lpr.value, nch.value, f32) + 1) * nch.value * (f32 ? 5 : 3) * block * 16;
+      const int smem = row_slots(lpr.value, nch.value, f32) * nch.value * (f32 ? 5 : 3) * block * 16;
       err = allow_smem(kern, 200 * 1024);
       if (err == cudaSuccess) kern<<<nblk, block, smem, st>>>(p);
     };
@@ -454,6 +514,6 @@ extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
   count_launch();
   MXG_TRY(cudaGetLastError());
   if (nblk == 1) return MXG_OK;
-  MXG_TRY(launch_after(norm_dweight_kernel, dim3((A->H + 31) / 32), dim3(256), 0, st, p.part, nblk, A->H, A->dweight));
+  MXG_TRY(launch_after(norm_dweight_kernel, dim3((A->H + 31) / 32), dim3(1024), 0, st, p.part, nblk, A->H, A->dweight));
   return MXG_OK;
 }
