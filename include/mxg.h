@@ -375,7 +375,7 @@ int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* args, void* stream);
  *   norm = sqrt(sum of g^2 over all tensors)
  *   out  = g min(1, max_norm / norm)     (in g's type, rounded once)
  * The tensors (bf16 and fp32 mixed) are a host array, read during the call only.
- * Squares are added in fp32 within 32 elements and in fp64 beyond, in a fixed
+ * Squares are added in fp32 within 64 elements and in fp64 beyond, in a fixed
  * order; sums that leave fp32's range are taken in fp64 throughout, so norms of
  * gradients of any finite size are right (written as infinity beyond fp32, while
  * mxg_grad_clip's own factor still has its value).  An infinite norm clips to
@@ -387,7 +387,7 @@ int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* args, void* stream);
  * untouched where the factor is 1); other buffers do not overlap, and no tensor
  * is listed twice as an output.  Tensors may have no elements and any
  * element-aligned address (16-byte aligned ones move in 16-byte pieces).
- * Requires n > 0, max_norm > 0, fewer than 2^31 pieces of 16384 elements. */
+ * Requires n > 0, max_norm > 0, fewer than 2^31 pieces of 4096 elements. */
 typedef struct {
   const void* in;
   void* out;                  /* mxg_grad_clip only                                      */

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -204,9 +205,9 @@ def lib() -> ctypes.CDLL:
         "mxg_muon_update": (I32, [ctypes.POINTER(MuonArgs), P]),
         "mxg_route_scores_fwd": (I32, [P, P, I32, I32, I32, I32, I32, I32, I32, I32, F32, P, P, P]),
         "mxg_route_scores_bwd": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, P, P]),
-        "mxg_rms_norm_fwd": (I32, [ctypes.POINTER(RmsNormFwdArgs), P]),
+        "mxg_rms_norm_fwd": (I32, [P, P]),
         "mxg_rms_norm_bwd_workspace_bytes": (SZ, [I32, I32]),
-        "mxg_rms_norm_bwd": (I32, [ctypes.POINTER(RmsNormBwdArgs), P]),
+        "mxg_rms_norm_bwd": (I32, [P, P]),
         "mxg_grad_norm_workspace_bytes": (SZ, [I32]),
         "mxg_grad_norm": (I32, [P, I32, P, P, SZ, P]),
         "mxg_grad_clip": (I32, [P, I32, F32, P, P, P, SZ, P]),
@@ -522,14 +523,42 @@ def _matrix(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _here(**tensors):
-    """The library runs on the current device, so that is where its tensors have to be."""
-    dev = None
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda:
-            dev = torch._C._cuda_getDevice() if dev is None else dev
-            if t.get_device() != dev:
-                raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+def _real(t: torch.Tensor | None, name: str):
+    if t is not None and t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _pointers(names, tensors, dtypes, shapes) -> list:
+    """Addresses of tensors (0 for None) that have these types and shapes (None: any) and are contiguous and on the
+    current device, where the library runs.  Small calls take as long as this, so it looks at each tensor once."""
+    out, dev = [], None
+    for t, dtype, shape in zip(tensors, dtypes, shapes):
+        if t is None:
+            out.append(0)
+            continue
+        d = t.get_device()
+        if dev is None and d >= 0:
+            dev = torch._C._cuda_getDevice()
+        if d != dev or t.dtype is not dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
+            _refuse(names, tensors, dtypes, shapes)
+        out.append(t.data_ptr())
+    return out
+
+
+def _refuse(names, tensors, dtypes, shapes):
+    for name, t, shape in zip(names, tensors, shapes):
+        if shape is not None:
+            _shape(t, shape, name)
+    for name, t, dtype in zip(names, tensors, dtypes):
+        _ptr(t, dtype, name)
+    here = torch._C._cuda_getDevice()
+    for name, t in zip(names, tensors):
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
+_ROUTE_FWD = ("logits", "bias", "ids", "probs")
+_ROUTE_FWD_TYPES = (torch.float32, torch.float32, torch.int32, torch.float32)
 
 
 def mxg_route_scores_fwd(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
@@ -543,15 +572,14 @@ def mxg_route_scores_fwd(logits, k: int, score: str = "softmax", bias=None, grou
     kind = _score(score)
     ids = _empty((T, k), torch.int32, logits.device, stream) if ids is None else ids
     probs = _empty((T, k), torch.float32, logits.device, stream) if probs is None else probs
-    _shape(bias, (E,), "bias")
-    _shape(ids, (T, k), "ids")
-    _shape(probs, (T, k), "probs")
-    _here(logits=logits, bias=bias, ids=ids, probs=probs)
-    _check("mxg_route_scores_fwd", lib().mxg_route_scores_fwd(
-        _ptr(logits, torch.float32, "logits"), _ptr(bias, torch.float32, "bias"), T, E, k, kind, groups,
-        top_groups, group_top, int(renormalize), scale, _ptr(ids, torch.int32, "ids"),
-        _ptr(probs, torch.float32, "probs"), _stream(stream)))
+    z, b, i, p = _pointers(_ROUTE_FWD, (logits, bias, ids, probs), _ROUTE_FWD_TYPES, (None, (E,), (T, k), (T, k)))
+    _check("mxg_route_scores_fwd", lib().mxg_route_scores_fwd(z, b, T, E, k, kind, groups, top_groups, group_top,
+                                                              renormalize, scale, i, p, _stream(stream)))
     return ids, probs
+
+
+_ROUTE_BWD = ("logits", "ids", "probs", "dprobs", "dlogits_in", "dlogits", "dev_status")
+_ROUTE_BWD_TYPES = (torch.float32, torch.int32, torch.float32, torch.float32, torch.float32, torch.float32, torch.int32)
 
 
 def mxg_route_scores_bwd(logits, ids, probs, dprobs, dev_status, score: str = "softmax", renormalize: bool = True,
@@ -562,23 +590,17 @@ def mxg_route_scores_bwd(logits, ids, probs, dprobs, dev_status, score: str = "s
     k = _matrix(ids, "ids")[1]
     kind = _score(score)
     dlogits = _empty((T, E), torch.float32, logits.device, stream) if dlogits is None else dlogits
-    for name, t in (("ids", ids), ("probs", probs), ("dprobs", dprobs)):
-        _shape(t, (T, k), name)
-    _shape(dlogits_in, (T, E), "dlogits_in")
-    _shape(dlogits, (T, E), "dlogits")
-    _here(logits=logits, ids=ids, probs=probs, dprobs=dprobs, dlogits_in=dlogits_in, dlogits=dlogits,
-          dev_status=dev_status)
-    _check("mxg_route_scores_bwd", lib().mxg_route_scores_bwd(
-        _ptr(logits, torch.float32, "logits"), _ptr(ids, torch.int32, "ids"), _ptr(probs, torch.float32, "probs"),
-        _ptr(dprobs, torch.float32, "dprobs"), _ptr(dlogits_in, torch.float32, "dlogits_in"), T, E, k, kind,
-        int(renormalize), scale, _ptr(dlogits, torch.float32, "dlogits"),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    z, i, p, dp, add, d, st = _pointers(_ROUTE_BWD, (logits, ids, probs, dprobs, dlogits_in, dlogits, dev_status),
+                                        _ROUTE_BWD_TYPES, (None, (T, k), (T, k), (T, k), (T, E), (T, E), None))
+    _check("mxg_route_scores_bwd", lib().mxg_route_scores_bwd(z, i, p, dp, add, T, E, k, kind, renormalize, scale, d, st,
+                                                              _stream(stream)))
     return dlogits
 
 
-def _real(t: torch.Tensor | None, name: str):
-    if t is not None and t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+# the C structures as the bytes that a call passes: one call of struct where ctypes takes a step per field
+_PACK_NORM_FWD = struct.Struct("@iiPPPiiPfiPPPP")
+_PACK_NORM_BWD = struct.Struct("@iiPPiiPPPPPPPQ")
+_NORM_FWD = ("x", "weight", "residual", "residual_out", "y", "q", "s", "rstd")
 
 
 def mxg_rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None, q=None, s=None, rstd=None,
@@ -587,37 +609,33 @@ def mxg_rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, residual_out=N
     sum, residual_out), with codes (or q and s given) 'q' uint8 [T, H] and 's' uint8 (T * H / 32 bytes, `layout`).
 
     residual and weight are bf16 or fp32.  residual_out may be residual, y may be x.  bf16 False: codes alone, no y."""
-    T, H = _matrix(x, "x")
+    T, H = TH = _matrix(x, "x")
     dev = x.device
     if (q is None) != (s is None):
         raise ValueError("q and s are given together")
     if residual_out is not None and residual is None:
         raise ValueError("residual_out needs residual")
-    _real(residual, "residual")
-    _real(weight, "weight")
     if not bf16 and y is not None:
         raise ValueError("y is given but bf16 is False")
-    y = _empty((T, H), torch.bfloat16, dev, stream) if y is None and bf16 else y
+    _real(residual, "residual")
+    _real(weight, "weight")
+    stream_type = torch.float32 if residual is None else residual.dtype
+    y = _empty(TH, torch.bfloat16, dev, stream) if y is None and bf16 else y
     rstd = _empty(T, torch.float32, dev, stream) if rstd is None else rstd
     if residual is not None and residual_out is None:
-        residual_out = _empty((T, H), residual.dtype, dev, stream)
+        residual_out = _empty(TH, stream_type, dev, stream)
     if codes and q is None:
-        q = _empty((T, H), torch.uint8, dev, stream)
+        q = _empty(TH, torch.uint8, dev, stream)
         s = _empty((T, H // 32), torch.uint8, dev, stream)
-    _shape(weight, (H,), "weight")
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y), ("q", q)):
-        _shape(t, (T, H), name)
-    _shape(rstd, (T,), "rstd")
     if s is not None and s.numel() != T * H // 32:
         raise ValueError(f"s must have {T * H // 32} elements, got {s.numel()}")
-    _here(x=x, weight=weight, residual=residual, residual_out=residual_out, y=y, q=q, s=s, rstd=rstd)
-    args = RmsNormFwdArgs(T, H, _ptr(x, torch.bfloat16, "x"), _ptr(residual, None, "residual"),
-                          _ptr(residual_out, None if residual is None else residual.dtype, "residual_out"),
-                          int(residual is not None and residual.dtype == torch.float32),
-                          int(weight.dtype == torch.float32), _ptr(weight, None, "weight"), eps, layout,
-                          _ptr(y, torch.bfloat16, "y"), _ptr(q, torch.uint8, "q"), _ptr(s, torch.uint8, "s"),
-                          _ptr(rstd, torch.float32, "rstd"))
-    _check("mxg_rms_norm_fwd", lib().mxg_rms_norm_fwd(ctypes.byref(args), _stream(stream)))
+    px, pw, pr, po, py, pq, ps, pn = _pointers(
+        _NORM_FWD, (x, weight, residual, residual_out, y, q, s, rstd),
+        (torch.bfloat16, weight.dtype, stream_type, stream_type, torch.bfloat16, torch.uint8, torch.uint8, torch.float32),
+        (None, (H,), TH, TH, TH, TH, None, (T,)))
+    args = _PACK_NORM_FWD.pack(T, H, px, pr, po, residual is not None and stream_type is torch.float32,
+                               weight.dtype is torch.float32, pw, eps, layout, py, pq, ps, pn)
+    _check("mxg_rms_norm_fwd", lib().mxg_rms_norm_fwd(args, _stream(stream)))
     out = {"rstd": rstd}
     if y is not None:
         out["y"] = y
@@ -632,6 +650,9 @@ def mxg_rms_norm_bwd_workspace_bytes(T, H) -> int:
     return int(lib().mxg_rms_norm_bwd_workspace_bytes(T, H))
 
 
+_NORM_BWD = ("dy", "r", "weight", "rstd", "dresidual", "dx", "dresidual_out", "dweight")
+
+
 def mxg_rms_norm_bwd(dy, r, weight, rstd, dresidual=None, dx=None, dresidual_out=None, dweight=None, workspace=None,
                      stream=None):
     """Backward of mxg_rms_norm_fwd for r = its 'residual' (or x, without one), bf16 or fp32 -> (dx bf16 [T, H],
@@ -639,33 +660,25 @@ def mxg_rms_norm_bwd(dy, r, weight, rstd, dresidual=None, dx=None, dresidual_out
 
     dresidual (r's type) is the gradient that reaches the sum from elsewhere.  With a bf16 residual, dx is the gradient
     of x and of the residual alike.  dx may be dy or dresidual, dresidual_out may be dresidual."""
-    T, H = _matrix(dy, "dy")
+    T, H = TH = _matrix(dy, "dy")
     dev = dy.device
     _real(r, "r")
     _real(weight, "weight")
-    f32 = r.dtype == torch.float32
+    f32 = r.dtype is torch.float32
     if dresidual_out is not None and not f32:
         raise ValueError("dresidual_out is for an fp32 residual: dx is the gradient of a bf16 one")
-    dx = _empty((T, H), torch.bfloat16, dev, stream) if dx is None else dx
+    dx = _empty(TH, torch.bfloat16, dev, stream) if dx is None else dx
     if f32 and dresidual_out is None:
-        dresidual_out = _empty((T, H), torch.float32, dev, stream)
+        dresidual_out = _empty(TH, torch.float32, dev, stream)
     dweight = _empty(H, torch.float32, dev, stream) if dweight is None else dweight
-    for name, t in (("r", r), ("dresidual", dresidual), ("dx", dx), ("dresidual_out", dresidual_out)):
-        _shape(t, (T, H), name)
-    _shape(weight, (H,), "weight")
-    _shape(rstd, (T,), "rstd")
-    _shape(dweight, (H,), "dweight")
-    _here(dy=dy, r=r, weight=weight, rstd=rstd, dresidual=dresidual, dx=dx, dresidual_out=dresidual_out,
-          dweight=dweight, workspace=workspace)
-    args = RmsNormBwdArgs(T, H, _ptr(dy, torch.bfloat16, "dy"), _ptr(r, None, "r"), int(f32),
-                          int(weight.dtype == torch.float32), _ptr(weight, None, "weight"),
-                          _ptr(rstd, torch.float32, "rstd"), _ptr(dresidual, r.dtype, "dresidual"),
-                          _ptr(dx, torch.bfloat16, "dx"), _ptr(dresidual_out, torch.float32, "dresidual_out"),
-                          _ptr(dweight, torch.float32, "dweight"))
+    py, pr, pw, pn, pd, px, po, pg = _pointers(
+        _NORM_BWD, (dy, r, weight, rstd, dresidual, dx, dresidual_out, dweight),
+        (torch.bfloat16, r.dtype, weight.dtype, torch.float32, r.dtype, torch.bfloat16, torch.float32, torch.float32),
+        (None, TH, (H,), (T,), TH, TH, TH, (H,)))
+    w32 = weight.dtype is torch.float32
 
     def call(ws, n, st):
-        args.workspace, args.workspace_bytes = ws, n
-        return lib().mxg_rms_norm_bwd(ctypes.byref(args), st)
+        return lib().mxg_rms_norm_bwd(_PACK_NORM_BWD.pack(T, H, py, pr, f32, w32, pw, pn, pd, px, po, pg, ws, n), st)
 
     _call_with_scratch("mxg_rms_norm_bwd", call, lambda: mxg_rms_norm_bwd_workspace_bytes(T, H), workspace, dev, stream)
     return dx, dresidual_out, dweight
@@ -675,30 +688,37 @@ def mxg_grad_norm_workspace_bytes(n) -> int:
     return int(lib().mxg_grad_norm_workspace_bytes(n))
 
 
+_PACK_TENSOR = struct.Struct("@PPqii").pack
+
+
 def _tensor_refs(grads, out):
-    """The tensors as the library's table; out None: no outputs."""
-    n = len(grads)
-    if n == 0:
+    """The library's table of the tensors, as bytes; out None: no outputs."""
+    if not grads:
         raise ValueError("no gradients given")
-    if out is not None and len(out) != n:
-        raise ValueError(f"{n} gradients but {len(out)} outputs")
-    refs = (TensorRef * n)()
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients but {len(out)} outputs")
+    table, used, dev = [], set(), None
     for i, t in enumerate(grads):
-        _real(t, f"grads[{i}]")
-        _here(grads=t)
-        r = refs[i]
-        r.ptr, r.numel, r.f32 = _ptr(t, None, f"grads[{i}]"), t.numel(), int(t.dtype == torch.float32)
-        if out is not None:
-            o = out[i]
-            if o is not t:
-                _shape(o, t.shape, f"out[{i}]")
-                _here(out=o)
-            r.out = _ptr(o, t.dtype, f"out[{i}]")
-    if out is not None:
-        used = [r.out for r in refs if r.numel]
-        if len(set(used)) != len(used):
-            raise ValueError("a tensor is listed twice as an output")
-    return refs, n
+        o = None if out is None else out[i]
+        d, dtype, n = t.get_device(), t.dtype, t.numel()
+        if dev is None and d >= 0:
+            dev = torch._C._cuda_getDevice()
+        if d != dev or (dtype is not torch.float32 and dtype is not torch.bfloat16) or not t.is_contiguous():
+            _real(t, f"grads[{i}]")
+            _refuse((f"grads[{i}]",), (t,), (dtype,), (None,))
+        p = t.data_ptr()
+        if o is None or o is t:
+            q = p
+        else:
+            if o.get_device() != dev or o.dtype is not dtype or o.shape != t.shape or not o.is_contiguous():
+                _refuse((f"out[{i}]",), (o,), (dtype,), (t.shape,))
+            q = o.data_ptr()
+        if out is not None and n:
+            if q in used:
+                raise ValueError("a tensor is listed twice as an output")
+            used.add(q)
+        table.append(_PACK_TENSOR(p, q, n, dtype is torch.float32, 0))
+    return b"".join(table), len(grads)
 
 
 def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
@@ -706,9 +726,7 @@ def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
     refs, n = _tensor_refs(grads, None)
     dev = grads[0].device
     norm = _empty(1, torch.float32, dev, stream) if norm is None else norm
-    _shape(norm, (1,), "norm")
-    _here(norm=norm, workspace=workspace)
-    to = _ptr(norm, torch.float32, "norm")
+    to, = _pointers(("norm",), (norm,), (torch.float32,), ((1,),))
     _call_with_scratch("mxg_grad_norm", lambda ws, b, st: lib().mxg_grad_norm(refs, n, to, ws, b, st),
                        lambda: mxg_grad_norm_workspace_bytes(n), workspace, dev, stream)
     return norm
@@ -724,11 +742,8 @@ def mxg_grad_clip(grads, max_norm: float, out=None, norm=None, norm_out=None, wo
     dev = grads[0].device
     if norm is None and norm_out is None:
         norm_out = _empty(1, torch.float32, dev, stream)
-    _shape(norm, (1,), "norm")
-    _shape(norm_out, (1,), "norm_out")
-    _here(norm=norm, norm_out=norm_out, workspace=workspace)
-    by, to = _ptr(norm, torch.float32, "norm"), _ptr(norm_out, torch.float32, "norm_out")
-    if by is not None:
+    by, to = _pointers(("norm", "norm_out"), (norm, norm_out), (torch.float32, torch.float32), ((1,), (1,)))
+    if norm is not None:
         _check("mxg_grad_clip", lib().mxg_grad_clip(refs, n, max_norm, by, None, None, 0, _stream(stream)))
         return norm, out
     _call_with_scratch("mxg_grad_clip", lambda ws, b, st: lib().mxg_grad_clip(refs, n, max_norm, None, to, ws, b, st),

@@ -2,17 +2,20 @@
 //
 //   norm = sqrt(sum of g^2 over all tensors),  out = g min(1, max_norm / norm)
 //
-// The tensors are cut into chunks of kChunk elements, numbered through; the
-// tensor table is a kernel argument (a graph keeps its own copy, and nothing is
-// copied to the device).  A CTA takes chunks blockIdx, blockIdx + grid, ... and
-// writes the sum of their squares as one fp64 number; the numbers are added up
-// in order.  Both passes are bound by HBM.
+// The tensors are cut into chunks of VEC 16-byte pieces a thread, numbered
+// through; the tensor table is a kernel argument (a graph keeps its own copy, and
+// nothing is copied to the device).  A CTA takes chunks blockIdx, blockIdx + grid,
+// ... and writes the sum of their squares as one fp64 number; the numbers are
+// added up in order, by every CTA of the second pass for itself.  Both passes are
+// bound by HBM: a set that is larger than L2 is read twice.  The second pass goes
+// backwards, so that what the first read last comes from L2, and its own traffic
+// is marked to leave L2 first.
 //
-// A chunk's squares are added in fp32.  Where that sum is not finite or so small
-// that squares may have vanished, the chunk is added again in fp64: gradients of
-// 1e30 and of 1e-30 have norms.
+// A thread's squares of a chunk are added in fp32.  Where that sum is not finite
+// or so small that squares may have vanished, they are added again in fp64:
+// gradients of 1e30 and of 1e-30 have norms.
 #include <cmath>
-#include <cstring>
+#include <type_traits>
 
 #include "api_common.h"
 #include "common.cuh"
@@ -23,10 +26,9 @@ namespace mxg {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kPer = 32;                          // elements of a chunk per thread
-constexpr int kChunk = kThreads * kPer;
 constexpr int kMaxBlocks = 152 * 4;
 constexpr int kTable = 512;                       // tensors per launch
+constexpr int kLong = 8, kShort = 2;              // 16-byte pieces of a chunk per thread
 
 struct Tensor {
   const void* in;
@@ -41,6 +43,9 @@ struct Table {
   uint32_t n, chunks;
 };
 
+// Elements of a chunk.
+constexpr int64_t chunk_elements(int vec, bool f32) { return static_cast<int64_t>(kThreads) * vec * (f32 ? 4 : 8); }
+
 template <int N>
 __device__ __forceinline__ int tensor_of(const Table<N>& tab, uint32_t chunk) {
   int lo = 0, hi = static_cast<int>(tab.n) - 1;
@@ -52,37 +57,38 @@ __device__ __forceinline__ int tensor_of(const Table<N>& tab, uint32_t chunk) {
   return lo;
 }
 
-__device__ __forceinline__ float get(const void* p, bool f32, int64_t i) {
-  return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
+template <bool F32>
+__device__ __forceinline__ float get(const void* p, int64_t i) {
+  return F32 ? static_cast<const float*>(p)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
 }
 
-// The thread's elements of a chunk: kPer / 8 runs of eight; the last elements of
-// a tensor, and all of one whose memory does not start on 16 bytes, singly.
-template <typename F8, typename F1>
-__device__ __forceinline__ void for_chunk(bool wide, int64_t base, int64_t left, F8 f8, F1 f1) {
-  if (wide && left >= kChunk) {
+// A 16-byte piece as its 4 or 8 numbers.
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < kPer / 8; ++i) f8(base + 8 * (threadIdx.x + i * kThreads));
-  } else {
-    const int n = static_cast<int>(left < kChunk ? left : kChunk), runs = wide ? n / 8 : 0;
-    for (int i = threadIdx.x; i < runs; i += kThreads) f8(base + 8 * i);
-    for (int i = 8 * runs + threadIdx.x; i < n; i += kThreads) f1(base + i);
-  }
-}
-
-__device__ __forceinline__ void load8(const void* p, bool f32, int64_t i, float (&v)[8]) {
-  if (f32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (F32) {
+      v[j] = __uint_as_float(w[j]);
+    } else {
       v[2 * j] = __uint_as_float(w[j] << 16);
       v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
+  }
+}
+
+// A chunk's elements: all VEC pieces of each thread at once (whole), or, at the
+// end of a tensor and where memory does not start on 16 bytes, pieces and single
+// elements in turn.
+template <int VEC, bool F32, typename W, typename P, typename S>
+__device__ __forceinline__ void for_chunk(bool wide, int64_t base, int64_t left, W whole, P piece, S single) {
+  constexpr int kE = F32 ? 4 : 8;
+  if (wide && left >= chunk_elements(VEC, F32)) {
+    whole();
+  } else {
+    const int n = static_cast<int>(min(left, chunk_elements(VEC, F32))), pieces = wide ? n / kE : 0;
+    for (int i = threadIdx.x; i < pieces; i += kThreads) piece(base + static_cast<int64_t>(i) * kE);
+    for (int i = pieces * kE + threadIdx.x; i < n; i += kThreads) single(base + i);
   }
 }
 
@@ -98,53 +104,66 @@ __device__ __forceinline__ double block_sum(double v, double* s_sum) {
   return v;
 }
 
-template <int N>
+// The thread's squares of one chunk.
+template <int VEC, bool F32>
+__device__ __forceinline__ double chunk_squares(const void* in, int64_t base, int64_t left) {
+  constexpr int kE = F32 ? 4 : 8;
+  const bool wide = (reinterpret_cast<uintptr_t>(in) & 15u) == 0;
+  const auto at = [&](int64_t i) { return static_cast<const uint8_t*>(in) + i * (F32 ? 4 : 2); };
+  float sum = 0.f;
+  uint32_t any = 0;
+  const auto add = [&](const uint4& q) {
+    float v[8], s = 0.f;
+    unpack<F32>(q, v);
+#pragma unroll
+    for (int j = 0; j < kE; ++j) s = fmaf(v[j], v[j], s);
+    sum += s;
+    any |= F32 ? (q.x | q.y | q.z | q.w) & 0x7fffffffu : (q.x | q.y | q.z | q.w) & 0x7fff7fffu;
+  };
+  for_chunk<VEC, F32>(
+      wide, base, left,
+      [&] {
+        uint4 q[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          q[i] = *reinterpret_cast<const uint4*>(at(base + static_cast<int64_t>(threadIdx.x + i * kThreads) * kE));
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) add(q[i]);
+      },
+      [&](int64_t i) { add(*reinterpret_cast<const uint4*>(at(i))); },
+      [&](int64_t i) {
+        const float v = get<F32>(in, i);
+        sum = fmaf(v, v, sum);
+        any |= __float_as_uint(v) & 0x7fffffffu;
+      });
+  // squares below 2^-126 lose digits, at most 64 x 2^-149 of a sum that is over 2^-100
+  if (any == 0 || (sum > 0x1p-100f && sum < INFINITY)) return static_cast<double>(sum);
+  double exact = 0.0;
+  const auto one = [&](int64_t i) {
+    const double v = get<F32>(in, i);
+    exact = fma(v, v, exact);
+  };
+  const auto eight = [&](int64_t i) {
+    for (int j = 0; j < kE; ++j) one(i + j);
+  };
+  for_chunk<VEC, F32>(
+      wide, base, left,
+      [&] {
+        for (int i = 0; i < VEC; ++i) eight(base + static_cast<int64_t>(threadIdx.x + i * kThreads) * kE);
+      },
+      eight, one);
+  return exact;
+}
+
+template <int N, int VEC>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ Table<N> tab, double* part) {
   __shared__ double s_sum[kThreads / 32];
   launch_dependents();
   double total = 0.0;
   for (uint32_t c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     const Tensor& t = tab.t[tensor_of(tab, c)];
-    const bool f32 = t.f32 != 0;
-    const bool wide = (reinterpret_cast<uintptr_t>(t.in) & 15u) == 0;
-    const int64_t base = static_cast<int64_t>(c - t.first) * kChunk, left = t.numel - base;
-    float sum = 0.f;
-    uint32_t any = 0;
-    for_chunk(
-        wide, base, left,
-        [&](int64_t i) {
-          float v[8];
-          load8(t.in, f32, i, v);
-          float q = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            q = fmaf(v[j], v[j], q);
-            any |= __float_as_uint(v[j]) << 1;
-          }
-          sum += q;
-        },
-        [&](int64_t i) {
-          const float v = get(t.in, f32, i);
-          sum = fmaf(v, v, sum);
-          any |= __float_as_uint(v) << 1;
-        });
-    // squares below 2^-126 lose digits, at most 32 x 2^-149 of a sum that is over 2^-100
-    if (any != 0 && !(sum > 0x1p-100f && sum < INFINITY)) {
-      double exact = 0.0;
-      const auto add = [&](int64_t i) {
-        const double v = get(t.in, f32, i);
-        exact = fma(v, v, exact);
-      };
-      for_chunk(
-          wide, base, left,
-          [&](int64_t i) {
-            for (int j = 0; j < 8; ++j) add(i + j);
-          },
-          add);
-      total += exact;
-    } else {
-      total += static_cast<double>(sum);
-    }
+    const int64_t base = static_cast<int64_t>(c - t.first) * chunk_elements(VEC, t.f32 != 0), left = t.numel - base;
+    total += t.f32 != 0 ? chunk_squares<VEC, true>(t.in, base, left) : chunk_squares<VEC, false>(t.in, base, left);
   }
   total = block_sum(total, s_sum);
   if (threadIdx.x == 0) part[blockIdx.x] = total;
@@ -164,9 +183,43 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int 
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
+template <int VEC, bool F32>
+__device__ __forceinline__ void chunk_scale(const void* in, void* out, float coef, int64_t base, int64_t left) {
+  constexpr int kE = F32 ? 4 : 8;
+  const bool wide = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+  const auto from = [&](int64_t i) {
+    return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(in) + i * (F32 ? 4 : 2));
+  };
+  const auto store = [&](int64_t i, const uint4& q) {
+    float v[8];
+    unpack<F32>(q, v);
+#pragma unroll
+    for (int j = 0; j < kE; ++j) v[j] *= coef;
+    uint4 r;
+    if constexpr (F32) r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else r = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + i * (F32 ? 4 : 2)), r);
+  };
+  for_chunk<VEC, F32>(
+      wide, base, left,
+      [&] {
+        uint4 q[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) q[i] = __ldcs(from(base + static_cast<int64_t>(threadIdx.x + i * kThreads) * kE));
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) store(base + static_cast<int64_t>(threadIdx.x + i * kThreads) * kE, q[i]);
+      },
+      [&](int64_t i) { store(i, __ldcs(from(i))); },
+      [&](int64_t i) {
+        const float v = get<F32>(in, i) * coef;
+        if constexpr (F32) static_cast<float*>(out)[i] = v;
+        else static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+      });
+}
+
 // out = g coef.  The norm comes from the partial sums (part), or from the caller
 // (norm_in).
-template <int N>
+template <int N, int VEC>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<N> tab, const double* part, int nparts,
                                                          const float* norm_in, float max_norm, float* norm_out) {
   __shared__ double s_sum[kThreads / 32];
@@ -181,35 +234,18 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   // NaN makes everything NaN, infinity everything zero (and NaN what is infinite)
   const float coef = norm <= max_norm ? 1.f : static_cast<float>(max_norm / norm);
   for (uint32_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
-    const uint32_t c = tab.chunks - 1 - k;        // what was read last is still in L2
+    const uint32_t c = tab.chunks - 1 - k;
     const Tensor& t = tab.t[tensor_of(tab, c)];
-    const bool f32 = t.f32 != 0;
     if (coef == 1.f && t.in == t.out) continue;
-    const bool wide = ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
-    const int64_t base = static_cast<int64_t>(c - t.first) * kChunk, left = t.numel - base;
-    for_chunk(
-        wide, base, left,
-        [&](int64_t i) {
-          float v[8];
-          load8(t.in, f32, i, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= coef;
-          if (f32) {
-            float4* q = reinterpret_cast<float4*>(static_cast<float*>(t.out) + i);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.out) + i) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                           pack_bf16x2(v[6], v[7]));
-          }
-        },
-        [&](int64_t i) {
-          const float v = get(t.in, f32, i) * coef;
-          if (f32) static_cast<float*>(t.out)[i] = v;
-          else static_cast<uint16_t*>(t.out)[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-        });
+    const int64_t base = static_cast<int64_t>(c - t.first) * chunk_elements(VEC, t.f32 != 0), left = t.numel - base;
+    if (t.f32 != 0) chunk_scale<VEC, true>(t.in, t.out, coef, base, left);
+    else chunk_scale<VEC, false>(t.in, t.out, coef, base, left);
   }
+}
+
+int64_t chunks_of(const mxg_tensor& t, int vec) {
+  const int64_t e = chunk_elements(vec, t.f32 != 0);
+  return (t.numel + e - 1) / e;
 }
 
 int check_tensors(const mxg_tensor* t, int n, bool out) {
@@ -223,7 +259,7 @@ int check_tensors(const mxg_tensor* t, int n, bool out) {
     if (reinterpret_cast<uintptr_t>(t[i].in) % size != 0) return MXG_ERR_ALIGN;
     if (out && reinterpret_cast<uintptr_t>(t[i].out) % size != 0) return MXG_ERR_ALIGN;
     if (t[i].numel > (1ll << 45)) return MXG_ERR_SHAPE;
-    chunks += (t[i].numel + kChunk - 1) / kChunk;
+    chunks += chunks_of(t[i], kShort);
     if (chunks > INT32_MAX) return MXG_ERR_SHAPE;
   }
   return MXG_OK;
@@ -231,11 +267,15 @@ int check_tensors(const mxg_tensor* t, int n, bool out) {
 
 int blocks_of(uint32_t chunks) { return chunks < kMaxBlocks ? static_cast<int>(chunks) : kMaxBlocks; }
 
-// Calls f(table of up to N tensors) for every launch the tensors need; a small
-// set travels in a small argument.  Tensors without elements take no entry.
+// Calls f(table of up to N tensors, pieces of a chunk) for every launch the
+// tensors need; a small set travels in a small argument, and in short chunks
+// where long ones would be fewer than SMs.  Tensors without elements take no entry.
 template <typename F>
 cudaError_t for_tables(const mxg_tensor* t, int n, F f) {
   int at = 0;
+  int64_t all = 0;
+  for (int i = 0; i < n; ++i) all += chunks_of(t[i], kLong);
+  const int vec = all < 152 ? kShort : kLong;
   while (true) {
     while (at < n && t[at].numel == 0) ++at;
     if (at >= n) return cudaSuccess;
@@ -245,18 +285,18 @@ cudaError_t for_tables(const mxg_tensor* t, int n, F f) {
       for (; at < n && tab.n < most; ++at) {
         if (t[at].numel == 0) continue;
         tab.t[tab.n++] = Tensor{t[at].in, t[at].out, t[at].numel, tab.chunks, static_cast<uint32_t>(t[at].f32)};
-        tab.chunks += static_cast<uint32_t>((t[at].numel + kChunk - 1) / kChunk);
+        tab.chunks += static_cast<uint32_t>(chunks_of(t[at], vec));
       }
     };
     cudaError_t err;
     if (n - at <= 16) {
       Table<16> tab;
       fill(tab);
-      err = f(tab);
+      err = vec == kLong ? f(tab, std::integral_constant<int, kLong>{}) : f(tab, std::integral_constant<int, kShort>{});
     } else {
       static thread_local Table<kTable> tab;
       fill(tab);
-      err = f(tab);
+      err = vec == kLong ? f(tab, std::integral_constant<int, kLong>{}) : f(tab, std::integral_constant<int, kShort>{});
     }
     if (err != cudaSuccess) return err;
   }
@@ -267,10 +307,10 @@ int table_count(int n) { return (n + kTable - 1) / kTable; }
 // The partial sums of all tensors; their number to *nparts.
 cudaError_t launch_square_sums(const mxg_tensor* t, int n, double* part, int* nparts, cudaStream_t s) {
   *nparts = 0;
-  return for_tables(t, n, [&](const auto& tab) {
+  return for_tables(t, n, [&](const auto& tab, auto vec) {
     constexpr int N = sizeof(tab.t) / sizeof(tab.t[0]);
     const int blocks = blocks_of(tab.chunks);
-    square_sum_kernel<N><<<blocks, kThreads, 0, s>>>(tab, part + *nparts);
+    square_sum_kernel<N, vec.value><<<blocks, kThreads, 0, s>>>(tab, part + *nparts);
     count_launch();
     *nparts += blocks;
     return cudaGetLastError();
@@ -313,11 +353,11 @@ extern "C" int mxg_grad_clip(const mxg_tensor* tensors, int n, float max_norm, c
   double* part = static_cast<double*>(workspace);
   if (!norm_in) MXG_TRY(launch_square_sums(tensors, n, part, &nparts, s));
   bool told = norm_out == nullptr;
-  MXG_TRY(for_tables(tensors, n, [&](const auto& tab) {
+  MXG_TRY(for_tables(tensors, n, [&](const auto& tab, auto vec) {
     constexpr int N = sizeof(tab.t) / sizeof(tab.t[0]);
     float* to = told ? nullptr : norm_out;
     told = true;
-    return launch_after(scale_kernel<N>, dim3(blocks_of(tab.chunks)), dim3(kThreads), 0, s, tab,
+    return launch_after(scale_kernel<N, vec.value>, dim3(blocks_of(tab.chunks)), dim3(kThreads), 0, s, tab,
                         static_cast<const double*>(norm_in ? nullptr : part), nparts, norm_in, max_norm, to);
   }));
   if (!told)                                      // no tensor has elements: the norm is zero

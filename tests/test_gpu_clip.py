@@ -10,9 +10,10 @@ pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 B = 2.0 ** -8
-# the squares of 32 elements in fp32: a chain of 8, of 4 runs, each square's rounding (in the fma), all under a root;
-# the rest is fp64 and rounded once
-NORM = (8 + 4) / 2 * U + 2 * U
+# a thread's squares of a chunk in fp32: a chain of 8 in a 16-byte piece, of 8 pieces, and a last single one, each square
+# rounded in its fma, all under a root; the rest is fp64 and rounded once
+NORM = (8 + 8 + 1) / 2 * U + 2 * U
+SINGLY = 64 / 2 * U + 2 * U   # memory that starts on no 16 bytes: a chain of 64
 SETS = {
     "one": [(1,)],
     "short": [(3,), (1, 1), (7, 5)],
@@ -31,11 +32,11 @@ def _grads(shapes, seed=0, std=0.01):
             for i, s in enumerate(shapes)]
 
 
-def _check(got, grads, norm, most):
+def _check(got, grads, norm, most, tol=NORM):
     coef = min(1.0, most / norm) if norm else 1.0
     for a, g in zip(got, grads):
         ref = g.double().numpy() * coef
-        rel = 0.0 if coef == 1.0 else NORM + 3 * U + (U if g.dtype == torch.float32 else B)
+        rel = 0.0 if coef == 1.0 else tol + 3 * U + (U if g.dtype == torch.float32 else B)
         assert a.dtype == g.dtype and (np.abs(np_(a.double()) - ref) <= rel * np.abs(ref) + 1e-44).all()
 
 
@@ -73,8 +74,8 @@ def test_any_element_address(dtype, offset):
     grads = [flat[a:a + n] for a, n in views]
     norm, got = m.mxg_grad_clip([dev[a:a + n] for a, n in views], 3.0, out=[out[a:a + n] for a, n in views])
     ref = block.grad_norm([v.double().numpy() for v in grads])
-    assert abs(float(norm) - ref) <= NORM * ref
-    _check(got, grads, ref, 3.0)
+    assert abs(float(norm) - ref) <= SINGLY * ref
+    _check(got, grads, ref, 3.0, SINGLY)
     rest = torch.ones(50000, dtype=torch.bool, device="cuda")
     for a, n in views:
         rest[a:a + n] = False
