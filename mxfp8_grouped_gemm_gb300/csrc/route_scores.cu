@@ -769,108 +769,136 @@ struct RouteBwdParams {
   int32_t* status;
 };
 
-// dlogits of a token by LPT lanes.  The lanes build the row in shared memory, the
-// chosen experts' lanes add theirs there, and it leaves in 16-byte pieces.
-template <int LPT, bool VEC>
-__global__ void __launch_bounds__(kThreads) route_scores_bwd_kernel(const RouteBwdParams P) {
+// A warp takes NB tokens.  KP lanes to a token, one to a choice, make the chosen
+// experts' gradients; LPT lanes to a token lay down what every expert gets, in
+// rows of shared memory, where the choices are added; and the rows leave in
+// 16-byte pieces.  (With LPT lanes to a token for the choices as well, 65536 x 256
+// took 31 us.)
+template <int LPT>
+__global__ void __launch_bounds__(kThreads, 4) route_scores_bwd_kernel(const __grid_constant__ RouteBwdParams P) {
   constexpr int TPW = 32 / LPT;
-  constexpr int SEL = 32 / LPT < kVals ? 32 / LPT : kVals;
-  __shared__ __align__(16) float s_row[kWarps][32 * kVals];
+  constexpr int NB = TPW > 4 ? TPW : 4;
+  constexpr int MOST = LPT * kVals < 32 ? LPT * kVals : 32;
+  __shared__ __align__(16) float s_row[kWarps][NB][LPT * kVals];
+  __shared__ __align__(8) float2 s_pick[kWarps][NB][MOST];      // expert (-1: none) and gradient of a choice
+  __shared__ float s_inner[kWarps][NB];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane % LPT, grp = lane / LPT;
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * TPW + grp;
-  if (t - grp >= P.T) return;
-  const bool in = t < P.T;
-  const int64_t row = (in ? t : 0) * P.E, pick = (in ? t : 0) * P.k;
-  float* mine = s_row[warp] + grp * LPT * kVals;
-  const auto expert = [&](int i) { return VEC ? 4 * (gl + LPT * (i >> 2)) + (i & 3) : gl + LPT * i; };
-  const auto load = [&](const float* p, float fill, float (&v)[kVals]) {
-    if constexpr (VEC) {
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * NB;
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(NB), P.T - t0));
+  if (ntok <= 0) return;
+  const bool dense = P.score == SOFTMAX && !P.renorm, vec = P.E % 4 == 0;
+  int kp_log = 0;
+  while ((1 << kp_log) < P.k) ++kp_log;
+  const int kp = 1 << kp_log;
+
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += 32 >> kp_log) {
+    const int j = lane & (kp - 1), n = n0 + (lane >> kp_log);
+    const bool here = n < ntok && j < P.k;
+    const int64_t at = (t0 + n) * P.k + j;
+    int e = here ? P.ids[at] : -1;
+    const float p = here ? P.probs[at] : 0.f, dp = here ? P.dprobs[at] : 0.f;
+    const bool valid = static_cast<unsigned>(e) < static_cast<unsigned>(P.E);
+    float z = 0.f;
+    if (P.score == SIGMOID && valid) z = P.logits[(t0 + n) * P.E + e];
+    if (here && !valid) report(P.status, MXG_ERR_EXPERT_ID);
+    // sum of p_i (dp_i - dp_0), or of p_i dp_i where the weights are not renormalised
+    const float first = P.renorm ? __shfl_sync(kAll, dp, lane & ~(kp - 1)) : 0.f;
+    float inner = here ? p * (dp - first) : 0.f;
+    for (int off = kp >> 1; off > 0; off >>= 1) inner += __shfl_xor_sync(kAll, inner, off);
+    float g = p * ((dp - first) - (P.renorm ? inner * P.inv_scale : 0.f));
+    if (P.score == SIGMOID) g *= sigmoid_of(-z);
+    // an id that stands twice: the first adds up all of them, in their order
+    const unsigned same = __match_any_sync(kAll, here && valid ? (lane >> kp_log) * 256 + e : -1 - lane);
+    if (__any_sync(kAll, (same & (same - 1)) != 0)) {
+      float sum = 0.f;
+      for (int l = 0; l < 32; ++l) {
+        const float o = __shfl_sync(kAll, g, l);
+        if (same >> l & 1u) sum += o;
+      }
+      g = sum;
+      if ((same & ((1u << lane) - 1u)) != 0) e = -1;
+    }
+    if (here) s_pick[warp][n][j] = make_float2(__int_as_float(valid ? e : -1), g);
+    if (here && j == 0) s_inner[warp][n] = inner;
+  }
+  __syncwarp();
+
+  const auto expert = [&](int i) { return vec ? 4 * (gl + LPT * (i >> 2)) + (i & 3) : gl + LPT * i; };
+  const auto load = [&](const float* row, float fill, float (&v)[kVals]) {
+    if (vec) {
 #pragma unroll
       for (int i = 0; i < kVals; i += 4) {
         float4 q = make_float4(fill, fill, fill, fill);
-        if (expert(i) < P.E) q = *reinterpret_cast<const float4*>(p + row + expert(i));
+        if (expert(i) < P.E) q = *reinterpret_cast<const float4*>(row + expert(i));
         v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) v[i] = expert(i) < P.E ? p[row + expert(i)] : fill;
+      for (int i = 0; i < kVals; ++i) v[i] = expert(i) < P.E ? row[expert(i)] : fill;
     }
   };
-  int id[SEL];
-  float p[SEL], dp[SEL];
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += TPW) {
+    const int n = n0 + grp;
+    const int64_t row = (t0 + (n < ntok ? n : 0)) * P.E;
+    float d[kVals];
 #pragma unroll
-  for (int r = 0; r < SEL; ++r) {
-    const int j = gl + r * LPT;
-    id[r] = j < P.k ? P.ids[pick + j] : -1;
-    p[r] = j < P.k ? P.probs[pick + j] : 0.f;
-    dp[r] = j < P.k ? P.dprobs[pick + j] : 0.f;
-  }
-  float d[kVals];
+    for (int i = 0; i < kVals; ++i) d[i] = 0.f;
+    if (P.dlogits_in != nullptr) load(P.dlogits_in + row, 0.f, d);
+    if (dense) {
+      float z[kVals], top = -INFINITY, sum = 0.f;
+      load(P.logits + row, -INFINITY, z);
 #pragma unroll
-  for (int i = 0; i < kVals; ++i) d[i] = 0.f;
-  if (P.dlogits_in != nullptr) load(P.dlogits_in, 0.f, d);
-  // sum of p_i (dp_i - dp_0), or of p_i dp_i where the weights are not renormalised
-  const float first = P.renorm ? __shfl_sync(kAll, dp[0], grp * LPT) : 0.f;
-  float inner = 0.f;
+      for (int i = 0; i < kVals; ++i) top = fmaxf(top, z[i]);
+      top = lanes_max<LPT>(top);
+      if (top == -INFINITY) top = 0.f;
 #pragma unroll
-  for (int r = 0; r < SEL; ++r)
-    if (gl + r * LPT < P.k) inner = fmaf(p[r], dp[r] - first, inner);
-  inner = lanes_sum<LPT>(inner);
-  if (P.score == SOFTMAX && !P.renorm) {
-    float z[kVals], top = -INFINITY, sum = 0.f;
-    load(P.logits, -INFINITY, z);
+      for (int i = 0; i < kVals; ++i) {
+        z[i] = expf(z[i] - top);
+        sum += z[i];
+      }
+      sum = lanes_sum<LPT>(sum);
+      const float f = sum == 0.f ? 0.f : s_inner[warp][n < ntok ? n : 0] / sum;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) top = fmaxf(top, z[i]);
-    top = lanes_max<LPT>(top);
-    if (top == -INFINITY) top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      z[i] = expf(z[i] - top);
-      sum += z[i];
+      for (int i = 0; i < kVals; ++i) d[i] = fmaf(-z[i], f, d[i]);
     }
-    sum = lanes_sum<LPT>(sum);
-    const float f = sum == 0.f ? 0.f : inner / sum;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) d[i] = fmaf(-z[i], f, d[i]);
-  }
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < kVals; i += 4)
-      *reinterpret_cast<float4*>(mine + expert(i)) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) mine[expert(i)] = d[i];
-  }
-  __syncwarp();
-  const float mean = P.renorm ? inner * P.inv_scale : 0.f;
-#pragma unroll
-  for (int r = 0; r < SEL; ++r) {
-    const int e = id[r];
-    const bool chosen = gl + r * LPT < P.k, valid = static_cast<unsigned>(e) < static_cast<unsigned>(P.E);
-    if (in && chosen && !valid) report(P.status, MXG_ERR_EXPERT_ID);
-    float g = p[r] * ((dp[r] - first) - mean);
-    if (P.score == SIGMOID && chosen && valid) g *= sigmoid_of(-P.logits[row + e]);
-    // an id that stands twice adds in its order
-    const int tag = chosen && valid ? grp * 256 + e : -1 - lane;
-    const unsigned same = __match_any_sync(kAll, tag);
-    unsigned turn = __popc(same & ((1u << lane) - 1u));
-    const unsigned turns = __reduce_max_sync(kAll, turn);
-    for (unsigned n = 0; n <= turns; ++n) {
-      if (tag >= 0 && turn == n) mine[e] += g;
-      __syncwarp();
-    }
-  }
-  if (in) {
-    if constexpr (VEC) {
+    float* mine = s_row[warp][n];
+    if (vec) {
 #pragma unroll
       for (int i = 0; i < kVals; i += 4)
-        if (expert(i) < P.E)
-          *reinterpret_cast<float4*>(P.dlogits + row + expert(i)) = *reinterpret_cast<const float4*>(mine + expert(i));
+        *reinterpret_cast<float4*>(mine + expert(i)) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) mine[expert(i)] = d[i];
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += 32 >> kp_log) {
+    const int j = lane & (kp - 1), n = n0 + (lane >> kp_log);
+    if (n < ntok && j < P.k) {
+      const float2 pick = s_pick[warp][n][j];
+      const int e = __float_as_int(pick.x);
+      if (e >= 0) s_row[warp][n][e] += pick.y;
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int n0 = 0; n0 < ntok; n0 += TPW) {
+    const int n = n0 + grp;
+    if (n >= ntok) break;
+    float* out = P.dlogits + (t0 + n) * P.E;
+    const float* mine = s_row[warp][n];
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < kVals; i += 4)
+        if (expert(i) < P.E) *reinterpret_cast<float4*>(out + expert(i)) = *reinterpret_cast<const float4*>(mine + expert(i));
     } else {
 #pragma unroll
       for (int i = 0; i < kVals; ++i)
-        if (expert(i) < P.E) P.dlogits[row + expert(i)] = mine[expert(i)];
+        if (expert(i) < P.E) out[expert(i)] = mine[expert(i)];
     }
   }
 }
@@ -967,8 +995,8 @@ extern "C" int mxg_route_scores_bwd(const float* logits, const int32_t* ids, con
                          E,      k,     score, renormalize != 0, 1.f / scale, dev_status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   with_lanes(E, [&](auto l) {
-    if (E % 4 == 0) route_scores_bwd_kernel<l.value, true><<<token_blocks(T, E), kThreads, 0, st>>>(p);
-    else route_scores_bwd_kernel<l.value, false><<<token_blocks(T, E), kThreads, 0, st>>>(p);
+    constexpr int at_once = 32 / l.value, set = kWarps * (at_once > 4 ? at_once : 4);
+    route_scores_bwd_kernel<l.value><<<static_cast<unsigned>((static_cast<int64_t>(T) + set - 1) / set), kThreads, 0, st>>>(p);
   });
   count_launch();
   return api::cuda_status(cudaGetLastError());
