@@ -302,8 +302,8 @@ int mxg_route_scores_fwd(const float* logits, const float* bias, int T, int E, i
  *   times 1 - sigmoid(z_j)  (MXG_SCORE_SIGMOID),
  * and, for a softmax that is not renormalised, minus softmax(z)[e] S everywhere.
  *   logits, ids, probs   the forward's;  dprobs fp32 [T][k]
- *   dlogits_in  nullable fp32 [T][E] (e.g. mxg_balance_loss_bwd's); may be dlogits
- *   dlogits     fp32 [T][E] out
+ *   dlogits_in  nullable fp32 [T][E] (e.g. mxg_balance_loss_bwd's)
+ *   dlogits     fp32 [T][E] out; may be dlogits_in or logits
  * Ids outside [0, E) add nothing at an expert and are reported as
  * MXG_ERR_EXPERT_ID; an id that stands twice adds twice.  Requirements as
  * mxg_route_scores_fwd. */

@@ -92,15 +92,17 @@ __device__ __forceinline__ void for_chunk(bool wide, int64_t base, int64_t left,
   }
 }
 
-// Block-wide sum in fp64, on every thread.
+// Block-wide sum in fp64, on the threads of warp 0.
 __device__ __forceinline__ double block_sum(double v, double* s_sum) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += s_sum[i];
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kThreads / 32 ? s_sum[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int off = kThreads / 64; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  }
   return v;
 }
 
@@ -169,18 +171,34 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
   if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
-// The norm from the partial sums, in a fixed order (the whole block gets it).
-__device__ __forceinline__ double norm_of(const double* part, int n, double* s_sum) {
+// The sum of squares from the partial sums, in a fixed order, on the threads of
+// warp 0.
+__device__ __forceinline__ double squares_of(const double* part, int n, double* s_sum) {
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += blockDim.x) v += part[i];
-  return sqrt(block_sum(v, s_sum));
+  return block_sum(v, s_sum);
+}
+
+// The norm, and max_norm / norm where that is below 1.  fp64 only where fp32 has
+// not the range: the sum's rounding to fp32 is halved by the root.
+__device__ __forceinline__ float norm_of(double squares) {
+  return squares > 0x1p-100 && squares < 0x1p100 ? sqrtf(static_cast<float>(squares))
+                                                 : static_cast<float>(sqrt(squares));
+}
+__device__ __forceinline__ float factor_of(double squares, float max_norm) {
+  if (squares > 0x1p-100 && squares < 0x1p100) {
+    const float norm = sqrtf(static_cast<float>(squares));
+    return norm <= max_norm ? 1.f : max_norm / norm;
+  }
+  const double norm = sqrt(squares);
+  return norm <= max_norm ? 1.f : static_cast<float>(max_norm / norm);
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int n, float* norm) {
   __shared__ double s_sum[kThreads / 32];
   dependency_wait();
-  const double v = norm_of(part, n, s_sum);
-  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+  const double v = squares_of(part, n, s_sum);
+  if (threadIdx.x == 0) *norm = norm_of(v);
 }
 
 template <int VEC, bool F32>
@@ -223,16 +241,22 @@ template <int N, int VEC>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<N> tab, const double* part, int nparts,
                                                          const float* norm_in, float max_norm, float* norm_out) {
   __shared__ double s_sum[kThreads / 32];
+  __shared__ float s_coef;
   dependency_wait();
-  double norm;
-  if (part != nullptr) {
-    norm = norm_of(part, nparts, s_sum);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = static_cast<float>(norm);
-  } else {
-    norm = *norm_in;
-  }
   // NaN makes everything NaN, infinity everything zero (and NaN what is infinite)
-  const float coef = norm <= max_norm ? 1.f : static_cast<float>(max_norm / norm);
+  float coef;
+  if (part != nullptr) {
+    const double squares = squares_of(part, nparts, s_sum);
+    if (threadIdx.x == 0) {
+      s_coef = factor_of(squares, max_norm);
+      if (blockIdx.x == 0 && norm_out != nullptr) *norm_out = norm_of(squares);
+    }
+    __syncthreads();
+    coef = s_coef;
+  } else {
+    const float norm = *norm_in;
+    coef = norm <= max_norm ? 1.f : max_norm / norm;
+  }
   for (uint32_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
     const uint32_t c = tab.chunks - 1 - k;
     const Tensor& t = tab.t[tensor_of(tab, c)];

@@ -64,6 +64,13 @@ class GroupedMLP:
         """Top-k routing into this object's ids/probs buffers."""
         return _lib.mxg_route_topk(logits, self.k, self.ids, self.probs, stream=stream)
 
+    def route_scores(self, logits, score="softmax", bias=None, groups=1, top_groups=1, group_top=2, renormalize=True,
+                     scale=1.0, stream=None):
+        """Routing by scores (mxg_route_scores_fwd) into this object's ids/probs buffers."""
+        return _lib.mxg_route_scores_fwd(logits, self.k, score=score, bias=bias, groups=groups, top_groups=top_groups,
+                                         group_top=group_top, renormalize=renormalize, scale=scale, ids=self.ids,
+                                         probs=self.probs, stream=stream)
+
     def quantize_weights(self, w_gate_up, w_down, stream=None):
         """Quantise the weights once into this layer's weight cache (MXFP8 path):
         forward calls given no weights then read it, e.g. for every micro-batch
