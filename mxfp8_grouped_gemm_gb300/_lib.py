@@ -688,37 +688,36 @@ def mxg_grad_norm_workspace_bytes(n) -> int:
     return int(lib().mxg_grad_norm_workspace_bytes(n))
 
 
-_PACK_TENSOR = struct.Struct("@PPqii").pack
-
-
 def _tensor_refs(grads, out):
-    """The library's table of the tensors, as bytes; out None: no outputs."""
-    if not grads:
+    """The library's table of the tensors, as bytes; out None: no outputs.  A model's worth of small gradients takes
+    longer here than on the GPU, so each tensor is asked for each thing once."""
+    n = len(grads)
+    if n == 0:
         raise ValueError("no gradients given")
-    if out is not None and len(out) != len(grads):
-        raise ValueError(f"{len(grads)} gradients but {len(out)} outputs")
-    table, used, dev = [], set(), None
+    if out is not None and len(out) != n:
+        raise ValueError(f"{n} gradients but {len(out)} outputs")
+    f32, bf16 = torch.float32, torch.bfloat16
+    fields, used = [], []
+    dev = torch._C._cuda_getDevice() if grads[0].is_cuda else None
     for i, t in enumerate(grads):
-        o = None if out is None else out[i]
-        d, dtype, n = t.get_device(), t.dtype, t.numel()
-        if dev is None and d >= 0:
-            dev = torch._C._cuda_getDevice()
-        if d != dev or (dtype is not torch.float32 and dtype is not torch.bfloat16) or not t.is_contiguous():
+        dtype = t.dtype
+        if t.get_device() != dev or (dtype is not f32 and dtype is not bf16) or not t.is_contiguous():
             _real(t, f"grads[{i}]")
             _refuse((f"grads[{i}]",), (t,), (dtype,), (None,))
-        p = t.data_ptr()
-        if o is None or o is t:
-            q = p
-        else:
-            if o.get_device() != dev or o.dtype is not dtype or o.shape != t.shape or not o.is_contiguous():
-                _refuse((f"out[{i}]",), (o,), (dtype,), (t.shape,))
-            q = o.data_ptr()
-        if out is not None and n:
-            if q in used:
-                raise ValueError("a tensor is listed twice as an output")
-            used.add(q)
-        table.append(_PACK_TENSOR(p, q, n, dtype is torch.float32, 0))
-    return b"".join(table), len(grads)
+        p = q = t.data_ptr()
+        size = t.numel()
+        if out is not None:
+            o = out[i]
+            if o is not t:
+                if o.get_device() != dev or o.dtype is not dtype or o.numel() != size or not o.is_contiguous():
+                    _refuse((f"out[{i}]",), (o,), (dtype,), (t.shape,))
+                q = o.data_ptr()
+            if size:
+                used.append(q)
+        fields += (p, q, size, dtype is f32, 0)
+    if len(set(used)) != len(used):
+        raise ValueError("a tensor is listed twice as an output")
+    return struct.pack("@" + "PPqii" * n, *fields), n
 
 
 def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
