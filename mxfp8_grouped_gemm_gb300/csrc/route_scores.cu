@@ -647,16 +647,17 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
         // two scores and the rounding of their sum
         const float most = BY == BY_SOFTMAX ? inv : 1.f, err = 2.f * (error_of<BY>(most, reach) + kU * (most + reach));
         if (!(worst - next > 2.f * err)) close = true;
-        if (GROUPS == LANE_GROUPS && !close && out != 0) {
+      }
+      // experts that take no part are found neither by their values nor by rank_close
+      if (SCORED && GROUPS == LANE_GROUPS && !close && out != 0) {
 #pragma unroll
-          for (int i = 0; i < kVals; i += 4)
-            *reinterpret_cast<float4*>(row_c + gl * kVals + i) = make_float4(NAN, NAN, NAN, NAN);
-        }
-        if (GROUPS == ANY_GROUPS && !close) {
+        for (int i = 0; i < kVals; i += 4)
+          *reinterpret_cast<float4*>(row_c + gl * kVals + i) = make_float4(NAN, NAN, NAN, NAN);
+      }
+      if (GROUPS == ANY_GROUPS && !close) {
 #pragma unroll
-          for (int i = 0; i < kVals; ++i)
-            if (out >> i & 1u) row_c[gl * kVals + i] = NAN;
-        }
+        for (int i = 0; i < kVals; ++i)
+          if (out >> i & 1u) row_c[gl * kVals + i] = NAN;
       }
     }
 
