@@ -278,7 +278,8 @@ int mxg_muon_update(const mxg_muon_args* args, void* stream);
  *           the logits.
  *   weights probs[t][j] = scale s_j, or, with renormalize, scale s_j / (sum of
  *           the k chosen s; 0 if that is 0).  The bias takes no part in them.
- * The ids are those of scores in 64 bits, whatever fp32 would round.  An expert
+ * The ids are those of scores in 64 bits, whatever fp32 would round (sums that
+ * tie but for the rounding of 64 bits themselves go either way).  An expert
  * with z = -inf (or NaN, or a bias of -inf) is off: it ranks behind all others,
  * by id, and adds nothing to its group's score (a group with none left ranks
  * last); where fewer than k are left, experts that are off fill the route, with

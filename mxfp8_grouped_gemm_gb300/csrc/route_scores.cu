@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
         const bool keep = score >= worst, first = (gl & (P.lanes_of_group - 1)) == 0 && gl * kVals < P.E;
         if (__popc(__ballot_sync(kAll, keep && first) & mask) != P.top_groups) close = true;     // equal scores
         out = keep ? 0u : 0xffu;
-        if (!keep) h[0] = -INFINITY;                            // its lane is never picked
+        if (!keep) h[0] = -INFINITY;                            // and no more comes behind it (end_of_list)
       } else {
         const Kept kept = kept_groups<LPT>(P, row_c, reinterpret_cast<float*>(win), 2 * (MOST + 2), lane);
         worst = kept.worst;
@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
     for (int i = 0; i < kVals; i += 4)
       *reinterpret_cast<float4*>(list + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
     float head = h[0];
-    uint32_t at = smem_u32(list);
-    const uint32_t end_of_list = at + 4 * kVals;
+    const uint32_t end_of_list = smem_u32(list) + 4 * kVals;
+    uint32_t at = GROUPS == LANE_GROUPS && h[0] == -INFINITY ? end_of_list : smem_u32(list);
     const uint32_t to = smem_u32(win);
 #pragma unroll 4
     for (int j = 0; j < P.k; ++j) take(head, at, end_of_list, to + 8 * j, lanes_max<LPT>(head), gl, ahead);

@@ -122,6 +122,20 @@ def test_route_fwd_equal_logits_in_and_out_of_the_groups(E, groups, top_groups, 
         _check(m, z.reshape(T, E), bias, k, dict(groups=groups, top_groups=top_groups, group_top=1))
 
 
+@pytest.mark.parametrize("E,groups,top_groups,k", [(16, 2, 1, 4), (32, 2, 1, 5), (64, 8, 3, 14), (256, 8, 2, 32)])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_route_fwd_groups_with_few_experts_left(E, groups, top_groups, k, group_top):
+    """Most experts off: what fills the route comes from the groups that take part, never from the others."""
+    m = require_gpu()
+    rng = np.random.default_rng(E + group_top)
+    z = rng.standard_normal((500, E)).astype(np.float32)
+    z[rng.random(z.shape) < 0.8] = -np.inf
+    bias = (rng.standard_normal(E) * 0.3).astype(np.float32)
+    for kind in ("softmax", "sigmoid"):
+        for b in (None, bias):
+            _check(m, z, b, k, dict(score=kind, groups=groups, top_groups=top_groups, group_top=group_top))
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("size", [30.0, 60.0, 1e4])
 def test_route_fwd_far_logits(kind, size):
