@@ -292,9 +292,18 @@ int mxg_muon_update(const mxg_muon_args* args, void* stream);
  * Requires 1 <= k <= E <= 256, k <= 32, E % groups == 0, k <= top_groups * E /
  * groups, group_top <= E / groups (where groups > 1), scale > 0. */
 enum { MXG_SCORE_SOFTMAX = 0, MXG_SCORE_SIGMOID = 1 };
-int mxg_route_scores_fwd(const float* logits, const float* bias, int T, int E, int k, int score, int groups,
-                         int top_groups, int group_top, int renormalize, float scale, int32_t* ids, float* probs,
-                         void* stream);
+typedef struct {
+  int32_t T, E, k;
+  int32_t score;
+  int32_t groups, top_groups, group_top;
+  int32_t renormalize;
+  float scale;
+  const float* logits;
+  const float* bias;          /* nullable                                                */
+  int32_t* ids;
+  float* probs;
+} mxg_route_scores_fwd_args;
+int mxg_route_scores_fwd(const mxg_route_scores_fwd_args* args, void* stream);
 
 /* Gradient of the weights of mxg_route_scores_fwd (the choice carries none), as
  * one dense matrix for mxg_router_linear_bwd.  With p, dp a token's probs and
@@ -308,9 +317,19 @@ int mxg_route_scores_fwd(const float* logits, const float* bias, int T, int E, i
  * Ids outside [0, E) add nothing at an expert and are reported as
  * MXG_ERR_EXPERT_ID; an id that stands twice adds twice.  Requirements as
  * mxg_route_scores_fwd. */
-int mxg_route_scores_bwd(const float* logits, const int32_t* ids, const float* probs, const float* dprobs,
-                         const float* dlogits_in, int T, int E, int k, int score, int renormalize, float scale,
-                         float* dlogits, int32_t* dev_status, void* stream);
+typedef struct {
+  int32_t T, E, k;
+  int32_t score, renormalize;
+  float scale;
+  const float* logits;
+  const int32_t* ids;
+  const float* probs;
+  const float* dprobs;
+  const float* dlogits_in;    /* nullable                                                */
+  float* dlogits;
+  int32_t* dev_status;
+} mxg_route_scores_bwd_args;
+int mxg_route_scores_bwd(const mxg_route_scores_bwd_args* args, void* stream);
 
 /* ----------------------------------------------------------------------------
  * Residual addition and root-mean-square norm: the layer's input from the

@@ -15,7 +15,8 @@ from ._lib import (  # noqa: F401
     mxg_balance_loss_bwd, mxg_balance_loss_fwd, mxg_balance_loss_workspace_bytes,
     mxg_router_linear_bwd, mxg_router_linear_bwd_workspace_bytes,
     mxg_route_scores_bwd, mxg_route_scores_fwd, mxg_rms_norm_bwd, mxg_rms_norm_bwd_workspace_bytes, mxg_rms_norm_fwd,
-    mxg_grad_clip, mxg_grad_norm, mxg_grad_norm_workspace_bytes, RmsNormBwdArgs, RmsNormFwdArgs, TensorRef,
+    mxg_grad_clip, mxg_grad_norm, mxg_grad_norm_workspace_bytes, RmsNormBwdArgs, RmsNormFwdArgs, RouteScoresBwdArgs,
+    RouteScoresFwdArgs, TensorRef,
     MUON_COEFFICIENTS, MuonArgs, mxg_muon_form, mxg_muon_update, mxg_muon_workspace_bytes,
 )
 from .layer import GroupedExperts, GroupedMLP  # noqa: F401

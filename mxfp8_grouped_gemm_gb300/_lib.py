@@ -7,6 +7,7 @@ tensors, the call raises."""
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 import threading
@@ -124,6 +125,20 @@ class RmsNormBwdArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_uint64)]
 
 
+class RouteScoresFwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("logits", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("probs", ctypes.c_void_p)]
+
+
+class RouteScoresBwdArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("logits", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("probs", ctypes.c_void_p), ("dprobs", ctypes.c_void_p),
+                ("dlogits_in", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
 class TensorRef(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("f32", ctypes.c_int32), ("reserved", ctypes.c_int32)]
@@ -203,8 +218,8 @@ def lib() -> ctypes.CDLL:
         "mxg_muon_workspace_bytes": (SZ, [I32, I32, I32]),
         "mxg_muon_form": (I32, [I32, I32, I32, ctypes.POINTER(I32)]),
         "mxg_muon_update": (I32, [ctypes.POINTER(MuonArgs), P]),
-        "mxg_route_scores_fwd": (I32, [P, P, I32, I32, I32, I32, I32, I32, I32, I32, F32, P, P, P]),
-        "mxg_route_scores_bwd": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, P, P]),
+        "mxg_route_scores_fwd": (I32, [P, P]),
+        "mxg_route_scores_bwd": (I32, [P, P]),
         "mxg_rms_norm_fwd": (I32, [P, P]),
         "mxg_rms_norm_bwd_workspace_bytes": (SZ, [I32, I32]),
         "mxg_rms_norm_bwd": (I32, [P, P]),
@@ -557,6 +572,9 @@ def _refuse(names, tensors, dtypes, shapes):
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
 
 
+# the C structures as the bytes that a call passes: one call of struct where ctypes takes a step per field
+_PACK_ROUTE_FWD = struct.Struct("@iiiiiiiifPPPP")
+_PACK_ROUTE_BWD = struct.Struct("@iiiiifPPPPPPP")
 _ROUTE_FWD = ("logits", "bias", "ids", "probs")
 _ROUTE_FWD_TYPES = (torch.float32, torch.float32, torch.int32, torch.float32)
 
@@ -573,8 +591,8 @@ def mxg_route_scores_fwd(logits, k: int, score: str = "softmax", bias=None, grou
     ids = _empty((T, k), torch.int32, logits.device, stream) if ids is None else ids
     probs = _empty((T, k), torch.float32, logits.device, stream) if probs is None else probs
     z, b, i, p = _pointers(_ROUTE_FWD, (logits, bias, ids, probs), _ROUTE_FWD_TYPES, (None, (E,), (T, k), (T, k)))
-    _check("mxg_route_scores_fwd", lib().mxg_route_scores_fwd(z, b, T, E, k, kind, groups, top_groups, group_top,
-                                                              renormalize, scale, i, p, _stream(stream)))
+    args = _PACK_ROUTE_FWD.pack(T, E, k, kind, groups, top_groups, group_top, renormalize, scale, z, b, i, p)
+    _check("mxg_route_scores_fwd", lib().mxg_route_scores_fwd(args, _stream(stream)))
     return ids, probs
 
 
@@ -592,12 +610,11 @@ def mxg_route_scores_bwd(logits, ids, probs, dprobs, dev_status, score: str = "s
     dlogits = _empty((T, E), torch.float32, logits.device, stream) if dlogits is None else dlogits
     z, i, p, dp, add, d, st = _pointers(_ROUTE_BWD, (logits, ids, probs, dprobs, dlogits_in, dlogits, dev_status),
                                         _ROUTE_BWD_TYPES, (None, (T, k), (T, k), (T, k), (T, E), (T, E), None))
-    _check("mxg_route_scores_bwd", lib().mxg_route_scores_bwd(z, i, p, dp, add, T, E, k, kind, renormalize, scale, d, st,
-                                                              _stream(stream)))
+    args = _PACK_ROUTE_BWD.pack(T, E, k, kind, renormalize, scale, z, i, p, dp, add, d, st)
+    _check("mxg_route_scores_bwd", lib().mxg_route_scores_bwd(args, _stream(stream)))
     return dlogits
 
 
-# the C structures as the bytes that a call passes: one call of struct where ctypes takes a step per field
 _PACK_NORM_FWD = struct.Struct("@iiPPPiiPfiPPPP")
 _PACK_NORM_BWD = struct.Struct("@iiPPiiPPPPPPPQ")
 _NORM_FWD = ("x", "weight", "residual", "residual_out", "y", "q", "s", "rstd")
@@ -688,35 +705,39 @@ def mxg_grad_norm_workspace_bytes(n) -> int:
     return int(lib().mxg_grad_norm_workspace_bytes(n))
 
 
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_get_device, _is_contiguous, _dtype = torch.Tensor.get_device, torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+_REAL = {torch.float32, torch.bfloat16}
+
+
 def _tensor_refs(grads, out):
     """The library's table of the tensors, as bytes; out None: no outputs.  A model's worth of small gradients takes
-    longer here than on the GPU, so each tensor is asked for each thing once."""
+    longer here than on the GPU, so the tensors are asked for one thing after the other, without a loop over them."""
     n = len(grads)
     if n == 0:
         raise ValueError("no gradients given")
     if out is not None and len(out) != n:
         raise ValueError(f"{n} gradients but {len(out)} outputs")
-    f32, bf16 = torch.float32, torch.bfloat16
-    fields, used = [], []
-    dev = torch._C._cuda_getDevice() if grads[0].is_cuda else None
-    for i, t in enumerate(grads):
-        dtype = t.dtype
-        if t.get_device() != dev or (dtype is not f32 and dtype is not bf16) or not t.is_contiguous():
+    types, sizes, ptrs = list(map(_dtype, grads)), list(map(_numel, grads)), list(map(_data_ptr, grads))
+    devices = set(map(_get_device, grads))
+    if devices != {torch._C._cuda_getDevice() if grads[0].is_cuda else None} or not _REAL.issuperset(types) or not all(
+            map(_is_contiguous, grads)):
+        for i, t in enumerate(grads):
             _real(t, f"grads[{i}]")
-            _refuse((f"grads[{i}]",), (t,), (dtype,), (None,))
-        p = q = t.data_ptr()
-        size = t.numel()
-        if out is not None:
-            o = out[i]
-            if o is not t:
-                if o.get_device() != dev or o.dtype is not dtype or o.numel() != size or not o.is_contiguous():
-                    _refuse((f"out[{i}]",), (o,), (dtype,), (t.shape,))
-                q = o.data_ptr()
-            if size:
-                used.append(q)
-        fields += (p, q, size, dtype is f32, 0)
-    if len(set(used)) != len(used):
-        raise ValueError("a tensor is listed twice as an output")
+            _refuse((f"grads[{i}]",), (t,), (t.dtype,), (None,))
+    to = ptrs
+    if out is not None and out is not grads:
+        if (set(map(_get_device, out)) != devices or list(map(_dtype, out)) != types or list(map(_numel, out)) != sizes
+                or not all(map(_is_contiguous, out))):
+            for i, (t, o) in enumerate(zip(grads, out)):
+                _refuse((f"out[{i}]",), (o,), (t.dtype,), (t.shape,))
+        to = list(map(_data_ptr, out))
+    if out is not None and len(set(to)) != n:           # the same address twice: tensors without elements may share one
+        used = [p for p, size in zip(to, sizes) if size]
+        if len(set(used)) != len(used):
+            raise ValueError("a tensor is listed twice as an output")
+    f32 = torch.float32
+    fields = [f for p, q, size, d in zip(ptrs, to, sizes, types) for f in (p, q, size, d is f32, 0)]
     return struct.pack("@" + "PPqii" * n, *fields), n
 
 

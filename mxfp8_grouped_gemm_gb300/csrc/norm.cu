@@ -93,8 +93,10 @@ __device__ __forceinline__ void load_weight(const void* w, int w32, int col, flo
   else load8(static_cast<const uint16_t*>(w) + col, v);
 }
 
+// Ten CTAs an SM where a lane holds 32 values (48 registers; with 64 and eight CTAs
+// 65536 x 1024 took 97.6 us instead of 94.3, 5003 x 1000 in fp32 14.4 instead of 13.3).
 template <int LPR, int NCH, int RES>
-__global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads) norm_fwd_kernel(const NormFwdParams P) {
+__global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads, LPR != 0 && NCH == 4 ? 10 : 0) norm_fwd_kernel(const NormFwdParams P) {
   __shared__ float s_part[2][32];
   const int threads = LPR != 0 ? LPR : static_cast<int>(blockDim.x);
   const int th = LPR != 0 ? static_cast<int>(threadIdx.x) % LPR : static_cast<int>(threadIdx.x);
@@ -438,10 +440,14 @@ int bwd_chunks(int H) { return H <= 8192 ? 2 : 4; }
 int bwd_threads(int H) { return H <= 1024 ? kRowThreads : wide_threads(H, bwd_chunks(H)); }
 
 // CTAs of the backward: what fits on the SMs at once (their partial sums of
-// dweight are read again), at most one for each set of rows.
+// dweight are read again), at most one for each set of rows.  Up to kAlone sets
+// that one SM reads in about a microsecond are left to one CTA, which needs no
+// second launch.
+constexpr int kAlone = 8, kAloneElements = 32768;
 int bwd_ctas(int H) { return H <= 256 ? 8 : H <= 512 ? 4 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1; }
 int bwd_blocks(int T, int H) {
   const int64_t need = (static_cast<int64_t>(T) + rows_at_once(H) - 1) / rows_at_once(H);
+  if (need <= kAlone && static_cast<int64_t>(T) * H <= kAloneElements) return 1;
   const int64_t most = static_cast<int64_t>(kSms) * bwd_ctas(H);
   return static_cast<int>(need < most ? need : most);
 }

@@ -950,26 +950,25 @@ int route_shape(int T, int E, int k, int score, float scale) {
 
 using namespace mxg;
 
-extern "C" int mxg_route_scores_fwd(const float* logits, const float* bias, int T, int E, int k, int score, int groups,
-                                    int top_groups, int group_top, int renormalize, float scale, int32_t* ids,
-                                    float* probs, void* stream) {
-  if (!logits || !ids || !probs) return MXG_ERR_ARG;
-  if (const int err = route_shape(T, E, k, score, scale)) return err;
+extern "C" int mxg_route_scores_fwd(const mxg_route_scores_fwd_args* A, void* stream) {
+  if (!A || !A->logits || !A->ids || !A->probs) return MXG_ERR_ARG;
+  const int T = A->T, E = A->E, k = A->k, groups = A->groups, top_groups = A->top_groups, group_top = A->group_top;
+  if (const int err = route_shape(T, E, k, A->score, A->scale)) return err;
   if (groups <= 0 || top_groups <= 0 || (group_top != 1 && group_top != 2)) return MXG_ERR_ARG;
   if (groups > E || E % groups != 0 || top_groups > groups) return MXG_ERR_SHAPE;
   const int size = E / groups;
   if (k > top_groups * size || (groups > 1 && group_top > size)) return MXG_ERR_SHAPE;
-  if (!api::aligned32(logits) || !api::aligned32(bias) || !api::aligned32(ids) || !api::aligned32(probs))
+  if (!api::aligned32(A->logits) || !api::aligned32(A->bias) || !api::aligned32(A->ids) || !api::aligned32(A->probs))
     return MXG_ERR_ALIGN;
   api::NvtxRange nvtx("mxg.route_scores_fwd");
   const int lanes = lanes_per_token(E);
-  RouteParams p{logits, bias, T, E, k, score, groups, top_groups, group_top, size, 0, 1, renormalize != 0, scale, ids,
-                probs};
+  RouteParams p{A->logits, A->bias, T,    E, k, A->score,            groups,   top_groups, group_top,
+                size,      0,       1,    A->renormalize != 0, A->scale, A->ids,   A->probs};
   const int whole = size % kVals == 0 ? size / kVals : 0;
   if ((whole & (whole - 1)) == 0) p.lanes_of_group = whole;
   while (2 * p.spread * groups <= lanes) p.spread *= 2;
-  const bool scored = bias != nullptr || (top_groups < groups && group_top == 2);
-  const int by = !scored ? BY_LOGIT : score == SIGMOID ? BY_SIGMOID : BY_SOFTMAX;
+  const bool scored = A->bias != nullptr || (top_groups < groups && group_top == 2);
+  const int by = !scored ? BY_LOGIT : A->score == SIGMOID ? BY_SIGMOID : BY_SOFTMAX;
   const int kind = top_groups == groups ? NO_GROUPS : p.lanes_of_group != 0 ? LANE_GROUPS : ANY_GROUPS;
   // all that fit at once (three blocks an SM), fewer where a warp would get less than a set of tokens
   const unsigned most = 3 * 152, need = token_blocks(T, E), grid = need < most ? need : most;
@@ -983,17 +982,16 @@ extern "C" int mxg_route_scores_fwd(const float* logits, const float* bias, int 
   return api::cuda_status(cudaGetLastError());
 }
 
-extern "C" int mxg_route_scores_bwd(const float* logits, const int32_t* ids, const float* probs, const float* dprobs,
-                                    const float* dlogits_in, int T, int E, int k, int score, int renormalize,
-                                    float scale, float* dlogits, int32_t* dev_status, void* stream) {
-  if (!logits || !ids || !probs || !dprobs || !dlogits || !dev_status) return MXG_ERR_ARG;
-  if (const int err = route_shape(T, E, k, score, scale)) return err;
-  if (!api::aligned32(logits) || !api::aligned32(ids) || !api::aligned32(probs) || !api::aligned32(dprobs) ||
-      !api::aligned32(dlogits_in) || !api::aligned32(dlogits))
+extern "C" int mxg_route_scores_bwd(const mxg_route_scores_bwd_args* A, void* stream) {
+  if (!A || !A->logits || !A->ids || !A->probs || !A->dprobs || !A->dlogits || !A->dev_status) return MXG_ERR_ARG;
+  const int T = A->T, E = A->E;
+  if (const int err = route_shape(T, E, A->k, A->score, A->scale)) return err;
+  if (!api::aligned32(A->logits) || !api::aligned32(A->ids) || !api::aligned32(A->probs) ||
+      !api::aligned32(A->dprobs) || !api::aligned32(A->dlogits_in) || !api::aligned32(A->dlogits))
     return MXG_ERR_ALIGN;
   api::NvtxRange nvtx("mxg.route_scores_bwd");
-  const RouteBwdParams p{logits, ids,   probs, dprobs,           dlogits_in,   dlogits,   T,
-                         E,      k,     score, renormalize != 0, 1.f / scale, dev_status};
+  const RouteBwdParams p{A->logits, A->ids, A->probs, A->dprobs, A->dlogits_in,        A->dlogits,      T,
+                         E,         A->k,   A->score, A->renormalize != 0, 1.f / A->scale, A->dev_status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   with_lanes(E, [&](auto l) {
     constexpr int at_once = 32 / l.value, set = kWarps * (at_once > 4 ? at_once : 4);

@@ -20,9 +20,10 @@ def m():
 
 def test_route_fwd(m):
     def call(logits=F, bias=None, T=64, E=16, k=2, score=0, groups=1, top=1, gt=1, renorm=1, scale=1.0, ids=F, probs=F):
-        return m.lib().mxg_route_scores_fwd(logits, bias, T, E, k, score, groups, top, gt, renorm, scale, ids, probs,
-                                            None)
+        a = m.RouteScoresFwdArgs(T, E, k, score, groups, top, gt, renorm, scale, logits, bias, ids, probs)
+        return m.lib().mxg_route_scores_fwd(ctypes.byref(a), None)
 
+    assert m.lib().mxg_route_scores_fwd(None, None) == ARG
     for name in ("logits", "ids", "probs"):
         assert call(**{name: None}) == ARG and call(**{name: BAD}) == ALIGN, name
     assert call(bias=BAD) == ALIGN
@@ -36,9 +37,10 @@ def test_route_fwd(m):
 
 def test_route_bwd(m):
     def call(logits=F, ids=F, probs=F, dprobs=F, add=None, T=64, E=16, k=2, score=1, renorm=1, scale=1.0, out=F, st=F):
-        return m.lib().mxg_route_scores_bwd(logits, ids, probs, dprobs, add, T, E, k, score, renorm, scale, out, st,
-                                            None)
+        a = m.RouteScoresBwdArgs(T, E, k, score, renorm, scale, logits, ids, probs, dprobs, add, out, st)
+        return m.lib().mxg_route_scores_bwd(ctypes.byref(a), None)
 
+    assert m.lib().mxg_route_scores_bwd(None, None) == ARG
     for name in ("logits", "ids", "probs", "dprobs", "out", "st"):
         assert call(**{name: None}) == ARG, name
     for name in ("logits", "ids", "probs", "dprobs", "add", "out"):
