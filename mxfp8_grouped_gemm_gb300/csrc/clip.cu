@@ -11,6 +11,10 @@
 // backwards, so that what the first read last comes from L2, and its own traffic
 // is marked to leave L2 first.
 //
+// Measured: 805 M elements (3.2 GB) into other memory 1452 us, 6.66 TB/s over the
+// three passes of the data; with chunks of elements instead of pieces and plain
+// caching 1601.  1.6 MB in four tensors 5.4 us, two launches.
+//
 // A thread's squares of a chunk are added in fp32.  Where that sum is not finite
 // or so small that squares may have vanished, they are added again in fp64:
 // gradients of 1e30 and of 1e-30 have norms.

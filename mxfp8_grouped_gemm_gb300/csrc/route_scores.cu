@@ -16,6 +16,12 @@
 // LPT lanes take a token, eight consecutive experts a lane, so the lowest lane
 // has the lowest ids.  Each lane sorts its eight in registers (19 exchanges);
 // then a round picks the largest head, and its lane moves up by one.
+//
+// Measured, launch included: 65536 x 256, top-8, sigmoid, bias, 4 of 8 groups 41
+// us, without groups 33, by logits 29; 8191 x 64 softmax 4.3 us.  Bound by
+// instructions (416 a warp and token with groups, 293 by logits) at two thirds of
+// the issue slots, 24 warps an SM; the logits' stream would take 10 us.  Its
+// gradient 21 us, bound by HBM (118 MB: a chosen logit is a 64-byte access).
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -362,7 +368,8 @@ __device__ __noinline__ void rank_all(const RouteParams& P, const float* row, fl
 // are ranked.  (All in fp64 for every such token cost 14 us of the 57 that
 // 65536 x 256 took: a few dozen tokens, but the last to finish.)
 //   row_c   fp32 c; -inf: off, NaN: its group does not take part
-//   kth     the k-th largest c, unless the groups are to be decided as well
+//   win     the choices by fp32 (the k-th bounds the others), then inverse sums
+//   groups_close  the groups are to be decided as well: row_c has all of them
 template <int BY, int GROUPS, int N>
 __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, const float* row_c, float2* win,
                                         uint8_t* list, float reach, float most, bool groups_close) {
