@@ -451,17 +451,18 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
       live += c[i] > -INFINITY;
     }
     if (static_cast<int>(__reduce_add_sync(kAll, live)) < P.k) return rank_all<true>(P, row, win);
-    float bound = INFINITY;                            // the k-th largest of what is left
-    for (int j = 0; j < P.k;) {
+    // the k-th largest of what is left, by distinct values: at most k rounds, as each finds one (a bias of +inf too)
+    int found = 0;
+    for (int j = 0; j < P.k && found < P.k; ++j) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kVals; ++i)
-        if (c[i] < bound) m = fmaxf(m, c[i]);
-      kth = bound = lanes_max<32>(m);
+        if (j == 0 || c[i] < kth) m = fmaxf(m, c[i]);
+      kth = lanes_max<32>(m);
       int equal = 0;
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) equal += c[i] == bound;
-      j += static_cast<int>(__reduce_add_sync(kAll, equal));
+      for (int i = 0; i < kVals; ++i) equal += c[i] == kth;
+      found += static_cast<int>(__reduce_add_sync(kAll, equal));
     }
   } else {
     kth = win[P.k - 1].x;

@@ -136,6 +136,23 @@ def test_route_fwd_groups_with_few_experts_left(E, groups, top_groups, k, group_
             _check(m, z, b, k, dict(score=kind, groups=groups, top_groups=top_groups, group_top=group_top))
 
 
+@pytest.mark.parametrize("E,groups,top_groups,k", [(8, 1, 1, 3), (16, 2, 1, 8), (64, 8, 2, 9), (30, 5, 2, 12), (256, 8, 4, 8)])
+def test_route_fwd_infinite_biases(E, groups, top_groups, k):
+    """Experts that are always chosen (a bias of +inf), in one group and in several, beside some that never are."""
+    m = require_gpu()
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((300, E)).astype(np.float32)
+    z[rng.random(z.shape) < 0.1] = -np.inf
+    for always in (1, 2, E // 2, E):
+        bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+        bias[rng.choice(E, always, replace=False)] = np.inf
+        if always < E:
+            bias[rng.choice(np.flatnonzero(np.isfinite(bias)))] = -np.inf
+        for group_top in (1, 2):
+            if group_top <= E // groups:
+                _check(m, z, bias, k, dict(score="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top))
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("size", [30.0, 60.0, 1e4])
 def test_route_fwd_far_logits(kind, size):
