@@ -10,10 +10,11 @@
 // (8 values each, so four neighbouring lanes hold one MX block).  Rows of up to
 // 1024 values are handled by 8 to 32 lanes of a warp, several rows a CTA; wider
 // ones by a CTA of their own.  Both passes are bound by HBM.  Measured, bf16
-// streams, launches included: forward 16384 x 4096 with codes 94 us (6.4 TB/s),
+// streams, launches included: forward 16384 x 4096 with codes 92 us (6.6 TB/s),
 // 262144 x 128 46 us (6.6), 4096 x 16384 111 us (5.5: two CTAs of 512 threads an
-// SM, whose loads and stores take turns); backward 16384 x 4096 83 us (6.5 TB/s),
-// 65536 x 1024 86 (6.2), 8192 x 4096 in fp32 98 (5.5), 4096 x 16384 125 (4.3).
+// SM, whose loads and stores take turns; shared by a cluster of four 127); backward 16384 x 4096 83 us (6.5 TB/s),
+// 65536 x 1024 86 (6.2), 8192 x 4096 in fp32 98 (5.5), 4096 x 16384 121 (4.4; by
+// clusters of four CTAs, whose barrier a row waits for, 118).
 #include <cmath>
 
 #include "api_common.h"
@@ -438,10 +439,12 @@ int wide_threads(int H, int chunks) { return (H / 8 + chunks * 32 - 1) / (chunks
 
 int rows_at_once(int H) { return H <= 64 ? 16 : H <= 128 ? 8 : H <= 1024 ? 4 : 1; }
 
-// The backward's chunks per thread of a wide row, its threads, and the shared
-// memory of its rows (in the widest case, fp32 streams).
-int bwd_chunks(int H) { return H <= 8192 ? 2 : 4; }
-int bwd_threads(int H) { return H <= 1024 ? kRowThreads : wide_threads(H, bwd_chunks(H)); }
+// Chunks per thread of a wide row: two, so that a CTA has the threads to ask for a
+// row at once (forward 16384 x 4096 94.5 us with four, 91.9 with two, 20000 x 2048
+// 59.2 and 55.8), up to the 512 threads of a CTA (4096 x 16384 with 1024 threads
+// 128 us instead of 111).
+int wide_chunks(int H) { return H <= 8192 ? 2 : 4; }
+int bwd_threads(int H) { return H <= 1024 ? kRowThreads : wide_threads(H, wide_chunks(H)); }
 
 // CTAs of the backward: what fits on the SMs at once (their partial sums of
 // dweight are read again), at most one for each set of rows.  Up to kAlone sets
@@ -478,7 +481,7 @@ extern "C" int mxg_rms_norm_fwd(const mxg_rms_norm_fwd_args* A, void* stream) {
                   static_cast<float>(1.0 / A->H), A->y, A->q, A->s, A->layout, A->rstd};
   const int rows = rows_at_once(A->H);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(A->T) + rows - 1) / rows);
-  with_width(A->H, 4, [&](auto lpr, auto nch) {
+  with_width(A->H, wide_chunks(A->H), [&](auto lpr, auto nch) {
     const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H, nch.value);
     if (!A->residual) norm_fwd_kernel<lpr.value, nch.value, RES_NONE><<<grid, block, 0, st>>>(p);
     else if (A->residual_f32) norm_fwd_kernel<lpr.value, nch.value, RES_F32><<<grid, block, 0, st>>>(p);
@@ -511,7 +514,7 @@ extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
                   nblk == 1 ? A->dweight : static_cast<float*>(A->workspace)};
   const int block = bwd_threads(A->H);
   cudaError_t err = cudaSuccess;
-  with_width(A->H, bwd_chunks(A->H), [&](auto lpr, auto nch) {
+  with_width(A->H, wide_chunks(A->H), [&](auto lpr, auto nch) {
     const auto launch = [&](auto* kern, bool f32) {
       const int smem = row_slots(lpr.value, nch.value, f32) * nch.value * (f32 ? 5 : 3) * block * 16;
       err = allow_smem(kern, 200 * 1024);
