@@ -204,7 +204,7 @@ __device__ __forceinline__ void copies_wait() {
 // CTAs an SM runs (bwd_ctas); one of 16384 fp32 values.
 constexpr int row_slots(int lpr, int nch, bool f32) {
   const bool widest = lpr == 0 && nch == 4;
-  return f32 ? (widest ? 1 : 2) : widest ? 2 : nch == 1 ? 3 : 4;
+  return f32 ? (widest ? 1 : 2) : widest ? 2 : nch == 1 || nch == 3 ? 3 : 4;
 }
 
 // A CTA takes rows blockIdx, + grid, ... and keeps the sums of its columns of
@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* __restr
 }
 
 // Calls f(lanes per row or 0, chunks per thread) with the form of a width, as
-// compile-time numbers.
-template <typename F>
+// compile-time numbers (THREE: wide rows may have three chunks a thread).
+template <bool THREE, typename F>
 void with_width(int H, int wide_chunks, F f) {
   const int n8 = H / 8;
   using std::integral_constant;
@@ -432,6 +432,7 @@ void with_width(int H, int wide_chunks, F f) {
   else if (n8 <= 64) f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
   else if (n8 <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
   else if (wide_chunks == 2) f(integral_constant<int, 0>{}, integral_constant<int, 2>{});
+  else if (THREE && wide_chunks == 3) f(integral_constant<int, 0>{}, integral_constant<int, THREE ? 3 : 2>{});
   else f(integral_constant<int, 0>{}, integral_constant<int, 4>{});
 }
 
@@ -444,7 +445,10 @@ int rows_at_once(int H) { return H <= 64 ? 16 : H <= 128 ? 8 : H <= 1024 ? 4 : 1
 // 59.2 and 55.8), up to the 512 threads of a CTA (4096 x 16384 with 1024 threads
 // 128 us instead of 111).
 int wide_chunks(int H) { return H <= 8192 ? 2 : 4; }
-int bwd_threads(int H) { return H <= 1024 ? kRowThreads : wide_threads(H, wide_chunks(H)); }
+// The backward of a bf16 stream keeps three chunks in registers up to 12288 (7000
+// x 8200 170 us with four that are read twice, 12288 values 103).
+int bwd_chunks(int H, bool f32) { return !f32 && H > 8192 && H <= 12288 ? 3 : wide_chunks(H); }
+int bwd_threads(int H, bool f32) { return H <= 1024 ? kRowThreads : wide_threads(H, bwd_chunks(H, f32)); }
 
 // CTAs of the backward: what fits on the SMs at once (their partial sums of
 // dweight are read again), at most one for each set of rows.  Up to kAlone sets
@@ -481,7 +485,7 @@ extern "C" int mxg_rms_norm_fwd(const mxg_rms_norm_fwd_args* A, void* stream) {
                   static_cast<float>(1.0 / A->H), A->y, A->q, A->s, A->layout, A->rstd};
   const int rows = rows_at_once(A->H);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(A->T) + rows - 1) / rows);
-  with_width(A->H, wide_chunks(A->H), [&](auto lpr, auto nch) {
+  with_width<false>(A->H, wide_chunks(A->H), [&](auto lpr, auto nch) {
     const int block = lpr.value != 0 ? kRowThreads : wide_threads(A->H, nch.value);
     if (!A->residual) norm_fwd_kernel<lpr.value, nch.value, RES_NONE><<<grid, block, 0, st>>>(p);
     else if (A->residual_f32) norm_fwd_kernel<lpr.value, nch.value, RES_F32><<<grid, block, 0, st>>>(p);
@@ -512,16 +516,18 @@ extern "C" int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* A, void* stream) {
   NormBwdParams p{A->T, A->H, A->dy, A->r, A->weight, A->weight_f32 != 0, A->rstd, static_cast<float>(1.0 / A->H),
                   A->dresidual, A->dx, A->dresidual_out,
                   nblk == 1 ? A->dweight : static_cast<float*>(A->workspace)};
-  const int block = bwd_threads(A->H);
+  const int block = bwd_threads(A->H, A->r_f32 != 0);
   cudaError_t err = cudaSuccess;
-  with_width(A->H, wide_chunks(A->H), [&](auto lpr, auto nch) {
+  with_width<true>(A->H, bwd_chunks(A->H, A->r_f32 != 0), [&](auto lpr, auto nch) {
     const auto launch = [&](auto* kern, bool f32) {
       const int smem = row_slots(lpr.value, nch.value, f32) * nch.value * (f32 ? 5 : 3) * block * 16;
-      err = allow_smem(kern, 200 * 1024);
+      err = allow_smem(kern, 226 * 1024);
       if (err == cudaSuccess) kern<<<nblk, block, smem, st>>>(p);
     };
-    if (A->r_f32) launch(norm_bwd_kernel<lpr.value, nch.value, true>, true);
-    else launch(norm_bwd_kernel<lpr.value, nch.value, false>, false);
+    if constexpr (nch.value != 3) {               // three chunks: bf16 alone (bwd_chunks)
+      if (A->r_f32) return launch(norm_bwd_kernel<lpr.value, nch.value, true>, true);
+    }
+    launch(norm_bwd_kernel<lpr.value, nch.value, false>, false);
   });
   MXG_TRY(err);
   count_launch();

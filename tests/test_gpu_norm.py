@@ -30,6 +30,11 @@ CASES = [                 # T, H, residual, fp32 weight
     (5, 5472, "f32", True),
     (3, 8192, "bf16", True),
     (2, 16376, "f32", False),
+    (7, 8200, "bf16", False),         # one past two chunks a thread
+    (3, 12288, "bf16", True),
+    (2, 12296, "bf16", True),         # one past three
+    (200, 9000, None, False),
+    (5, 8200, "f32", True),
     (2, 16384, "bf16", True),
     (5003, 128, "bf16", True),        # many rows to a lane group
     (1300, 4096, "bf16", False),
