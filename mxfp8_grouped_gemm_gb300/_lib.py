@@ -6,7 +6,9 @@ There is no fallback: if the library is missing or the tensors are not CUDA
 tensors, the call raises."""
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
 import operator
 import os
 import struct
@@ -547,16 +549,17 @@ def _pointers(names, tensors, dtypes, shapes) -> list:
     """Addresses of tensors (0 for None) that have these types and shapes (None: any) and are contiguous and on the
     current device, where the library runs.  Small calls take as long as this, so it looks at each tensor once."""
     out, dev = [], None
+    add = out.append
     for t, dtype, shape in zip(tensors, dtypes, shapes):
         if t is None:
-            out.append(0)
+            add(0)
             continue
         d = t.get_device()
         if dev is None and d >= 0:
             dev = torch._C._cuda_getDevice()
         if d != dev or t.dtype is not dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
             _refuse(names, tensors, dtypes, shapes)
-        out.append(t.data_ptr())
+        add(t.data_ptr())
     return out
 
 
@@ -711,8 +714,9 @@ _REAL = {torch.float32, torch.bfloat16}
 
 
 def _tensor_refs(grads, out):
-    """The library's table of the tensors, as bytes; out None: no outputs.  A model's worth of small gradients takes
-    longer here than on the GPU, so the tensors are asked for one thing after the other, without a loop over them."""
+    """The library's table of the tensors (mxg_tensor, four 64-bit words each); out None: no outputs.  A model's worth of
+    small gradients takes longer here than on the GPU, so the tensors are asked for one thing after the other, without a
+    loop over them."""
     n = len(grads)
     if n == 0:
         raise ValueError("no gradients given")
@@ -737,17 +741,25 @@ def _tensor_refs(grads, out):
         if len(set(used)) != len(used):
             raise ValueError("a tensor is listed twice as an output")
     f32 = torch.float32
-    fields = [f for p, q, size, d in zip(ptrs, to, sizes, types) for f in (p, q, size, d is f32, 0)]
-    return struct.pack("@" + "PPqii" * n, *fields), n
+    words = itertools.chain.from_iterable(zip(ptrs, to, sizes, [d is f32 for d in types]))
+    return array.array("q", words), n
+
+
+def _norm_ptr(norm, name: str) -> int:
+    return _pointers((name,), (norm,), (torch.float32,), ((1,),))[0]
 
 
 def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
     """Norm over all tensors of a list (bf16, fp32; contiguous, any shapes) -> fp32 [1]."""
     refs, n = _tensor_refs(grads, None)
     dev = grads[0].device
-    norm = _empty(1, torch.float32, dev, stream) if norm is None else norm
-    to, = _pointers(("norm",), (norm,), (torch.float32,), ((1,),))
-    _call_with_scratch("mxg_grad_norm", lambda ws, b, st: lib().mxg_grad_norm(refs, n, to, ws, b, st),
+    if norm is None:
+        norm = _empty(1, torch.float32, dev, stream)
+        to = norm.data_ptr()
+    else:
+        to = _norm_ptr(norm, "norm")
+    table = refs.buffer_info()[0]
+    _call_with_scratch("mxg_grad_norm", lambda ws, b, st: lib().mxg_grad_norm(table, n, to, ws, b, st),
                        lambda: mxg_grad_norm_workspace_bytes(n), workspace, dev, stream)
     return norm
 
@@ -759,14 +771,18 @@ def mxg_grad_clip(grads, max_norm: float, out=None, norm=None, norm_out=None, wo
         raise ValueError("norm_out is for the norm that is taken here")
     out = grads if out is None else out
     refs, n = _tensor_refs(grads, out)
-    dev = grads[0].device
-    if norm is None and norm_out is None:
-        norm_out = _empty(1, torch.float32, dev, stream)
-    by, to = _pointers(("norm", "norm_out"), (norm, norm_out), (torch.float32, torch.float32), ((1,), (1,)))
+    table = refs.buffer_info()[0]
     if norm is not None:
-        _check("mxg_grad_clip", lib().mxg_grad_clip(refs, n, max_norm, by, None, None, 0, _stream(stream)))
+        by = _norm_ptr(norm, "norm")
+        _check("mxg_grad_clip", lib().mxg_grad_clip(table, n, max_norm, by, None, None, 0, _stream(stream)))
         return norm, out
-    _call_with_scratch("mxg_grad_clip", lambda ws, b, st: lib().mxg_grad_clip(refs, n, max_norm, None, to, ws, b, st),
+    dev = grads[0].device
+    if norm_out is None:
+        norm_out = _empty(1, torch.float32, dev, stream)
+        to = norm_out.data_ptr()
+    else:
+        to = _norm_ptr(norm_out, "norm_out")
+    _call_with_scratch("mxg_grad_clip", lambda ws, b, st: lib().mxg_grad_clip(table, n, max_norm, None, to, ws, b, st),
                        lambda: mxg_grad_norm_workspace_bytes(n), workspace, dev, stream)
     return norm_out, out
 
