@@ -17,7 +17,7 @@
 // has the lowest ids.  Each lane sorts its eight in registers (19 exchanges);
 // then a round picks the largest head, and its lane moves up by one.
 //
-// Measured, launch included: 65536 x 256, top-8, sigmoid, bias, 4 of 8 groups 41
+// Measured, launch included: 65536 x 256, top-8, sigmoid, bias, 4 of 8 groups 40
 // us, without groups 33, by logits 29; 8191 x 64 softmax 4.3 us.  Bound by
 // instructions (416 a warp and token with groups, 293 by logits) at two thirds of
 // the issue slots, 24 warps an SM; the logits' stream would take 10 us.  Its
@@ -366,7 +366,8 @@ __device__ __noinline__ void rank_all(const RouteParams& P, const float* row, fl
 // within the error of them); these are evaluated in fp64, one to a lane.  Where
 // they are more than lanes, or experts that are off have to fill the route, all
 // are ranked.  (All in fp64 for every such token cost 14 us of the 57 that
-// 65536 x 256 took: a few dozen tokens, but the last to finish.)
+// 65536 x 256 took: a few dozen tokens, but the last to finish; they are 4 us now,
+// 6 with the loops over candidates not unrolled and a division in them.)
 //   row_c   fp32 c; -inf: off, NaN: its group does not take part
 //   win     the choices by fp32 (the k-th bounds the others), then inverse sums
 //   groups_close  the groups are to be decided as well: row_c has all of them
@@ -390,11 +391,31 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
     for (int e = lane; e < P.E; e += 32) sum += exp(static_cast<double>(row[e]) - top);
     sum = warp_sum(sum);
   }
-  // The experts with c at least `from`: their number; lane n gets the n-th and its key.
-  int mine = 0;
-  uint64_t key = 0;
-  const auto evaluate = [&](float from) {
-    int n = 0;
+  // First (groups_close) each group's largest, which decide the groups, then what
+  // is at least as large as the k-th.
+  bool by_group = GROUPS == LANE_GROUPS && groups_close;
+  float kth = -INFINITY, from;
+  if (by_group) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) top_two(a, b, c[i], -INFINITY);
+    for (int off = 1; off < P.lanes_of_group; off <<= 1) {
+      const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
+      top_two(a, b, a2, b2);
+    }
+    from = (P.group_top == 2 ? b : a) - slack;
+  } else {
+    kth = win[P.k - 1].x;
+    __syncwarp();
+    if (kth == -INFINITY) return rank_all<true>(P, row, win);
+    from = kth - slack;
+  }
+  int n, mine;
+  uint64_t key;
+#pragma unroll 1
+  while (true) {
+    // the experts with c at least `from`: their number; lane n gets the n-th and its key
+    n = 0;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       const bool w = c[i] >= from && c[i] != -INFINITY;
@@ -404,43 +425,38 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
       n += __popc(who);
     }
     __syncwarp();
-    if (n <= 32) {
-      mine = lane < n ? list[lane] : -1;
-      const double z = row[lane < n ? mine : 0];
-      const double x = exp(BY == BY_SIGMOID ? -z : z - top);
-      double v = BY == BY_SIGMOID ? 1.0 / (1.0 + x) : x / sum;
-      if (P.bias != nullptr && lane < n) v += static_cast<double>(P.bias[mine]);
-      key = lane < n ? key_of(v) : 0;
-    }
-    __syncwarp();
-    return n;
-  };
-  float kth = -INFINITY;
-  if (GROUPS == LANE_GROUPS && groups_close) {
-    float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) top_two(a, b, c[i], -INFINITY);
-    for (int off = 1; off < P.lanes_of_group; off <<= 1) {
-      const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
-      top_two(a, b, a2, b2);
-    }
-    const int n = evaluate((P.group_top == 2 ? b : a) - slack);
     if (n > 32) return rank_all<true>(P, row, win);
+    mine = lane < n ? list[lane] : -1;
+    const double z = row[lane < n ? mine : 0];
+    const double x = exp(BY == BY_SIGMOID ? -z : z - top);
+    double v = BY == BY_SIGMOID ? 1.0 / (1.0 + x) : x / sum;
+    if (P.bias != nullptr && lane < n) v += static_cast<double>(P.bias[mine]);
+    key = lane < n ? key_of(v) : 0;
+    __syncwarp();
+    if (!by_group) break;
+    by_group = false;
     uint64_t best = 0, second = 0;                     // of group `lane`
+    const int group = mine < 0 ? -1 : mine / kVals / P.lanes_of_group;
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const uint64_t v = __shfl_sync(kAll, key, i);
-      if (__shfl_sync(kAll, mine, i) / P.size == lane) {
-        second = max(second, min(best, v));
-        best = max(best, v);
+    for (int i0 = 0; i0 < n; i0 += 4) {
+#pragma unroll
+      for (int i = i0; i < i0 + 4; ++i) {              // past n: key 0, group -1
+        const uint64_t u = __shfl_sync(kAll, key, i);
+        if (__shfl_sync(kAll, group, i) == lane) {
+          second = max(second, min(best, u));
+          best = max(best, u);
+        }
       }
     }
     const uint64_t score = P.group_top == 2 && second != 0 ? key_of(of_key(best) + of_key(second)) : best;
     int ahead = 0;
 #pragma unroll 1
-    for (int g = 0; g < P.groups; ++g) {
-      const uint64_t v = __shfl_sync(kAll, score, g);
-      ahead += v > score || (v == score && g < lane);
+    for (int g0 = 0; g0 < P.groups; g0 += 4) {
+#pragma unroll
+      for (int g = g0; g < g0 + 4; ++g) {              // past the last: score 0, and behind
+        const uint64_t u = __shfl_sync(kAll, score, g);
+        ahead += u > score || (u == score && g < lane);
+      }
     }
     const unsigned kept = __ballot_sync(kAll, lane < P.groups && ahead < P.top_groups);
     const bool in = lane / P.lanes_of_group < 32 && (kept >> (lane / P.lanes_of_group) & 1u);
@@ -451,32 +467,27 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
       live += c[i] > -INFINITY;
     }
     if (static_cast<int>(__reduce_add_sync(kAll, live)) < P.k) return rank_all<true>(P, row, win);
-    // the k-th largest of what is left, by distinct values: at most k rounds, as each finds one (a bias of +inf too)
-    int found = 0;
-    for (int j = 0; j < P.k && found < P.k; ++j) {
+    // the k-th largest value of what is left (values that stand twice count once, which leaves more candidates)
+#pragma unroll 1
+    for (int j = 0; j < P.k; ++j) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kVals; ++i)
         if (j == 0 || c[i] < kth) m = fmaxf(m, c[i]);
       kth = lanes_max<32>(m);
-      int equal = 0;
-#pragma unroll
-      for (int i = 0; i < kVals; ++i) equal += c[i] == kth;
-      found += static_cast<int>(__reduce_add_sync(kAll, equal));
     }
-  } else {
-    kth = win[P.k - 1].x;
-    __syncwarp();
+    if (kth == -INFINITY) return rank_all<true>(P, row, win);
+    from = kth - slack;
   }
-  if (kth == -INFINITY) return rank_all<true>(P, row, win);
-  const int n = evaluate(kth - slack);
-  if (n > 32) return rank_all<true>(P, row, win);
   int ahead = 0;
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const uint64_t v = __shfl_sync(kAll, key, i);
-    const int o = __shfl_sync(kAll, mine, i);
-    ahead += v > key || (v == key && o < mine);
+  for (int i0 = 0; i0 < n; i0 += 4) {
+#pragma unroll
+    for (int i = i0; i < i0 + 4; ++i) {                // past n: key 0
+      const uint64_t u = __shfl_sync(kAll, key, i);
+      const int o = __shfl_sync(kAll, mine, i);
+      ahead += u > key || (u == key && o < mine);
+    }
   }
   if (lane < n && ahead < P.k) win[ahead].y = __int_as_float(mine);
   __syncwarp();
