@@ -189,13 +189,28 @@ __device__ __forceinline__ float norm_of(double squares) {
   return squares > 0x1p-100 && squares < 0x1p100 ? sqrtf(static_cast<float>(squares))
                                                  : static_cast<float>(sqrt(squares));
 }
-__device__ __forceinline__ float factor_of(double squares, float max_norm) {
-  if (squares > 0x1p-100 && squares < 0x1p100) {
+// As two factors: out = (g x) y.  x is a power of two, 1 but for quotients that
+// fp32 holds with fewer bits or not at all (a norm of 1e38 clipped to 1e-3): there
+// g x is exact for every g whose output is not zero, and y a normal number, or
+// the output next to the smallest.
+__device__ __forceinline__ float2 split(float q) { return make_float2(1.f, q); }
+__device__ __forceinline__ float2 split(double q) {
+  if (q < 0x1p-200) return make_float2(0x1p-126f, static_cast<float>(q * 0x1p126));
+  if (q < 0x1p-100) return make_float2(0x1p-76f, static_cast<float>(q * 0x1p76));
+  return split(static_cast<float>(q));
+}
+__device__ __forceinline__ float2 factor_of(double squares, float max_norm) {
+  if (squares > 0x1p-100 && squares < 0x1p100 && max_norm > 0x1p-50f) {
     const float norm = sqrtf(static_cast<float>(squares));
-    return norm <= max_norm ? 1.f : max_norm / norm;
+    return split(norm <= max_norm ? 1.f : max_norm / norm);
   }
   const double norm = sqrt(squares);
-  return norm <= max_norm ? 1.f : static_cast<float>(max_norm / norm);
+  return split(norm <= max_norm ? 1.0 : max_norm / norm);
+}
+// The same of a norm in fp32.
+__device__ __forceinline__ float2 factor_of(float norm, float max_norm) {
+  if (norm < 0x1p50f && max_norm > 0x1p-50f) return split(norm <= max_norm ? 1.f : max_norm / norm);
+  return split(norm <= max_norm ? 1.0 : static_cast<double>(max_norm) / norm);
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int n, float* norm) {
@@ -206,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int 
 }
 
 template <int VEC, bool F32>
-__device__ __forceinline__ void chunk_scale(const void* in, void* out, float coef, int64_t base, int64_t left) {
+__device__ __forceinline__ void chunk_scale(const void* in, void* out, float2 f, int64_t base, int64_t left) {
   constexpr int kE = F32 ? 4 : 8;
   const bool wide = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
   const auto from = [&](int64_t i) {
@@ -216,7 +231,7 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, float coe
     float v[8];
     unpack<F32>(q, v);
 #pragma unroll
-    for (int j = 0; j < kE; ++j) v[j] *= coef;
+    for (int j = 0; j < kE; ++j) v[j] = v[j] * f.x * f.y;
     uint4 r;
     if constexpr (F32) r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     else r = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -233,41 +248,40 @@ __device__ __forceinline__ void chunk_scale(const void* in, void* out, float coe
       },
       [&](int64_t i) { store(i, __ldcs(from(i))); },
       [&](int64_t i) {
-        const float v = get<F32>(in, i) * coef;
+        const float v = get<F32>(in, i) * f.x * f.y;
         if constexpr (F32) static_cast<float*>(out)[i] = v;
         else static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
       });
 }
 
-// out = g coef.  The norm comes from the partial sums (part), or from the caller
+// out = g min(1, max_norm / norm).  The norm comes from the partial sums (part), or from the caller
 // (norm_in).
 template <int N, int VEC>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<N> tab, const double* part, int nparts,
                                                          const float* norm_in, float max_norm, float* norm_out) {
   __shared__ double s_sum[kThreads / 32];
-  __shared__ float s_coef;
+  __shared__ float2 s_factor;
   dependency_wait();
   // NaN makes everything NaN, infinity everything zero (and NaN what is infinite)
-  float coef;
+  float2 f;
   if (part != nullptr) {
     const double squares = squares_of(part, nparts, s_sum);
     if (threadIdx.x == 0) {
-      s_coef = factor_of(squares, max_norm);
+      s_factor = factor_of(squares, max_norm);
       if (blockIdx.x == 0 && norm_out != nullptr) *norm_out = norm_of(squares);
     }
     __syncthreads();
-    coef = s_coef;
+    f = s_factor;
   } else {
-    const float norm = *norm_in;
-    coef = norm <= max_norm ? 1.f : max_norm / norm;
+    f = factor_of(*norm_in, max_norm);
   }
   for (uint32_t k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
     const uint32_t c = tab.chunks - 1 - k;
     const Tensor& t = tab.t[tensor_of(tab, c)];
-    if (coef == 1.f && t.in == t.out) continue;
+    if (f.y == 1.f && t.in == t.out) continue;
     const int64_t base = static_cast<int64_t>(c - t.first) * chunk_elements(VEC, t.f32 != 0), left = t.numel - base;
-    if (t.f32 != 0) chunk_scale<VEC, true>(t.in, t.out, coef, base, left);
-    else chunk_scale<VEC, false>(t.in, t.out, coef, base, left);
+    if (t.f32 != 0) chunk_scale<VEC, true>(t.in, t.out, f, base, left);
+    else chunk_scale<VEC, false>(t.in, t.out, f, base, left);
   }
 }
 

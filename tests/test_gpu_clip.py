@@ -137,3 +137,20 @@ def test_same_output_twice_is_refused():
     assert abs(float(m.mxg_grad_norm([a, a])) - 80 ** 0.5) <= NORM * 9
     with pytest.raises(ValueError, match="contiguous"):
         m.mxg_grad_norm([torch.ones(4, 4, device="cuda").t()[1:]])
+
+
+@pytest.mark.parametrize("size,most", [(1e35, 1e-3), (1e35, 1e-12), (1e37, 1.0), (1e37, 1e-20), (1e37, 1e-28), (1e30, 1e-25),
+                                       (1e20, 1e-25)])
+def test_factors_below_normal_numbers(size, most):
+    """max_norm / norm below what fp32 holds in full (2^-126, or nothing left at 2^-150), whose products fp32 holds."""
+    m = require_gpu()
+    rng = np.random.default_rng(4)
+    a = torch.from_numpy((rng.uniform(-3.0, 3.0, 70001) * size).astype(np.float32))
+    b = a[:999].bfloat16()
+    ref = block.grad_norm([a.double().numpy(), b.double().numpy()])
+    most = np.float32(most)
+    norm, got = m.mxg_grad_clip([a.cuda(), b.cuda()], float(most), out=[torch.empty_like(t).cuda() for t in (a, b)])
+    _check(got, [a, b], ref, np.float64(most))
+    if ref < 3e38:                                        # by the norm that was taken before
+        got = m.mxg_grad_clip([a.cuda(), b.cuda()], float(most), out=[torch.empty_like(t).cuda() for t in (a, b)], norm=norm)[1]
+        _check(got, [a, b], ref, np.float64(most))
