@@ -740,6 +740,11 @@ def _tensor_refs(grads, out):
         used = [p for p, size in zip(to, sizes) if size]
         if len(set(used)) != len(used):
             raise ValueError("a tensor is listed twice as an output")
+    if to is not ptrs and not set(to).isdisjoint(ptrs):     # in the place of another gradient, which the pass still reads
+        at = {p: i for i, (p, size) in enumerate(zip(ptrs, sizes)) if size}
+        for i, (p, size) in enumerate(zip(to, sizes)):
+            if size and at.get(p, i) != i:
+                raise ValueError(f"out[{i}] is another gradient (grads[{at[p]}])")
     f32 = torch.float32
     words = itertools.chain.from_iterable(zip(ptrs, to, sizes, [d is f32 for d in types]))
     return array.array("q", words), n
@@ -766,7 +771,8 @@ def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
 
 def mxg_grad_clip(grads, max_norm: float, out=None, norm=None, norm_out=None, workspace=None, stream=None):
     """Gradients times min(1, max_norm / norm) -> (norm fp32 [1], outputs), into `out` (a list like grads) or, without
-    one, in place.  norm: fp32 [1] to clip by, e.g. joined over ranks; else the norm over grads is taken (norm_out)."""
+    one, in place.  norm: fp32 [1] to clip by, e.g. joined over ranks; else the norm over grads is taken (norm_out).
+    An output may be its own gradient and overlaps no other tensor."""
     if norm is not None and norm_out is not None:
         raise ValueError("norm_out is for the norm that is taken here")
     out = grads if out is None else out

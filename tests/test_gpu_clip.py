@@ -154,3 +154,19 @@ def test_factors_below_normal_numbers(size, most):
     if ref < 3e38:                                        # by the norm that was taken before
         got = m.mxg_grad_clip([a.cuda(), b.cuda()], float(most), out=[torch.empty_like(t).cuda() for t in (a, b)], norm=norm)[1]
         _check(got, [a, b], ref, np.float64(most))
+
+
+def test_an_output_is_no_other_gradient():
+    """The scaling pass would read a gradient that other blocks have overwritten."""
+    m = require_gpu()
+    a, b, c = torch.full((40,), 1.0, device="cuda"), torch.full((40,), 2.0, device="cuda"), torch.empty(40, device="cuda")
+    none = torch.empty(0, device="cuda")
+    for grads, out in (([a, b], [b, a]), ([a, b], [b, c]), ([a, b], [c, a]), ([a, a], [a, c])):
+        with pytest.raises(ValueError, match="gradient"):
+            m.mxg_grad_clip(grads, 1.0, out=out)
+        with pytest.raises(ValueError, match="gradient"):
+            m.mxg_grad_clip(grads, 1.0, out=out, norm=torch.ones(1, device="cuda"))
+    assert bool((a == 1.0).all()) and bool((b == 2.0).all())
+    norm, out = m.mxg_grad_clip([a, none, b], 1.0, out=[a, torch.empty(0, device="cuda"), c])     # some in place
+    _check([out[0], out[2]], [torch.full((40,), 1.0), torch.full((40,), 2.0)], 200 ** 0.5, 1.0)
+    assert abs(float(norm) - 200 ** 0.5) <= NORM * 200 ** 0.5
