@@ -709,7 +709,8 @@ def mxg_grad_norm_workspace_bytes(n) -> int:
 
 
 _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
-_get_device, _is_contiguous, _dtype = torch.Tensor.get_device, torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_dtype, _sizes = operator.attrgetter("dtype"), operator.attrgetter("shape")
 _REAL = {torch.float32, torch.bfloat16}
 
 
@@ -731,8 +732,8 @@ def _tensor_refs(grads, out):
             _refuse((f"grads[{i}]",), (t,), (t.dtype,), (None,))
     to = ptrs
     if out is not None and out is not grads:
-        if (set(map(_get_device, out)) != devices or list(map(_dtype, out)) != types or list(map(_numel, out)) != sizes
-                or not all(map(_is_contiguous, out))):
+        if (set(map(_get_device, out)) != devices or list(map(_dtype, out)) != types
+                or not all(map(operator.eq, map(_sizes, out), map(_sizes, grads))) or not all(map(_is_contiguous, out))):
             for i, (t, o) in enumerate(zip(grads, out)):
                 _refuse((f"out[{i}]",), (o,), (t.dtype,), (t.shape,))
         to = list(map(_data_ptr, out))

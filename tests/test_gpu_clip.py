@@ -170,3 +170,12 @@ def test_an_output_is_no_other_gradient():
     norm, out = m.mxg_grad_clip([a, none, b], 1.0, out=[a, torch.empty(0, device="cuda"), c])     # some in place
     _check([out[0], out[2]], [torch.full((40,), 1.0), torch.full((40,), 2.0)], 200 ** 0.5, 1.0)
     assert abs(float(norm) - 200 ** 0.5) <= NORM * 200 ** 0.5
+
+
+def test_outputs_are_like_the_gradients():
+    m = require_gpu()
+    a, b = torch.ones(6, 4, device="cuda"), torch.ones(6, 4, device="cuda")
+    for out in ([torch.empty(4, 6, device="cuda"), b], [torch.empty(24, device="cuda"), b], [b, torch.empty(4, 6, device="cuda")]):
+        with pytest.raises(ValueError, match="shape"):
+            m.mxg_grad_clip([a, b], 1.0, out=out)
+    assert bool((a == 1.0).all()) and bool((b == 1.0).all())
