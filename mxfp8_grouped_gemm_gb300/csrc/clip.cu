@@ -344,7 +344,7 @@ cudaError_t for_tables(const mxg_tensor* t, int n, F f) {
   }
 }
 
-int table_count(int n) { return (n + kTable - 1) / kTable; }
+int table_count(int n) { return (n - 1) / kTable + 1; }                // n > 0
 
 // The partial sums of all tensors; their number to *nparts.
 cudaError_t launch_square_sums(const mxg_tensor* t, int n, double* part, int* nparts, cudaStream_t s) {

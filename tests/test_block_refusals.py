@@ -150,3 +150,9 @@ def test_binding(m):
                        (lambda: m.mxg_grad_clip([z], 1.0, norm=p, norm_out=p), "norm_out")):
         with pytest.raises(ValueError, match=text):
             call()
+
+
+def test_clip_workspace_of_any_count(m):
+    """Eight bytes for each of 608 blocks, per 512 tensors: also where n + 511 passes 31 bits."""
+    for n in (1, 512, 513, 10 ** 6, 2 ** 31 - 512, 2 ** 31 - 511, 2 ** 31 - 1):
+        assert m.mxg_grad_norm_workspace_bytes(n) == -(-n // 512) * 608 * 8, n
