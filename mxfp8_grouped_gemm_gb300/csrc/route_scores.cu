@@ -22,6 +22,7 @@
 // instructions (416 a warp and token with groups, 293 by logits) at two thirds of
 // the issue slots, 24 warps an SM; the logits' stream would take 10 us.  Its
 // gradient 21 us, bound by HBM (118 MB: a chosen logit is a 64-byte access).
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -172,8 +173,16 @@ __device__ __forceinline__ void top_two(float& a, float& b, float a2, float b2) 
   a = fmaxf(a, a2);
 }
 
+// |v|, the largest finite number in place of infinity (whose distance to any other
+// number still passes every bound made of it).
+__device__ __forceinline__ float size_of(float v) { return fminf(fabsf(v), FLT_MAX); }
+// Half of what |a| + |b| is above |a + b|: for the two largest c of a group, a >= b
+// (0 without a second).
+__device__ __forceinline__ float apart_of(float a, float b) { return b != -INFINITY ? fmaxf(fminf(a, -b), 0.f) : 0.f; }
+
 struct Kept {
   float worst, next;    // scores of the last group kept and of the best one left out
+  float apart;          // largest apart_of, of sums
   uint32_t experts;     // of the lane's eight, those in groups that are kept
   bool close;           // groups of equal scores on both sides
 };
@@ -184,7 +193,7 @@ template <int LPT>
 __device__ __forceinline__ Kept kept_groups(const RouteParams& P, const float* row_c, float* scratch, int room, int lane) {
   const int gl = lane % LPT;
   const unsigned mask = group_mask<LPT>(lane);
-  Kept out{-INFINITY, -INFINITY, 0u, false};
+  Kept out{-INFINITY, -INFINITY, 0.f, 0u, false};
   __syncwarp();
   // entry x = gl + LPT r of the lanes' list: group x / spread, scanned with step `spread`
   float score[kVals];
@@ -204,9 +213,11 @@ __device__ __forceinline__ Kept kept_groups(const RouteParams& P, const float* r
         top_two(a, b, a2, b2);
       }
       score[r] = P.group_top == 2 && b != -INFINITY ? a + b : a;
+      if (P.group_top == 2) out.apart = fmaxf(out.apart, apart_of(a, b));
       first[r] = g < P.groups && sub == 0;
     }
   }
+  out.apart = lanes_max<LPT>(out.apart);
   float cur[kVals];
 #pragma unroll
   for (int r = 0; r < kVals; ++r) cur[r] = score[r];
@@ -249,14 +260,23 @@ enum { BY_LOGIT = 0, BY_SIGMOID = 1, BY_SOFTMAX = 2 };
 // Groups: all take part, each is a power of two of whole lanes, any size.
 enum { NO_GROUPS = 0, LANE_GROUPS = 1, ANY_GROUPS = 2 };
 
-// Absolute error of c in fp32, in units of 2^-24 (see below), for scores of at
-// most `most` (1, or the softmax's largest) and biases of at most `reach`.
+constexpr float kU = 1.f / 16777216.f;  // 2^-24
+
+// Absolute error of c in fp32 (see below) for scores of at most `most` (1, or the
+// softmax's largest) and a |c| of at most `at`.  Both c + error and c - error grow
+// with c, so what holds for a decision's two numbers holds for all behind them,
+// experts with a bias of -1e9 among them.
 template <int BY>
-__device__ __forceinline__ float error_of(float most, float reach) {
-  constexpr float kU = 1.f / 16777216.f;
+__device__ __forceinline__ float error_of(float most, float at) {
   if constexpr (BY == BY_LOGIT) return 0.f;
-  else if constexpr (BY == BY_SIGMOID) return kU * (4.1f + 1.f + reach);
-  else return kU * (38.f * most + reach);
+  else if constexpr (BY == BY_SIGMOID) return kU * (4.1f + at);
+  else return kU * (37.f * most + at);
+}
+// What an expert that may have to go ahead of one with c = `edge` lies below it at
+// most: both errors, and the rounding of the difference.
+template <int BY>
+__device__ __forceinline__ float slack_of(float most, float edge) {
+  return 2.1f * (error_of<BY>(most, size_of(edge)) + kU * size_of(edge)) + 1e-37f;
 }
 
 // The warp's largest key (expert 8 lane + i) among those that `in` names, ties
@@ -373,13 +393,12 @@ __device__ __noinline__ void rank_all(const RouteParams& P, const float* row, fl
 //   groups_close  the groups are to be decided as well: row_c has all of them
 template <int BY, int GROUPS, int N>
 __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, const float* row_c, float2* win,
-                                        uint8_t* list, float reach, float most, bool groups_close) {
+                                        uint8_t* list, float most, bool groups_close) {
   const int lane = threadIdx.x & 31;
   if (BY == BY_LOGIT || (GROUPS == ANY_GROUPS && groups_close)) return rank_all<BY != BY_LOGIT>(P, row, win);
   float c[kVals];
 #pragma unroll
   for (int i = 0; i < kVals; ++i) c[i] = lane * kVals < N ? row_c[lane * kVals + i] : NAN;
-  const float slack = 2.1f * error_of<BY>(most, reach) + 1e-37f;
   float top = 0.f;
   double sum = 1.0;
   if (BY == BY_SOFTMAX) {
@@ -403,12 +422,13 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
       const float a2 = __shfl_xor_sync(kAll, a, off), b2 = __shfl_xor_sync(kAll, b, off);
       top_two(a, b, a2, b2);
     }
-    from = (P.group_top == 2 ? b : a) - slack;
+    const float edge = P.group_top == 2 ? b : a;
+    from = edge - slack_of<BY>(most, edge);
   } else {
     kth = win[P.k - 1].x;
     __syncwarp();
     if (kth == -INFINITY) return rank_all<true>(P, row, win);
-    from = kth - slack;
+    from = kth - slack_of<BY>(most, kth);
   }
   int n, mine;
   uint64_t key;
@@ -477,7 +497,7 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
       kth = lanes_max<32>(m);
     }
     if (kth == -INFINITY) return rank_all<true>(P, row, win);
-    from = kth - slack;
+    from = kth - slack_of<BY>(most, kth);
   }
   int ahead = 0;
 #pragma unroll 1
@@ -504,14 +524,15 @@ __device__ __noinline__ void rank_close(const RouteParams& P, const float* row, 
 // |z| <= 88, 138.  A softmax: e^d (d <= 0) is off by (2.5 |d| + 2.83) e^d <= 3.8,
 // the sum by 30 of itself (the mean of |d| over a softmax of 256 is below 5.6; 13
 // additions), reciprocal and product 3: 37 of the largest score; relative to a
-// score, with |d| <= 88, 256.  c = s + bias adds a rounding of c.
+// score, with |d| <= 88, 256.  c = s + bias adds a rounding of c, 2^-24 |c|: of the
+// numbers compared, not of the largest bias (by which one bias of -1e9 sent every
+// token to 64 bits, 65536 x 256 took 1050 us).
 template <int LPT, int BY, int GROUPS>
 __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_constant__ RouteParams P) {
   constexpr bool SCORED = BY != BY_LOGIT;
   constexpr int TPW = 32 / LPT;                                 // tokens at a time
   constexpr int NB = TPW > 4 ? TPW : 4;                         // tokens of the warp
   constexpr int MOST = LPT * kVals < 32 ? LPT * kVals : 32;     // choices of a token
-  constexpr float kU = 1.f / 16777216.f;                        // 2^-24
   constexpr float kTiny = 1e-37f;                               // below that scores have no relative error
   struct __align__(16) Shared {
     float c[NB][LPT * kVals];           // what ranks a token's experts
@@ -530,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
 
   __shared__ __align__(16) float s_bias[SCORED ? LPT * kVals : 4];
   float reach = 0.f;                                            // largest |bias|
+  float apart = 0.f;                                            // at least apart_of every group of whole lanes
   if constexpr (SCORED) {
     for (int e = threadIdx.x; e < LPT * kVals; e += kThreads) {
       float b = P.bias != nullptr && e < P.E ? P.bias[e] : 0.f;
@@ -542,6 +564,20 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
       if (b < INFINITY) reach = fmaxf(reach, b);
     }
     reach = lanes_max<LPT>(reach);
+    if (GROUPS == LANE_GROUPS && P.group_top == 2) {
+      // s lies in [0, 1], and c between the least bias and 1 + the largest: found for each token, it took 4 us of 43
+      float lo = 0.f, hi = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) {
+        const float b = s_bias[gl * kVals + i];
+        if (fabsf(b) < INFINITY) lo = fminf(lo, b), hi = fmaxf(hi, b);
+      }
+      for (int off = 1; off < P.lanes_of_group; off <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(kAll, lo, off));
+        hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, off));
+      }
+      apart = lanes_max<LPT>(fmaxf(fminf(1.f + hi, -lo), 0.f));
+    }
   }
 
   // the warp's share of the tokens, NB at a time
@@ -655,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
         const Kept kept = kept_groups<LPT>(P, row_c, reinterpret_cast<float*>(win), 2 * (MOST + 2), lane);
         worst = kept.worst;
         next = kept.next;
+        apart = kept.apart;
         close = kept.close;
         out = ~kept.experts;
 #pragma unroll
@@ -663,9 +700,10 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
       }
       if (worst == -INFINITY) close = true;                     // groups without an expert left
       if constexpr (SCORED) {
-        // two scores and the rounding of their sum
-        const float most = BY == BY_SOFTMAX ? inv : 1.f, err = 2.f * (error_of<BY>(most, reach) + kU * (most + reach));
-        if (!(worst - next > 2.f * err)) close = true;
+        // a sum's error: two numbers' and the rounding of the sum; |a| + |b| is at most |a + b| + 2 apart
+        const float at = fmaxf(size_of(worst), size_of(next));
+        const float err = 2.f * (error_of<BY>(BY == BY_SOFTMAX ? inv : 1.f, at) + kU * apart);
+        if (!(fminf(worst, FLT_MAX) - next > 2.01f * err)) close = true;
       }
       // experts that take no part are found neither by their values nor by rank_close
       if (SCORED && GROUPS == LANE_GROUPS && !close && out != 0) {
@@ -715,12 +753,11 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
     bool close = groups_close || v == -INFINITY;                // or fewer than k experts are left
     int skip = 0;
     if constexpr (SCORED) {
-      // an absolute bound on the error of a score, and one relative to it (its size is at most |c| + reach)
+      // an absolute bound on the error of a score, and one relative to it (which is at most |c| + reach)
       const float abs_err = BY == BY_SOFTMAX ? 37.f * kU * inv : 4.1f * kU;
       const float rel_err = BY == BY_SOFTMAX ? 256.f * kU : 138.f * kU;
-      const float w = win[jj + 1].x;
-      const float size = fmaxf(fabsf(v), w == -INFINITY ? 0.f : fabsf(w)) + reach;
-      if (!(v - w > 2.f * (fminf(abs_err, rel_err * size) + kU * size) + kTiny)) close = true;
+      const float w = win[jj + 1].x, at = fmaxf(size_of(v), size_of(w));
+      if (!(v - w > 2.01f * (fminf(abs_err, rel_err * (at + reach)) + kU * at) + kTiny)) close = true;
     } else {
       // equal logits of one lane, chosen one after another
       while (skip < jj && win[jj - 1 - skip].x == v && __float_as_int(win[jj - 1 - skip].y) == o) ++skip;
@@ -763,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
     float2* win = S.win[n];
     __syncwarp();
     const float2 stat = win[P.k + 1];
-    rank_close<BY, GROUPS, LPT * kVals>(P, row, S.c[n], win, reinterpret_cast<uint8_t*>(S.h), reach, stat.y,
+    rank_close<BY, GROUPS, LPT * kVals>(P, row, S.c[n], win, reinterpret_cast<uint8_t*>(S.h), stat.y,
                                         win[P.k].y != 0.f);
     const int sel = __float_as_int(win[lane < P.k ? lane : 0].y);
     const float w = weight_of(P, lane < P.k ? row[sel] : -INFINITY, 32, stat.x, stat.y);

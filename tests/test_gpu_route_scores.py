@@ -295,3 +295,60 @@ def test_route_rows_behind_the_last_stay(E):
     m.mxg_route_scores_fwd(z, k, score="sigmoid", bias=torch.zeros(E, device="cuda"), ids=ids[:T], probs=probs[:T])
     m.mxg_route_scores_bwd(z, ids[:T], probs[:T], probs[:T], st, score="sigmoid", dlogits=d[:T])
     assert bool((ids[T:] == 77).all()) and bool((probs[T:] == 77).all()) and bool((d[T:] == 77).all())
+
+
+MASKS = [(-10.0, 1), (-1e4, 1), (-1e9, 1), (-1e9, 40), (1e4, 1), (1e4, 3), (-float(np.finfo(np.float32).max), 5)]
+
+
+@pytest.mark.parametrize("E,groups,top_groups,group_top,k", [
+    (256, 1, 1, 1, 8), (256, 8, 4, 2, 8), (256, 8, 4, 1, 8), (256, 128, 60, 2, 8), (64, 1, 1, 1, 8), (64, 8, 3, 2, 4),
+    (64, 16, 6, 2, 8), (90, 9, 4, 2, 8), (90, 45, 20, 2, 5)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_fwd_large_finite_biases(kind, E, groups, top_groups, group_top, k):
+    """A finite bias that keeps experts out or forces them in, beside small ones; in a group with one of the other sign
+    the sum of the two is small, but not its error."""
+    m = require_gpu()
+    rng = np.random.default_rng(E + groups)
+    z = (rng.standard_normal((700, E)) * 1.5).astype(np.float32)
+    opts = dict(score=kind, groups=groups, top_groups=top_groups, group_top=group_top)
+    for value, experts in MASKS:
+        b = (rng.standard_normal(E) * 0.05).astype(np.float32)
+        at = rng.choice(E, min(experts, E // 4), replace=False)
+        b[at] = value
+        _check(m, z, b, k, opts)
+        if groups > 1:
+            b[:] = (rng.standard_normal(E) * 0.05).astype(np.float32)
+            size = E // groups
+            for g in rng.choice(groups, max(groups // 2, 1), replace=False):           # |value| and -|value| in a group
+                b[g * size:(g + 1) * size] = -abs(value)
+                b[g * size] = abs(value)
+            _check(m, z, b, k, opts)
+
+
+def _time(call, n=20):
+    """Shortest of n calls in us, on the GPU's clock."""
+    best = float("inf")
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 4), (16, 8)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_fwd_a_masked_expert_costs_nothing(kind, groups, top_groups):
+    """Experts far from every decision do not send the others' to 64 bits: the same call with one bias of -1e9 (or +1e4,
+    or +inf) takes at most half as long again.  In 64 bits it took 20 times as long."""
+    m = require_gpu()
+    z, b, _ = _inputs(65536, 256, 8, 0.05, std=1.5)
+    z, b = _dev(z), _dev(b)
+    opts = dict(score=kind, groups=groups, top_groups=top_groups)
+    plain = _time(lambda: m.mxg_route_scores_fwd(z, 8, bias=b, **opts))
+    for value in (-1e3, -1e9, -float(np.finfo(np.float32).max), 1e4, float("inf")):
+        b2 = b.clone()
+        b2[100] = value
+        assert _time(lambda: m.mxg_route_scores_fwd(z, 8, bias=b2, **opts)) <= 1.5 * plain, value
