@@ -1,6 +1,7 @@
 """Host-side checks of the C ABI (no GPU needed): the library builds and loads,
 exports every function include/mxg.h declares, and rejects bad arguments on
 the host before anything is launched."""
+import array
 import ctypes
 import os
 import re
@@ -301,3 +302,38 @@ def test_saved_gu_tile_layout_reads_back_in_row_order():
             flat[off] = want[row, col]
     assert bool((flat >= 0).all())
     assert torch.equal(gu_rows_from_tiles(flat, m_cap, I), want)
+
+
+def test_block_structures_match_header(tmp_path):
+    """The structures of the block operators: the ctypes mirrors, and the formats that the binding's calls pack, have
+    every field where the C compiler has it."""
+    import mxfp8_grouped_gemm_gb300 as m
+    from mxfp8_grouped_gemm_gb300 import _lib
+    packed = {"mxg_route_scores_fwd_args": (m.RouteScoresFwdArgs, _lib._PACK_ROUTE_FWD),
+              "mxg_route_scores_bwd_args": (m.RouteScoresBwdArgs, _lib._PACK_ROUTE_BWD),
+              "mxg_rms_norm_fwd_args": (m.RmsNormFwdArgs, _lib._PACK_NORM_FWD),
+              "mxg_rms_norm_bwd_args": (m.RmsNormBwdArgs, _lib._PACK_NORM_BWD),
+              "mxg_tensor": (m.TensorRef, None)}
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "mxg.h"', "int main(void) {"]
+    for cname, (cls, _) in packed.items():
+        lines.append(f'printf("{cname} size %zu\\n", sizeof({cname}));')
+        for f, _ in cls._fields_:
+            f = "in" if f == "ptr" else f
+            lines.append(f'printf("{cname} {f} %zu\\n", offsetof({cname}, {f}));')
+    (tmp_path / "layout.c").write_text("\n".join(lines + ["return 0; }"]))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(tmp_path / "layout.c"), "-o", str(exe)], check=True)
+    rows = [line.split() for line in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines()]
+    table = {(s, f): int(v) for s, f, v in rows}
+    for cname, (cls, form) in packed.items():
+        assert table[(cname, "size")] == ctypes.sizeof(cls), cname
+        for f, _ in cls._fields_:
+            assert table[(cname, "in" if f == "ptr" else f)] == getattr(cls, f).offset, (cname, f)
+        if form is not None:
+            assert form.size == ctypes.sizeof(cls), cname
+            values = [float(i) + 1.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(cls._fields_)]
+            args = cls.from_buffer_copy(form.pack(*values))
+            assert [getattr(args, f) for f, _ in cls._fields_] == values, cname
+    # a list of gradients is packed as four 64-bit words a tensor
+    ref = m.TensorRef.from_buffer_copy(array.array("q", [1, 2, 3, 1]).tobytes())
+    assert (ref.ptr, ref.out, ref.numel, ref.f32, ref.reserved) == (1, 2, 3, 1, 0)
