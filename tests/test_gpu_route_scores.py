@@ -352,3 +352,33 @@ def test_route_fwd_a_masked_expert_costs_nothing(kind, groups, top_groups):
         b2 = b.clone()
         b2[100] = value
         assert _time(lambda: m.mxg_route_scores_fwd(z, 8, bias=b2, **opts)) <= 1.5 * plain, value
+
+
+# More tokens than the warps of a full grid take at once (456 blocks of 8 warps, 4 tokens each, 16 at 16 experts and 32 at
+# 8), so that every warp takes several sets and one that is not whole.
+SETS = [   # T, E, k, kind, bias, groups, top_groups, group_top, renormalize, scale
+    (40001, 256, 8, "sigmoid", 0.05, 8, 4, 2, True, 2.5),
+    (40001, 256, 8, "softmax", 0.002, 1, 1, 1, True, 1.0),
+    (37003, 240, 6, "sigmoid", 0.05, 12, 5, 2, False, 1.0),     # groups across lanes
+    (40001, 64, 8, "sigmoid", 0.05, 8, 4, 1, True, 1.0),
+    (44449, 64, 32, "softmax", 0.01, 1, 1, 1, False, 1.0),
+    (40001, 60, 4, "softmax", None, 10, 3, 2, True, 1.0),       # groups across lanes
+    (50001, 64, 8, "softmax", None, 1, 1, 1, True, 1.0),        # by logits
+    (150001, 16, 4, "sigmoid", 0.05, 2, 1, 2, True, 1.0),
+    (300007, 8, 2, "sigmoid", 0.1, 4, 2, 2, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", SETS, ids=[f"{c[0]}x{c[1]}{c[3]}g{c[5]}" for c in SETS])
+def test_route_fwd_several_sets_to_a_warp(case):
+    """Tokens that fp32 cannot decide stand in the first, the middle and the last sets, alone and side by side."""
+    m = require_gpu()
+    T, E, k, kind, bias = case[:5]
+    z, b, rng = _inputs(T, E, k, bias, seed=5, std=1.5)
+    at = np.unique(np.concatenate([np.arange(3), np.arange(T - 3, T), np.arange(T // 2, T // 2 + 9),
+                                   rng.choice(T, T // 50, replace=False)]))
+    near = (0.25 + rng.integers(0, 4, (at.size, E)) * np.float32(2.0 ** -24)).astype(np.float32)
+    near[::5] = np.where(rng.random((near[::5].shape)) < 0.7, -np.inf, z[at[::5]])      # masked ones among them
+    near[1::5, k // 2:] = z[at[1::5], k // 2:]                                           # a few that are close
+    z[at] = near
+    _check(m, z, b, k, _options(case))
