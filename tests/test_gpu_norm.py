@@ -212,3 +212,77 @@ def test_norm_gradient_is_the_difference():
         e[j] = h
         diff = (loss(R, W + e) - loss(R, W - e)) / (2 * h)
         assert abs(diff - float(dw[j])) <= 1e-5 * max(1.0, abs(diff))
+
+
+# Widths of every form of the backward (lanes and chunks of a row), with as many rows as make each slot of each CTA's ring
+# carry three rows, and the last rows fewer than a CTA takes: rows at a time x CTAs x (2 slots + 1) + a few.
+RING = [(136203, 56), (68101, 128), (34051, 248), (21895, 504), (10949, 1000), (5473, 2040), (1369, 8192), (1065, 12280),
+        (761, 16384)]
+
+
+def _ring_inputs(T, H, f32):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dt = torch.float32 if f32 else torch.bfloat16
+    r, dres = (torch.randn((T, H), generator=g, device="cuda") * s for s in (2.0, 0.01))
+    r[T // 2] = 0.0
+    dy = (torch.randn((T, H), generator=g, device="cuda") * 0.01).bfloat16()
+    w = 1.0 + 0.2 * torch.randn(H, generator=g, device="cuda")
+    r = r.to(dt)
+    rstd = (1.0 / (r.double().square().mean(dim=1) + EPS).sqrt()).float()
+    return dy, r, w if f32 else w.bfloat16(), rstd, dres.to(dt)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,H", RING)
+def test_norm_bwd_many_rows_to_a_slot(T, H, f32):
+    m = require_gpu()
+    dy, r, w, rstd, dres = _ring_inputs(T, H, f32)
+    for d_in in (dres, None):
+        dx, dr, dw = m.mxg_rms_norm_bwd(dy, r, w, rstd, dresidual=d_in)
+        k = rstd.double()[:, None]
+        xh, g = r.double() * k, dy.double() * w.double()
+        mean = (g * xh).mean(dim=1, keepdim=True)
+        d = k * (g - xh * mean)
+        if d_in is not None:
+            d = d + d_in.double()
+        # the roundings of test_norm_bwd
+        err = k * (3 * U * g.abs() + xh.abs() * (g * xh).abs().mean(dim=1, keepdim=True) * (3 + 32 + 10 + 2 + 4) * U)
+        err += U * d.abs()
+        assert bool(((dx.double() - d).abs() <= err + B * d.abs() + 1e-38).all())
+        if f32:
+            assert bool(((dr.double() - d).abs() <= err + 1e-38).all())
+        # dweight: a lane group's rows in a chain, up to 16 groups, the CTAs' partials by 32 threads, and those in 5 halvings
+        ctas = m.mxg_rms_norm_bwd_workspace_bytes(T, H) // (4 * H)
+        rows = 16 if H <= 64 else 8 if H <= 128 else 4 if H <= 1024 else 1
+        chain = -(-T // (ctas * rows)) + rows + -(-ctas // 32) + 5 + 3
+        terms = dy.double() * xh
+        assert bool(((dw.double() - terms.sum(dim=0)).abs() <= chain * U * terms.abs().sum(dim=0) + 1e-38).all())
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,H", RING)
+def test_norm_bwd_in_place_with_rows_on_their_way(T, H, f32):
+    """Outputs over dy or dresidual while later rows of both are being copied."""
+    m = require_gpu()
+    dy, r, w, rstd, dres = _ring_inputs(T, H, f32)
+    dx, dr, dw = m.mxg_rms_norm_bwd(dy, r, w, rstd, dresidual=dres)
+    for into in ("dy", "dresidual"):
+        a, b = dy.clone(), dres.clone()
+        if f32:
+            got = m.mxg_rms_norm_bwd(a, r, w, rstd, dresidual=b, dx=a if into == "dy" else None, dresidual_out=b)
+            assert torch.equal(got[1], dr)
+        else:
+            got = m.mxg_rms_norm_bwd(a, r, w, rstd, dresidual=b, dx=a if into == "dy" else b)
+        assert torch.equal(got[0], dx) and torch.equal(got[2], dw)
+
+
+@pytest.mark.parametrize("T,H,residual", [(128, 128, "bf16"), (256, 1024, "f32"), (128, 16384, None)])
+def test_norm_codes_without_y_in_the_mma_layout(T, H, residual):
+    m = require_gpu()
+    x, res, w, _ = _inputs(T, H, residual, False)
+    out = m.mxg_rms_norm_fwd(x.cuda(), w.cuda(), EPS, residual=_cuda(res))
+    only = m.mxg_rms_norm_fwd(x.cuda(), w.cuda(), EPS, residual=_cuda(res), codes=True, bf16=False,
+                              layout=m.MXG_LAYOUT_MMA)
+    ref = m.mxg_mxfp8_quantize(out["y"], layout=m.MXG_LAYOUT_MMA)
+    assert "y" not in only
+    assert torch.equal(only["q"], ref["q_row"]) and torch.equal(only["s"].view(-1), ref["s_row"])
