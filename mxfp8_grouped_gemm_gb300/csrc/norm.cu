@@ -98,8 +98,9 @@ __device__ __forceinline__ void load_weight(const void* w, int w32, int col, flo
   else load8(static_cast<const uint16_t*>(w) + col, v);
 }
 
-// Ten CTAs an SM where a lane holds 32 values (48 registers; with 64 and eight CTAs
-// 65536 x 1024 took 97.6 us instead of 94.3, 5003 x 1000 in fp32 14.4 instead of 13.3).
+// Ten CTAs an SM where a lane holds 32 values (48 registers, and 32 to 108 bytes of
+// spills; with 64 registers and eight CTAs, which spill nothing, 65536 x 1024 took
+// 97.6 us instead of 94.3, 5003 x 1000 in fp32 14.4 instead of 13.3).
 template <int LPR, int NCH, int RES>
 __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads, LPR != 0 && NCH == 4 ? 10 : 0) norm_fwd_kernel(const NormFwdParams P) {
   __shared__ float s_part[2][32];
@@ -451,9 +452,11 @@ int bwd_chunks(int H, bool f32) { return !f32 && H > 8192 && H <= 12288 ? 3 : wi
 int bwd_threads(int H, bool f32) { return H <= 1024 ? kRowThreads : wide_threads(H, bwd_chunks(H, f32)); }
 
 // CTAs of the backward: what fits on the SMs at once (their partial sums of
-// dweight are read again), at most one for each set of rows.  Up to kAlone sets
-// that one SM reads in about a microsecond are left to one CTA, which needs no
-// second launch.
+// dweight are read again), at most one for each set of rows.  Of the fp32 forms up
+// to 256 values (80 registers) six of the eight fit, and the others start as these
+// end: no slower than a grid of six (262144 x 128 91.7 us, 92.3 with six).  Up to
+// kAlone sets that one SM reads in about a microsecond are left to one CTA, which
+// needs no second launch.
 constexpr int kAlone = 8, kAloneElements = 32768;
 int bwd_ctas(int H) { return H <= 256 ? 8 : H <= 512 ? 4 : H <= 1024 ? 2 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1; }
 int bwd_blocks(int T, int H) {

@@ -156,7 +156,8 @@ __device__ __forceinline__ void take(float& head, uint32_t& list, uint32_t end, 
       : "memory");
 }
 
-// Descending.
+// Descending, by a network of 19 exchanges, the fewest for eight (Knuth, The Art of
+// Computer Programming 3, section 5.3.4, gives the count).
 __device__ __forceinline__ void sort8(float (&h)[kVals]) {
   constexpr int net[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
                               {4, 5}, {6, 7}, {2, 4}, {3, 5}, {1, 4}, {3, 6}, {1, 2}, {3, 4}, {5, 6}};
@@ -382,10 +383,12 @@ __device__ __noinline__ void rank_all(const RouteParams& P, const float* row, fl
 
 // One token by the whole warp, its decisions in fp64: the j-th choice to
 // win[j].y.  fp32 scores and their error bound name the few experts that a
-// decision can hang on (a group's largest, and the k largest, with what lies
-// within the error of them); these are evaluated in fp64, one to a lane.  Where
-// they are more than lanes, or experts that are off have to fill the route, all
-// are ranked.  (All in fp64 for every such token cost 14 us of the 57 that
+// decision can hang on (each group's group_top largest, and the k largest, with
+// what lies within the error of them); these are evaluated in fp64, one to a lane.
+// Where they are more than lanes, or experts that are off have to fill the route,
+// all are ranked: always where groups are undecided and more than 32 / group_top
+// of them have group_top experts on (65536 x 256 with 32 groups takes 65 us for
+// that, 41 with 16).  (All in fp64 for every such token cost 14 us of the 57 that
 // 65536 x 256 took: a few dozen tokens, but the last to finish; they are 4 us now,
 // 6 with the loops over candidates not unrolled and a division in them.)
 //   row_c   fp32 c; -inf: off, NaN: its group does not take part
