@@ -96,12 +96,15 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t pair_bits(uint32_t m) {
+  m &= 0x7fff7fffu;
+  return max(m << 16, m & 0xffff0000u);
+}
 __device__ __forceinline__ uint32_t pair_max_bits(const uint32_t* w, int n) {
   uint32_t m = w[0];
 #pragma unroll
   for (int i = 1; i < n; ++i) m = absmax_bf16x2(m, w[i]);
-  m &= 0x7fff7fffu;
-  return max(m << 16, m & 0xffff0000u);
+  return pair_bits(m);
 }
 
 // Two fp32 -> two E4M3 codes (round to nearest even, saturate to +-448);

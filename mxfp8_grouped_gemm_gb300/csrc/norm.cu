@@ -156,12 +156,12 @@ __global__ void __launch_bounds__(LPR != 0 ? kRowThreads : kMaxThreads, LPR != 0
     const uint4 y = pack8(r[i]);
     if (in && P.y != nullptr) *reinterpret_cast<uint4*>(P.y + base + 8 * c) = y;
     if (P.q != nullptr) {
-      // the codes of the bf16 values, so that they are mxg_mxfp8_quantize's on y
-      const uint32_t words[4] = {y.x, y.y, y.z, y.w};
-      uint32_t amax = pair_max_bits(words, 4);
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const uint32_t sb = mx_scale_byte(amax);
+      // the codes of the bf16 values, so that they are mxg_mxfp8_quantize's on y; pairs stay pairs between the
+      // lanes, so that a NaN gives way to the block's numbers as it does there
+      uint32_t pair = absmax_bf16x2(absmax_bf16x2(y.x, y.y), absmax_bf16x2(y.z, y.w));
+      pair = absmax_bf16x2(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
+      pair = absmax_bf16x2(pair, __shfl_xor_sync(0xffffffffu, pair, 2));
+      const uint32_t sb = mx_scale_byte(pair_bits(pair));
       const float inv = mx_inv_scale(sb);
       float v[8];
       unpack8(y, v);

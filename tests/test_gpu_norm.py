@@ -286,3 +286,23 @@ def test_norm_codes_without_y_in_the_mma_layout(T, H, residual):
     ref = m.mxg_mxfp8_quantize(out["y"], layout=m.MXG_LAYOUT_MMA)
     assert "y" not in only
     assert torch.equal(only["q"], ref["q_row"]) and torch.equal(only["s"].view(-1), ref["s_row"])
+
+
+@pytest.mark.parametrize("layout", ["canonical", "mma"])
+def test_norm_codes_beside_nan(layout):
+    """Blocks of y that are NaN in part (weights that are NaN, a row with infinities, whose rstd is zero): the quantiser
+    takes the scale from the rest of the block, and so do the codes."""
+    m = require_gpu()
+    T, H = 128, 256
+    x, res, w, _ = _inputs(T, H, "bf16", True)
+    w[8:16] = float("nan")
+    w[33:64:2] = float("nan")
+    w[70] = float("nan")
+    w[96:128] = float("nan")
+    x[3, 160:168] = float("inf")
+    x[4, 192:200:2] = float("-inf")
+    layout = m.MXG_LAYOUT_MMA if layout == "mma" else m.MXG_LAYOUT_CANONICAL
+    for weight in (w, torch.nan_to_num(w, nan=float("inf")), torch.ones(H)):
+        out = m.mxg_rms_norm_fwd(x.cuda(), weight.cuda(), EPS, residual=res.cuda(), codes=True, layout=layout)
+        ref = m.mxg_mxfp8_quantize(out["y"], layout=layout)
+        assert torch.equal(out["q"], ref["q_row"]) and torch.equal(out["s"].view(-1), ref["s_row"].view(-1))
