@@ -709,8 +709,7 @@ def mxg_grad_norm_workspace_bytes(n) -> int:
 
 
 _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
-_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
-_dtype, _sizes = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_get_device, _is_contiguous, _dtype = torch.Tensor.get_device, torch.Tensor.is_contiguous, operator.attrgetter("dtype")
 _REAL = {torch.float32, torch.bfloat16}
 
 
@@ -732,16 +731,18 @@ def _tensor_refs(grads, out):
             _refuse((f"grads[{i}]",), (t,), (t.dtype,), (None,))
     to = ptrs
     if out is not None and out is not grads:
-        if (set(map(_get_device, out)) != devices or list(map(_dtype, out)) != types
-                or not all(map(operator.eq, map(_sizes, out), map(_sizes, grads))) or not all(map(_is_contiguous, out))):
-            for i, (t, o) in enumerate(zip(grads, out)):
-                _refuse((f"out[{i}]",), (o,), (t.dtype,), (t.shape,))
+        if (set(map(_get_device, out)) != devices or list(map(_dtype, out)) != types or list(map(_numel, out)) != sizes
+                or not all(map(_is_contiguous, out))):
+            for i, (t, o, size) in enumerate(zip(grads, out, sizes)):
+                if o.numel() != size:
+                    raise ValueError(f"out[{i}] must have {size} elements, got {list(o.shape)}")
+                _refuse((f"out[{i}]",), (o,), (t.dtype,), (None,))
         to = list(map(_data_ptr, out))
-    if out is not None and len(set(to)) != n:           # the same address twice: tensors without elements may share one
-        used = [p for p, size in zip(to, sizes) if size]
+    if out is not None and len({*ptrs, *to}) != (n if to is ptrs else 2 * n):     # an address that stands twice
+        used = [p for p, size in zip(to, sizes) if size]                          # (without elements it may)
         if len(set(used)) != len(used):
             raise ValueError("a tensor is listed twice as an output")
-    if to is not ptrs and not set(to).isdisjoint(ptrs):     # in the place of another gradient, which the pass still reads
+        # an output in the place of another gradient, which the pass still reads
         at = {p: i for i, (p, size) in enumerate(zip(ptrs, sizes)) if size}
         for i, (p, size) in enumerate(zip(to, sizes)):
             if size and at.get(p, i) != i:
@@ -773,7 +774,8 @@ def mxg_grad_norm(grads, norm=None, workspace=None, stream=None):
 def mxg_grad_clip(grads, max_norm: float, out=None, norm=None, norm_out=None, workspace=None, stream=None):
     """Gradients times min(1, max_norm / norm) -> (norm fp32 [1], outputs), into `out` (a list like grads) or, without
     one, in place.  norm: fp32 [1] to clip by, e.g. joined over ranks; else the norm over grads is taken (norm_out).
-    An output may be its own gradient and overlaps no other tensor."""
+    An output has its gradient's type and number of elements, in the order of the memory (a flat view will do); it may be
+    that gradient and overlaps no other tensor."""
     if norm is not None and norm_out is not None:
         raise ValueError("norm_out is for the norm that is taken here")
     out = grads if out is None else out

@@ -172,10 +172,16 @@ def test_an_output_is_no_other_gradient():
     assert abs(float(norm) - 200 ** 0.5) <= NORM * 200 ** 0.5
 
 
-def test_outputs_are_like_the_gradients():
+def test_outputs_of_another_shape():
+    """An output takes its gradient's elements in the order of the memory: views of one flat buffer, as buckets are."""
     m = require_gpu()
-    a, b = torch.ones(6, 4, device="cuda"), torch.ones(6, 4, device="cuda")
-    for out in ([torch.empty(4, 6, device="cuda"), b], [torch.empty(24, device="cuda"), b], [b, torch.empty(4, 6, device="cuda")]):
-        with pytest.raises(ValueError, match="shape"):
-            m.mxg_grad_clip([a, b], 1.0, out=out)
-    assert bool((a == 1.0).all()) and bool((b == 1.0).all())
+    grads = [g.cuda() for g in _grads([(6, 4), (5,), (3, 2, 7)])]
+    ref = m.mxg_grad_clip(grads, 0.01, out=[torch.empty_like(g) for g in grads])[1]
+    flat = {t: torch.full((71,), 7.0, dtype=t, device="cuda") for t in (torch.float32, torch.bfloat16)}
+    out = [flat[grads[0].dtype][:24], flat[grads[1].dtype][:5], flat[grads[2].dtype][24:66]]
+    got = m.mxg_grad_clip(grads, 0.01, out=out)[1]
+    assert all(torch.equal(a, b.view(-1)) for a, b in zip(got, ref))
+    assert bool((flat[grads[0].dtype][66:] == 7.0).all())
+    for bad in (torch.empty(23, dtype=grads[0].dtype, device="cuda"), torch.empty(0, dtype=grads[0].dtype, device="cuda")):
+        with pytest.raises(ValueError, match="24 elements"):
+            m.mxg_grad_clip(grads, 0.01, out=[bad, *out[1:]])
