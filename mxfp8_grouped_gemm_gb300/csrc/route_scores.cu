@@ -19,7 +19,7 @@
 //
 // Measured, launch included: 65536 x 256, top-8, sigmoid, bias, 4 of 8 groups 40
 // us, without groups 33, by logits 29; 8191 x 64 softmax 4.3 us.  Bound by
-// instructions (416 a warp and token with groups, 293 by logits) at two thirds of
+// instructions (424 a warp and token with groups, 293 by logits) at two thirds of
 // the issue slots, 24 warps an SM; the logits' stream would take 10 us.  Its
 // gradient 21 us, bound by HBM (118 MB: a chosen logit is a 64-byte access).
 #include <cfloat>
@@ -703,10 +703,11 @@ __global__ void __launch_bounds__(kThreads, 3) route_scores_kernel(const __grid_
       }
       if (worst == -INFINITY) close = true;                     // groups without an expert left
       if constexpr (SCORED) {
-        // a sum's error: two numbers' and the rounding of the sum; |a| + |b| is at most |a + b| + 2 apart
+        // a sum's error: two numbers' and the rounding of the sum; |a| + |b| is at most |a + b| + 2 apart.  Both sums'
+        // are 4 times that of one number with a |c| of at + apart
         const float at = fmaxf(size_of(worst), size_of(next));
-        const float err = 2.f * (error_of<BY>(BY == BY_SOFTMAX ? inv : 1.f, at) + kU * apart);
-        if (!(fminf(worst, FLT_MAX) - next > 2.01f * err)) close = true;
+        const float scores = 4.02f * (error_of<BY>(BY == BY_SOFTMAX ? inv : 1.f, 0.f) + kU * apart);
+        if (!(fminf(worst, FLT_MAX) - next > fmaf(4.02f * kU, at, scores))) close = true;
       }
       // experts that take no part are found neither by their values nor by rank_close
       if (SCORED && GROUPS == LANE_GROUPS && !close && out != 0) {
