@@ -283,7 +283,8 @@ int mxg_muon_update(const mxg_muon_args* args, void* stream);
  * with z = -inf (or NaN, or a bias of -inf) is off: it ranks behind all others,
  * by id, and adds nothing to its group's score (a group with none left ranks
  * last); where fewer than k are left, experts that are off fill the route, with
- * weight 0 where z = -inf.  In a softmax a NaN or +inf makes the weights NaN
+ * weight 0 where z = -inf.  A finite bias, however large, leaves an expert on (its
+ * group's score has it).  In a softmax a NaN or +inf makes the weights NaN
  * (renormalised ones where it is among the chosen), and all experts off where
  * scores are ranked.
  *   logits      fp32 [T][E] (device);  bias nullable fp32 [E]
@@ -340,7 +341,8 @@ int mxg_route_scores_bwd(const mxg_route_scores_bwd_args* args, void* stream);
  *   rstd = 1 / sqrt(mean(r^2) + eps);  y = r rstd weight  (bf16, rounded once,
  *   from the r that is not rounded)
  *   q, s = y in MXFP8: what mxg_mxfp8_quantize writes for it, bit for bit
- * All arithmetic is fp32; a row whose sum of squares passes fp32 gives rstd 0.
+ * All arithmetic is fp32; a row whose sum of squares passes fp32 gives rstd 0,
+ * and with eps 0 one whose sum vanishes gives infinity (a row of zeros NaN).
  * y may be x and residual_out may be residual; other buffers do not overlap.
  * Pointers are 32-byte aligned.
  * Requires H % 8 == 0, H <= 16384; with q H % 128 == 0, and T % 128 == 0 in the
@@ -399,7 +401,8 @@ int mxg_rms_norm_bwd(const mxg_rms_norm_bwd_args* args, void* stream);
  * order; sums that leave fp32's range are taken in fp64 throughout, so norms of
  * gradients of any finite size are right (written as infinity beyond fp32, while
  * mxg_grad_clip's own factor still has its value).  An infinite norm clips to
- * zero (an infinite element to NaN), one that is NaN makes every output NaN.
+ * zero (an infinite element to NaN), one that is NaN makes every output NaN; a
+ * max_norm of infinity clips nothing.
  *   workspace  >= mxg_grad_norm_workspace_bytes(n) bytes
  * mxg_grad_clip takes the norm itself and writes it to norm_out (nullable), or,
  * given norm_in (fp32 [1], device; e.g. joined over ranks), scales by that and
